@@ -412,6 +412,129 @@ MOK_API mok_status mok_ep_backward(const mok_schedule* sched, const mok_ep_group
 MOK_API mok_status mok_ep_combine(const mok_shape* shape, const mok_ep_group* ep, const int32_t* topk_ids,
                                   const float* topk_weights, const void* recv, void* out, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Dense operators around the layer: what a transformer sublayer built on the routed experts needs
+ * next to them.  The residual stream is bf16 or fp32 (stream_type); branches, normalised rows and
+ * their gradients are bf16.  Rows are contiguous; widths are multiples of 8 values and every bf16,
+ * fp32 or E4M3 tensor starts on a 16-byte boundary (MOK_ERR_INVALID_ARG otherwise).  All of it
+ * follows the conventions at the top: enqueue only, no allocation, bitwise repeatable results,
+ * safe to capture.
+ * ------------------------------------------------------------------------------------------- */
+typedef enum { MOK_DT_BF16 = 0, MOK_DT_FP32 = 1 } mok_dtype;
+
+/* Dropout from a counter-based generator; no mask is stored.  Values are taken in groups of 8 in
+ * memory order; group i's eight 16-bit draws are the words of Philox4x32-10 (Salmon et al., 2011) with key
+ * = rng[0] and counter = (i, rng[1]), low half of each word first.  A value is dropped when its draw is
+ * below t = floor(p * 65536 + 0.5), else scaled by 65536 / (65536 - t), in fp32: p acts in steps of
+ * 2^-16 and the scale belongs to the step taken.  A dropped value contributes exactly 0, whatever it
+ * holds (an infinity or a NaN too).  p in [0, 1] (at t = 65536 everything is dropped).
+ *   rng   DEVICE pointer to two 64-bit words {seed, offset}, 8-byte aligned, read when the kernel
+ *         runs: a captured step draws new masks when the caller advances them between replays, and a
+ *         backward draws its forward's mask while they are unchanged. */
+typedef struct {
+  float p;
+  const uint64_t* rng;
+} mok_dropout;
+
+/* out = residual + dropout(x).  x [n] bf16; residual [n] of stream_type or NULL (0); out [n] of
+ * stream_type (may be the residual's buffer, or x's when stream_type is MOK_DT_BF16).  n >= 0, a
+ * multiple of 8. */
+MOK_API mok_status mok_dropout_forward(int64_t n, int32_t stream_type, const mok_dropout* drop, const void* x,
+                                       const void* residual, void* out, void* stream);
+
+/* Gradient of the branch: dx [n] bf16 = dropout's factors times dout [n] of stream_type (the
+ * residual's gradient is dout itself).  dx may be dout's buffer when stream_type is MOK_DT_BF16. */
+MOK_API mok_status mok_dropout_backward(int64_t n, int32_t stream_type, const mok_dropout* drop, const void* dout,
+                                        void* dx, void* stream);
+
+/* Root-mean-square norm of the residual stream.  T >= 0 rows of H values, 8 <= H <= 16384, H a
+ * multiple of 8 (of 32 for the MXFP8 output); eps finite and >= 0. */
+typedef struct {
+  int64_t T;
+  int32_t H;
+  int32_t stream_type; /* mok_dtype of residual, h and their gradients */
+  float eps;
+} mok_norm_shape;
+
+/* h = residual + dropout(x); y = h * rstd * weight, rstd = 1 / sqrt(mean over the row of h^2 + eps).
+ * The norm is of h as stored (rounded to the stream's type): the backward, which reads h,
+ * differentiates the same function.  Statistics and products in fp32, each output rounded once.
+ *   x [T, H] bf16; residual [T, H] of stream_type or NULL (h = dropout(x)); drop NULL: no dropout;
+ *   weight [H] bf16.
+ *   h [T, H] of stream_type, may be the residual's buffer; NULL only where h is x itself (no residual, no
+ *   dropout, bf16 stream);
+ *   y [T, H] bf16 and / or yq [T, H] E4M3 with ys [T, H/32] E8M0: the unrounded y in the format of
+ *   mok_mxfp8_quantize.  y NULL, or yq and ys NULL, leaves that output out, not both;
+ *   rstd [T] fp32, for the backward; may be NULL. */
+MOK_API mok_status mok_rmsnorm_forward(const mok_norm_shape* shape, const void* x, const void* residual,
+                                       const mok_dropout* drop, const void* weight, void* h, void* y, uint8_t* yq,
+                                       uint8_t* ys, float* rstd, void* stream);
+
+/* Bytes of device workspace of mok_rmsnorm_backward (256-byte aligned): partial sums of dweight.  0
+ * for an unsupported shape. */
+MOK_API size_t mok_rmsnorm_workspace_bytes(const mok_norm_shape* shape);
+
+/* With xh = h rstd and g = dy weight: dh = rstd (g - xh mean over the row of (g xh)) + dres, the
+ * gradient of the residual; dx = dropout's factors times dh, the branch's; dweight = sum over rows of
+ * dy xh, in a fixed order.
+ *   h, rstd: the forward's; dy [T, H] bf16 = dL/dy; dres [T, H] of stream_type = dL/dh from the stream's
+ *   other uses, or NULL (0); drop: the forward's, or NULL;
+ *   dh [T, H] of stream_type, may be dres's buffer; NULL if not wanted;
+ *   dx [T, H] bf16, may be dy's buffer; NULL if not wanted (without dropout on a bf16 stream dh is dx);
+ *   dweight [H] fp32 (T = 0 gives zeros). */
+MOK_API mok_status mok_rmsnorm_backward(const mok_norm_shape* shape, const void* h, const float* rstd,
+                                        const void* weight, const void* dy, const void* dres, const mok_dropout* drop,
+                                        void* dh, void* dx, float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* Dense gated feed-forward block (the shared expert next to the routed ones, or a dense layer):
+ *   g = x Wg^T, u = x Wu^T, a = act(g) u, out = a Wd^T + residual
+ * with weights in the layer's [out, in] convention: w_gate, w_up [I, H], w_down [H, I] bf16.  T >= 0 tokens,
+ * from the single token of a decoding step up; H and I multiples of 8, 8 <= H, I <= 65536.  fp32
+ * accumulation; a is rounded to bf16 between the two products, and dg, du in the backward (they feed the
+ * tensor cores), everything else once at the end.
+ * act: MOK_ACT_SILU  act(g) = g sigmoid(g);
+ *      MOK_ACT_GELU  the tanh form, 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))). */
+typedef enum { MOK_ACT_SILU = 0, MOK_ACT_GELU = 1 } mok_activation;
+typedef struct {
+  int64_t T;
+  int32_t H, I;
+  int32_t act; /* mok_activation */
+} mok_ffn_shape;
+
+/* Bytes of the block's context (256-byte aligned device buffer).  save = 0: what one forward needs (a);
+ * save = 1: with g and u in fp32 for mok_ffn_backward.  0 for an unsupported shape. */
+MOK_API size_t mok_ffn_ctx_bytes(const mok_ffn_shape* shape, int32_t save);
+
+/* Forward.  x [T, H] bf16; residual [T, H] bf16 or NULL (0); out [T, H] bf16 (may be the residual's
+ * buffer); ctx, ctx_bytes: as sized by mok_ffn_ctx_bytes with the same `save`; status: device word
+ * (bit (1 << mok_status code) per problem seen, never cleared here) or NULL. */
+MOK_API mok_status mok_ffn_forward(const mok_ffn_shape* shape, const void* x, const void* w_gate, const void* w_up,
+                                   const void* w_down, const void* residual, void* out, void* ctx, size_t ctx_bytes,
+                                   int32_t save, uint32_t* status, void* stream);
+
+/* Gradients, overwritten: dx [T, H] bf16; dw_gate, dw_up [I, H] and dw_down [H, I] of dw_type (mok_dtype;
+ * T = 0 gives zeros).  dx, dw_down, or dw_gate and dw_up together, may be NULL: not computed. */
+typedef struct {
+  void* dx;
+  void* dw_gate;
+  void* dw_up;
+  void* dw_down;
+  int32_t dw_type;
+} mok_ffn_grads;
+
+/* Bytes of device workspace of mok_ffn_backward (256-byte aligned): dg and du.  0 for an unsupported
+ * shape. */
+MOK_API size_t mok_ffn_workspace_bytes(const mok_ffn_shape* shape);
+
+/* Backward from dy [T, H] bf16 = dL/dout (the residual's gradient is dy itself):
+ *   da = dy Wd, dg = da u act'(g), du = da act(g), dx = dg Wg + du Wu,
+ *   dWg = dg^T x, dWu = du^T x, dWd = dy^T a.
+ * ctx: the matching mok_ffn_forward's, with save = 1. */
+MOK_API mok_status mok_ffn_backward(const mok_ffn_shape* shape, const void* x, const void* w_gate, const void* w_up,
+                                    const void* w_down, const void* ctx, size_t ctx_bytes, const void* dy,
+                                    const mok_ffn_grads* grads, void* ws, size_t ws_bytes, uint32_t* status,
+                                    void* stream);
+
 /* Copy the schedule's device status word to *out (host pointer) after synchronising the stream.
  * The only call that blocks. */
 MOK_API mok_status mok_read_device_status(const mok_schedule* sched, uint32_t* out, void* stream);

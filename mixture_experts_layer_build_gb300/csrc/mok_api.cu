@@ -624,7 +624,9 @@ const char* mok_kernel_name(int32_t kind) {
       "gemm_dgrad2",     "dx_reduce",     "gemm_wgrad_gu", "gemm_wgrad_d",   "mxfp8_quantize",
       "mx_scale_atoms",  "router_logits", "router_topk",   "router_transpose", "router_dx",
       "router_dw",       "selftest_wait", "push_y",        "push_dx",        "ep_combine",
-      "ep_dx_reduce",    "ds_push"};
+      "ep_dx_reduce",    "ds_push",       "rmsnorm_fwd",   "rmsnorm_bwd",    "rmsnorm_dw",
+      "dropout_fwd",     "dropout_bwd",   "ffn_gateup",    "ffn_down",      "ffn_dact",
+      "ffn_dx",          "ffn_dwgu",      "ffn_dwd"};
   return (kind >= 0 && kind < K_NUM_KINDS) ? names[kind] : "?";
 }
 

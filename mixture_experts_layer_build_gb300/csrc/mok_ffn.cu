@@ -1,0 +1,127 @@
+// mok_ffn.cu -- the C ABI of the dense gated feed-forward block: checks, buffers and the order of its
+// contractions.
+#include "mok_ffn.cuh"
+
+namespace mok {
+namespace {
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+bool ffn_shape_ok(const mok_ffn_shape* s) {
+  return s && s->T >= 0 && s->T < (int64_t{1} << 31) - 256 && s->H >= 8 && s->I >= 8 && s->H <= 65536 &&
+         s->I <= 65536 && s->H % 8 == 0 && s->I % 8 == 0 && (s->act == MOK_ACT_SILU || s->act == MOK_ACT_GELU);
+}
+
+// The context: a [T, I] bf16, then (saved) g and u [T, I] fp32.
+struct FfnCtx {
+  uint16_t* a;
+  float* g;
+  float* u;
+  size_t bytes;
+  FfnCtx(const mok_ffn_shape& s, bool save, const void* p) {
+    char* base = static_cast<char*>(const_cast<void*>(p));
+    const size_t n = static_cast<size_t>(s.T) * s.I;
+    const size_t og = up256(2 * n), ou = og + up256(4 * n);
+    a = reinterpret_cast<uint16_t*>(base);
+    g = save ? reinterpret_cast<float*>(base + og) : nullptr;
+    u = save ? reinterpret_cast<float*>(base + ou) : nullptr;
+    bytes = save ? ou + up256(4 * n) : og;
+    if (bytes < 256) bytes = 256;
+  }
+};
+
+bool unaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+bool need16(const void* p) { return p && !unaligned(p, 16); }
+
+}  // namespace
+}  // namespace mok
+
+using namespace mok;
+
+extern "C" {
+
+size_t mok_ffn_ctx_bytes(const mok_ffn_shape* s, int32_t save) {
+  return ffn_shape_ok(s) ? FfnCtx(*s, save != 0, nullptr).bytes : 0;
+}
+
+size_t mok_ffn_workspace_bytes(const mok_ffn_shape* s) {
+  if (!ffn_shape_ok(s)) return 0;
+  const size_t n = up256(static_cast<size_t>(s->T) * s->I * 2);
+  return n ? 2 * n : 256;
+}
+
+mok_status mok_ffn_forward(const mok_ffn_shape* s, const void* x, const void* w_gate, const void* w_up,
+                           const void* w_down, const void* residual, void* out, void* ctx, size_t ctx_bytes,
+                           int32_t save, uint32_t* status, void* stream) {
+  if (!ffn_shape_ok(s) || !ctx || unaligned(ctx, 256) || unaligned(status, 4)) return MOK_ERR_INVALID_ARG;
+  const FfnCtx c(*s, save != 0, ctx);
+  if (ctx_bytes < c.bytes) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  if (s->T == 0) return MOK_OK;
+  if (!need16(x) || !need16(w_gate) || !need16(w_up) || !need16(w_down) || !need16(out) || unaligned(residual, 16))
+    return MOK_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  FfnArgs a{};
+  a.act = s->act;
+  a.status = status;
+  a.out0 = c.a;
+  a.g = c.g;
+  a.u = c.u;
+  if (launch_ffn_gemm(F_GATEUP, s->T, s->I, s->H, {x, nullptr, w_gate, w_up}, a, st)) return MOK_ERR_CUDA;
+  a.out0 = out;
+  a.g = a.u = nullptr;
+  a.residual = static_cast<const uint16_t*>(residual);
+  return launch_ffn_gemm(F_DOWN, s->T, s->H, s->I, {c.a, nullptr, w_down, nullptr}, a, st) ? MOK_ERR_CUDA : MOK_OK;
+}
+
+mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w_gate, const void* w_up,
+                            const void* w_down, const void* ctx, size_t ctx_bytes, const void* dy,
+                            const mok_ffn_grads* gr, void* ws, size_t ws_bytes, uint32_t* status, void* stream) {
+  if (!ffn_shape_ok(s) || !gr || (gr->dw_type != MOK_DT_BF16 && gr->dw_type != MOK_DT_FP32) || unaligned(status, 4))
+    return MOK_ERR_INVALID_ARG;
+  if ((gr->dw_gate == nullptr) != (gr->dw_up == nullptr) || unaligned(gr->dx, 16) || unaligned(gr->dw_gate, 16) ||
+      unaligned(gr->dw_up, 16) || unaligned(gr->dw_down, 16))
+    return MOK_ERR_INVALID_ARG;
+  if (!ctx || unaligned(ctx, 256) || !ws || unaligned(ws, 256)) return MOK_ERR_INVALID_ARG;
+  const FfnCtx c(*s, true, ctx);
+  if (ctx_bytes < c.bytes || ws_bytes < mok_ffn_workspace_bytes(s)) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->T == 0) {  // sums over no tokens
+    const size_t n = static_cast<size_t>(s->H) * s->I * (gr->dw_type == MOK_DT_FP32 ? 4 : 2);
+    for (void* p : {gr->dw_gate, gr->dw_up, gr->dw_down})
+      if (p && cudaMemsetAsync(p, 0, n, st) != cudaSuccess) return MOK_ERR_CUDA;
+    return MOK_OK;
+  }
+  if (!need16(x) || !need16(w_gate) || !need16(w_up) || !need16(w_down) || !need16(dy)) return MOK_ERR_INVALID_ARG;
+  uint16_t* dg = static_cast<uint16_t*>(ws);
+  uint16_t* du = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + up256(static_cast<size_t>(s->T) * s->I * 2));
+  FfnArgs a{};
+  a.act = s->act;
+  a.status = status;
+  a.out_f32 = gr->dw_type == MOK_DT_FP32;
+  if (gr->dx || gr->dw_gate) {
+    a.out0 = dg;
+    a.out1 = du;
+    a.g = c.g;
+    a.u = c.u;
+    if (launch_ffn_gemm(F_DACT, s->T, s->I, s->H, {dy, nullptr, w_down, nullptr}, a, st)) return MOK_ERR_CUDA;
+    a.g = a.u = nullptr;
+  }
+  if (gr->dx) {
+    a.out0 = gr->dx;
+    a.out1 = nullptr;
+    if (launch_ffn_gemm(F_DX, s->T, s->H, s->I, {dg, du, w_gate, w_up}, a, st)) return MOK_ERR_CUDA;
+  }
+  if (gr->dw_gate) {
+    a.out0 = gr->dw_gate;
+    a.out1 = gr->dw_up;
+    if (launch_ffn_gemm(F_DWGU, s->I, s->H, s->T, {dg, du, x, nullptr}, a, st)) return MOK_ERR_CUDA;
+  }
+  if (gr->dw_down) {
+    a.out0 = gr->dw_down;
+    a.out1 = nullptr;
+    if (launch_ffn_gemm(F_DWD, s->H, s->I, s->T, {dy, nullptr, c.a, nullptr}, a, st)) return MOK_ERR_CUDA;
+  }
+  return MOK_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,85 @@
+// mok_ffn.cuh -- the dense gated feed-forward block: what its kernels share (sizes, arguments, the
+// activations).
+//
+// Six contractions over tokens t, hidden h and intermediate i (row-major operands; K is the summed
+// index):
+//   GATEUP  [g | u] = x [Wg | Wu]^T, epilogue a = act(g) u           M = T, N = I (twice), K = H
+//   DOWN    out = a Wd^T + residual                                  M = T, N = H, K = I
+//   DACT    da = dy Wd, epilogue dg = da u act'(g), du = da act(g)   M = T, N = I, K = H
+//   DX      dx = dg Wg + du Wu                                       M = T, N = H, K = I twice
+//   DWGU    [dWg ; dWu] = [dg | du]^T x                              M = I twice, N = H, K = T
+//   DWD     dWd = dy^T a                                             M = H, N = I, K = T
+// An operand whose rows run along K is K-major for the MMA, one whose rows run along M or N is
+// MN-major: weights in DACT and DX, both operands in DWGU and DWD.
+#pragma once
+#include <cuda.h>
+
+#include "mok_internal.cuh"
+#include "mok_once.h"
+#include "mok_ptx.cuh"
+
+namespace mok {
+
+enum FfnVariant : int { F_GATEUP = 0, F_DOWN, F_DACT, F_DX, F_DWGU, F_DWD };
+
+__host__ __device__ constexpr bool ffn_a_mn(int v) { return v == F_DWGU || v == F_DWD; }
+__host__ __device__ constexpr bool ffn_b_mn(int v) { return v >= F_DACT; }
+
+constexpr int kFfnBK = 64;  // bf16 of K per block: one 128-byte swizzle row
+
+struct FfnArgs {
+  int32_t M, N;         // rows and columns of the output (DWGU: rows of one of its two outputs)
+  int32_t m_tiles, n_tiles;
+  int32_t m_half;       // DWGU: M tiles of dWg; the rest are dWu's
+  int32_t k_blocks;
+  int32_t kb_split;     // DX: K blocks over (dg, Wg), then the same over (du, Wu)
+  int32_t act;
+  int32_t out_f32;      // DWGU, DWD: fp32 outputs instead of bf16
+  void* out0;           // a | out | dg | dx | dWg | dWd
+  void* out1;           // - | -   | du | -  | dWu | -
+  float* g;             // GATEUP: saved when not null; DACT: read
+  float* u;
+  const uint16_t* residual;  // DOWN, may be null
+  uint32_t* status;
+};
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+// act(g) and, for the backward, act'(g).  The tanh form of GELU is g sigmoid(2 z), z = c (g + k g^3),
+// since (1 + tanh z) / 2 = sigmoid(2 z): no cancellation for negative g.  The exponential and the
+// division are the fast approximations (a few ulp of fp32): what they feed is rounded to bf16 (2^-9).
+__device__ __forceinline__ float act_fwd(float g, int act) {
+  if (act == MOK_ACT_SILU) return g * sigmoid_fast(g);
+  return g * sigmoid_fast(1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.0f));
+}
+__device__ __forceinline__ void act_bwd(float g, int act, float& f, float& df) {
+  if (act == MOK_ACT_SILU) {
+    const float s = sigmoid_fast(g);
+    f = g * s;
+    df = s * fmaf(g, 1.0f - s, 1.0f);
+  } else {
+    const float s = sigmoid_fast(1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.0f));
+    f = g * s;
+    df = fmaf(f * (1.0f - s), 1.5957691216057308f * fmaf(3.0f * 0.044715f * g, g, 1.0f), s);
+  }
+}
+#endif
+
+// Host: maps and launches (mok_ffn_tile.cu: one tile per CTA).
+struct FfnMaps {
+  CUtensorMap a, a2, b, b2;
+};
+bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                    uint32_t box_outer);
+
+struct FfnOperands {
+  const void* a;   // x | a | dy | dg | dg | dy
+  const void* a2;  // -         du   du
+  const void* b;   // Wg | Wd | Wd | Wg | x | a
+  const void* b2;  // Wu            Wu
+};
+// One GEMM: M, N, K of the variant (K of one half for DX), operands and args' epilogue fields set.
+int launch_ffn_gemm(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, FfnArgs a, cudaStream_t stream);
+
+}  // namespace mok

@@ -149,6 +149,17 @@ enum KernelKind : int {
   K_EP_COMBINE,
   K_EP_DX_REDUCE,
   K_DS_PUSH,
+  K_RMSNORM_FWD,
+  K_RMSNORM_BWD,
+  K_RMSNORM_DW,
+  K_DROPOUT_FWD,
+  K_DROPOUT_BWD,
+  K_FFN_GATEUP,  // the feed-forward block's kinds in the order of FfnVariant
+  K_FFN_DOWN,
+  K_FFN_DACT,
+  K_FFN_DX,
+  K_FFN_DWGU,
+  K_FFN_DWD,
   K_NUM_KINDS
 };
 void trace_begin(cudaStream_t s, int kind);  // no-ops unless a trace is set

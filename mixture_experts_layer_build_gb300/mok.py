@@ -124,7 +124,9 @@ EXPORTED = ("mok_version", "mok_status_string", "mok_workspace_bytes", "mok_fwd_
             "mok_build_schedule", "mok_forward", "mok_backward", "mok_read_device_status", "mok_set_trace",
             "mok_kernel_name", "mok_build_schedule_noalloc", "mok_mx_operands_of", "mok_router_workspace_bytes",
             "mok_router_forward", "mok_router_backward", "mok_selftest_wait_timeout", "mok_ep_build_schedule",
-            "mok_ep_forward", "mok_ep_backward", "mok_ep_combine")
+            "mok_ep_forward", "mok_ep_backward", "mok_ep_combine", "mok_dropout_forward", "mok_dropout_backward",
+            "mok_rmsnorm_forward", "mok_rmsnorm_workspace_bytes", "mok_rmsnorm_backward", "mok_ffn_ctx_bytes",
+            "mok_ffn_forward", "mok_ffn_workspace_bytes", "mok_ffn_backward")
 _lib.mok_router_workspace_bytes.restype = ctypes.c_size_t
 _lib.mok_router_workspace_bytes.argtypes = [ctypes.POINTER(mok_shape)]
 _lib.mok_router_forward.restype = ctypes.c_int
@@ -516,6 +518,255 @@ class Layer:
 
     def backward(self, dy, weights: mok_weights, stream=None) -> Grads:
         return mok_backward(self.sched, self.ctx, dy, weights, self.grads, stream)
+
+
+# ---------------------------------------------------------------------------------------------
+# dense operators around the layer: dropout, norm of the residual stream, gated feed-forward block
+# ---------------------------------------------------------------------------------------------
+MOK_DT_BF16 = 0
+MOK_DT_FP32 = 1
+MOK_ACT_SILU = 0
+MOK_ACT_GELU = 1
+_ACTS = {"silu": MOK_ACT_SILU, "gelu": MOK_ACT_GELU}
+_STREAM_TYPES = {torch.bfloat16: MOK_DT_BF16, torch.float32: MOK_DT_FP32}
+
+
+class mok_dropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("rng", _P)]
+
+
+class mok_norm_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("stream_type", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class mok_ffn_shape(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("I", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+class mok_ffn_grads(ctypes.Structure):
+    _fields_ = [("dx", _P), ("dw_gate", _P), ("dw_up", _P), ("dw_down", _P), ("dw_type", ctypes.c_int32)]
+
+
+_DROP, _NORM, _FFN = ctypes.POINTER(mok_dropout), ctypes.POINTER(mok_norm_shape), ctypes.POINTER(mok_ffn_shape)
+_lib.mok_dropout_forward.restype = ctypes.c_int
+_lib.mok_dropout_forward.argtypes = [ctypes.c_int64, ctypes.c_int32, _DROP, _P, _P, _P, _P]
+_lib.mok_dropout_backward.restype = ctypes.c_int
+_lib.mok_dropout_backward.argtypes = [ctypes.c_int64, ctypes.c_int32, _DROP, _P, _P, _P]
+_lib.mok_rmsnorm_forward.restype = ctypes.c_int
+_lib.mok_rmsnorm_forward.argtypes = [_NORM, _P, _P, _DROP, _P, _P, _P, _P, _P, _P, _P]
+_lib.mok_rmsnorm_workspace_bytes.restype = ctypes.c_size_t
+_lib.mok_rmsnorm_workspace_bytes.argtypes = [_NORM]
+_lib.mok_rmsnorm_backward.restype = ctypes.c_int
+_lib.mok_rmsnorm_backward.argtypes = [_NORM, _P, _P, _P, _P, _P, _DROP, _P, _P, _P, _P, ctypes.c_size_t, _P]
+_lib.mok_ffn_ctx_bytes.restype = ctypes.c_size_t
+_lib.mok_ffn_ctx_bytes.argtypes = [_FFN, ctypes.c_int32]
+_lib.mok_ffn_forward.restype = ctypes.c_int
+_lib.mok_ffn_forward.argtypes = [_FFN, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, ctypes.c_int32, _P, _P]
+_lib.mok_ffn_workspace_bytes.restype = ctypes.c_size_t
+_lib.mok_ffn_workspace_bytes.argtypes = [_FFN]
+_lib.mok_ffn_backward.restype = ctypes.c_int
+_lib.mok_ffn_backward.argtypes = [_FFN, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, ctypes.POINTER(mok_ffn_grads), _P,
+                                  ctypes.c_size_t, _P, _P]
+
+
+def _arg(t: torch.Tensor | None, shape, dtype, name: str):
+    """data_ptr of a contiguous CUDA tensor of that shape and dtype (None passes as NULL)."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _ptr(t, dtype, name)
+
+
+class Dropout:
+    """Dropout probability and generator state: rng, int64 [2] on the device, the bit patterns of
+    {seed, offset}, read by the kernels when they run.  Each call that draws masks uses them all
+    from the same state: advance the offset (``rng[1] += 1``) between calls."""
+
+    def __init__(self, p: float, rng: torch.Tensor):
+        self.rng = rng  # kept alive with the pointer
+        self.c = mok_dropout(p, _arg(rng, (2,), torch.int64, "rng"))
+        self.ref = ctypes.byref(self.c)
+
+
+def _stream_type(t: torch.Tensor, name: str) -> int:
+    st = _STREAM_TYPES.get(t.dtype)
+    if st is None:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return st
+
+
+def dropout_forward(x: torch.Tensor, dropout: Dropout, residual: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """residual + dropout(x): x bf16, residual bf16 or fp32 of x's shape; out of the residual's type
+    (bf16 without one).  The number of values is a multiple of 8."""
+    like = residual if residual is not None else x
+    if out is None:
+        out = torch.empty_like(like)
+    st = _stream_type(like, "residual")
+    _check(_lib.mok_dropout_forward(x.numel(), st, dropout.ref, _ptr(x, torch.bfloat16, "x"),
+                                    _arg(residual, x.shape, like.dtype, "residual"),
+                                    _arg(out, x.shape, like.dtype, "out"), _stream(stream)), "mok_dropout_forward")
+    return out
+
+
+def dropout_backward(dout: torch.Tensor, dropout: Dropout, dx: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """The branch's gradient (bf16) for dout of the stream's type, under the forward's masks."""
+    if dx is None:
+        dx = torch.empty(dout.shape, dtype=torch.bfloat16, device=dout.device)
+    _check(_lib.mok_dropout_backward(dout.numel(), _stream_type(dout, "dout"), dropout.ref, _ptr(dout, None, "dout"),
+                                     _arg(dx, dout.shape, torch.bfloat16, "dx"), _stream(stream)),
+           "mok_dropout_backward")
+    return dx
+
+
+@dataclass
+class NormOut:
+    h: torch.Tensor               # the residual stream after the addition
+    y: torch.Tensor | None        # normalised rows, bf16
+    q: torch.Tensor | None        # the same in MXFP8: E4M3 codes (uint8) ...
+    s: torch.Tensor | None        # ... and E8M0 scales (uint8) [T, H / 32]
+    rstd: torch.Tensor            # 1 / rms of each row, fp32
+
+
+def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: torch.Tensor | None = None,
+                    dropout: Dropout | None = None, bf16: bool = True, mx: bool = False, stream=None) -> NormOut:
+    """h = residual + dropout(x) and its root-mean-square norm times weight (mok_rmsnorm_forward):
+    x [T, H] bf16, residual [T, H] bf16 or fp32 (the type of h), weight [H] bf16.  bf16 / mx choose the
+    outputs.  Without residual and dropout h is x."""
+    T, H = x.shape
+    like = residual if residual is not None else x
+    st = _stream_type(like, "residual")
+    dev = x.device
+    h = torch.empty_like(like) if residual is not None or dropout is not None else None
+    y = torch.empty_like(x) if bf16 else None
+    q = torch.empty((T, H), dtype=torch.uint8, device=dev) if mx else None
+    s = torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if mx else None
+    rstd = torch.empty((T,), dtype=torch.float32, device=dev)
+    shape = mok_norm_shape(T, H, st, eps)
+    _check(_lib.mok_rmsnorm_forward(ctypes.byref(shape), _ptr(x, torch.bfloat16, "x"),
+                                    _arg(residual, x.shape, like.dtype, "residual"),
+                                    dropout.ref if dropout is not None else None,
+                                    _arg(weight, (H,), torch.bfloat16, "weight"), None if h is None else h.data_ptr(),
+                                    None if y is None else y.data_ptr(), None if q is None else q.data_ptr(),
+                                    None if s is None else s.data_ptr(), rstd.data_ptr(), _stream(stream)),
+           "mok_rmsnorm_forward")
+    return NormOut(x if h is None else h, y, q, s, rstd)
+
+
+@dataclass
+class NormGrads:
+    dh: torch.Tensor         # of the residual, in the stream's type
+    dx: torch.Tensor         # of the branch, bf16 (dh itself without dropout on a bf16 stream)
+    dweight: torch.Tensor    # fp32 [H]
+
+
+def mok_rmsnorm_workspace_bytes(shape: mok_norm_shape) -> int:
+    n = _lib.mok_rmsnorm_workspace_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise MokError(MOK_ERR_INVALID_ARG, "mok_rmsnorm_workspace_bytes")
+    return n
+
+
+def rmsnorm_backward(h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
+                     dres: torch.Tensor | None = None, dropout: Dropout | None = None, stream=None) -> NormGrads:
+    """Gradients of rmsnorm_forward from dy [T, H] bf16 = dL/dy and dres = dL/dh from the stream's other
+    uses (h's type, or None), under the forward's masks."""
+    T, H = h.shape
+    dev = h.device
+    shape = mok_norm_shape(T, H, _stream_type(h, "h"), 0.0)
+    dh = torch.empty_like(h)
+    own_dx = dropout is not None or h.dtype != torch.bfloat16
+    dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if own_dx else None
+    dw = torch.empty((H,), dtype=torch.float32, device=dev)
+    ws = torch.empty(mok_rmsnorm_workspace_bytes(shape), dtype=torch.uint8, device=dev)
+    _check(_lib.mok_rmsnorm_backward(ctypes.byref(shape), _ptr(h, None, "h"), _arg(rstd, (T,), torch.float32, "rstd"),
+                                     _arg(weight, (H,), torch.bfloat16, "weight"),
+                                     _arg(dy, h.shape, torch.bfloat16, "dy"), _arg(dres, h.shape, h.dtype, "dres"),
+                                     dropout.ref if dropout is not None else None, dh.data_ptr(),
+                                     None if dx is None else dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws.numel(),
+                                     _stream(stream)), "mok_rmsnorm_backward")
+    return NormGrads(dh, dh if dx is None else dx, dw)
+
+
+def mok_ffn_ctx_bytes(shape: mok_ffn_shape, save: bool) -> int:
+    n = _lib.mok_ffn_ctx_bytes(ctypes.byref(shape), 1 if save else 0)
+    if n == 0:
+        raise MokError(MOK_ERR_INVALID_ARG, "mok_ffn_ctx_bytes")
+    return n
+
+
+def mok_ffn_workspace_bytes(shape: mok_ffn_shape) -> int:
+    n = _lib.mok_ffn_workspace_bytes(ctypes.byref(shape))
+    if n == 0:
+        raise MokError(MOK_ERR_INVALID_ARG, "mok_ffn_workspace_bytes")
+    return n
+
+
+@dataclass
+class FFNGrads:
+    dx: torch.Tensor
+    dw_gate: torch.Tensor
+    dw_up: torch.Tensor
+    dw_down: torch.Tensor
+
+
+class FFN:
+    """Owner of the buffers of one dense gated feed-forward block (mok_ffn_forward / _backward):
+    act(x Wg^T) * (x Wu^T) Wd^T + residual for T tokens, w_gate, w_up [I, H] and w_down [H, I] bf16.  act:
+    "silu" or "gelu" (tanh form).  train: the forward saves what the backward reads.  dw_dtype: type
+    of the weight gradients, torch.bfloat16 or torch.float32.  Outputs are the plan's own buffers,
+    overwritten by the next call."""
+
+    def __init__(self, T: int, H: int, I: int, act: str = "silu", train: bool = True, dw_dtype=torch.bfloat16,
+                 device="cuda"):
+        if act not in _ACTS:
+            raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+        if dw_dtype not in _STREAM_TYPES:
+            raise ValueError(f"dw_dtype must be torch.bfloat16 or torch.float32, got {dw_dtype}")
+        self.T, self.H, self.I, self.train = T, H, I, train
+        self.shape = mok_ffn_shape(T, H, I, _ACTS[act])
+        self.ctx = torch.empty(mok_ffn_ctx_bytes(self.shape, train), dtype=torch.uint8, device=device)
+        self.out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+        self.status = torch.zeros((1,), dtype=torch.int32, device=device)
+        self._ref = ctypes.byref(self.shape)
+        self._fwd_ptrs = (self.out.data_ptr(), self.ctx.data_ptr(), self.ctx.numel(), 1 if train else 0,
+                          self.status.data_ptr())
+        if train:
+            e = lambda *s: torch.empty(s, dtype=dw_dtype, device=device)  # noqa: E731
+            self.grads = FFNGrads(torch.empty_like(self.out), e(I, H), e(I, H), e(H, I))
+            self.ws = torch.empty(mok_ffn_workspace_bytes(self.shape), dtype=torch.uint8, device=device)
+            g = self.grads
+            self._grads = mok_ffn_grads(g.dx.data_ptr(), g.dw_gate.data_ptr(), g.dw_up.data_ptr(),
+                                        g.dw_down.data_ptr(), _STREAM_TYPES[dw_dtype])
+
+    def _in(self, x, w_gate, w_up, w_down):
+        xs, ws, bf = (self.T, self.H), (self.I, self.H), torch.bfloat16
+        return (_arg(x, xs, bf, "x"), _arg(w_gate, ws, bf, "w_gate"), _arg(w_up, ws, bf, "w_up"),
+                _arg(w_down, (self.H, self.I), bf, "w_down"))
+
+    def forward(self, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+                residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        out, ctx, n, save, status = self._fwd_ptrs
+        _check(_lib.mok_ffn_forward(self._ref, *self._in(x, w_gate, w_up, w_down),
+                                    _arg(residual, (self.T, self.H), torch.bfloat16, "residual"), out, ctx, n, save,
+                                    status, _stream(stream)), "mok_ffn_forward")
+        return self.out
+
+    def backward(self, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
+                 dy: torch.Tensor, stream=None) -> FFNGrads:
+        if not self.train:
+            raise ValueError("backward needs a plan made with train=True")
+        _check(_lib.mok_ffn_backward(self._ref, *self._in(x, w_gate, w_up, w_down), self.ctx.data_ptr(),
+                                     self.ctx.numel(), _arg(dy, (self.T, self.H), torch.bfloat16, "dy"),
+                                     ctypes.byref(self._grads), self.ws.data_ptr(), self.ws.numel(),
+                                     self.status.data_ptr(), _stream(stream)), "mok_ffn_backward")
+        return self.grads
+
+    def device_status(self) -> int:
+        """The block's device status word, bits (1 << status code); synchronises."""
+        return int(self.status.item())
 
 
 def mok_kernel_name(kind: int) -> str:
