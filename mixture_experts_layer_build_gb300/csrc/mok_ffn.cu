@@ -12,7 +12,7 @@ bool ffn_shape_ok(const mok_ffn_shape* s) {
          s->I <= 65536 && s->H % 8 == 0 && s->I % 8 == 0 && (s->act == MOK_ACT_SILU || s->act == MOK_ACT_GELU);
 }
 
-// The context: a [T, I] bf16, then (saved) g and u [T, I] fp32.
+// The context: a [T, I] bf16, then (saved) g and u fp32 in the layout of ffn_saved_offset.
 struct FfnCtx {
   uint16_t* a;
   float* g;
@@ -21,17 +21,27 @@ struct FfnCtx {
   FfnCtx(const mok_ffn_shape& s, bool save, const void* p) {
     char* base = static_cast<char*>(const_cast<void*>(p));
     const size_t n = static_cast<size_t>(s.T) * s.I;
-    const size_t og = up256(2 * n), ou = og + up256(4 * n);
+    const size_t ns = (static_cast<size_t>(s.T) + 31) / 32 * 32 * s.I;
+    const size_t og = up256(2 * n), ou = og + up256(4 * ns);
     a = reinterpret_cast<uint16_t*>(base);
     g = save ? reinterpret_cast<float*>(base + og) : nullptr;
     u = save ? reinterpret_cast<float*>(base + ou) : nullptr;
-    bytes = save ? ou + up256(4 * n) : og;
+    bytes = save ? ou + up256(4 * ns) : og;
     if (bytes < 256) bytes = 256;
   }
 };
 
 bool unaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 bool need16(const void* p) { return p && !unaligned(p, 16); }
+
+// Pairs (256-row tiles) from the tokens on that fill half of one round of them; the tile kernel below.
+int launch_ffn_gemm(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
+                    cudaStream_t stream) {
+  const int cols = var == F_GATEUP ? 128 : 256;
+  const int64_t units = (M + 255) / 256 * ((N + cols - 1) / cols);
+  return 4 * units >= sm_count() ? launch_ffn_pair(var, M, N, K, o, a, stream)
+                                 : launch_ffn_tile(var, M, N, K, o, a, stream);
+}
 
 }  // namespace
 }  // namespace mok
@@ -97,7 +107,6 @@ mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w
   FfnArgs a{};
   a.act = s->act;
   a.status = status;
-  a.out_f32 = gr->dw_type == MOK_DT_FP32;
   if (gr->dx || gr->dw_gate) {
     a.out0 = dg;
     a.out1 = du;
@@ -111,16 +120,8 @@ mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w
     a.out1 = nullptr;
     if (launch_ffn_gemm(F_DX, s->T, s->H, s->I, {dg, du, w_gate, w_up}, a, st)) return MOK_ERR_CUDA;
   }
-  if (gr->dw_gate) {
-    a.out0 = gr->dw_gate;
-    a.out1 = gr->dw_up;
-    if (launch_ffn_gemm(F_DWGU, s->I, s->H, s->T, {dg, du, x, nullptr}, a, st)) return MOK_ERR_CUDA;
-  }
-  if (gr->dw_down) {
-    a.out0 = gr->dw_down;
-    a.out1 = nullptr;
-    if (launch_ffn_gemm(F_DWD, s->H, s->I, s->T, {dy, nullptr, c.a, nullptr}, a, st)) return MOK_ERR_CUDA;
-  }
+  const FfnGradOperands go{dg, du, x, dy, c.a, gr->dw_gate, gr->dw_up, gr->dw_down};
+  if (launch_ffn_dw(s->T, s->H, s->I, go, gr->dw_type == MOK_DT_FP32, status, st)) return MOK_ERR_CUDA;
   return MOK_OK;
 }
 

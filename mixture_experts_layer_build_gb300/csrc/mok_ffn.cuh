@@ -7,10 +7,10 @@
 //   DOWN    out = a Wd^T + residual                                  M = T, N = H, K = I
 //   DACT    da = dy Wd, epilogue dg = da u act'(g), du = da act(g)   M = T, N = I, K = H
 //   DX      dx = dg Wg + du Wu                                       M = T, N = H, K = I twice
-//   DWGU    [dWg ; dWu] = [dg | du]^T x                              M = I twice, N = H, K = T
-//   DWD     dWd = dy^T a                                             M = H, N = I, K = T
+//   DW      dWg = dg^T x, dWu = du^T x                               M = I, N = H, K = T
+//           dWd = dy^T a                                             M = H, N = I, K = T
 // An operand whose rows run along K is K-major for the MMA, one whose rows run along M or N is
-// MN-major: weights in DACT and DX, both operands in DWGU and DWD.
+// MN-major: weights in DACT and DX, both operands in DW.
 #pragma once
 #include <cuda.h>
 
@@ -20,28 +20,33 @@
 
 namespace mok {
 
-enum FfnVariant : int { F_GATEUP = 0, F_DOWN, F_DACT, F_DX, F_DWGU, F_DWD };
+enum FfnVariant : int { F_GATEUP = 0, F_DOWN, F_DACT, F_DX };  // the row-tiled ones (M = T)
 
-__host__ __device__ constexpr bool ffn_a_mn(int v) { return v == F_DWGU || v == F_DWD; }
 __host__ __device__ constexpr bool ffn_b_mn(int v) { return v >= F_DACT; }
 
 constexpr int kFfnBK = 64;  // bf16 of K per block: one 128-byte swizzle row
 
 struct FfnArgs {
-  int32_t M, N;         // rows and columns of the output (DWGU: rows of one of its two outputs)
+  int32_t M, N;         // rows and columns of the output
   int32_t m_tiles, n_tiles;
-  int32_t m_half;       // DWGU: M tiles of dWg; the rest are dWu's
   int32_t k_blocks;
   int32_t kb_split;     // DX: K blocks over (dg, Wg), then the same over (du, Wu)
   int32_t act;
-  int32_t out_f32;      // DWGU, DWD: fp32 outputs instead of bf16
-  void* out0;           // a | out | dg | dx | dWg | dWd
-  void* out1;           // - | -   | du | -  | dWu | -
+  int32_t out_f32;      // DW: fp32 outputs instead of bf16
+  void* out0;           // a | out | dg | dx
+  void* out1;           // - | -   | du | -
   float* g;             // GATEUP: saved when not null; DACT: read
   float* u;
   const uint16_t* residual;  // DOWN, may be null
   uint32_t* status;
 };
+
+// Element offset of (row, column) of the saved g and u, columns a multiple of 4 wide: blocks of 32 rows x 4
+// columns, so that a warp whose lanes hold 32 rows of an accumulator moves 512 contiguous bytes per
+// 4 columns straight from and to its registers.  Rows are padded to a multiple of 32.
+__host__ __device__ __forceinline__ int64_t ffn_saved_offset(int64_t row, int col, int I) {
+  return ((row >> 5) * (I >> 2) + (col >> 2)) * 128 + (row & 31) * 4 + (col & 3);
+}
 
 #ifdef __CUDACC__
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
@@ -66,20 +71,38 @@ __device__ __forceinline__ void act_bwd(float g, int act, float& f, float& df) {
 }
 #endif
 
-// Host: maps and launches (mok_ffn_tile.cu: one tile per CTA).
-struct FfnMaps {
-  CUtensorMap a, a2, b, b2;
-};
 bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
                     uint32_t box_outer);
+bool make_tmap_bf16_sw64(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                         uint32_t box_outer);
+bool make_tmap_f32_sw64(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                        uint32_t box_outer);
 
 struct FfnOperands {
-  const void* a;   // x | a | dy | dg | dg | dy
-  const void* a2;  // -         du   du
-  const void* b;   // Wg | Wd | Wd | Wg | x | a
-  const void* b2;  // Wu            Wu
+  const void* a;   // x  | a  | dy | dg
+  const void* a2;  // -    -    -    du
+  const void* b;   // Wg | Wd | Wd | Wg
+  const void* b2;  // Wu   -    -    Wu
 };
-// One GEMM: M, N, K of the variant (K of one half for DX), operands and args' epilogue fields set.
-int launch_ffn_gemm(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, FfnArgs a, cudaStream_t stream);
+struct FfnGradOperands {  // dw_gate == nullptr, dw_down == nullptr: not computed
+  const void* dg;
+  const void* du;
+  const void* x;
+  const void* dy;
+  const void* a;
+  void* dw_gate;
+  void* dw_up;
+  void* dw_down;
+};
+// One row-tiled contraction: M, N, K of the variant (K of one half for DX), operands and the epilogue's
+// fields of `a` set.  The tile kernel (one tile per CTA, K split when there are few tiles; mok_ffn_tile.cu)
+// and persistent CTA pairs (mok_ffn_pair.cu).
+int launch_ffn_tile(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
+                    cudaStream_t stream);
+int launch_ffn_pair(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
+                    cudaStream_t stream);
+// The weight gradients, in one launch.
+int launch_ffn_dw(int64_t T, int64_t H, int64_t I, const FfnGradOperands& o, int out_f32, uint32_t* status,
+                  cudaStream_t stream);
 
 }  // namespace mok

@@ -1,0 +1,545 @@
+// mok_ffn_pair.cu -- the feed-forward block's contractions for many tokens: persistent CTA pairs.
+//
+// A cluster of two CTAs computes 256 x BN tiles with tcgen05.mma.cta_group::2 (M = 256): each CTA loads its
+// own 128 rows of A and half of B's columns, so a CTA takes in 32 KB per 64-wide K block of a 256 x 256
+// tile and keeps six blocks in flight.  Two TMEM accumulators let one tile's epilogue run under the next
+// tile's MMAs.  Per CTA: warp 0 issues TMA loads, warp 1 (of the first CTA) the MMAs, eight warps
+// drain the accumulator, two per TMEM lane quarter with half of the columns each.
+//
+// Tiles are dealt out round robin over one pair per two SMs, in an order that keeps the tiles running
+// together in a near-square block of the output (ordered_tile), so that both operands are read from
+// L2.  The three weight gradients share one launch: alike in K, they fill the last round together.
+#include "mok_ffn.cuh"
+
+namespace mok {
+namespace {
+
+constexpr int kPairThreads = 64 + 32 * 8;
+constexpr int kGroupM = 8;  // M tiles of one band of the tile order
+
+struct PairArgs {
+  FfnArgs f;
+  int32_t units;
+  // DW: units [0, u1) are dWg, [u1, u2) dWu, [u2, units) dWd, whose M and N are h and i
+  int32_t u1, u2;
+  int32_t m_tiles2, n_tiles2;  // dWd's tiles
+};
+
+struct PairMaps {
+  CUtensorMap a[3], b[3], o[3];
+};
+
+// What one launch computes: the four row-tiled contractions, or the three weight gradients together.
+enum PairVariant : int { P_GATEUP = 0, P_DOWN, P_DACT, P_DX, P_DW };
+
+template <int VAR, int BN>
+struct PairCfg {
+  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr uint32_t kABytes = 128 * 128;
+  static constexpr uint32_t kBBytes = BN / 2 * 128;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes;
+  static constexpr uint32_t kTxBytes = 2 * kStageBytes;  // both CTAs' loads count on the first CTA's barrier
+  static constexpr uint32_t kStagingOff = kStages * kStageBytes;
+  static constexpr uint32_t kStagingBytes = 8 * 2 * 2048;  // two 32-row x 64-byte tiles per epilogue warp
+  static constexpr uint32_t kBarOff = kStagingOff + kStagingBytes;
+  static constexpr uint32_t kSmemBytes = 1024 + kBarOff + 256;
+  static constexpr uint32_t kTmemCols = 2 * BN;
+  static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+  static_assert(2 * kStages + 5 <= 24, "barriers fit");
+};
+
+struct PairUnit {
+  int m, n;      // tile of 256 rows x BN columns
+  int which;     // DW: 0 dWg, 1 dWu, 2 dWd
+};
+
+// Tile u of an m_tiles x n_tiles output in bands of kGroupM M tiles, M fastest within a band.
+__device__ __forceinline__ void ordered_tile(int u, int m_tiles, int n_tiles, int& m, int& n) {
+  const int band = u / (kGroupM * n_tiles), r = u - band * (kGroupM * n_tiles);
+  const int rows = min(kGroupM, m_tiles - band * kGroupM);
+  n = r / rows;
+  m = band * kGroupM + (r - n * rows);
+}
+
+template <int VAR>
+__device__ __forceinline__ PairUnit pair_unit(const PairArgs& p, int u) {
+  PairUnit w;
+  w.which = 0;
+  if constexpr (VAR == P_DW) {
+    if (u >= p.u2) {
+      w.which = 2;
+      ordered_tile(u - p.u2, p.m_tiles2, p.n_tiles2, w.m, w.n);
+      return w;
+    }
+    if (u >= p.u1) {
+      w.which = 1;
+      u -= p.u1;
+    }
+  }
+  ordered_tile(u, p.f.m_tiles, p.f.n_tiles, w.m, w.n);
+  return w;
+}
+
+// This CTA's loads of one K block: its 128 rows of A and its half of B's columns.
+template <int VAR, int BN>
+__device__ __forceinline__ void pair_load(const PairArgs& p, const PairMaps& t, const PairUnit& w, int kb,
+                                          uint32_t sa, uint32_t sb, uint32_t bar, int rank) {
+  constexpr int HB = BN / 2;
+  const int k0 = kb * kFfnBK, m0 = w.m * 256 + rank * 128;
+  if constexpr (VAR == P_DW) {
+    const CUtensorMap* ta = &t.a[w.which];
+    tma_load_2d_pair(sa, ta, bar, m0, k0);
+    tma_load_2d_pair(sa + 8192, ta, bar, m0 + 64, k0);
+    const CUtensorMap* tb = &t.b[w.which == 2 ? 1 : 0];
+#pragma unroll
+    for (int j = 0; j < HB / 64; ++j) tma_load_2d_pair(sb + j * 8192, tb, bar, w.n * BN + rank * HB + j * 64, k0);
+  } else if constexpr (VAR == P_DX) {
+    const int half = kb < p.f.kb_split ? 0 : 1;
+    const int kr = k0 - half * p.f.kb_split * kFfnBK;
+    tma_load_2d_pair(sa, &t.a[half], bar, kr, m0);
+#pragma unroll
+    for (int j = 0; j < HB / 64; ++j)
+      tma_load_2d_pair(sb + j * 8192, &t.b[half], bar, w.n * BN + rank * HB + j * 64, kr);
+  } else {
+    tma_load_2d_pair(sa, &t.a[0], bar, k0, m0);
+    if constexpr (VAR == P_GATEUP) {  // the first CTA holds the gate rows, the second the same up rows
+      tma_load_2d_pair(sb, &t.b[rank], bar, k0, w.n * HB);
+    } else if constexpr (VAR == P_DOWN) {
+      tma_load_2d_pair(sb, &t.b[0], bar, k0, w.n * BN + rank * HB);
+    } else {
+#pragma unroll
+      for (int j = 0; j < HB / 64; ++j)
+        tma_load_2d_pair(sb + j * 8192, &t.b[0], bar, w.n * BN + rank * HB + j * 64, k0);
+    }
+  }
+}
+
+// One epilogue warp's output staging: two shared tiles of 32 rows x 64 bytes in the 64-byte TMA swizzle
+// (chunk j of row r at j ^ ((r >> 1) & 3)), each stored by one TMA store that clips at the tensor's
+// edges; a tile is refilled once its previous store has read it.
+struct WarpStage {
+  uint32_t base;
+  int cur, lane;
+  __device__ __forceinline__ void put(const uint4 (&ch)[4], const CUtensorMap* tm, int c0, int r0) {
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+    const uint32_t b = base + static_cast<uint32_t>(cur) * 2048u;
+    cur ^= 1;
+    const uint32_t row = b + static_cast<uint32_t>(lane) * 64u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) st_shared_v4(row + (static_cast<uint32_t>(j ^ ((lane >> 1) & 3)) << 4), ch[j]);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d(tm, b, c0, r0);
+      bulk_commit();
+    }
+  }
+  __device__ __forceinline__ void put_bf16(const float (&v)[32], const CUtensorMap* tm, int c0, int r0) {
+    uint4 ch[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      ch[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                         pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+    put(ch, tm, c0, r0);
+  }
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  tmem_ld_32x32b_x32(taddr, r);
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 32 columns (8 float4) of this lane's row of a saved g or u (ffn_saved_offset), columns past I skipped.
+__device__ __forceinline__ void saved_load(const float* p, int64_t off, int left, float4 (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = 4 * j < left ? __ldcs(reinterpret_cast<const float4*>(p + off) + 32 * j) : make_float4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void saved_store(float* p, int64_t off, int left, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (4 * j < left)
+      __stcs(reinterpret_cast<float4*>(p + off) + 32 * j,
+             make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+}
+
+// Epilogue of one tile for one warp: accumulator rows q * 32 ... (lane = row), column half h.
+template <int VAR, int BN>
+__device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps& t, const PairUnit& w, int rank, int q,
+                                              int h, int lane, uint32_t taddr, WarpStage& st, uint32_t tempty) {
+  const FfnArgs& f = p.f;
+  const int r0 = w.m * 256 + rank * 128 + q * 32;  // the warp's first row
+  const bool rows = r0 < f.M;                       // (DWd: M below)
+  auto release = [&] {  // the accumulator's last column has been read
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(tempty);
+  };
+  if constexpr (VAR == P_GATEUP) {
+    const int c0 = w.n * (BN / 2) + h * (BN / 4);
+#pragma unroll
+    for (int c = 0; c < BN / 4; c += 32) {
+      float g[32], u[32];
+      tmem_ld32(taddr + h * (BN / 4) + c, g);
+      tmem_ld32(taddr + BN / 2 + h * (BN / 4) + c, u);
+      if (c + 32 >= BN / 4) release();
+      if (!rows || c0 + c >= f.N) continue;
+      if (f.g) {
+        const int64_t off = ffn_saved_offset(r0 + lane, c0 + c, f.N);
+        saved_store(f.g, off, f.N - c0 - c, g);
+        saved_store(f.u, off, f.N - c0 - c, u);
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) g[i] = act_fwd(g[i], f.act) * u[i];
+      st.put_bf16(g, &t.o[0], c0 + c, r0);
+    }
+  } else if constexpr (VAR == P_DACT) {
+    const int c0 = w.n * BN + h * (BN / 2);
+#pragma unroll 1
+    for (int c = 0; c < BN / 2; c += 32) {
+      const bool in = rows && c0 + c < f.N;
+      float4 g4[8], u4[8];
+      if (in) {
+        const int64_t off = ffn_saved_offset(r0 + lane, c0 + c, f.N);
+        saved_load(f.g, off, f.N - c0 - c, g4);
+        saved_load(f.u, off, f.N - c0 - c, u4);
+      }
+      float v[32];
+      tmem_ld32(taddr + h * (BN / 2) + c, v);
+      if (c + 32 >= BN / 2) release();
+      if (!in) continue;
+      float dg[32];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float g[4] = {g4[j].x, g4[j].y, g4[j].z, g4[j].w}, u[4] = {u4[j].x, u4[j].y, u4[j].z, u4[j].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float a, da;
+          act_bwd(g[k], f.act, a, da);
+          dg[4 * j + k] = v[4 * j + k] * u[k] * da;
+          v[4 * j + k] *= a;
+        }
+      }
+      st.put_bf16(dg, &t.o[0], c0 + c, r0);
+      st.put_bf16(v, &t.o[1], c0 + c, r0);
+    }
+  } else {
+    const int M = VAR == P_DW && w.which == 2 ? f.N : f.M, N = VAR == P_DW && w.which == 2 ? f.M : f.N;
+    const CUtensorMap* to = &t.o[VAR == P_DW ? w.which : 0];
+    const int c0 = w.n * BN + h * (BN / 2);
+#pragma unroll 1
+    for (int c = 0; c < BN / 2; c += 32) {
+      const bool in = r0 < M && c0 + c < N;
+      uint4 res[4];
+      if constexpr (VAR == P_DOWN) {
+        if (f.residual && in && r0 + lane < M) {
+          const uint4* s = reinterpret_cast<const uint4*>(f.residual + static_cast<int64_t>(r0 + lane) * N + c0 + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) res[j] = c0 + c + 8 * j < N ? s[j] : make_uint4(0, 0, 0, 0);
+        }
+      }
+      float v[32];
+      tmem_ld32(taddr + h * (BN / 2) + c, v);
+      if (c + 32 >= BN / 2) release();
+      if (!in) continue;
+      if constexpr (VAR == P_DOWN) {
+        if (f.residual && r0 + lane < M) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t r[4] = {res[j].x, res[j].y, res[j].z, res[j].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[8 * j + 2 * k] += bf16_lo(r[k]);
+              v[8 * j + 2 * k + 1] += bf16_hi(r[k]);
+            }
+          }
+        }
+      }
+      if (VAR == P_DW && f.out_f32) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 16) {
+          uint4 ch[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            ch[j] = make_uint4(__float_as_uint(v[k + 4 * j]), __float_as_uint(v[k + 4 * j + 1]),
+                               __float_as_uint(v[k + 4 * j + 2]), __float_as_uint(v[k + 4 * j + 3]));
+          if (c0 + c + k < N) st.put(ch, to, c0 + c + k, r0);
+        }
+      } else {
+        st.put_bf16(v, to, c0 + c, r0);
+      }
+    }
+  }
+}
+
+// Bounded wait that ignores the abort flag: only while winding down.
+__device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
+  }
+}
+
+template <int VAR, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    ffn_pair_kernel(const __grid_constant__ PairMaps t, const PairArgs p) {
+  using C = PairCfg<VAR, BN>;
+  constexpr int S = C::kStages;
+  constexpr bool kAmn = VAR == P_DW, kBmn = VAR >= P_DACT;
+  constexpr uint32_t kIdesc = idesc_bf16(256, BN, kAmn, kBmn);
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms: 1024-byte aligned
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem_raw + (base - raw) + C::kBarOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t bar0 = smem_u32(bars);
+  // the pair counts loads and accumulator releases on the first CTA's full / tempty barriers; each
+  // CTA has its own empty, tfull and drain barriers, on which the first CTA's commits arrive
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tfull = [&](int a) { return bar0 + 8u * (2 * S + a); };
+  auto tempty = [&](int a) { return bar0 + 8u * (2 * S + 2 + a); };
+  const uint32_t drain = bar0 + 8u * (2 * S + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int u0 = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+  uint32_t* status = p.f.status;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), 16);  // eight warps of each CTA
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    if (VAR != P_DW) {  // (DW: only the maps of the gradients asked for are set)
+      tma_prefetch_desc(&t.a[0]);
+      tma_prefetch_desc(&t.b[0]);
+      tma_prefetch_desc(&t.o[0]);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // the peer's barriers exist before anything arrives on them
+  pdl_wait();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int st = 0, issued = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = u0; u < p.units && ok; u += step) {
+        const PairUnit w = pair_unit<VAR>(p, u);
+        for (int kb = 0; kb < p.f.k_blocks; ++kb) {
+          if (!mbar_wait(empty(st), ph ^ 1u, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sa = base + st * C::kStageBytes;
+          if (rank == 0) mbar_arrive_expect_tx(full(st), C::kTxBytes);
+          pair_load<VAR, BN>(p, t, w, kb, sa, sa + C::kABytes, mapa_shared(full(st), 0), rank);
+          ++issued;
+          if (++st == S) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok && rank == 0)  // let the copies in flight land: the last one of each stage
+        for (int b = issued > S ? issued - S : 0; b < issued; ++b)
+          wait_landed(full(b % S), static_cast<uint32_t>(b / S) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int st = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (int u = u0; u < p.units && ok; u += step) {
+        if (!mbar_wait<true>(tempty(acc), aph ^ 1u, abort_flag, status)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+        for (int kb = 0; kb < p.f.k_blocks; ++kb) {
+          if (!mbar_wait(full(st), ph, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + st * C::kStageBytes, sb = sa + C::kABytes;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint64_t ad = kAmn ? sdesc_sw128(sa + ks * 2048, 8192, 1024) : sdesc_sw128(sa + ks * 32, 16, 1024);
+            const uint64_t bd = kBmn ? sdesc_sw128(sb + ks * 2048, 8192, 1024) : sdesc_sw128(sb + ks * 32, 16, 1024);
+            umma_bf16_pair(d, ad, bd, kIdesc, (kb | ks) != 0 ? 1u : 0u);
+          }
+          umma_commit_pair(empty(st));
+          if (++st == S) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair(tfull(acc));
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1u;
+        }
+      }
+      umma_commit_pair(drain);  // every MMA issued has ended before TMEM is freed, in both CTAs
+      wait_landed(drain, 0);
+    } else if (lane == 0) {
+      wait_landed(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    WarpStage st{base + C::kStagingOff + static_cast<uint32_t>(warp - 2) * 4096u, 0, lane};
+    int acc = 0;
+    uint32_t aph = 0;
+    for (int u = u0; u < p.units; u += step) {
+      const PairUnit w = pair_unit<VAR>(p, u);
+      int ok = 0;
+      if (lane == 0) ok = mbar_wait(tfull(acc), aph, abort_flag, status) ? 1 : 0;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      tc_fence_after();
+      pair_epilogue<VAR, BN>(p, t, w, rank, q, h, lane,
+                             tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN), st,
+                             mapa_shared(tempty(acc), 0));
+      if (++acc == 2) {
+        acc = 0;
+        aph ^= 1u;
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  if (*abort_flag) {  // failure path: copies or arrivals of the peer may still be in flight
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < kWaitLimitNs / 100) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the other may still address it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, C::kTmemCols);
+  }
+}
+
+template <int VAR, int BN>
+int launch_pair(const PairMaps& maps, const PairArgs& p, cudaStream_t stream) {
+  using C = PairCfg<VAR, BN>;
+  static DeviceOnce once;
+  const int se = once.run([](int* d) { return static_cast<int>(cudaGetDevice(d)); },
+                          [] {
+                            return static_cast<int>(cudaFuncSetAttribute(ffn_pair_kernel<VAR, BN>,
+                                                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                                         static_cast<int>(C::kSmemBytes)));
+                          },
+                          static_cast<int>(cudaErrorInvalidDevice));
+  if (se) return se;
+  const int pairs = sm_count() / 2;
+  if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
+  const int grid = 2 * (p.units < pairs ? p.units : pairs);
+  constexpr int kKind = VAR == P_DW ? static_cast<int>(K_FFN_DW) : K_FFN_GATEUP + VAR;
+  trace_begin(stream, kKind);
+  const cudaError_t e =
+      launch_pdl(ffn_pair_kernel<VAR, BN>, dim3(grid), dim3(kPairThreads), C::kSmemBytes, stream, maps, p);
+  trace_end(stream);
+  return static_cast<int>(e);
+}
+
+int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
+
+// Row-tiled contraction over M rows, N output columns, K (of one half for DX).
+template <int VAR, int BN>
+int pair_rows(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& f, cudaStream_t stream) {
+  constexpr int kCols = VAR == P_GATEUP ? BN / 2 : BN;
+  PairArgs p{};
+  p.f = f;
+  p.f.M = static_cast<int32_t>(M);
+  p.f.N = static_cast<int32_t>(N);
+  p.f.m_tiles = static_cast<int32_t>(tiles_of(M, 256));
+  p.f.n_tiles = static_cast<int32_t>(tiles_of(N, kCols));
+  p.f.kb_split = static_cast<int32_t>(tiles_of(K, kFfnBK));
+  p.f.k_blocks = p.f.kb_split * (VAR == P_DX ? 2 : 1);
+  const int64_t units = static_cast<int64_t>(p.f.m_tiles) * p.f.n_tiles;
+  if (units >= (int64_t{1} << 30)) return static_cast<int>(cudaErrorInvalidValue);
+  p.units = static_cast<int32_t>(units);
+  const uint64_t m = static_cast<uint64_t>(M), n = static_cast<uint64_t>(N), k = static_cast<uint64_t>(K);
+  PairMaps t;
+  bool good = make_tmap_bf16(&t.a[0], o.a, k, m, 64, 128);
+  if constexpr (VAR == P_DX) good = good && make_tmap_bf16(&t.a[1], o.a2, k, m, 64, 128);
+  if constexpr (VAR >= P_DACT) good = good && make_tmap_bf16(&t.b[0], o.b, n, k, 64, 64);
+  else good = good && make_tmap_bf16(&t.b[0], o.b, k, n, 64, BN / 2);
+  if constexpr (VAR == P_DX) good = good && make_tmap_bf16(&t.b[1], o.b2, n, k, 64, 64);
+  if constexpr (VAR == P_GATEUP) good = good && make_tmap_bf16(&t.b[1], o.b2, k, n, 64, BN / 2);
+  good = good && make_tmap_bf16_sw64(&t.o[0], f.out0, n, m, 32, 32);
+  if constexpr (VAR == P_DACT) good = good && make_tmap_bf16_sw64(&t.o[1], f.out1, n, m, 32, 32);
+  if (!good) return static_cast<int>(cudaErrorInvalidValue);
+  return launch_pair<VAR, BN>(t, p, stream);
+}
+
+}  // namespace
+
+int launch_ffn_pair(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
+                    cudaStream_t stream) {
+  switch (var) {
+    case F_GATEUP: return pair_rows<P_GATEUP, 256>(M, N, K, o, a, stream);
+    case F_DOWN: return pair_rows<P_DOWN, 256>(M, N, K, o, a, stream);
+    case F_DACT: return pair_rows<P_DACT, 256>(M, N, K, o, a, stream);
+    default: return pair_rows<P_DX, 256>(M, N, K, o, a, stream);
+  }
+}
+
+int launch_ffn_dw(int64_t T, int64_t H, int64_t I, const FfnGradOperands& o, int out_f32, uint32_t* status,
+                  cudaStream_t stream) {
+  constexpr int BN = 256;
+  PairArgs p{};
+  p.f.M = static_cast<int32_t>(I);
+  p.f.N = static_cast<int32_t>(H);
+  p.f.m_tiles = static_cast<int32_t>(tiles_of(I, 256));
+  p.f.n_tiles = static_cast<int32_t>(tiles_of(H, BN));
+  p.m_tiles2 = static_cast<int32_t>(tiles_of(H, 256));
+  p.n_tiles2 = static_cast<int32_t>(tiles_of(I, BN));
+  p.f.k_blocks = p.f.kb_split = static_cast<int32_t>(tiles_of(T, kFfnBK));
+  p.f.out_f32 = out_f32;
+  p.f.status = status;
+  const int gu = o.dw_gate ? p.f.m_tiles * p.f.n_tiles : 0;
+  p.u1 = gu;
+  p.u2 = 2 * gu;
+  p.units = 2 * gu + (o.dw_down ? p.m_tiles2 * p.n_tiles2 : 0);
+  if (p.units == 0) return 0;
+  const uint64_t t = static_cast<uint64_t>(T), h = static_cast<uint64_t>(H), i = static_cast<uint64_t>(I);
+  PairMaps m{};
+  auto out_map = [&](CUtensorMap* tm, void* d, uint64_t inner, uint64_t outer) {
+    return out_f32 ? make_tmap_f32_sw64(tm, d, inner, outer, 16, 32) : make_tmap_bf16_sw64(tm, d, inner, outer, 32, 32);
+  };
+  bool good = true;
+  if (o.dw_gate)
+    good = make_tmap_bf16(&m.a[0], o.dg, i, t, 64, 64) && make_tmap_bf16(&m.a[1], o.du, i, t, 64, 64) &&
+           make_tmap_bf16(&m.b[0], o.x, h, t, 64, 64) && out_map(&m.o[0], o.dw_gate, h, i) &&
+           out_map(&m.o[1], o.dw_up, h, i);
+  if (good && o.dw_down)
+    good = make_tmap_bf16(&m.a[2], o.dy, h, t, 64, 64) && make_tmap_bf16(&m.b[1], o.a, i, t, 64, 64) &&
+           out_map(&m.o[2], o.dw_down, i, h);
+  if (!good) return static_cast<int>(cudaErrorInvalidValue);
+  return launch_pair<P_DW, BN>(m, p, stream);
+}
+
+}  // namespace mok

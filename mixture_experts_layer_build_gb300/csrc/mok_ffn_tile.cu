@@ -23,6 +23,10 @@ struct TileArgs {
   uint32_t b_off;   // shared memory: A stages, then B stages
 };
 
+struct TileMaps {
+  CUtensorMap a, a2, b, b2;
+};
+
 template <int VAR, int BN>
 struct TileCfg {
   static constexpr uint32_t kBBytes = BN * 128;
@@ -49,14 +53,13 @@ __device__ __forceinline__ void store_bf16x8(void* p, int64_t i, const float (&v
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
       make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
-__device__ __forceinline__ void store_f32x8(void* p, int64_t i, const float (&v)[8]) {
-  float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-  d[0] = make_float4(v[0], v[1], v[2], v[3]);
-  d[1] = make_float4(v[4], v[5], v[6], v[7]);
+// 8 columns of a saved g or u: two blocks of 4 columns, 128 elements apart.
+__device__ __forceinline__ void saved_store8(float* p, int64_t off, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p + off) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + off + 128) = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ void load_f32x8(const float* p, int64_t i, float (&v)[8]) {
-  const float4* s = reinterpret_cast<const float4*>(p + i);
-  const float4 a = s[0], b = s[1];
+__device__ __forceinline__ void saved_load8(const float* p, int64_t off, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p + off), b = *reinterpret_cast<const float4*>(p + off + 128);
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
@@ -64,13 +67,7 @@ template <int VAR, int BN>
 __device__ __forceinline__ void tile_load_a(const TileArgs& t, int m, int kb, uint32_t sa, uint32_t bar,
                                             const CUtensorMap* tA, const CUtensorMap* tA2) {
   const int k0 = kb * kFfnBK;
-  if constexpr (ffn_a_mn(VAR)) {  // two boxes of 64 M columns x 64 K rows
-    const bool second = VAR == F_DWGU && m >= t.f.m_half;
-    const CUtensorMap* tm = second ? tA2 : tA;
-    const int m0 = (second ? m - t.f.m_half : m) * 128;
-    tma_load_2d(sa, tm, bar, m0, k0);
-    tma_load_2d(sa + 8192, tm, bar, m0 + 64, k0);
-  } else if constexpr (VAR == F_DX) {
+  if constexpr (VAR == F_DX) {
     const bool first = kb < t.f.kb_split;
     tma_load_2d(sa, first ? tA : tA2, bar, first ? k0 : k0 - t.f.kb_split * kFfnBK, m * 128);
   } else {
@@ -96,13 +93,12 @@ __device__ __forceinline__ void tile_load_b(const TileArgs& t, int n, int kb, ui
 
 // Epilogue of 8 columns (GATEUP: v = 8 gate and w the same 8 up columns) at row m, column c of the output.
 template <int VAR>
-__device__ __forceinline__ void tile_epilogue8(const FfnArgs& f, int64_t m, int c, bool second, float (&v)[8],
-                                               float (&w)[8]) {
+__device__ __forceinline__ void tile_epilogue8(const FfnArgs& f, int64_t m, int c, float (&v)[8], float (&w)[8]) {
   const int64_t i = m * f.N + c;
   if constexpr (VAR == F_GATEUP) {
     if (f.g) {
-      store_f32x8(f.g, i, v);
-      store_f32x8(f.u, i, w);
+      saved_store8(f.g, ffn_saved_offset(m, c, f.N), v);
+      saved_store8(f.u, ffn_saved_offset(m, c, f.N), w);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = act_fwd(v[k], f.act) * w[k];
@@ -116,8 +112,8 @@ __device__ __forceinline__ void tile_epilogue8(const FfnArgs& f, int64_t m, int 
     store_bf16x8(f.out0, i, v);
   } else if constexpr (VAR == F_DACT) {
     float g[8], u[8];
-    load_f32x8(f.g, i, g);
-    load_f32x8(f.u, i, u);
+    saved_load8(f.g, ffn_saved_offset(m, c, f.N), g);
+    saved_load8(f.u, ffn_saved_offset(m, c, f.N), u);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       float a, da;
@@ -127,12 +123,8 @@ __device__ __forceinline__ void tile_epilogue8(const FfnArgs& f, int64_t m, int 
     }
     store_bf16x8(f.out0, i, g);
     store_bf16x8(f.out1, i, u);
-  } else if constexpr (VAR == F_DX) {
-    store_bf16x8(f.out0, i, v);
   } else {
-    void* o = second ? f.out1 : f.out0;
-    if (f.out_f32) store_f32x8(o, i, v);
-    else store_bf16x8(o, i, v);
+    store_bf16x8(f.out0, i, v);
   }
 }
 
@@ -142,7 +134,7 @@ __global__ void __launch_bounds__(kTileThreads)
                     const __grid_constant__ CUtensorMap tB, const __grid_constant__ CUtensorMap tB2,
                     const TileArgs t) {
   using C = TileCfg<VAR, BN>;
-  constexpr uint32_t kIdesc = idesc_bf16(128, BN, ffn_a_mn(VAR), ffn_b_mn(VAR));
+  constexpr uint32_t kIdesc = idesc_bf16(128, BN, false, ffn_b_mn(VAR));
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kTileMaxStages + 1];
   __shared__ uint32_t tmem_slot;
@@ -158,7 +150,7 @@ __global__ void __launch_bounds__(kTileThreads)
   const int n = tile / t.f.m_tiles, m = tile - n * t.f.m_tiles;
   const int kb0 = static_cast<int>(static_cast<int64_t>(t.f.k_blocks) * rank / S);
   const int kb1 = static_cast<int>(static_cast<int64_t>(t.f.k_blocks) * (rank + 1) / S);
-  const uint32_t a_bytes = ffn_a_mn(VAR) ? 16384u : static_cast<uint32_t>(t.a_rows) * 128u;
+  const uint32_t a_bytes = static_cast<uint32_t>(t.a_rows) * 128u;
   if (threadIdx.x == 0) {
     for (int s = 0; s < t.stages; ++s) {
       mbar_init(full(s), 1);
@@ -215,7 +207,7 @@ __global__ void __launch_bounds__(kTileThreads)
         const uint32_t sa = base + st * a_bytes, sb = base + t.b_off + st * C::kBBytes;
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          const uint64_t ad = ffn_a_mn(VAR) ? sdesc_sw128(sa + ks * 2048, 8192, 1024) : sdesc_sw128(sa + ks * 32, 16, 1024);
+          const uint64_t ad = sdesc_sw128(sa + ks * 32, 16, 1024);
           const uint64_t bd = ffn_b_mn(VAR) ? sdesc_sw128(sb + ks * 2048, 8192, 1024) : sdesc_sw128(sb + ks * 32, 16, 1024);
           umma_bf16(tmem, ad, bd, kIdesc, (kb > kb0 || ks > 0) ? 1u : 0u);
         }
@@ -243,7 +235,7 @@ __global__ void __launch_bounds__(kTileThreads)
   __syncthreads();
   if (*abort_flag) ok = false;
   tc_fence_after();
-  const int rows = min(128, t.f.M - (VAR == F_DWGU && m >= t.f.m_half ? m - t.f.m_half : m) * 128);
+  const int rows = min(128, t.f.M - m * 128);
   if (warp >= 2 && ok) {
     const int q = warp & 3;  // this warp's TMEM lane quarter
     if (q * 32 < rows) {
@@ -263,8 +255,7 @@ __global__ void __launch_bounds__(kTileThreads)
   if (S > 1) cluster_sync();
   else __syncthreads();
   if (ok) {
-    const bool second = VAR == F_DWGU && m >= t.f.m_half;
-    const int64_t m0 = static_cast<int64_t>(second ? m - t.f.m_half : m) * 128;
+    const int64_t m0 = static_cast<int64_t>(m) * 128;
     constexpr int kCols = VAR == F_GATEUP ? BN / 2 : BN;  // output columns of a tile
     constexpr int kChunks = kCols / 8;
     const int c0 = n * kCols;
@@ -285,7 +276,7 @@ __global__ void __launch_bounds__(kTileThreads)
           w[0] += z.x, w[1] += z.y, w[2] += z.z, w[3] += z.w, w[4] += q.x, w[5] += q.y, w[6] += q.z, w[7] += q.w;
         }
       }
-      tile_epilogue8<VAR>(t.f, m0 + r, c0 + c, second, v, w);
+      tile_epilogue8<VAR>(t.f, m0 + r, c0 + c, v, w);
     }
   }
   if (S > 1) cluster_sync();  // no CTA leaves while a peer may read its partials
@@ -294,7 +285,7 @@ __global__ void __launch_bounds__(kTileThreads)
 }
 
 template <int VAR, int BN>
-int launch_tile(const FfnMaps& maps, TileArgs t, cudaStream_t stream) {
+int launch_tile(const TileMaps& maps, TileArgs t, cudaStream_t stream) {
   using C = TileCfg<VAR, BN>;
   static DeviceOnce once;
   const int se = once.run([](int* d) { return static_cast<int>(cudaGetDevice(d)); },
@@ -305,7 +296,7 @@ int launch_tile(const FfnMaps& maps, TileArgs t, cudaStream_t stream) {
                           },
                           static_cast<int>(cudaErrorInvalidDevice));
   if (se) return se;
-  const uint32_t a_bytes = ffn_a_mn(VAR) ? 16384u : static_cast<uint32_t>(t.a_rows) * 128u;
+  const uint32_t a_bytes = static_cast<uint32_t>(t.a_rows) * 128u;
   const uint32_t stage = a_bytes + C::kBBytes;
   const uint32_t budget = kTileMaxSmem - 4096;  // static shared memory and the alignment slack
   int stages = static_cast<int>((budget - 16384u) / stage);
@@ -349,8 +340,7 @@ int launch_var(int64_t M, int64_t N, int64_t K, int split, const FfnOperands& o,
   const int64_t mt = (M + 127) / 128, nt = (N + kCols - 1) / kCols;
   f.M = static_cast<int32_t>(M);
   f.N = static_cast<int32_t>(N);
-  f.m_half = static_cast<int32_t>(mt);
-  f.m_tiles = static_cast<int32_t>(VAR == F_DWGU ? 2 * mt : mt);
+  f.m_tiles = static_cast<int32_t>(mt);
   f.n_tiles = static_cast<int32_t>(nt);
   const int64_t kb = (K + kFfnBK - 1) / kFfnBK;
   f.kb_split = static_cast<int32_t>(kb);
@@ -360,13 +350,10 @@ int launch_var(int64_t M, int64_t N, int64_t K, int split, const FfnOperands& o,
   t.a_rows = M >= 128 ? 128 : static_cast<int32_t>((M + 7) / 8 * 8);
   t.split = split;
   const uint64_t um = static_cast<uint64_t>(M), un = static_cast<uint64_t>(N), uk = static_cast<uint64_t>(K);
-  FfnMaps p;
-  bool good;
-  if constexpr (ffn_a_mn(VAR)) good = make_tmap_bf16(&p.a, o.a, um, uk, 64, 64);
-  else good = make_tmap_bf16(&p.a, o.a, uk, um, 64, static_cast<uint32_t>(t.a_rows));
+  TileMaps p;
+  bool good = make_tmap_bf16(&p.a, o.a, uk, um, 64, static_cast<uint32_t>(t.a_rows));
   p.a2 = p.a;
   if constexpr (VAR == F_DX) good = good && make_tmap_bf16(&p.a2, o.a2, uk, um, 64, static_cast<uint32_t>(t.a_rows));
-  if constexpr (VAR == F_DWGU) good = good && make_tmap_bf16(&p.a2, o.a2, um, uk, 64, 64);
   if constexpr (ffn_b_mn(VAR)) good = good && make_tmap_bf16(&p.b, o.b, un, uk, 64, 64);
   else good = good && make_tmap_bf16(&p.b, o.b, uk, un, 64, kCols);
   p.b2 = p.b;
@@ -378,35 +365,30 @@ int launch_var(int64_t M, int64_t N, int64_t K, int split, const FfnOperands& o,
 
 // Columns of a tile and CTAs per tile.  With few tiles the K range is split over a cluster until about
 // every SM has a CTA, leaving each at least four K blocks; 64-column tiles first, since they need fewer
-// CTAs per tile.  (Weight gradients have K = tokens and many tiles: never split.)
+// CTAs per tile.
 template <int VAR>
 int launch_tiles(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& f, cudaStream_t stream) {
-  if constexpr (VAR == F_DWGU || VAR == F_DWD) {
-    return launch_var<VAR, 128>(M, N, K, 1, o, f, stream);
-  } else {
-    const int sms = sm_count();
-    if (sms <= 0) return static_cast<int>(cudaErrorInvalidDevice);
-    auto tiles = [&](int bn) { return (M + 127) / 128 * ((N + bn - 1) / bn); };
-    constexpr int kPer = VAR == F_GATEUP ? 2 : 1;  // tile columns per output column
-    if (2 * tiles(64 / kPer) > 3 * sms) return launch_var<VAR, 128>(M, N, K, 1, o, f, stream);
-    const int64_t kb = (K + kFfnBK - 1) / kFfnBK * (VAR == F_DX ? 2 : 1);
-    int64_t split = sms / tiles(64 / kPer);
-    if (split > kb / 4) split = kb / 4;
-    split = split < 1 ? 1 : split > 8 ? 8 : split;
-    return launch_var<VAR, 64>(M, N, K, static_cast<int>(split), o, f, stream);
-  }
+  const int sms = sm_count();
+  if (sms <= 0) return static_cast<int>(cudaErrorInvalidDevice);
+  auto tiles = [&](int bn) { return (M + 127) / 128 * ((N + bn - 1) / bn); };
+  constexpr int kPer = VAR == F_GATEUP ? 2 : 1;  // tile columns per output column
+  if (2 * tiles(64 / kPer) > 3 * sms) return launch_var<VAR, 128>(M, N, K, 1, o, f, stream);
+  const int64_t kb = (K + kFfnBK - 1) / kFfnBK * (VAR == F_DX ? 2 : 1);
+  int64_t split = sms / tiles(64 / kPer);
+  if (split > kb / 4) split = kb / 4;
+  split = split < 1 ? 1 : split > 8 ? 8 : split;
+  return launch_var<VAR, 64>(M, N, K, static_cast<int>(split), o, f, stream);
 }
 
 }  // namespace
 
-int launch_ffn_gemm(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, FfnArgs a, cudaStream_t stream) {
+int launch_ffn_tile(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
+                    cudaStream_t stream) {
   switch (var) {
     case F_GATEUP: return launch_tiles<F_GATEUP>(M, N, K, o, a, stream);
     case F_DOWN: return launch_tiles<F_DOWN>(M, N, K, o, a, stream);
     case F_DACT: return launch_tiles<F_DACT>(M, N, K, o, a, stream);
-    case F_DX: return launch_tiles<F_DX>(M, N, K, o, a, stream);
-    case F_DWGU: return launch_tiles<F_DWGU>(M, N, K, o, a, stream);
-    default: return launch_tiles<F_DWD>(M, N, K, o, a, stream);
+    default: return launch_tiles<F_DX>(M, N, K, o, a, stream);
   }
 }
 

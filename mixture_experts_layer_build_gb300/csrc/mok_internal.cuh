@@ -158,8 +158,7 @@ enum KernelKind : int {
   K_FFN_DOWN,
   K_FFN_DACT,
   K_FFN_DX,
-  K_FFN_DWGU,
-  K_FFN_DWD,
+  K_FFN_DW,
   K_NUM_KINDS
 };
 void trace_begin(cudaStream_t s, int kind);  // no-ops unless a trace is set
