@@ -18,7 +18,7 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", 
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["mok_api.cu", "mok_sched.cu", "mok_move.cu", "mok_gemm_fwd.cu", "mok_gemm_dgrad.cu", "mok_gemm_wgrad.cu",
            "mok_router.cu", "mok_noalloc.cu", "mok_norm.cu",
-           "mok_ffn.cu", "mok_ffn_tile.cu", "mok_ffn_pair.cu"]
+           "mok_ffn.cu", "mok_ffn_tile.cu", "mok_ffn_pair.cu", "mok_ffn_row.cu"]
 
 
 def _stale(target: str, deps) -> bool:

@@ -37,6 +37,7 @@ bool need16(const void* p) { return p && !unaligned(p, 16); }
 // Pairs (256-row tiles) from the tokens on that fill half of one round of them; the tile kernel below.
 int launch_ffn_gemm(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
                     cudaStream_t stream) {
+  if (M <= kFfnRowTokens && (var == F_GATEUP || var == F_DOWN)) return launch_ffn_row(var, M, N, K, o, a, stream);
   const int cols = var == F_GATEUP ? 128 : 256;
   const int64_t units = (M + 255) / 256 * ((N + cols - 1) / cols);
   return 4 * units >= sm_count() ? launch_ffn_pair(var, M, N, K, o, a, stream)

@@ -99,6 +99,10 @@ struct FfnGradOperands {  // dw_gate == nullptr, dw_down == nullptr: not compute
 // and persistent CTA pairs (mok_ffn_pair.cu).
 int launch_ffn_tile(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
                     cudaStream_t stream);
+// GATEUP and DOWN for at most kFfnRowTokens tokens (mok_ffn_row.cu).
+constexpr int kFfnRowTokens = 4;
+int launch_ffn_row(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
+                   cudaStream_t stream);
 int launch_ffn_pair(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
                     cudaStream_t stream);
 // The weight gradients, in one launch.

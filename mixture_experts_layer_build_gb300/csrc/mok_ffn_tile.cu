@@ -1,11 +1,17 @@
 // mok_ffn_tile.cu -- the feed-forward block's contractions, one output tile per CTA.
 //
 // A CTA computes a 128 x BN tile, or (split) one of S CTAs of a cluster computes a share of its K
-// range; the S partial tiles meet in shared memory.  Warp 0 issues TMA loads into a ring of
-// stages, warp 1 issues the tcgen05.mma (M = 128, N = BN, K = 16) into one TMEM accumulator; warps 2 to 5
-// copy it to shared memory as fp32, and then all threads take 8 columns of a row at a time: they sum the
-// cluster's partials in ascending order through distributed shared memory, apply the epilogue and write
-// 16-byte vectors.  Every output has a fixed order of summation.
+// range.  Warp 0 issues TMA loads into a ring of stages, warp 1 issues the tcgen05.mma (M = 128, N = BN,
+// K = 16) into one TMEM accumulator.  Then warps 2 to 5 push the accumulator, 8 columns of a row at a
+// time, into the shared memory of the CTA of the cluster that owns them (dealt out round robin), and after one
+// cluster barrier every owner adds its sources in ascending order, applies the epilogue and writes 16-byte
+// vectors.  Every output has a fixed order of summation.
+//
+// With few tokens the weights' bytes bound it, and what stands in the way is latency: so the loops of
+// warps 0 and 1 are warp-uniform with one elected lane at each asynchronous instruction (issued from a
+// single-lane branch, a K block took 240 ns to issue whatever its size), the first loads are issued
+// before the CTA's set-up has finished, and the contractions that follow another of this block
+// load their weights before they wait for it.
 #include "mok_ffn.cuh"
 
 namespace mok {
@@ -13,14 +19,18 @@ namespace {
 
 constexpr int kTileThreads = 192;
 constexpr int kTileMaxStages = 16;
-constexpr uint32_t kTileMaxSmem = 232448;
+constexpr uint32_t kTileMaxSmem = 230400;  // what a launch may ask for
+constexpr uint32_t kTileSmem = 116224;  // two CTAs per SM
 
 struct TileArgs {
   FfnArgs f;
   int32_t split;    // CTAs per tile (the cluster's size)
   int32_t stages;
-  int32_t a_rows;   // rows of one A box (K-major A): 128, or all of M rounded up to 8
-  uint32_t b_off;   // shared memory: A stages, then B stages
+  int32_t a_rows;   // rows of one A box: 128, or all of M rounded up to 8
+  int32_t early_b;  // the previous kernel of the stream is one of this block's: weights may be read before it ends
+  uint32_t b_off;   // shared memory: A stages, then B stages, then (split) the pushed partials
+  uint32_t push_off;
+  uint32_t src_bytes;  // pushed bytes per source CTA
 };
 
 struct TileMaps {
@@ -30,8 +40,14 @@ struct TileMaps {
 template <int VAR, int BN>
 struct TileCfg {
   static constexpr uint32_t kBBytes = BN * 128;
-  static constexpr uint32_t kStride = BN + 4;  // fp32 per row of the staged tile
-  static constexpr uint32_t kStaged = 128u * kStride * 4u;
+  static constexpr int kCols = VAR == F_GATEUP ? BN / 2 : BN;  // output columns of a tile
+  static constexpr int kChunks = kCols / 8;
+  static constexpr uint32_t kChunkBytes = VAR == F_GATEUP ? 64 : 32;  // 8 fp32 columns (gate, then up)
+  // chunk `slot` of a pushed or staged tile; 16 bytes between rows keep the lanes (rows) off each
+  // other's banks
+  static __host__ __device__ uint32_t slot_off(uint32_t slot) {
+    return slot * kChunkBytes + slot / kChunks * 16u;
+  }
 };
 
 // Bounded wait that ignores the abort flag: only while winding down.
@@ -40,14 +56,29 @@ __device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity) {
   while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
   }
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// The whole warp waits; the same answer on every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(addr)
                : "memory");
   return v;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
 }
 __device__ __forceinline__ void store_bf16x8(void* p, int64_t i, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
@@ -149,139 +180,163 @@ __global__ void __launch_bounds__(kTileThreads)
   const int S = t.split, rank = static_cast<int>(blockIdx.x) % S, tile = static_cast<int>(blockIdx.x) / S;
   const int n = tile / t.f.m_tiles, m = tile - n * t.f.m_tiles;
   const int kb0 = static_cast<int>(static_cast<int64_t>(t.f.k_blocks) * rank / S);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(t.f.k_blocks) * (rank + 1) / S);
+  const int count = static_cast<int>(static_cast<int64_t>(t.f.k_blocks) * (rank + 1) / S) - kb0;
   const uint32_t a_bytes = static_cast<uint32_t>(t.a_rows) * 128u;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < t.stages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+  const int ahead = min(count, t.stages);  // K blocks loaded before anything is consumed
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < t.stages; ++s) {
+        mbar_init(full(s), 1);
+        mbar_init(empty(s), 1);
+      }
+      mbar_init(done, 1);
+      abort_word = 0;
+      fence_barrier_init();
     }
-    mbar_init(done, 1);
-    abort_word = 0;
-    fence_barrier_init();
-    tma_prefetch_desc(&tA);
-    tma_prefetch_desc(&tB);
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_slot), BN);
-    tmem_relinquish();
+    __syncwarp();
+    // the first round of weight loads: the barriers are this warp's own, and the stages are empty
+    if (!t.early_b) pdl_wait();
+    for (int i = 0; i < ahead; ++i)
+      if (elect_one()) {
+        mbar_arrive_expect_tx(full(i), a_bytes + C::kBBytes);
+        tile_load_b<VAR, BN>(t, n, kb0 + i, base + t.b_off + i * C::kBBytes, full(i), &tB, &tB2);
+      }
+    if (t.early_b) pdl_wait();
+  } else {
+    if (warp == 1) {
+      tmem_alloc(smem_u32(&tmem_slot), BN < 32 ? 32 : BN);
+      tmem_relinquish();
+    }
+    pdl_wait();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
+  // every kernel before this one has ended: the next one of this block may start loading its weights.  (After
+  // this CTA's TMEM allocation: one of the next kernel's CTAs that took the columns first would wait for
+  // this grid while holding them.)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const uint32_t tmem = tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      int st = 0, issued = 0;
-      uint32_t ph = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(empty(st), ph ^ 1u, abort_flag, t.f.status)) {
-          ok = false;
-          break;
-        }
-        mbar_arrive_expect_tx(full(st), a_bytes + C::kBBytes);
-        tile_load_a<VAR, BN>(t, m, kb, base + st * a_bytes, full(st), &tA, &tA2);
-        tile_load_b<VAR, BN>(t, n, kb, base + t.b_off + st * C::kBBytes, full(st), &tB, &tB2);
-        ++issued;
-        if (++st == t.stages) {
-          st = 0;
-          ph ^= 1u;
+  if (warp == 0 || warp == 2) {  // weights and, by another warp, tokens: a load takes about 35 ns to issue
+    const bool b_side = warp == 0;
+    bool ok = true;
+    int st = 0, i = b_side ? ahead : 0;
+    uint32_t ph = b_side ? 0u : 1u;  // parity of the empty barrier's phase to wait for
+    if (b_side && ahead < t.stages) st = ahead;
+    for (; i < count; ++i) {
+      if (i >= t.stages && !warp_wait(empty(st), ph, abort_flag, t.f.status)) {
+        ok = false;
+        break;
+      }
+      if (elect_one()) {
+        if (b_side) {
+          mbar_arrive_expect_tx(full(st), a_bytes + C::kBBytes);
+          tile_load_b<VAR, BN>(t, n, kb0 + i, base + t.b_off + st * C::kBBytes, full(st), &tB, &tB2);
+        } else {
+          tile_load_a<VAR, BN>(t, m, kb0 + i, base + st * a_bytes, full(st), &tA, &tA2);
         }
       }
-      if (!ok) {  // let the copies in flight land: the last one of each stage
-        for (int b = issued > t.stages ? issued - t.stages : 0; b < issued; ++b)
-          wait_landed(full(b % t.stages), static_cast<uint32_t>(b / t.stages) & 1u);
+      if (++st == t.stages) {
+        st = 0;
+        ph ^= 1u;
       }
+    }
+    if (!ok && lane == 0) {  // let the copies in flight land: the last one of each stage
+      for (int b = i > t.stages ? i - t.stages : 0; b < i; ++b)
+        wait_landed(full(b % t.stages), static_cast<uint32_t>(b / t.stages) & 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      int st = 0;
-      uint32_t ph = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(full(st), ph, abort_flag, t.f.status)) break;
-        tc_fence_after();
-        const uint32_t sa = base + st * a_bytes, sb = base + t.b_off + st * C::kBBytes;
+    int st = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < count; ++i) {
+      if (!warp_wait(full(st), ph, abort_flag, t.f.status)) break;
+      tc_fence_after();
+      const uint32_t sa = base + st * a_bytes, sb = base + t.b_off + st * C::kBBytes;
+      const uint64_t ad = sdesc_sw128(sa, 16, 1024);
+      const uint64_t bd = ffn_b_mn(VAR) ? sdesc_sw128(sb, 8192, 1024) : sdesc_sw128(sb, 16, 1024);
+      if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const uint64_t ad = sdesc_sw128(sa + ks * 32, 16, 1024);
-          const uint64_t bd = ffn_b_mn(VAR) ? sdesc_sw128(sb + ks * 2048, 8192, 1024) : sdesc_sw128(sb + ks * 32, 16, 1024);
-          umma_bf16(tmem, ad, bd, kIdesc, (kb > kb0 || ks > 0) ? 1u : 0u);
-        }
+        for (int ks = 0; ks < 4; ++ks)  // descriptors count 16-byte units
+          umma_bf16(tmem, ad + ks * 2, bd + ks * (ffn_b_mn(VAR) ? 128 : 2), kIdesc, (i > 0 || ks > 0) ? 1u : 0u);
         umma_commit(empty(st));
-        if (++st == t.stages) {
-          st = 0;
-          ph ^= 1u;
-        }
       }
-      umma_commit(done);  // also after an abort: what was issued completes before TMEM is freed
+      if (++st == t.stages) {
+        st = 0;
+        ph ^= 1u;
+      }
     }
+    if (elect_one()) umma_commit(done);  // also after an abort: what was issued completes before TMEM is freed
     __syncwarp();
   }
-  // the accumulator to shared memory, over the stages: every copy into them has been consumed
-  bool ok = true;
-  {
-    int w = 0;
-    if (lane == 0) {
-      w = mbar_wait(done, 0, abort_flag, t.f.status) ? 1 : 0;
-      // after an abort the MMAs already issued still end before TMEM is freed
-      if (!w && warp == 1) wait_landed(done, 0);
-    }
-    ok = __shfl_sync(0xffffffffu, w, 0) != 0;
-  }
-  __syncthreads();
-  if (*abort_flag) ok = false;
+  bool ok = warp_wait(done, 0, abort_flag, t.f.status);
+  if (!ok && warp == 1) wait_landed(done, 0);
+  if (S > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every peer has started
   tc_fence_after();
+  // the accumulator's chunks to their owners: chunk j (row-major over the tile's valid rows) is slot j / S
+  // of CTA j % S.  Without a split they are staged over the stages, every copy into which has been consumed.
   const int rows = min(128, t.f.M - m * 128);
-  if (warp >= 2 && ok) {
-    const int q = warp & 3;  // this warp's TMEM lane quarter
+  const uint32_t push = S > 1 ? base + t.push_off : base;
+  if (warp >= 2) {
+    const int q = warp & 3, r = q * 32 + lane;  // this warp's TMEM lane quarter; the lane's row
     if (q * 32 < rows) {
-      const uint32_t row = base + static_cast<uint32_t>(q * 32 + lane) * (C::kStride * 4u);
+      const uint32_t src = push + static_cast<uint32_t>(rank) * t.src_bytes;
+      const uint32_t j0 = static_cast<uint32_t>(r * C::kChunks);
+      const uint32_t slot0 = j0 / static_cast<uint32_t>(S), own0 = j0 - slot0 * static_cast<uint32_t>(S);
+      auto put = [&](const uint32_t* v, uint32_t chunk, uint32_t sub) {
+        if (r >= rows) return;
+        if (S == 1) {
+          const uint32_t d = src + C::slot_off(j0 + chunk) + sub;
+          st_shared_v4(d, make_uint4(v[0], v[1], v[2], v[3]));
+          st_shared_v4(d + 16, make_uint4(v[4], v[5], v[6], v[7]));
+        } else {
+          uint32_t slot = slot0, own = own0 + chunk;
+          while (own >= static_cast<uint32_t>(S)) own -= S, ++slot;
+          const uint32_t d = mapa_shared(src + C::slot_off(slot) + sub, own);
+          st_cluster_v4(d, v);
+          st_cluster_v4(d + 16, v + 4);
+        }
+      };
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, r);
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, v);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          st_shared_v4(row + 4u * c + 16u * j, make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]));
+        for (int j = 0; j < 4; ++j) {
+          const int col = c + 8 * j;
+          if (VAR == F_GATEUP && col >= C::kCols) put(v + 8 * j, (col - C::kCols) / 8, 32);
+          else put(v + 8 * j, col / 8, 0);
+        }
       }
     }
   }
   tc_fence_before();
-  if (S > 1) cluster_sync();
+  if (S > 1) cluster_sync();  // release / acquire: the pushed chunks are there
   else __syncthreads();
-  if (ok) {
-    const int64_t m0 = static_cast<int64_t>(m) * 128;
-    constexpr int kCols = VAR == F_GATEUP ? BN / 2 : BN;  // output columns of a tile
-    constexpr int kChunks = kCols / 8;
-    const int c0 = n * kCols;
-    const int items = rows * kChunks;
-    for (int it = rank * kTileThreads + threadIdx.x; it < items; it += S * kTileThreads) {
-      const int r = it / kChunks, c = (it - r * kChunks) * 8;
-      if (c0 + c >= t.f.N) continue;
-      float v[8], w[8];
+  if (warp == 1) tmem_dealloc(tmem, BN < 32 ? 32 : BN);
+  if (*abort_flag) return;  // the partials are not whole (recorded in the status word)
+  const int64_t m0 = static_cast<int64_t>(m) * 128;
+  const int c0 = n * C::kCols, items = rows * C::kChunks;
+  for (int slot = threadIdx.x; slot * S + rank < items; slot += kTileThreads) {
+    const int j = slot * S + rank, r = j / C::kChunks, c = (j - r * C::kChunks) * 8;
+    if (c0 + c >= t.f.N) continue;
+    float v[8], w[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = w[k] = 0.0f;
-      const uint32_t off = base + static_cast<uint32_t>(r) * (C::kStride * 4u) + 4u * c;
-      for (int p = 0; p < S; ++p) {
-        const uint32_t src = S > 1 ? mapa_shared(off, p) : off;
-        const float4 x = ld_cluster_f4(src), y = ld_cluster_f4(src + 16);
-        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-        if constexpr (VAR == F_GATEUP) {
-          const float4 z = ld_cluster_f4(src + kCols * 4), q = ld_cluster_f4(src + kCols * 4 + 16);
-          w[0] += z.x, w[1] += z.y, w[2] += z.z, w[3] += z.w, w[4] += q.x, w[5] += q.y, w[6] += q.z, w[7] += q.w;
-        }
+    for (int k = 0; k < 8; ++k) v[k] = w[k] = 0.0f;
+    uint32_t d = push + C::slot_off(static_cast<uint32_t>(slot));
+    for (int p = 0; p < S; ++p, d += t.src_bytes) {
+      const float4 x = ld_shared_f4(d), y = ld_shared_f4(d + 16);
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w, v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+      if constexpr (VAR == F_GATEUP) {
+        const float4 z = ld_shared_f4(d + 32), q = ld_shared_f4(d + 48);
+        w[0] += z.x, w[1] += z.y, w[2] += z.z, w[3] += z.w, w[4] += q.x, w[5] += q.y, w[6] += q.z, w[7] += q.w;
       }
-      tile_epilogue8<VAR>(t.f, m0 + r, c0 + c, v, w);
     }
+    tile_epilogue8<VAR>(t.f, m0 + r, c0 + c, v, w);
   }
-  if (S > 1) cluster_sync();  // no CTA leaves while a peer may read its partials
-  else __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, BN);
 }
 
 template <int VAR, int BN>
@@ -292,14 +347,19 @@ int launch_tile(const TileMaps& maps, TileArgs t, cudaStream_t stream) {
                           [] {
                             return static_cast<int>(cudaFuncSetAttribute(ffn_tile_kernel<VAR, BN>,
                                                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                                         static_cast<int>(kTileMaxSmem - 1024)));
+                                                                         static_cast<int>(kTileMaxSmem)));
                           },
                           static_cast<int>(cudaErrorInvalidDevice));
   if (se) return se;
   const uint32_t a_bytes = static_cast<uint32_t>(t.a_rows) * 128u;
   const uint32_t stage = a_bytes + C::kBBytes;
-  const uint32_t budget = kTileMaxSmem - 4096;  // static shared memory and the alignment slack
-  int stages = static_cast<int>((budget - 16384u) / stage);
+  const uint32_t rows = static_cast<uint32_t>(t.f.M < 128 ? t.f.M : 128);
+  const uint32_t slots = (rows * C::kChunks + t.split - 1) / t.split;
+  t.src_bytes = (C::slot_off(slots) + 31u) & ~15u;
+  const uint32_t push = t.split > 1 ? t.src_bytes * t.split : 0u;
+  const uint32_t budget = kTileSmem - 3072u - push;  // alignment slack, static and reserved shared memory
+  int stages = static_cast<int>(budget / stage);
+  if (stages < 2) stages = 2;
   if (stages > kTileMaxStages) stages = kTileMaxStages;
   const int per = (t.f.k_blocks + t.split - 1) / t.split;
   if (stages > per) stages = per;
@@ -310,8 +370,11 @@ int launch_tile(const TileMaps& maps, TileArgs t, cudaStream_t stream) {
   uint32_t smem = t.b_off + static_cast<uint32_t>(stages) * C::kBBytes;
   const uint32_t a_reach = static_cast<uint32_t>(stages - 1) * a_bytes + 16384u;
   if (smem < a_reach) smem = a_reach;
-  if (smem < C::kStaged) smem = C::kStaged;
+  t.push_off = smem;
+  smem += push;
+  if (t.split == 1 && smem < t.src_bytes) smem = t.src_bytes;
   smem += 1024;
+  if (smem > kTileMaxSmem) return static_cast<int>(cudaErrorInvalidValue);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(t.f.m_tiles) * t.f.n_tiles * t.split);
   cfg.blockDim = dim3(kTileThreads);
@@ -349,6 +412,7 @@ int launch_var(int64_t M, int64_t N, int64_t K, int split, const FfnOperands& o,
   t.f = f;
   t.a_rows = M >= 128 ? 128 : static_cast<int32_t>((M + 7) / 8 * 8);
   t.split = split;
+  t.early_b = VAR == F_DOWN || VAR == F_DX;  // always behind GATEUP and DACT
   const uint64_t um = static_cast<uint64_t>(M), un = static_cast<uint64_t>(N), uk = static_cast<uint64_t>(K);
   TileMaps p;
   bool good = make_tmap_bf16(&p.a, o.a, uk, um, 64, static_cast<uint32_t>(t.a_rows));
@@ -363,20 +427,20 @@ int launch_var(int64_t M, int64_t N, int64_t K, int split, const FfnOperands& o,
   return launch_tile<VAR, BN>(p, t, stream);
 }
 
-// Columns of a tile and CTAs per tile.  With few tiles the K range is split over a cluster until about
-// every SM has a CTA, leaving each at least four K blocks; 64-column tiles first, since they need fewer
-// CTAs per tile.
+// Columns of a tile and CTAs per tile.  64-column tiles, two CTAs resident per SM, and with few tiles the K
+// range split over a cluster until about every SM has its two, leaving each at least four K blocks; from three
+// rounds of them on, 128-column tiles.
 template <int VAR>
 int launch_tiles(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& f, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return static_cast<int>(cudaErrorInvalidDevice);
   auto tiles = [&](int bn) { return (M + 127) / 128 * ((N + bn - 1) / bn); };
   constexpr int kPer = VAR == F_GATEUP ? 2 : 1;  // tile columns per output column
-  if (2 * tiles(64 / kPer) > 3 * sms) return launch_var<VAR, 128>(M, N, K, 1, o, f, stream);
+  if (tiles(64 / kPer) > 6 * sms) return launch_var<VAR, 128>(M, N, K, 1, o, f, stream);
   const int64_t kb = (K + kFfnBK - 1) / kFfnBK * (VAR == F_DX ? 2 : 1);
-  int64_t split = sms / tiles(64 / kPer);
+  int64_t split = 2 * sms / tiles(64 / kPer);
   if (split > kb / 4) split = kb / 4;
-  split = split < 1 ? 1 : split > 8 ? 8 : split;
+  split = split >= 8 ? 8 : split >= 4 ? 4 : split >= 2 ? 2 : 1;  // (clusters of 3, 5 or 6 leave SMs of a GPC idle)
   return launch_var<VAR, 64>(M, N, K, static_cast<int>(split), o, f, stream);
 }
 

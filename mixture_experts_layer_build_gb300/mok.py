@@ -167,8 +167,14 @@ def _check(rc: int, where: str):
         raise MokError(rc, where)
 
 
+# the handle of a device's current stream without building a Stream object (0.1 against 2.9 us per call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -573,6 +579,8 @@ def _arg(t: torch.Tensor | None, shape, dtype, name: str):
     """data_ptr of a contiguous CUDA tensor of that shape and dtype (None passes as NULL)."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return _ptr(t, dtype, name)
