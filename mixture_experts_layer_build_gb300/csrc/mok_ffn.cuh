@@ -49,6 +49,28 @@ __host__ __device__ __forceinline__ int64_t ffn_saved_offset(int64_t row, int co
 }
 
 #ifdef __CUDACC__
+// Bounded wait that ignores the abort flag: only while winding down.
+__device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
+  }
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// The whole warp waits; the same answer on every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+// Let the stream's next kernel be scheduled.  Only after this thread's pdl_wait() -- all kernels before this
+// one have then ended, so that one that follows knows that of everything but this one -- and after the
+// CTA's TMEM is allocated: a CTA of the next kernel that took the columns first would wait for this
+// grid while holding them.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 
 // act(g) and, for the backward, act'(g).  The tanh form of GELU is g sigmoid(2 z), z = c (g + k g^3),

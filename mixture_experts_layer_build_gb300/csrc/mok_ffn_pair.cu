@@ -15,6 +15,7 @@ namespace mok {
 namespace {
 
 constexpr int kPairThreads = 64 + 32 * 8;
+constexpr uint32_t kPairTmemCols = 512;  // two accumulators, 256 columns apart
 constexpr int kGroupM = 8;  // M tiles of one band of the tile order
 
 struct PairArgs {
@@ -34,18 +35,21 @@ enum PairVariant : int { P_GATEUP = 0, P_DOWN, P_DACT, P_DX, P_DW };
 
 template <int VAR, int BN>
 struct PairCfg {
-  static constexpr int kStages = BN == 256 ? 6 : 8;
+  static constexpr bool kBmn = VAR >= P_DACT;
   static constexpr uint32_t kABytes = 128 * 128;
-  static constexpr uint32_t kBBytes = BN / 2 * 128;
+  // an MN-major B half is whole 64-column boxes (the columns past BN / 2 of the last one are not used)
+  static constexpr uint32_t kBBoxes = (BN / 2 + 63) / 64;
+  static constexpr uint32_t kBBytes = kBmn ? kBBoxes * 8192 : BN / 2 * 128;
   static constexpr uint32_t kStageBytes = kABytes + kBBytes;
   static constexpr uint32_t kTxBytes = 2 * kStageBytes;  // both CTAs' loads count on the first CTA's barrier
-  static constexpr uint32_t kStagingOff = kStages * kStageBytes;
   static constexpr uint32_t kStagingBytes = 8 * 2 * 2048;  // two 32-row x 64-byte tiles per epilogue warp
+  static constexpr int kStages = static_cast<int>((232448u - 1024u - 512u - kStagingBytes) / kStageBytes);
+  static constexpr uint32_t kStagingOff = kStages * kStageBytes;
   static constexpr uint32_t kBarOff = kStagingOff + kStagingBytes;
   static constexpr uint32_t kSmemBytes = 1024 + kBarOff + 256;
-  static constexpr uint32_t kTmemCols = 2 * BN;
   static_assert(kSmemBytes <= 232448, "shared memory per CTA");
   static_assert(2 * kStages + 5 <= 24, "barriers fit");
+  static_assert(kStageBytes % 1024 == 0, "swizzle atoms");
 };
 
 struct PairUnit {
@@ -80,37 +84,38 @@ __device__ __forceinline__ PairUnit pair_unit(const PairArgs& p, int u) {
   return w;
 }
 
-// This CTA's loads of one K block: its 128 rows of A and its half of B's columns.
-template <int VAR, int BN>
-__device__ __forceinline__ void pair_load(const PairArgs& p, const PairMaps& t, const PairUnit& w, int kb,
-                                          uint32_t sa, uint32_t sb, uint32_t bar, int rank) {
-  constexpr int HB = BN / 2;
+// This CTA's loads of one K block: its 128 rows of A, and its half of B's columns.
+template <int VAR>
+__device__ __forceinline__ void pair_load_a(const PairArgs& p, const PairMaps& t, const PairUnit& w, int kb,
+                                            uint32_t sa, uint32_t bar, int rank) {
   const int k0 = kb * kFfnBK, m0 = w.m * 256 + rank * 128;
   if constexpr (VAR == P_DW) {
     const CUtensorMap* ta = &t.a[w.which];
     tma_load_2d_pair(sa, ta, bar, m0, k0);
     tma_load_2d_pair(sa + 8192, ta, bar, m0 + 64, k0);
-    const CUtensorMap* tb = &t.b[w.which == 2 ? 1 : 0];
-#pragma unroll
-    for (int j = 0; j < HB / 64; ++j) tma_load_2d_pair(sb + j * 8192, tb, bar, w.n * BN + rank * HB + j * 64, k0);
   } else if constexpr (VAR == P_DX) {
     const int half = kb < p.f.kb_split ? 0 : 1;
-    const int kr = k0 - half * p.f.kb_split * kFfnBK;
-    tma_load_2d_pair(sa, &t.a[half], bar, kr, m0);
-#pragma unroll
-    for (int j = 0; j < HB / 64; ++j)
-      tma_load_2d_pair(sb + j * 8192, &t.b[half], bar, w.n * BN + rank * HB + j * 64, kr);
+    tma_load_2d_pair(sa, &t.a[half], bar, k0 - half * p.f.kb_split * kFfnBK, m0);
   } else {
     tma_load_2d_pair(sa, &t.a[0], bar, k0, m0);
-    if constexpr (VAR == P_GATEUP) {  // the first CTA holds the gate rows, the second the same up rows
-      tma_load_2d_pair(sb, &t.b[rank], bar, k0, w.n * HB);
-    } else if constexpr (VAR == P_DOWN) {
-      tma_load_2d_pair(sb, &t.b[0], bar, k0, w.n * BN + rank * HB);
-    } else {
+  }
+}
+template <int VAR, int BN>
+__device__ __forceinline__ void pair_load_b(const PairArgs& p, const PairMaps& t, const PairUnit& w, int kb,
+                                            uint32_t sb, uint32_t bar, int rank) {
+  constexpr int HB = BN / 2;
+  const int k0 = kb * kFfnBK;
+  if constexpr (VAR == P_GATEUP) {  // the first CTA holds the gate rows, the second the same up rows
+    tma_load_2d_pair(sb, &t.b[rank], bar, k0, w.n * HB);
+  } else if constexpr (VAR == P_DOWN) {
+    tma_load_2d_pair(sb, &t.b[0], bar, k0, w.n * BN + rank * HB);
+  } else {
+    const int half = VAR == P_DX && kb >= p.f.kb_split ? 1 : 0;
+    const CUtensorMap* tb = &t.b[VAR == P_DW ? (w.which == 2 ? 1 : 0) : half];
+    const int kr = k0 - half * p.f.kb_split * kFfnBK;
 #pragma unroll
-      for (int j = 0; j < HB / 64; ++j)
-        tma_load_2d_pair(sb + j * 8192, &t.b[0], bar, w.n * BN + rank * HB + j * 64, k0);
-    }
+    for (int j = 0; j < static_cast<int>(PairCfg<VAR, BN>::kBBoxes); ++j)
+      tma_load_2d_pair(sb + j * 8192, tb, bar, w.n * BN + rank * HB + j * 64, kr);
   }
 }
 
@@ -179,14 +184,17 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
     __syncwarp();
     if (lane == 0) mbar_arrive_cluster(tempty);
   };
+  // this warp's 32-column chunks of the tile's: the first half (rounded up) or the rest
+  constexpr int kChunks = (VAR == P_GATEUP ? BN / 2 : BN) / 32;
+  const int c_beg = h ? (kChunks + 1) / 2 * 32 : 0, c_end = h ? kChunks * 32 : (kChunks + 1) / 2 * 32;
   if constexpr (VAR == P_GATEUP) {
-    const int c0 = w.n * (BN / 2) + h * (BN / 4);
-#pragma unroll
-    for (int c = 0; c < BN / 4; c += 32) {
+    const int c0 = w.n * (BN / 2);
+#pragma unroll 1
+    for (int c = c_beg; c < c_end; c += 32) {
       float g[32], u[32];
-      tmem_ld32(taddr + h * (BN / 4) + c, g);
-      tmem_ld32(taddr + BN / 2 + h * (BN / 4) + c, u);
-      if (c + 32 >= BN / 4) release();
+      tmem_ld32(taddr + c, g);
+      tmem_ld32(taddr + BN / 2 + c, u);
+      if (c + 32 >= c_end) release();
       if (!rows || c0 + c >= f.N) continue;
       if (f.g) {
         const int64_t off = ffn_saved_offset(r0 + lane, c0 + c, f.N);
@@ -198,9 +206,9 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
       st.put_bf16(g, &t.o[0], c0 + c, r0);
     }
   } else if constexpr (VAR == P_DACT) {
-    const int c0 = w.n * BN + h * (BN / 2);
+    const int c0 = w.n * BN;
 #pragma unroll 1
-    for (int c = 0; c < BN / 2; c += 32) {
+    for (int c = c_beg; c < c_end; c += 32) {
       const bool in = rows && c0 + c < f.N;
       float4 g4[8], u4[8];
       if (in) {
@@ -209,8 +217,8 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
         saved_load(f.u, off, f.N - c0 - c, u4);
       }
       float v[32];
-      tmem_ld32(taddr + h * (BN / 2) + c, v);
-      if (c + 32 >= BN / 2) release();
+      tmem_ld32(taddr + c, v);
+      if (c + 32 >= c_end) release();
       if (!in) continue;
       float dg[32];
 #pragma unroll
@@ -230,9 +238,9 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
   } else {
     const int M = VAR == P_DW && w.which == 2 ? f.N : f.M, N = VAR == P_DW && w.which == 2 ? f.M : f.N;
     const CUtensorMap* to = &t.o[VAR == P_DW ? w.which : 0];
-    const int c0 = w.n * BN + h * (BN / 2);
+    const int c0 = w.n * BN;
 #pragma unroll 1
-    for (int c = 0; c < BN / 2; c += 32) {
+    for (int c = c_beg; c < c_end; c += 32) {
       const bool in = r0 < M && c0 + c < N;
       uint4 res[4];
       if constexpr (VAR == P_DOWN) {
@@ -243,8 +251,8 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
         }
       }
       float v[32];
-      tmem_ld32(taddr + h * (BN / 2) + c, v);
-      if (c + 32 >= BN / 2) release();
+      tmem_ld32(taddr + c, v);
+      if (c + 32 >= c_end) release();
       if (!in) continue;
       if constexpr (VAR == P_DOWN) {
         if (f.residual && r0 + lane < M) {
@@ -276,19 +284,12 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
   }
 }
 
-// Bounded wait that ignores the abort flag: only while winding down.
-__device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
-  }
-}
-
 template <int VAR, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     ffn_pair_kernel(const __grid_constant__ PairMaps t, const PairArgs p) {
   using C = PairCfg<VAR, BN>;
   constexpr int S = C::kStages;
-  constexpr bool kAmn = VAR == P_DW, kBmn = VAR >= P_DACT;
+  constexpr bool kAmn = VAR == P_DW, kBmn = C::kBmn;
   constexpr uint32_t kIdesc = idesc_bf16(256, BN, kAmn, kBmn);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -327,85 +328,107 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_alloc_pair(smem_u32(tmem_slot), kPairTmemCols);
     tmem_relinquish_pair();
   }
   tc_fence_before();
   cluster_sync();  // the peer's barriers exist before anything arrives on them
-  pdl_wait();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // DOWN and DX always follow another kernel of this block, which runs once everything before it has ended:
+  // their first weights are loaded before its end
+  constexpr bool kEarlyB = VAR == P_DOWN || VAR == P_DX;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int st = 0, issued = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int u = u0; u < p.units && ok; u += step) {
-        const PairUnit w = pair_unit<VAR>(p, u);
-        for (int kb = 0; kb < p.f.k_blocks; ++kb) {
-          if (!mbar_wait(empty(st), ph ^ 1u, abort_flag, status)) {
-            ok = false;
-            break;
+    int ahead = 0;
+    if constexpr (kEarlyB) {
+      ahead = min(p.f.k_blocks, S);
+      if (u0 < p.units) {
+        const PairUnit w = pair_unit<VAR>(p, u0);
+        for (int kb = 0; kb < ahead; ++kb)
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(full(kb), C::kTxBytes);
+            pair_load_b<VAR, BN>(p, t, w, kb, base + kb * C::kStageBytes + C::kABytes, mapa_shared(full(kb), 0), rank);
           }
-          const uint32_t sa = base + st * C::kStageBytes;
-          if (rank == 0) mbar_arrive_expect_tx(full(st), C::kTxBytes);
-          pair_load<VAR, BN>(p, t, w, kb, sa, sa + C::kABytes, mapa_shared(full(st), 0), rank);
-          ++issued;
-          if (++st == S) {
-            st = 0;
-            ph ^= 1u;
+      }
+    }
+    pdl_wait();
+    pdl_trigger();
+    int st = 0, issued = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int u = u0; u < p.units && ok; u += step) {
+      const PairUnit w = pair_unit<VAR>(p, u);
+      for (int kb = 0; kb < p.f.k_blocks; ++kb) {
+        if (!warp_wait(empty(st), ph ^ 1u, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = base + st * C::kStageBytes, bar = mapa_shared(full(st), 0);
+        if (elect_one()) {
+          if (issued >= ahead) {
+            if (rank == 0) mbar_arrive_expect_tx(full(st), C::kTxBytes);
+            pair_load_b<VAR, BN>(p, t, w, kb, sa + C::kABytes, bar, rank);
           }
+          pair_load_a<VAR>(p, t, w, kb, sa, bar, rank);
+        }
+        ++issued;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1u;
         }
       }
-      if (!ok && rank == 0)  // let the copies in flight land: the last one of each stage
-        for (int b = issued > S ? issued - S : 0; b < issued; ++b)
-          wait_landed(full(b % S), static_cast<uint32_t>(b / S) & 1u);
     }
+    if (!ok && rank == 0 && lane == 0)  // let the copies in flight land: the last one of each stage
+      for (int b = issued > S ? issued - S : 0; b < issued; ++b)
+        wait_landed(full(b % S), static_cast<uint32_t>(b / S) & 1u);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       int st = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
       for (int u = u0; u < p.units && ok; u += step) {
-        if (!mbar_wait<true>(tempty(acc), aph ^ 1u, abort_flag, status)) break;
+        if (!__all_sync(0xffffffffu, mbar_wait<true>(tempty(acc), aph ^ 1u, abort_flag, status))) break;
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+        const uint32_t d = tmem + static_cast<uint32_t>(acc) * 256u;
         for (int kb = 0; kb < p.f.k_blocks; ++kb) {
-          if (!mbar_wait(full(st), ph, abort_flag, status)) {
+          if (!warp_wait(full(st), ph, abort_flag, status)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sa = base + st * C::kStageBytes, sb = sa + C::kABytes;
+          const uint64_t ad = kAmn ? sdesc_sw128(sa, 8192, 1024) : sdesc_sw128(sa, 16, 1024);
+          const uint64_t bd = kBmn ? sdesc_sw128(sb, 8192, 1024) : sdesc_sw128(sb, 16, 1024);
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint64_t ad = kAmn ? sdesc_sw128(sa + ks * 2048, 8192, 1024) : sdesc_sw128(sa + ks * 32, 16, 1024);
-            const uint64_t bd = kBmn ? sdesc_sw128(sb + ks * 2048, 8192, 1024) : sdesc_sw128(sb + ks * 32, 16, 1024);
-            umma_bf16_pair(d, ad, bd, kIdesc, (kb | ks) != 0 ? 1u : 0u);
+            for (int ks = 0; ks < 4; ++ks)  // descriptors count 16-byte units
+              umma_bf16_pair(d, ad + ks * (kAmn ? 128 : 2), bd + ks * (kBmn ? 128 : 2), kIdesc,
+                             (kb | ks) != 0 ? 1u : 0u);
+            umma_commit_pair(empty(st));
           }
-          umma_commit_pair(empty(st));
           if (++st == S) {
             st = 0;
             ph ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit_pair(tfull(acc));
+        if (elect_one()) umma_commit_pair(tfull(acc));
         if (++acc == 2) {
           acc = 0;
           aph ^= 1u;
         }
       }
-      umma_commit_pair(drain);  // every MMA issued has ended before TMEM is freed, in both CTAs
-      wait_landed(drain, 0);
-    } else if (lane == 0) {
-      wait_landed(drain, 0);
+      // every MMA issued has ended before TMEM is freed, in both CTAs
+      if (elect_one()) umma_commit_pair(drain);
     }
+    __syncwarp();
+    if (lane == 0) wait_landed(drain, 0);
     __syncwarp();
   } else {
     const int q = warp & 3, h = (warp - 2) >> 2;
+    pdl_wait();  // the residual, the saved g and u, and outputs that an earlier kernel may still read
     WarpStage st{base + C::kStagingOff + static_cast<uint32_t>(warp - 2) * 4096u, 0, lane};
     int acc = 0;
     uint32_t aph = 0;
@@ -417,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (!ok) break;
       tc_fence_after();
       pair_epilogue<VAR, BN>(p, t, w, rank, q, h, lane,
-                             tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN), st,
+                             tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc) * 256u, st,
                              mapa_shared(tempty(acc), 0));
       if (++acc == 2) {
         acc = 0;
@@ -437,7 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync();  // neither CTA leaves while the other may still address it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, C::kTmemCols);
+    tmem_dealloc_pair(tmem, kPairTmemCols);
   }
 }
 
@@ -497,13 +520,47 @@ int pair_rows(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnAr
 
 }  // namespace
 
+namespace {
+
+// The tile width with the least time by rounds of pairs x columns per tile, 16 columns more for what a tile
+// costs besides them: the feed of its A rows.
+template <int... BNS>
+int best_width(int64_t m_tiles, int64_t n, int pairs) {
+  int best = 0;
+  int64_t cost = 0;
+  for (int bn : {BNS...}) {
+    const int64_t c = tiles_of(m_tiles * tiles_of(n, bn), pairs) * (bn + 16);
+    if (!best || c < cost) best = bn, cost = c;
+  }
+  return best;
+}
+
+template <int VAR>
+int pair_rows_any(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& f, cudaStream_t stream) {
+  const int pairs = sm_count() / 2;
+  if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
+  const int64_t mt = tiles_of(M, 256);
+  int bn;
+  if constexpr (VAR == P_GATEUP) {  // (half of the columns are gate columns, in whole 32-column chunks)
+    bn = best_width<256, 192, 128>(mt, 2 * N, pairs);
+  } else {
+    bn = best_width<256, 224, 192, 128>(mt, N, pairs);
+    if (bn == 224) return pair_rows<VAR, 224>(M, N, K, o, f, stream);
+  }
+  if (bn == 256) return pair_rows<VAR, 256>(M, N, K, o, f, stream);
+  if (bn == 192) return pair_rows<VAR, 192>(M, N, K, o, f, stream);
+  return pair_rows<VAR, 128>(M, N, K, o, f, stream);
+}
+
+}  // namespace
+
 int launch_ffn_pair(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
                     cudaStream_t stream) {
   switch (var) {
-    case F_GATEUP: return pair_rows<P_GATEUP, 256>(M, N, K, o, a, stream);
-    case F_DOWN: return pair_rows<P_DOWN, 256>(M, N, K, o, a, stream);
-    case F_DACT: return pair_rows<P_DACT, 256>(M, N, K, o, a, stream);
-    default: return pair_rows<P_DX, 256>(M, N, K, o, a, stream);
+    case F_GATEUP: return pair_rows_any<P_GATEUP>(M, N, K, o, a, stream);
+    case F_DOWN: return pair_rows_any<P_DOWN>(M, N, K, o, a, stream);
+    case F_DACT: return pair_rows_any<P_DACT>(M, N, K, o, a, stream);
+    default: return pair_rows_any<P_DX>(M, N, K, o, a, stream);
   }
 }
 

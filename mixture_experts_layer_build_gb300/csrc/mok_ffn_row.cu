@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) ffn_row_kernel(const RowArgs a
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) load_w(u, k0 + u * kStep);
   if (!kGate) pdl_wait();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   uint64_t acc[kRowRows][TT];
 #pragma unroll
   for (int r = 0; r < kRowRows; ++r)

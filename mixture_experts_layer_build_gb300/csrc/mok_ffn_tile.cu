@@ -50,23 +50,6 @@ struct TileCfg {
   }
 };
 
-// Bounded wait that ignores the abort flag: only while winding down.
-__device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
-  }
-}
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
-  return p != 0;
-}
-// The whole warp waits; the same answer on every lane.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
-}
-
 __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -212,10 +195,7 @@ __global__ void __launch_bounds__(kTileThreads)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // every kernel before this one has ended: the next one of this block may start loading its weights.  (After
-  // this CTA's TMEM allocation: one of the next kernel's CTAs that took the columns first would wait for
-  // this grid while holding them.)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const uint32_t tmem = tmem_slot;
 
