@@ -9,6 +9,8 @@
 // Tiles are dealt out round robin over one pair per two SMs, in an order that keeps the tiles running
 // together in a near-square block of the output (ordered_tile), so that both operands are read from
 // L2.  The three weight gradients share one launch: alike in K, they fill the last round together.
+#include <initializer_list>
+
 #include "mok_ffn.cuh"
 
 namespace mok {
@@ -150,6 +152,17 @@ struct WarpStage {
   }
 };
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   uint32_t r[32];
   tmem_ld_32x32b_x32(taddr, r);
@@ -158,11 +171,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 32 columns (8 float4) of this lane's row of a saved g or u (ffn_saved_offset), columns past I skipped.
-__device__ __forceinline__ void saved_load(const float* p, int64_t off, int left, float4 (&v)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    v[j] = 4 * j < left ? __ldcs(reinterpret_cast<const float4*>(p + off) + 32 * j) : make_float4(0, 0, 0, 0);
+// 32 columns of this lane's row of the saved g and u (ffn_saved_offset), 4 columns per entry.  DACT keeps one
+// chunk loaded ahead: its first one while the tile's MMAs run, the next one entry by entry as the current
+// one is used (a chunk's loads issued and awaited in place took 2.3 us, four of them per warp and tile).
+struct SavedChunk {
+  float4 g[8], u[8];
+};
+__device__ __forceinline__ void saved_fetch(const FfnArgs& f, int row0, int lane, int col, int j, SavedChunk& s) {
+  if (row0 < f.M && col + 4 * j < f.N) {
+    const int64_t off = ffn_saved_offset(row0 + lane, col, f.N);
+    s.g[j] = __ldcs(reinterpret_cast<const float4*>(f.g + off) + 32 * j);
+    s.u[j] = __ldcs(reinterpret_cast<const float4*>(f.u + off) + 32 * j);
+  }
 }
 __device__ __forceinline__ void saved_store(float* p, int64_t off, int left, const float (&v)[32]) {
 #pragma unroll
@@ -175,7 +195,8 @@ __device__ __forceinline__ void saved_store(float* p, int64_t off, int left, con
 // Epilogue of one tile for one warp: accumulator rows q * 32 ... (lane = row), column half h.
 template <int VAR, int BN>
 __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps& t, const PairUnit& w, int rank, int q,
-                                              int h, int lane, uint32_t taddr, WarpStage& st, uint32_t tempty) {
+                                              int h, int lane, uint32_t taddr, WarpStage& st, uint32_t tempty,
+                                              SavedChunk& pre) {
   const FfnArgs& f = p.f;
   const int r0 = w.m * 256 + rank * 128 + q * 32;  // the warp's first row
   const bool rows = r0 < f.M;                       // (DWd: M below)
@@ -209,31 +230,37 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
     const int c0 = w.n * BN;
 #pragma unroll 1
     for (int c = c_beg; c < c_end; c += 32) {
-      const bool in = rows && c0 + c < f.N;
-      float4 g4[8], u4[8];
-      if (in) {
-        const int64_t off = ffn_saved_offset(r0 + lane, c0 + c, f.N);
-        saved_load(f.g, off, f.N - c0 - c, g4);
-        saved_load(f.u, off, f.N - c0 - c, u4);
-      }
-      float v[32];
-      tmem_ld32(taddr + c, v);
-      if (c + 32 >= c_end) release();
-      if (!in) continue;
-      float dg[32];
+      uint4 dg[4], du[4];
+      uint32_t* pg = reinterpret_cast<uint32_t*>(dg);
+      uint32_t* pu = reinterpret_cast<uint32_t*>(du);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float g[4] = {g4[j].x, g4[j].y, g4[j].z, g4[j].w}, u[4] = {u4[j].x, u4[j].y, u4[j].z, u4[j].w};
+      for (int i = 0; i < 32; i += 16) {  // accumulator columns 16 at a time: registers
+        float v[16];
+        tmem_ld16(taddr + c + i, v);
+        if (i == 16 && c + 32 >= c_end) release();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float a, da;
-          act_bwd(g[k], f.act, a, da);
-          dg[4 * j + k] = v[4 * j + k] * u[k] * da;
-          v[4 * j + k] *= a;
+        for (int jj = 0; jj < 4; ++jj) {
+          const int j = i / 4 + jj;
+          const float g[4] = {pre.g[j].x, pre.g[j].y, pre.g[j].z, pre.g[j].w};
+          const float u[4] = {pre.u[j].x, pre.u[j].y, pre.u[j].z, pre.u[j].w};
+          if (c + 32 < c_end) saved_fetch(f, r0, lane, c0 + c + 32, j, pre);
+          float x[4], y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float a, da;
+            act_bwd(g[k], f.act, a, da);
+            x[k] = v[4 * jj + k] * u[k] * da;
+            y[k] = v[4 * jj + k] * a;
+          }
+          pg[2 * j] = pack_bf16x2(x[0], x[1]);
+          pg[2 * j + 1] = pack_bf16x2(x[2], x[3]);
+          pu[2 * j] = pack_bf16x2(y[0], y[1]);
+          pu[2 * j + 1] = pack_bf16x2(y[2], y[3]);
         }
       }
-      st.put_bf16(dg, &t.o[0], c0 + c, r0);
-      st.put_bf16(v, &t.o[1], c0 + c, r0);
+      if (!rows || c0 + c >= f.N) continue;
+      st.put(dg, &t.o[0], c0 + c, r0);
+      st.put(du, &t.o[1], c0 + c, r0);
     }
   } else {
     const int M = VAR == P_DW && w.which == 2 ? f.N : f.M, N = VAR == P_DW && w.which == 2 ? f.M : f.N;
@@ -434,6 +461,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint32_t aph = 0;
     for (int u = u0; u < p.units; u += step) {
       const PairUnit w = pair_unit<VAR>(p, u);
+      SavedChunk pre;
+      if constexpr (VAR == P_DACT) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          saved_fetch(p.f, w.m * 256 + rank * 128 + q * 32, lane, w.n * BN + (h ? (BN / 32 + 1) / 2 * 32 : 0), j, pre);
+      }
       int ok = 0;
       if (lane == 0) ok = mbar_wait(tfull(acc), aph, abort_flag, status) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -441,13 +474,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tc_fence_after();
       pair_epilogue<VAR, BN>(p, t, w, rank, q, h, lane,
                              tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc) * 256u, st,
-                             mapa_shared(tempty(acc), 0));
+                             mapa_shared(tempty(acc), 0), pre);
       if (++acc == 2) {
         acc = 0;
         aph ^= 1u;
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (lane == 0) bulk_wait_read<0>();  // the staging tiles have been read; the grid's end waits for the writes
     __syncwarp();
   }
   if (*abort_flag) {  // failure path: copies or arrivals of the peer may still be in flight
@@ -522,14 +555,17 @@ int pair_rows(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnAr
 
 namespace {
 
-// The tile width with the least time by rounds of pairs x columns per tile, 16 columns more for what a tile
-// costs besides them: the feed of its A rows.
-template <int... BNS>
-int best_width(int64_t m_tiles, int64_t n, int pairs) {
+// Cost of a launch of `units` tiles of bn columns, by rounds of pairs x columns per tile, 16 columns more for
+// what a tile costs besides them: the feed of its A rows.
+int64_t width_cost(int64_t units, int bn, int pairs) { return tiles_of(units, pairs) * (bn + 16); }
+
+// The tile width of the least cost; units(bn): tiles of that width.
+template <class Units>
+int best_width(std::initializer_list<int> widths, int pairs, Units&& units) {
   int best = 0;
   int64_t cost = 0;
-  for (int bn : {BNS...}) {
-    const int64_t c = tiles_of(m_tiles * tiles_of(n, bn), pairs) * (bn + 16);
+  for (int bn : widths) {
+    const int64_t c = width_cost(units(bn), bn, pairs);
     if (!best || c < cost) best = bn, cost = c;
   }
   return best;
@@ -542,9 +578,9 @@ int pair_rows_any(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const F
   const int64_t mt = tiles_of(M, 256);
   int bn;
   if constexpr (VAR == P_GATEUP) {  // (half of the columns are gate columns, in whole 32-column chunks)
-    bn = best_width<256, 192, 128>(mt, 2 * N, pairs);
+    bn = best_width({256, 192, 128}, pairs, [&](int w) { return mt * tiles_of(2 * N, w); });
   } else {
-    bn = best_width<256, 224, 192, 128>(mt, N, pairs);
+    bn = best_width({256, 224, 192, 128}, pairs, [&](int w) { return mt * tiles_of(N, w); });
     if (bn == 224) return pair_rows<VAR, 224>(M, N, K, o, f, stream);
   }
   if (bn == 256) return pair_rows<VAR, 256>(M, N, K, o, f, stream);
@@ -564,9 +600,11 @@ int launch_ffn_pair(int var, int64_t M, int64_t N, int64_t K, const FfnOperands&
   }
 }
 
-int launch_ffn_dw(int64_t T, int64_t H, int64_t I, const FfnGradOperands& o, int out_f32, uint32_t* status,
-                  cudaStream_t stream) {
-  constexpr int BN = 256;
+namespace {
+
+template <int BN>
+int pair_dw(int64_t T, int64_t H, int64_t I, const FfnGradOperands& o, int out_f32, uint32_t* status,
+            cudaStream_t stream) {
   PairArgs p{};
   p.f.M = static_cast<int32_t>(I);
   p.f.N = static_cast<int32_t>(H);
@@ -597,6 +635,20 @@ int launch_ffn_dw(int64_t T, int64_t H, int64_t I, const FfnGradOperands& o, int
            out_map(&m.o[2], o.dw_down, i, h);
   if (!good) return static_cast<int>(cudaErrorInvalidValue);
   return launch_pair<P_DW, BN>(m, p, stream);
+}
+
+}  // namespace
+
+int launch_ffn_dw(int64_t T, int64_t H, int64_t I, const FfnGradOperands& o, int out_f32, uint32_t* status,
+                  cudaStream_t stream) {
+  const int pairs = sm_count() / 2;
+  if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
+  const int bn = best_width({256, 192, 128}, pairs, [&](int w) {
+    return (o.dw_gate ? 2 * tiles_of(I, 256) * tiles_of(H, w) : 0) + (o.dw_down ? tiles_of(H, 256) * tiles_of(I, w) : 0);
+  });
+  if (bn == 256) return pair_dw<256>(T, H, I, o, out_f32, status, stream);
+  if (bn == 192) return pair_dw<192>(T, H, I, o, out_f32, status, stream);
+  return pair_dw<128>(T, H, I, o, out_f32, status, stream);
 }
 
 }  // namespace mok
