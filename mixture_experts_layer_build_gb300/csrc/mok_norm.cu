@@ -22,13 +22,47 @@ constexpr int kNormMaxH = 16384;
 constexpr int kNormThreads = 512;  // most threads of a block
 constexpr int kNormParts = 608;  // most partial dweight rows: four CTAs on each of 152 SMs
 
-__device__ __forceinline__ void unpack_bf16x8(uint4 q, float (&v)[8]) {
-  v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
-  v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
+// fp32 values in pairs: one instruction for two (add, mul, fma .f32x2), each rounded as the scalar one.
+using Pair = uint64_t;
+__device__ __forceinline__ Pair pair_of(uint32_t lo, uint32_t hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
 }
-__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ Pair splat(float v) { return pair_of(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ float2 floats_of(Pair p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_pair(Pair p) {
+  const float2 v = floats_of(p);
+  return pack_bf16x2(v.x, v.y);
+}
+__device__ __forceinline__ uint4 pack_pairs(const Pair (&v)[4]) {
+  return make_uint4(pack_pair(v[0]), pack_pair(v[1]), pack_pair(v[2]), pack_pair(v[3]));
+}
+// 8 bf16 as fp32 bit patterns, or as pairs.
+__device__ __forceinline__ void bits_of(uint4 q, uint32_t (&b)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[2 * i] = w[i] << 16, b[2 * i + 1] = w[i] & 0xFFFF0000u;
+}
+__device__ __forceinline__ void pairs_of(uint4 q, Pair (&v)[4]) {
+  uint32_t b[8];
+  bits_of(q, b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pair_of(b[2 * i], b[2 * i + 1]);
 }
 
 // 8 values of a bf16 or fp32 tensor, as loaded.  The loads are streaming (evict-first: no kernel
@@ -41,42 +75,45 @@ struct Vec8<false> {
   __device__ __forceinline__ void load(const void* p, int64_t i) {
     q = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const { unpack_bf16x8(q, v); }
-  // stores v and leaves in v what the stored values read back as
-  static __device__ __forceinline__ void store(void* p, int64_t i, float (&v)[8]) {
-    const uint4 q = pack_bf16x8(v);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = q;
-    unpack_bf16x8(q, v);
+  __device__ __forceinline__ void bits(uint32_t (&b)[8]) const { bits_of(q, b); }
+  __device__ __forceinline__ void get(Pair (&v)[4]) const { pairs_of(q, v); }
+  static __device__ __forceinline__ void store(void* p, int64_t i, const Pair (&v)[4]) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) = pack_pairs(v);
   }
-  static __device__ __forceinline__ void rounded(float (&v)[8]) { unpack_bf16x8(pack_bf16x8(v), v); }
+  // the values as the type stores them
+  static __device__ __forceinline__ void round(Pair (&v)[4]) { pairs_of(pack_pairs(v), v); }
 };
 template <>
 struct Vec8<true> {
-  float4 a, b;
+  uint4 a, b;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i);
     a = __ldcs(s);
     b = __ldcs(s + 1);
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
+  __device__ __forceinline__ void bits(uint32_t (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
-  static __device__ __forceinline__ void store(void* p, int64_t i, float (&v)[8]) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-    d[0] = make_float4(v[0], v[1], v[2], v[3]);
-    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+  __device__ __forceinline__ void get(Pair (&v)[4]) const {
+    v[0] = pair_of(a.x, a.y), v[1] = pair_of(a.z, a.w), v[2] = pair_of(b.x, b.y), v[3] = pair_of(b.z, b.w);
   }
-  static __device__ __forceinline__ void rounded(float (&)[8]) {}
+  static __device__ __forceinline__ void store(void* p, int64_t i, const Pair (&v)[4]) {
+    ulonglong2* d = reinterpret_cast<ulonglong2*>(static_cast<float*>(p) + i);
+    d[0] = make_ulonglong2(v[0], v[1]);
+    d[1] = make_ulonglong2(v[2], v[3]);
+  }
+  static __device__ __forceinline__ void round(Pair (&)[4]) {}
 };
 
-// Sum over the threads of one row (tpr of them, whole warps; a block holds blockDim.x / tpr rows), in
-// a fixed order: a butterfly within each warp, then the warps' sums in ascending order.  Every thread
-// gets it.  All threads of the block call it; `buf` (32 words) may be used again after the next call's
-// first barrier, so two calls in a row need two buffers.
+// Sum over the tpr threads of one row, in a fixed order; every thread gets it.  A row is a power of two of
+// lanes of a warp, or whole warps: a butterfly within the warp, then the warps' sums in ascending order.
+// All threads of the block call it; `buf` (32 words) may be used again after the next call's first
+// barrier, so two calls in a row need two buffers.
 __device__ __forceinline__ float row_sum(float v, int tpr, float* buf) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  if (tpr == 32) return v;  // the same for the whole grid
+  for (int off = 16; off > 0; off >>= 1)
+    if (off < tpr) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if (tpr <= 32) return v;  // the same for the whole grid
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
   __syncthreads();
   const int nw = tpr >> 5, w0 = static_cast<int>(threadIdx.x >> 5) / nw * nw;
@@ -100,87 +137,118 @@ struct NormFwdArgs {
   DropArgs drop;
 };
 
+// Largest magnitude of three fp32, NaN if any is NaN.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // MXFP8 of the 32 values held by four neighbouring lanes (8 each): shared = floor(log2 max) - 8,
 // clamped at -127; codes E4M3 of v 2^-shared, saturating; a block with an Inf or a NaN gets scale 0xFF
 // and codes 0x7F.
-__device__ __forceinline__ void mx_store8(const float (&v)[8], uint8_t* q, uint8_t* s, int64_t row, int H, int c) {
-  float m = fmax_abs_nan(fmax_abs_nan(fmax_abs_nan(v[0], v[1]), fmax_abs_nan(v[2], v[3])),
-                         fmax_abs_nan(fmax_abs_nan(v[4], v[5]), fmax_abs_nan(v[6], v[7])));
+__device__ __forceinline__ void mx_store8(const Pair (&v)[4], uint8_t* q, uint8_t* s, int64_t off, int64_t soff,
+                                          int c, bool in) {
+  const float2 f0 = floats_of(v[0]), f1 = floats_of(v[1]), f2 = floats_of(v[2]), f3 = floats_of(v[3]);
+  float m = max3_abs_nan(f0.x, f0.y, f1.x);
+  m = max3_abs_nan(m, f1.y, f2.x);
+  m = max3_abs_nan(m, f2.y, max3_abs_nan(f3.x, f3.y, 0.0f));
   m = fmax_abs_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = fmax_abs_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
   const uint32_t amax = __float_as_uint(m) & 0x7FFFFFFFu;
-  if (c >= H) return;  // after the shuffles
+  if (!in) return;  // after the shuffles
   const bool bad = amax > 0x7F7FFFFFu;
-  int shared = static_cast<int>(amax >> 23) - 127 - 8;
-  shared = shared < -127 ? -127 : shared;
-  const float dn = pow2f(bad ? 0 : -shared);
+  // scale byte = max(exponent field - 8, 0); 2^-shared has exponent field 254 - byte, at least 7 here
+  const int byte = max(static_cast<int>(amax >> 23) - 8, 0);
+  const Pair dn = splat(__uint_as_float(static_cast<uint32_t>(254 - byte) << 23));
   uint16_t e[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e[j]) : "f"(v[2 * j + 1] * dn), "f"(v[2 * j] * dn));
+  for (int j = 0; j < 4; ++j) {
+    const float2 t = floats_of(mul2(v[j], dn));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e[j]) : "f"(t.y), "f"(t.x));
+  }
   uint2 o = make_uint2(e[0] | static_cast<uint32_t>(e[1]) << 16, e[2] | static_cast<uint32_t>(e[3]) << 16);
   if (bad) o = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  *reinterpret_cast<uint2*>(q + row * H + c) = o;
-  if ((c & 31) == 0) s[row * (H / 32) + c / 32] = static_cast<uint8_t>(bad ? 0xFF : shared + 127);
+  *reinterpret_cast<uint2*>(q + off + c) = o;
+  if ((c & 31) == 0) s[soff + c / 32] = static_cast<uint8_t>(bad ? 0xFF : byte);
 }
 
-// Block = blockDim.x / tpr rows of tpr threads; thread t of a row holds vectors t, t + tpr, ...
-template <int V, bool F32>
-__global__ void __launch_bounds__(kNormThreads) rmsnorm_fwd_kernel(const NormFwdArgs a) {
+// Block = blockDim.x / tpr rows of tpr threads; thread t of a row holds vectors t, t + tpr, ... of 8 values.
+// The draws need no data: they are made while the row's loads fly.
+template <int V, bool F32, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) rmsnorm_fwd_kernel(const NormFwdArgs a) {
   pdl_wait();
   __shared__ float buf[32];
+  const int rows = static_cast<int>(blockDim.x) / a.tpr;
   const int rl = static_cast<int>(threadIdx.x) / a.tpr, t = static_cast<int>(threadIdx.x) - rl * a.tpr;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / a.tpr) + rl;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + rl, off = row * a.H;
   const bool live = row < a.T;
-  const int64_t base = row * a.H;
-  float v[V][8];
-  uint4 xq[V];
-  Vec8<F32> rq[V];
+  uint4 x[V];
+  Vec8<F32> r[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * a.tpr + t) * 8;
     if (live && c < a.H) {
-      xq[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + base + c));
-      if (a.residual) rq[j].load(a.residual, base + c);
+      x[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + off + c));
+      if (a.residual) r[j].load(a.residual, off + c);
     }
   }
-  uint64_t seed = 0, offset = 0;
-  if (a.drop.rng) seed = a.drop.rng[0], offset = a.drop.rng[1];
-  float ss = 0.0f;
+  uint32_t draws[V][4];
+  if (a.drop.rng) {
+    DropState ds;
+    ds.load(a.drop);
+#pragma unroll
+    for (int j = 0; j < V; ++j) philox8(ds, static_cast<uint64_t>(off + (j * a.tpr + t) * 8) >> 3, draws[j]);
+  }
+  const Pair scale = splat(a.drop.scale);
+  Pair v[V][4];
+  Pair ss = 0;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * a.tpr + t) * 8;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[j][k] = 0.0f;
+    for (int k = 0; k < 4; ++k) v[j][k] = 0;
     if (live && c < a.H) {
-      unpack_bf16x8(xq[j], v[j]);
-      if (a.drop.rng) drop8(v[j], a.drop, seed, offset, static_cast<uint64_t>(base + c) >> 3);
+      uint32_t xb[8];
+      bits_of(x[j], xb);
+      if (a.drop.rng) drop_bits(xb, a.drop, draws[j]);
+      Pair rr[4];
       if (a.residual) {
-        float r[8];
-        rq[j].get(r);
+        r[j].get(rr);
+      } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] += r[k];
+        for (int k = 0; k < 4; ++k) rr[k] = pair_of(0x80000000u, 0x80000000u);  // -0: x + -0 is x
       }
-      if (a.h) Vec8<F32>::store(a.h, base + c, v[j]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(v[j][k], v[j][k], ss);
+      for (int k = 0; k < 4; ++k) v[j][k] = fma2(pair_of(xb[2 * k], xb[2 * k + 1]), scale, rr[k]);
+      if (a.h) {
+        Vec8<F32>::store(a.h, off + c, v[j]);
+        Vec8<F32>::round(v[j]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) ss = fma2(v[j][k], v[j][k], ss);
     }
   }
-  ss = row_sum(ss, a.tpr, buf);
-  const float r = rsqrtf(ss / static_cast<float>(a.H) + a.eps);
-  if (live && t == 0 && a.rstd) a.rstd[row] = r;
+  uint4 wq[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c = (j * a.tpr + t) * 8;
+    wq[j] = c < a.H ? __ldg(reinterpret_cast<const uint4*>(a.w + c)) : make_uint4(0, 0, 0, 0);
+  }
+  const float2 s2 = floats_of(ss);
+  const float rs = rsqrtf(row_sum(s2.x + s2.y, a.tpr, buf) / static_cast<float>(a.H) + a.eps);
+  if (live && t == 0 && a.rstd) a.rstd[row] = rs;
+  const Pair rs2 = splat(rs);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * a.tpr + t) * 8;
     const bool in = live && c < a.H;
-    if (in) {
-      float w[8];
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(a.w + c)), w);
+    Pair w[4];
+    pairs_of(wq[j], w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] = v[j][k] * r * w[k];
-      if (a.y) *reinterpret_cast<uint4*>(a.y + base + c) = pack_bf16x8(v[j]);
-    }
-    if (a.yq) mx_store8(v[j], a.yq, a.ys, row, a.H, in ? c : a.H);
+    for (int k = 0; k < 4; ++k) v[j][k] = mul2(mul2(v[j][k], rs2), w[k]);
+    if (a.y && in) *reinterpret_cast<uint4*>(a.y + off + c) = pack_pairs(v[j]);
+    if (a.yq) mx_store8(v[j], a.yq, a.ys, off, off >> 5, c, in);
   }
 }
 
@@ -192,97 +260,133 @@ struct NormBwdArgs {
   const void* dres;
   void* dh;
   uint16_t* dx;
-  float* part;  // [parts, H]
+  float* part;  // [gridDim.x, H]
   int64_t T;
   int32_t H, tpr;
   DropArgs drop;
 };
 
-// The same layout; the grid strides over the rows and every thread sums dy xh of its columns over its
-// rows in ascending order: one partial row of dweight per row group (blockIdx, rl).
+// The same layout, the grid striding over the rows, and the next row loaded while one is worked on (not at four
+// vectors per thread: registers).  A row is kept as loaded and unpacked twice, before and after the row
+// reduction.  Every thread sums dy xh of its columns over its rows in ascending order, the row groups
+// of a block are added in ascending order at the end: one partial row of dweight per block.  (Rows copied ahead into
+// shared memory by cp.async, for four blocks per SM instead of two, were slower: 59 against 57 us at
+// 8192 x 4096 bf16 with dropout, 375 against 230 at 16384 x 7168 with an fp32 stream.)
 template <int V, bool F32>
 __global__ void __launch_bounds__(kNormThreads) rmsnorm_bwd_kernel(const NormBwdArgs a) {
   pdl_wait();
   __shared__ float buf[2][32];
+  extern __shared__ float group_dw[];  // [rows, H] when the block holds several rows
   const int rows = static_cast<int>(blockDim.x) / a.tpr;
   const int rl = static_cast<int>(threadIdx.x) / a.tpr, t = static_cast<int>(threadIdx.x) - rl * a.tpr;
-  float dw[V][8];
-#pragma unroll
-  for (int j = 0; j < V; ++j)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) dw[j][k] = 0.0f;
-  uint64_t seed = 0, offset = 0;
-  if (a.drop.rng) seed = a.drop.rng[0], offset = a.drop.rng[1];
-  int ph = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows; r0 < a.T;
-       r0 += static_cast<int64_t>(gridDim.x) * rows, ph ^= 1) {
-    const int64_t row = r0 + rl;
-    const bool live = row < a.T;
-    const int64_t base = row * a.H;
-    const float rs = live ? a.rstd[row] : 0.0f;
-    float g[V][8], xh[V][8];
-    uint4 dyq[V];
-    Vec8<F32> hq[V], dq[V];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows, hop = step * a.H;
+  int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows, row = r0 + rl, off = row * a.H;
+  constexpr bool kAhead = V < 4;
+  struct Row {
+    Vec8<F32> h[V], d[V];
+    uint4 dy[V];
+    float rs;
+  } next;
+  auto fetch = [&](int64_t at, int64_t rw) {
+    if (rw >= a.T) return;
+    next.rs = __ldg(a.rstd + rw);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * a.tpr + t) * 8;
-      if (live && c < a.H) {
-        hq[j].load(a.h, base + c);
-        dyq[j] = __ldcs(reinterpret_cast<const uint4*>(a.dy + base + c));
-        if (a.dres) dq[j].load(a.dres, base + c);
+      if (c < a.H) {
+        next.h[j].load(a.h, at + c);
+        next.dy[j] = __ldcs(reinterpret_cast<const uint4*>(a.dy + at + c));
+        if (a.dres) next.d[j].load(a.dres, at + c);
       }
     }
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (j * a.tpr + t) * 8;
-      if (live && c < a.H) {
-        float w[8];
-        unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(a.w + c)), w);
-        hq[j].get(xh[j]);
-        unpack_bf16x8(dyq[j], g[j]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          xh[j][k] *= rs;
-          dw[j][k] = fmaf(g[j][k], xh[j][k], dw[j][k]);
-          g[j][k] *= w[k];
-          s = fmaf(g[j][k], xh[j][k], s);
-        }
-      }
-    }
-    s = row_sum(s, a.tpr, buf[ph]) / static_cast<float>(a.H);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (j * a.tpr + t) * 8;
-      if (live && c < a.H) {
-        float d[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) d[k] = rs * fmaf(-xh[j][k], s, g[j][k]);
-        if (a.dres) {
-          float e[8];
-          dq[j].get(e);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) d[k] += e[k];
-        }
-        if (a.dx) {
-          float e[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) e[k] = d[k];
-          if (a.drop.rng) drop8(e, a.drop, seed, offset, static_cast<uint64_t>(base + c) >> 3);
-          *reinterpret_cast<uint4*>(a.dx + base + c) = pack_bf16x8(e);
-        }
-        if (a.dh) Vec8<F32>::store(a.dh, base + c, d);
-      }
-    }
-  }
-  float* p = a.part + (static_cast<int64_t>(blockIdx.x) * rows + rl) * a.H;
+  };
+  if constexpr (kAhead) fetch(off, row);
+  DropState ds;
+  ds.load(a.drop);
+  Pair dw[V][4];
+  uint4 wq[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * a.tpr + t) * 8;
-    if (c < a.H) {
-      float4* d = reinterpret_cast<float4*>(p + c);
-      d[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-      d[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    wq[j] = c < a.H ? __ldg(reinterpret_cast<const uint4*>(a.w + c)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) dw[j][k] = 0;
+  }
+  const Pair scale = splat(a.drop.scale);
+  const float inv_h = 1.0f / static_cast<float>(a.H);
+  for (int ph = 0; r0 < a.T; r0 += step, row += step, off += hop, ph ^= 1) {
+    const bool live = row < a.T;
+    if constexpr (!kAhead) fetch(off, row);
+    const Row cur = next;
+    if constexpr (kAhead) fetch(off + hop, row + step);
+    Pair ss = 0;
+    const Pair rs2 = splat(cur.rs);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = (j * a.tpr + t) * 8;
+      if (live && c < a.H) {
+        Pair dy[4], xh[4], w[4];
+        cur.h[j].get(xh);
+        pairs_of(cur.dy[j], dy);
+        pairs_of(wq[j], w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          xh[k] = mul2(xh[k], rs2);
+          dw[j][k] = fma2(dy[k], xh[k], dw[j][k]);
+          ss = fma2(mul2(dy[k], w[k]), xh[k], ss);
+        }
+      }
+    }
+    const float2 s2 = floats_of(ss);
+    const Pair c2 = splat(-row_sum(s2.x + s2.y, a.tpr, buf[ph]) * inv_h);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = (j * a.tpr + t) * 8;
+      if (live && c < a.H) {
+        Pair g[4], xh[4], w[4], e[4];
+        cur.h[j].get(xh);
+        pairs_of(cur.dy[j], g);
+        pairs_of(wq[j], w);
+        if (a.dres) {
+          cur.d[j].get(e);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e[k] = pair_of(0x80000000u, 0x80000000u);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) g[k] = fma2(fma2(mul2(xh[k], rs2), c2, mul2(g[k], w[k])), rs2, e[k]);
+        if (a.dh) Vec8<F32>::store(a.dh, off + c, g);
+        if (a.dx) {
+          if (a.drop.rng) {
+            uint32_t b[8], dr[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 f = floats_of(g[k]);
+              b[2 * k] = __float_as_uint(f.x), b[2 * k + 1] = __float_as_uint(f.y);
+            }
+            philox8(ds, static_cast<uint64_t>(off + c) >> 3, dr);
+            drop_bits(b, a.drop, dr);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) g[k] = mul2(pair_of(b[2 * k], b[2 * k + 1]), scale);
+          }
+          *reinterpret_cast<uint4*>(a.dx + off + c) = pack_pairs(g);
+        }
+      }
+    }
+  }
+  float* part = a.part + static_cast<int64_t>(blockIdx.x) * a.H;
+  float* p = rows > 1 ? group_dw + rl * a.H : part;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int c = (j * a.tpr + t) * 8;
+    if (c < a.H) Vec8<true>::store(p, c, dw[j]);
+  }
+  if (rows > 1) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
+      float v = group_dw[c];
+      for (int i = 1; i < rows; ++i) v += group_dw[i * a.H + c];
+      part[c] = v;
     }
   }
 }
@@ -296,7 +400,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* __restric
   const int c = static_cast<int>(blockIdx.x) * 32 + threadIdx.x;
   float s = 0.0f;
   if (c < H) {
-#pragma unroll 4
+#pragma unroll 10
     for (int p = threadIdx.y; p < parts; p += 32) s += part[static_cast<int64_t>(p) * H + c];
   }
   sm[threadIdx.y][threadIdx.x] = s;
@@ -309,22 +413,34 @@ __global__ void __launch_bounds__(1024) rmsnorm_dw_kernel(const float* __restric
   }
 }
 
-constexpr int kDropThreads = 256, kDropUnroll = 2;
+constexpr int kDropThreads = 256;
+
+// Groups a thread holds at a time, and blocks per SM of the grid, which strides over the groups (0: one block
+// for every 256 groups).  Measured at 16384 x 7168 values: forward bf16 108 us with two groups and four
+// blocks, 112 to 118 with one group; fp32 stream 166 with one group and no stride, 182 to 215 with strides;
+// backward 74.5 with one group and 32 blocks, 84 with two and eight.
+template <bool F32, bool BWD>
+constexpr int drop_unroll() { return !F32 && !BWD ? 2 : 1; }
+template <bool F32, bool BWD>
+constexpr int drop_blocks() { return BWD ? 32 : F32 ? 0 : 4; }
 
 // Forward (BWD = false): out = residual + dropout(x).  Backward: out (bf16) = factors * x, x of the
-// stream's type.
+// stream's type.  A thread loads its groups, draws, then uses them.
 template <bool F32, bool BWD>
 __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const void* x, const void* residual, void* out,
                                                                int64_t groups, DropArgs d) {
+  constexpr int kU = drop_unroll<F32, BWD>();
   pdl_wait();
-  const uint64_t seed = d.rng[0], offset = d.rng[1];
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (kDropThreads * kDropUnroll);
-  for (int64_t g0 = static_cast<int64_t>(blockIdx.x) * (kDropThreads * kDropUnroll) + threadIdx.x; g0 < groups;
+  DropState ds;
+  ds.load(d);
+  const Pair scale = splat(d.scale);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kDropThreads * kU);
+  for (int64_t g0 = static_cast<int64_t>(blockIdx.x) * (kDropThreads * kU) + threadIdx.x; g0 < groups;
        g0 += step) {
-    Vec8<F32 && BWD> xq[kDropUnroll];
-    Vec8<F32> rq[kDropUnroll];
+    Vec8<F32 && BWD> xq[kU];
+    Vec8<F32> rq[kU];
 #pragma unroll
-    for (int u = 0; u < kDropUnroll; ++u) {
+    for (int u = 0; u < kU; ++u) {
       const int64_t g = g0 + u * kDropThreads;
       if (g < groups) {
         xq[u].load(x, 8 * g);
@@ -332,18 +448,22 @@ __global__ void __launch_bounds__(kDropThreads) dropout_kernel(const void* x, co
       }
     }
 #pragma unroll
-    for (int u = 0; u < kDropUnroll; ++u) {
+    for (int u = 0; u < kU; ++u) {
       const int64_t g = g0 + u * kDropThreads;
       if (g >= groups) continue;
-      float v[8];
-      xq[u].get(v);
-      drop8(v, d, seed, offset, static_cast<uint64_t>(g));
+      uint32_t dr[4], b[8];
+      if (d.rng) philox8(ds, static_cast<uint64_t>(g), dr);
+      xq[u].bits(b);
+      if (d.rng) drop_bits(b, d, dr);
+      Pair v[4], r[4];
       if (!BWD && residual) {
-        float r[8];
         rq[u].get(r);
+      } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += r[k];
+        for (int k = 0; k < 4; ++k) r[k] = pair_of(0x80000000u, 0x80000000u);  // -0: v + -0 is v
       }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = fma2(pair_of(b[2 * k], b[2 * k + 1]), scale, r[k]);
       Vec8<F32 && !BWD>::store(out, 8 * g, v);
     }
   }
@@ -355,20 +475,28 @@ bool norm_shape_ok(const mok_norm_shape* s) {
          s->T <= (int64_t{1} << 40) / s->H;
 }
 
-// Threads per row (whole warps), vectors of 8 per thread, rows per block.
+// Threads per row (a power of two of lanes up to a warp, then whole warps), vectors of 8 per thread, rows per
+// block of 256 threads or one row of more.  More values per thread mean fewer threads to reduce over and more
+// loads in flight each, as long as the registers hold them: forward, bf16, H = 2048 with dropout, 4096
+// rows: 14.1 us with one vector per thread, 11.8 with two; H = 7168, MXFP8, 16384 rows: 172 with two, 161 with
+// four; fp32 stream: 204 with two, 253 with four.
 struct RowPlan {
   int tpr, v, rows;
-  RowPlan(int H) {
-    v = H <= 2048 ? 1 : H <= 16 * kNormThreads ? 2 : 4;
-    tpr = ((H / 8 + v - 1) / v + 31) / 32 * 32;
+  RowPlan(int H, bool four) {  // four: four vectors already from H > 4096 on
+    v = H <= 1024 ? 1 : H <= (four ? 4096 : 16 * kNormThreads) ? 2 : 4;
+    const int need = (H / 8 + v - 1) / v;
+    tpr = (need + 31) / 32 * 32;
+    if (need <= 16) tpr = need > 8 ? 16 : need > 4 ? 8 : 4;
     rows = tpr >= 256 ? 1 : 256 / tpr;
   }
 };
 
+// Blocks of the backward, and partial rows of dweight: two 256-thread blocks' worth of threads per SM of 152 (a
+// function of the shape alone, which the workspace is sized by).
 int norm_bwd_blocks(const mok_norm_shape& s) {
-  const RowPlan p(s.H);
+  const RowPlan p(s.H, false);
   const int64_t need = (s.T + p.rows - 1) / p.rows;
-  const int64_t cap = kNormParts / p.rows > 0 ? kNormParts / p.rows : 1;
+  const int64_t cap = p.tpr > 256 ? kNormParts / 4 : kNormParts / 2;
   return static_cast<int>(need < cap ? need : cap);
 }
 
@@ -382,6 +510,22 @@ int with_row_kernel(const RowPlan& p, int32_t f32, F&& f) {
   return typed(std::integral_constant<int, 4>{});
 }
 
+template <bool F32, bool BWD>
+mok_status launch_dropout(const void* x, const void* residual, void* out, int64_t groups, const DropArgs& d,
+                          void* stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return MOK_ERR_CUDA;
+  constexpr int kPer = kDropThreads * drop_unroll<F32, BWD>(), kBlocks = drop_blocks<F32, BWD>();
+  const int64_t need = (groups + kPer - 1) / kPer;
+  const int64_t cap = kBlocks ? static_cast<int64_t>(sms) * kBlocks : (int64_t{1} << 31) - 1;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  trace_begin(st, BWD ? K_DROPOUT_BWD : K_DROPOUT_FWD);
+  const cudaError_t e = launch_pdl(dropout_kernel<F32, BWD>, dim3(static_cast<unsigned>(need < cap ? need : cap)),
+                                   dim3(kDropThreads), 0, st, x, residual, out, groups, d);
+  trace_end(st);
+  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+}
+
 template <bool BWD>
 mok_status dropout_call(int64_t n, int32_t stream_type, const mok_dropout* drop, const void* x, const void* residual,
                         void* out, void* stream) {
@@ -391,19 +535,8 @@ mok_status dropout_call(int64_t n, int32_t stream_type, const mok_dropout* drop,
     return MOK_ERR_INVALID_ARG;
   if (n == 0) return MOK_OK;
   if (!x || !out || off16(x) || off16(out) || off16(residual)) return MOK_ERR_INVALID_ARG;
-  const int sms = sm_count();
-  if (sms <= 0) return MOK_ERR_CUDA;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int64_t groups = n / 8, per = kDropThreads * kDropUnroll, need = (groups + per - 1) / per;
-  const int64_t cap = static_cast<int64_t>(sms) * 8;
-  const dim3 grid(static_cast<unsigned>(need < cap ? need : cap));
-  trace_begin(st, BWD ? K_DROPOUT_BWD : K_DROPOUT_FWD);
-  const cudaError_t e =
-      stream_type == MOK_DT_FP32
-          ? launch_pdl(dropout_kernel<true, BWD>, grid, dim3(kDropThreads), 0, st, x, residual, out, groups, d)
-          : launch_pdl(dropout_kernel<false, BWD>, grid, dim3(kDropThreads), 0, st, x, residual, out, groups, d);
-  trace_end(st);
-  return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
+  return stream_type == MOK_DT_FP32 ? launch_dropout<true, BWD>(x, residual, out, n / 8, d, stream)
+                                    : launch_dropout<false, BWD>(x, residual, out, n / 8, d, stream);
 }
 
 }  // namespace
@@ -445,15 +578,20 @@ mok_status mok_rmsnorm_forward(const mok_norm_shape* s, const void* x, const voi
   a.T = s->T;
   a.H = s->H;
   a.eps = s->eps;
-  const RowPlan p(s->H);
+  const RowPlan p(s->H, s->stream_type == MOK_DT_BF16);
   a.tpr = p.tpr;
   const int64_t blocks = (s->T + p.rows - 1) / p.rows;
   if (blocks >= (int64_t{1} << 31)) return MOK_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   trace_begin(st, K_RMSNORM_FWD);
   const int e = with_row_kernel(p, s->stream_type == MOK_DT_FP32, [&](auto v, auto f32) {
-    return static_cast<int>(launch_pdl(rmsnorm_fwd_kernel<decltype(v)::value, decltype(f32)::value>,
-                                       dim3(static_cast<unsigned>(blocks)), dim3(p.tpr * p.rows), 0, st, a));
+    constexpr int kV = decltype(v)::value;
+    constexpr bool kF32 = decltype(f32)::value;
+    constexpr int kBlocks = kV == 4 ? 4 : 5;  // blocks of 256 threads per SM: as many as its registers hold
+    const dim3 grid(static_cast<unsigned>(blocks)), block(p.tpr * p.rows);
+    return static_cast<int>(p.tpr <= 256
+                                ? launch_pdl(rmsnorm_fwd_kernel<kV, kF32, 256, kBlocks>, grid, block, 0, st, a)
+                                : launch_pdl(rmsnorm_fwd_kernel<kV, kF32, 512, 2>, grid, block, 0, st, a));
   });
   trace_end(st);
   return e ? MOK_ERR_CUDA : MOK_OK;
@@ -461,7 +599,7 @@ mok_status mok_rmsnorm_forward(const mok_norm_shape* s, const void* x, const voi
 
 size_t mok_rmsnorm_workspace_bytes(const mok_norm_shape* s) {
   if (!norm_shape_ok(s)) return 0;
-  const size_t n = static_cast<size_t>(norm_bwd_blocks(*s)) * RowPlan(s->H).rows * s->H * sizeof(float);
+  const size_t n = static_cast<size_t>(norm_bwd_blocks(*s)) * s->H * sizeof(float);
   return n < 256 ? 256 : (n + 255) / 256 * 256;
 }
 
@@ -486,7 +624,7 @@ mok_status mok_rmsnorm_backward(const mok_norm_shape* s, const void* h, const fl
   a.part = static_cast<float*>(ws);
   a.T = s->T;
   a.H = s->H;
-  const RowPlan p(s->H);
+  const RowPlan p(s->H, false);
   a.tpr = p.tpr;
   const int blocks = norm_bwd_blocks(*s);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -494,14 +632,15 @@ mok_status mok_rmsnorm_backward(const mok_norm_shape* s, const void* h, const fl
     trace_begin(st, K_RMSNORM_BWD);
     const int e = with_row_kernel(p, s->stream_type == MOK_DT_FP32, [&](auto v, auto f32) {
       return static_cast<int>(launch_pdl(rmsnorm_bwd_kernel<decltype(v)::value, decltype(f32)::value>, dim3(blocks),
-                                         dim3(p.tpr * p.rows), 0, st, a));
+                                         dim3(p.tpr * p.rows),
+                                         p.rows > 1 ? static_cast<size_t>(p.rows) * s->H * sizeof(float) : 0, st, a));
     });
     trace_end(st);
     if (e) return MOK_ERR_CUDA;
   }
   trace_begin(st, K_RMSNORM_DW);
   const cudaError_t e = launch_pdl(rmsnorm_dw_kernel, dim3((s->H + 31) / 32), dim3(32, 32), 0, st,
-                                   static_cast<const float*>(a.part), blocks * p.rows, static_cast<int>(s->H), dweight);
+                                   static_cast<const float*>(a.part), blocks, static_cast<int>(s->H), dweight);
   trace_end(st);
   return e == cudaSuccess ? MOK_OK : MOK_ERR_CUDA;
 }
