@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kPairThreads = 64 + 32 * 8;
 constexpr uint32_t kPairTmemCols = 512;  // two accumulators, 256 columns apart
-constexpr int kGroupM = 8;  // M tiles of one band of the tile order
+constexpr int kGroupM = 4;  // M tiles of one band of the tile order
 
 struct PairArgs {
   FfnArgs f;

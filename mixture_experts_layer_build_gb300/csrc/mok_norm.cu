@@ -272,8 +272,8 @@ struct NormBwdArgs {
 // of a block are added in ascending order at the end: one partial row of dweight per block.  (Rows copied ahead into
 // shared memory by cp.async, for four blocks per SM instead of two, were slower: 59 against 57 us at
 // 8192 x 4096 bf16 with dropout, 375 against 230 at 16384 x 7168 with an fp32 stream.)
-template <int V, bool F32>
-__global__ void __launch_bounds__(kNormThreads) rmsnorm_bwd_kernel(const NormBwdArgs a) {
+template <int V, bool F32, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) rmsnorm_bwd_kernel(const NormBwdArgs a) {
   pdl_wait();
   __shared__ float buf[2][32];
   extern __shared__ float group_dw[];  // [rows, H] when the block holds several rows
@@ -631,9 +631,13 @@ mok_status mok_rmsnorm_backward(const mok_norm_shape* s, const void* h, const fl
   if (blocks > 0) {
     trace_begin(st, K_RMSNORM_BWD);
     const int e = with_row_kernel(p, s->stream_type == MOK_DT_FP32, [&](auto v, auto f32) {
-      return static_cast<int>(launch_pdl(rmsnorm_bwd_kernel<decltype(v)::value, decltype(f32)::value>, dim3(blocks),
-                                         dim3(p.tpr * p.rows),
-                                         p.rows > 1 ? static_cast<size_t>(p.rows) * s->H * sizeof(float) : 0, st, a));
+      constexpr int kV = decltype(v)::value;
+      constexpr bool kF32 = decltype(f32)::value;
+      const dim3 grid(blocks), block(p.tpr * p.rows);
+      const size_t smem = p.rows > 1 ? static_cast<size_t>(p.rows) * s->H * sizeof(float) : 0;
+      return static_cast<int>(p.tpr <= 256
+                                  ? launch_pdl(rmsnorm_bwd_kernel<kV, kF32, 256, 2>, grid, block, smem, st, a)
+                                  : launch_pdl(rmsnorm_bwd_kernel<kV, kF32, 512, 1>, grid, block, smem, st, a));
     });
     trace_end(st);
     if (e) return MOK_ERR_CUDA;
