@@ -165,7 +165,6 @@ __global__ void __launch_bounds__(kTileThreads)
   const int kb0 = static_cast<int>(static_cast<int64_t>(t.f.k_blocks) * rank / S);
   const int count = static_cast<int>(static_cast<int64_t>(t.f.k_blocks) * (rank + 1) / S) - kb0;
   const uint32_t a_bytes = static_cast<uint32_t>(t.a_rows) * 128u;
-  const int ahead = min(count, t.stages);  // K blocks loaded before anything is consumed
   if (warp == 0) {
     if (elect_one()) {
       for (int s = 0; s < t.stages; ++s) {
@@ -177,34 +176,23 @@ __global__ void __launch_bounds__(kTileThreads)
       fence_barrier_init();
     }
     __syncwarp();
-    // the first round of weight loads: the barriers are this warp's own, and the stages are empty
-    if (!t.early_b) pdl_wait();
-    for (int i = 0; i < ahead; ++i)
-      if (elect_one()) {
-        mbar_arrive_expect_tx(full(i), a_bytes + C::kBBytes);
-        tile_load_b<VAR, BN>(t, n, kb0 + i, base + t.b_off + i * C::kBBytes, full(i), &tB, &tB2);
-      }
-    if (t.early_b) pdl_wait();
-  } else {
-    if (warp == 1) {
-      tmem_alloc(smem_u32(&tmem_slot), BN < 32 ? 32 : BN);
-      tmem_relinquish();
-    }
-    pdl_wait();
+  } else if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), BN < 32 ? 32 : BN);
+    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_trigger();
   if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const uint32_t tmem = tmem_slot;
 
   if (warp == 0 || warp == 2) {  // weights and, by another warp, tokens: a load takes about 35 ns to issue
     const bool b_side = warp == 0;
+    if (!b_side || !t.early_b) pdl_wait();
+    if (!b_side) pdl_trigger();
     bool ok = true;
-    int st = 0, i = b_side ? ahead : 0;
-    uint32_t ph = b_side ? 0u : 1u;  // parity of the empty barrier's phase to wait for
-    if (b_side && ahead < t.stages) st = ahead;
+    int st = 0, i = 0;
+    uint32_t ph = 1;  // parity of the empty barrier's phase to wait for: none in the first round
     for (; i < count; ++i) {
       if (i >= t.stages && !warp_wait(empty(st), ph, abort_flag, t.f.status)) {
         ok = false;
@@ -251,6 +239,7 @@ __global__ void __launch_bounds__(kTileThreads)
     if (elect_one()) umma_commit(done);  // also after an abort: what was issued completes before TMEM is freed
     __syncwarp();
   }
+  pdl_wait();  // before anything is read or written below (at once for the warps that have passed it)
   bool ok = warp_wait(done, 0, abort_flag, t.f.status);
   if (!ok && warp == 1) wait_landed(done, 0);
   if (S > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every peer has started
