@@ -513,13 +513,16 @@ MOK_API mok_status mok_ffn_forward(const mok_ffn_shape* shape, const void* x, co
                                    int32_t save, uint32_t* status, void* stream);
 
 /* Gradients, overwritten: dx [T, H] bf16; dw_gate, dw_up [I, H] and dw_down [H, I] of dw_type (mok_dtype;
- * T = 0 gives zeros).  dx, dw_down, or dw_gate and dw_up together, may be NULL: not computed. */
+ * T = 0 gives zeros).  dx, dw_down, or dw_gate and dw_up together, may be NULL: not computed.
+ *   dx_add   [T, H] bf16 or NULL (0), added to dx before its one rounding: x's gradient from its other uses (the
+ *            routed layer's dx); may be dx's buffer. */
 typedef struct {
   void* dx;
   void* dw_gate;
   void* dw_up;
   void* dw_down;
   int32_t dw_type;
+  const void* dx_add;
 } mok_ffn_grads;
 
 /* Bytes of device workspace of mok_ffn_backward (256-byte aligned): dg and du.  0 for an unsupported
@@ -527,7 +530,7 @@ typedef struct {
 MOK_API size_t mok_ffn_workspace_bytes(const mok_ffn_shape* shape);
 
 /* Backward from dy [T, H] bf16 = dL/dout (the residual's gradient is dy itself):
- *   da = dy Wd, dg = da u act'(g), du = da act(g), dx = dg Wg + du Wu,
+ *   da = dy Wd, dg = da u act'(g), du = da act(g), dx = dg Wg + du Wu + dx_add,
  *   dWg = dg^T x, dWu = du^T x, dWd = dy^T a.
  * ctx: the matching mok_ffn_forward's, with save = 1. */
 MOK_API mok_status mok_ffn_backward(const mok_ffn_shape* shape, const void* x, const void* w_gate, const void* w_up,

@@ -92,7 +92,8 @@ mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w
                             const mok_ffn_grads* gr, void* ws, size_t ws_bytes, uint32_t* status, void* stream) {
   if (!ffn_shape_ok(s) || !gr || (gr->dw_type != MOK_DT_BF16 && gr->dw_type != MOK_DT_FP32) || unaligned(status, 4))
     return MOK_ERR_INVALID_ARG;
-  if ((gr->dw_gate == nullptr) != (gr->dw_up == nullptr) || unaligned(gr->dx, 16) || unaligned(gr->dw_gate, 16) ||
+  if ((gr->dw_gate == nullptr) != (gr->dw_up == nullptr) || unaligned(gr->dx, 16) || unaligned(gr->dx_add, 16) ||
+      unaligned(gr->dw_gate, 16) ||
       unaligned(gr->dw_up, 16) || unaligned(gr->dw_down, 16))
     return MOK_ERR_INVALID_ARG;
   if (!ctx || unaligned(ctx, 256) || !ws || unaligned(ws, 256)) return MOK_ERR_INVALID_ARG;
@@ -122,6 +123,7 @@ mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w
   if (gr->dx) {
     a.out0 = gr->dx;
     a.out1 = nullptr;
+    a.residual = static_cast<const uint16_t*>(gr->dx_add);
     if (launch_ffn_gemm(F_DX, s->T, s->H, s->I, {dg, du, w_gate, w_up}, a, st)) return MOK_ERR_CUDA;
   }
   const FfnGradOperands go{dg, du, x, dy, c.a, gr->dw_gate, gr->dw_up, gr->dw_down};

@@ -6,7 +6,7 @@
 //   GATEUP  [g | u] = x [Wg | Wu]^T, epilogue a = act(g) u           M = T, N = I (twice), K = H
 //   DOWN    out = a Wd^T + residual                                  M = T, N = H, K = I
 //   DACT    da = dy Wd, epilogue dg = da u act'(g), du = da act(g)   M = T, N = I, K = H
-//   DX      dx = dg Wg + du Wu                                       M = T, N = H, K = I twice
+//   DX      dx = dg Wg + du Wu + dx_add                              M = T, N = H, K = I twice
 //   DW      dWg = dg^T x, dWu = du^T x                               M = I, N = H, K = T
 //           dWd = dy^T a                                             M = H, N = I, K = T
 // An operand whose rows run along K is K-major for the MMA, one whose rows run along M or N is
@@ -37,7 +37,7 @@ struct FfnArgs {
   void* out1;           // - | -   | du | -
   float* g;             // GATEUP: saved when not null; DACT: read
   float* u;
-  const uint16_t* residual;  // DOWN, may be null
+  const uint16_t* residual;  // DOWN (the residual), DX (dx_add): added to the output, may be null
   uint32_t* status;
 };
 

@@ -270,7 +270,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
     for (int c = c_beg; c < c_end; c += 32) {
       const bool in = r0 < M && c0 + c < N;
       uint4 res[4];
-      if constexpr (VAR == P_DOWN) {
+      if constexpr (VAR == P_DOWN || VAR == P_DX) {
         if (f.residual && in && r0 + lane < M) {
           const uint4* s = reinterpret_cast<const uint4*>(f.residual + static_cast<int64_t>(r0 + lane) * N + c0 + c);
 #pragma unroll
@@ -281,7 +281,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
       tmem_ld32(taddr + c, v);
       if (c + 32 >= c_end) release();
       if (!in) continue;
-      if constexpr (VAR == P_DOWN) {
+      if constexpr (VAR == P_DOWN || VAR == P_DX) {
         if (f.residual && r0 + lane < M) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {

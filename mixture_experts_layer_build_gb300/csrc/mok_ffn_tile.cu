@@ -117,7 +117,7 @@ __device__ __forceinline__ void tile_epilogue8(const FfnArgs& f, int64_t m, int 
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = act_fwd(v[k], f.act) * w[k];
     store_bf16x8(f.out0, i, v);
-  } else if constexpr (VAR == F_DOWN) {
+  } else if constexpr (VAR == F_DOWN || VAR == F_DX) {
     if (f.residual) {
       const uint4 q = *reinterpret_cast<const uint4*>(f.residual + i);
       v[0] += bf16_lo(q.x), v[1] += bf16_hi(q.x), v[2] += bf16_lo(q.y), v[3] += bf16_hi(q.y);
@@ -137,8 +137,6 @@ __device__ __forceinline__ void tile_epilogue8(const FfnArgs& f, int64_t m, int 
     }
     store_bf16x8(f.out0, i, g);
     store_bf16x8(f.out1, i, u);
-  } else {
-    store_bf16x8(f.out0, i, v);
   }
 }
 

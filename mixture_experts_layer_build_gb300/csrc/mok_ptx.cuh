@@ -30,8 +30,9 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // launched with programmatic stream serialisation, so its CTAs may start launching as the previous
 // kernel's last CTAs exit, before that grid's completion has been processed; pdl_wait() then holds
 // them until the previous grid has completed and its memory is visible (it returns at once when
-// there is no such dependency).  No kernel signals its dependents earlier than its exit: CTAs
-// launched ahead of time to wait on an SM slowed the graph-replayed step.
+// there is no such dependency).  No kernel of the layer signals its dependents earlier than its exit:
+// CTAs launched ahead of time to wait on an SM slowed the graph-replayed step.  (The dense feed-forward block's
+// kernels do signal, pdl_trigger() in mok_ffn.cuh: theirs load weights while they wait.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Deadline of any single wait inside a kernel (ns).  Legitimate waits last microseconds.

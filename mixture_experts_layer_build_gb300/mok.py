@@ -550,7 +550,8 @@ class mok_ffn_shape(ctypes.Structure):
 
 
 class mok_ffn_grads(ctypes.Structure):
-    _fields_ = [("dx", _P), ("dw_gate", _P), ("dw_up", _P), ("dw_down", _P), ("dw_type", ctypes.c_int32)]
+    _fields_ = [("dx", _P), ("dw_gate", _P), ("dw_up", _P), ("dw_down", _P), ("dw_type", ctypes.c_int32),
+                ("dx_add", _P)]
 
 
 _DROP, _NORM, _FFN = ctypes.POINTER(mok_dropout), ctypes.POINTER(mok_norm_shape), ctypes.POINTER(mok_ffn_shape)
@@ -763,9 +764,11 @@ class FFN:
         return self.out
 
     def backward(self, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
-                 dy: torch.Tensor, stream=None) -> FFNGrads:
+                 dy: torch.Tensor, dx_add: torch.Tensor | None = None, stream=None) -> FFNGrads:
+        """Gradients of the last forward; dx_add: x's gradient from its other uses, added to dx."""
         if not self.train:
             raise ValueError("backward needs a plan made with train=True")
+        self._grads.dx_add = _arg(dx_add, (self.T, self.H), torch.bfloat16, "dx_add")
         _check(_lib.mok_ffn_backward(self._ref, *self._in(x, w_gate, w_up, w_down), self.ctx.data_ptr(),
                                      self.ctx.numel(), _arg(dy, (self.T, self.H), torch.bfloat16, "dy"),
                                      ctypes.byref(self._grads), self.ws.data_ptr(), self.ws.numel(),

@@ -159,3 +159,52 @@ def test_gradients_left_out(mok):
         assert rc == 0
         for k in want:
             assert torch.equal(got[k], want[k]) if k in keep else (got[k] == 0).all()
+
+
+# Sizes by the tile widths of the pair kernel: the width with the least rounds of 76 pairs x (columns + 16).  GATEUP
+# has 2 I columns, DOWN and DX H, DACT I; the weight gradients are (I x H) twice and (H x I).
+@pytest.mark.parametrize("T,H,I,widths", [
+    (512, 5000, 2600, "gate/up 192"), (1100, 2048, 1024, "128 columns"), (2048, 4096, 1536, "192, 224, 256"),
+    (700, 3400, 3400, "ragged 192 and 224"), (5120, 1792, 896, "224 and 256")])
+def test_every_tile_width(mok, T, H, I, widths):
+    check(mok, T, H, I, "silu" if T % 3 else "gelu")
+
+
+def test_dx_add(mok):
+    for T, H, I in ((40, 136, 72), (900, 1032, 520)):  # tile kernel and pairs
+        plan, d = check(mok, T, H, I, "silu", residual=False)
+        w = (d["wg"], d["wu"], d["wd"])
+        base = plan.grads.dx.double()
+        add = torch.randn((T, H), device="cuda").to(BF)
+        g = plan.backward(d["x"], *w, d["dy"], dx_add=add)
+        # base was rounded once (2^-8 of it), the sum once more
+        assert ((g.dx.double() - base - add.double()).abs() <= 2.0**-8 * (base.abs() + (base + add.double()).abs()) + 1e-6).all()
+        want = g.dx.clone()
+        plan.grads.dx.copy_(add)  # dx's own buffer
+        assert torch.equal(plan.backward(d["x"], *w, d["dy"], dx_add=plan.grads.dx).dx, want)
+
+
+def test_offsets_past_32_bits(mok):
+    T, H, I = 270_000, 8192, 64  # x, out and the residual: 2.2 G values each
+    x = torch.empty((T, H), dtype=BF, device="cuda").normal_()
+    d = draw(1, H, I, 3)
+    plan = mok.FFN(T, H, I, train=False)
+    out = plan.forward(x, d["wg"], d["wu"], d["wd"], residual=x)
+    for rows in (slice(0, 3), slice(T - 3, T)):
+        t = [v.double() for v in (x[rows], d["wg"], d["wu"], d["wd"])]
+        want, saved = ref.ffn(*t, "silu", t[0])
+        near(out[rows], want, saved[4].abs() @ t[3].T.abs() + t[0].abs(), "out")
+    assert plan.device_status() == 0
+
+
+def test_wrong_layouts_are_refused(mok):
+    d = draw(16, 64, 32, 2)
+    plan = mok.FFN(16, 64, 32)
+    for bad in (dict(x=d["x"].t().contiguous().t()), dict(wg=d["wg"].float()), dict(wd=d["wd"].t()), dict(x=d["x"][:8]),
+                dict(x=d["x"].cpu())):
+        a = {**d, **bad}
+        with pytest.raises(ValueError):
+            plan.forward(a["x"], a["wg"], a["wu"], a["wd"])
+    buf = torch.empty(16 * 64 + 8, dtype=BF, device="cuda")
+    with pytest.raises(mok.MokError):  # not 16-byte aligned
+        plan.forward(buf[4:4 + 16 * 64].view(16, 64), d["wg"], d["wu"], d["wd"])
