@@ -626,7 +626,7 @@ const char* mok_kernel_name(int32_t kind) {
       "router_dw",       "selftest_wait", "push_y",        "push_dx",        "ep_combine",
       "ep_dx_reduce",    "ds_push",       "rmsnorm_fwd",   "rmsnorm_bwd",    "rmsnorm_dw",
       "dropout_fwd",     "dropout_bwd",   "ffn_gateup",    "ffn_down",      "ffn_dact",
-      "ffn_dx",          "ffn_dw"};
+      "ffn_dx",          "ffn_bwd1",      "ffn_bwd2"};
   return (kind >= 0 && kind < K_NUM_KINDS) ? names[kind] : "?";
 }
 

@@ -34,17 +34,23 @@ struct FfnCtx {
 bool unaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 bool need16(const void* p) { return p && !unaligned(p, 16); }
 
-// One to four tokens on the CUDA cores (forward); pairs of CTAs where their narrowest tiles, 256 x 128, are
-// enough for half of the pairs; the tile kernel, which can split K, between.  Measured at H = 4096, I = 1536,
-// a training step with every contraction on the tile kernel and on pairs: 67.6 and 74.9 us for 256 tokens,
-// 86.8 and 80.3 for 512, 151 and 96.7 for 1024.
-int launch_ffn_gemm(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
-                    cudaStream_t stream) {
-  if (M <= kFfnRowTokens && (var == F_GATEUP || var == F_DOWN)) return launch_ffn_row(var, M, N, K, o, a, stream);
+// Whether a row-tiled contraction runs on pairs of CTAs: where their narrowest tiles, 256 x 128, are enough for
+// half of the pairs; below, the tile kernel, which can split K.  In the backward, where weight gradients fill the other
+// pairs, an eighth is enough, from 384 tokens on (below, much of the second row of tiles is empty).  Measured at H =
+// 4096, I = 1536, a training step with every contraction on the tile kernel and on pairs: 67.6 and 74.9 us for 256
+// tokens, 151 and 96.7 for 1024; the backward's rule: 77.0 -> 73.8 us for 512 tokens, 62.7 -> 52.3 for 1024 at H =
+// 2048, I = 1024; 384 tokens would lose 74.3 -> 78.7.
+bool on_pairs(int var, int64_t M, int64_t N) {
   const int cols = var == F_GATEUP ? 64 : 128;
-  const int64_t units = (M + 255) / 256 * ((N + cols - 1) / cols);
-  return M > 128 && 4 * units >= sm_count() ? launch_ffn_pair(var, M, N, K, o, a, stream)
-                                 : launch_ffn_tile(var, M, N, K, o, a, stream);
+  const int64_t tiles = (M + 255) / 256 * ((N + cols - 1) / cols);
+  return M > 128 && (var >= F_DACT && M > 384 ? 16 : 4) * tiles >= sm_count();
+}
+
+int launch_fwd(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
+               cudaStream_t stream) {
+  if (M <= kFfnRowTokens) return launch_ffn_row(var, M, N, K, o, a, stream);
+  return on_pairs(var, M, N) ? launch_ffn_pair_fwd(var, M, N, K, o, a, stream)
+                             : launch_ffn_tile(var, M, N, K, o, a, stream);
 }
 
 }  // namespace
@@ -80,11 +86,11 @@ mok_status mok_ffn_forward(const mok_ffn_shape* s, const void* x, const void* w_
   a.out0 = c.a;
   a.g = c.g;
   a.u = c.u;
-  if (launch_ffn_gemm(F_GATEUP, s->T, s->I, s->H, {x, nullptr, w_gate, w_up}, a, st)) return MOK_ERR_CUDA;
+  if (launch_fwd(F_GATEUP, s->T, s->I, s->H, {x, nullptr, w_gate, w_up}, a, st)) return MOK_ERR_CUDA;
   a.out0 = out;
   a.g = a.u = nullptr;
   a.residual = static_cast<const uint16_t*>(residual);
-  return launch_ffn_gemm(F_DOWN, s->T, s->H, s->I, {c.a, nullptr, w_down, nullptr}, a, st) ? MOK_ERR_CUDA : MOK_OK;
+  return launch_fwd(F_DOWN, s->T, s->H, s->I, {c.a, nullptr, w_down, nullptr}, a, st) ? MOK_ERR_CUDA : MOK_OK;
 }
 
 mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w_gate, const void* w_up,
@@ -109,25 +115,51 @@ mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w
   if (!need16(x) || !need16(w_gate) || !need16(w_up) || !need16(w_down) || !need16(dy)) return MOK_ERR_INVALID_ARG;
   uint16_t* dg = static_cast<uint16_t*>(ws);
   uint16_t* du = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + up256(static_cast<size_t>(s->T) * s->I * 2));
+  FfnBackward b{};
+  b.T = s->T;
+  b.H = s->H;
+  b.I = s->I;
+  b.act = s->act;
+  b.dw_f32 = gr->dw_type == MOK_DT_FP32;
+  b.x = x;
+  b.w_gate = w_gate;
+  b.w_up = w_up;
+  b.w_down = w_down;
+  b.a = c.a;
+  b.g = c.g;
+  b.u = c.u;
+  b.dy = dy;
+  b.dg = dg;
+  b.du = du;
+  b.dx = gr->dx;
+  b.dx_add = gr->dx_add;
+  b.dw_gate = gr->dw_gate;
+  b.dw_up = gr->dw_up;
+  b.dw_down = gr->dw_down;
+  b.status = status;
   FfnArgs a{};
   a.act = s->act;
   a.status = status;
-  if (gr->dx || gr->dw_gate) {
+  // DACT, then DX: each in its phase's launch with weight gradients, or before it on the tile kernel
+  const bool dact = gr->dx || gr->dw_gate;
+  b.dact = dact && on_pairs(F_DACT, s->T, s->I);
+  b.dx_rows = gr->dx && on_pairs(F_DX, s->T, s->H);
+  if (dact && !b.dact) {
     a.out0 = dg;
     a.out1 = du;
     a.g = c.g;
     a.u = c.u;
-    if (launch_ffn_gemm(F_DACT, s->T, s->I, s->H, {dy, nullptr, w_down, nullptr}, a, st)) return MOK_ERR_CUDA;
+    if (launch_ffn_tile(F_DACT, s->T, s->I, s->H, {dy, nullptr, w_down, nullptr}, a, st)) return MOK_ERR_CUDA;
     a.g = a.u = nullptr;
   }
-  if (gr->dx) {
+  if (launch_ffn_pair_bwd(1, b, st)) return MOK_ERR_CUDA;
+  if (gr->dx && !b.dx_rows) {
     a.out0 = gr->dx;
     a.out1 = nullptr;
     a.residual = static_cast<const uint16_t*>(gr->dx_add);
-    if (launch_ffn_gemm(F_DX, s->T, s->H, s->I, {dg, du, w_gate, w_up}, a, st)) return MOK_ERR_CUDA;
+    if (launch_ffn_tile(F_DX, s->T, s->H, s->I, {dg, du, w_gate, w_up}, a, st)) return MOK_ERR_CUDA;
   }
-  const FfnGradOperands go{dg, du, x, dy, c.a, gr->dw_gate, gr->dw_up, gr->dw_down};
-  if (launch_ffn_dw(s->T, s->H, s->I, go, gr->dw_type == MOK_DT_FP32, status, st)) return MOK_ERR_CUDA;
+  if (launch_ffn_pair_bwd(2, b, st)) return MOK_ERR_CUDA;
   return MOK_OK;
 }
 

@@ -32,7 +32,7 @@ struct FfnArgs {
   int32_t k_blocks;
   int32_t kb_split;     // DX: K blocks over (dg, Wg), then the same over (du, Wu)
   int32_t act;
-  int32_t out_f32;      // DW: fp32 outputs instead of bf16
+  int32_t out_f32;      // weight gradients: fp32 instead of bf16
   void* out0;           // a | out | dg | dx
   void* out1;           // - | -   | du | -
   float* g;             // GATEUP: saved when not null; DACT: read
@@ -106,15 +106,27 @@ struct FfnOperands {
   const void* b;   // Wg | Wd | Wd | Wg
   const void* b2;  // Wu   -    -    Wu
 };
-struct FfnGradOperands {  // dw_gate == nullptr, dw_down == nullptr: not computed
-  const void* dg;
-  const void* du;
+// The backward's operands.  dw_gate == nullptr, dw_down == nullptr: not computed.
+struct FfnBackward {
+  int64_t T, H, I;
+  int32_t act, dw_f32;
+  bool dact, dx_rows;  // DACT, DX in the phases' launches (else before them on the tile kernel, or not wanted)
   const void* x;
-  const void* dy;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
   const void* a;
+  const float* g;
+  const float* u;
+  const void* dy;
+  void* dg;
+  void* du;
+  void* dx;
+  const void* dx_add;
   void* dw_gate;
   void* dw_up;
   void* dw_down;
+  uint32_t* status;
 };
 // One row-tiled contraction: M, N, K of the variant (K of one half for DX), operands and the epilogue's
 // fields of `a` set.  The tile kernel (one tile per CTA, K split when there are few tiles; mok_ffn_tile.cu)
@@ -125,10 +137,9 @@ int launch_ffn_tile(int var, int64_t M, int64_t N, int64_t K, const FfnOperands&
 constexpr int kFfnRowTokens = 4;
 int launch_ffn_row(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
                    cudaStream_t stream);
-int launch_ffn_pair(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
-                    cudaStream_t stream);
-// The weight gradients, in one launch.
-int launch_ffn_dw(int64_t T, int64_t H, int64_t I, const FfnGradOperands& o, int out_f32, uint32_t* status,
-                  cudaStream_t stream);
+int launch_ffn_pair_fwd(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
+                        cudaStream_t stream);
+// Phase 1: DACT (if b.dact), perhaps dWd; phase 2, after it: DX (if b.dx_rows) and the other weight gradients.
+int launch_ffn_pair_bwd(int phase, const FfnBackward& b, cudaStream_t stream);
 
 }  // namespace mok

@@ -6,9 +6,13 @@
 // tile's MMAs.  Per CTA: warp 0 issues TMA loads, warp 1 (of the first CTA) the MMAs, eight warps
 // drain the accumulator, two per TMEM lane quarter with half of the columns each.
 //
-// Tiles are dealt out round robin over one pair per two SMs, in an order that keeps the tiles running
-// together in a near-square block of the output (ordered_tile), so that both operands are read from
-// L2.  The three weight gradients share one launch: alike in K, they fill the last round together.
+// Tiles are dealt out over one pair per two SMs, in an order that keeps the tiles running together in a
+// near-square block of the output (ordered_tile), so that both operands are read from L2.
+//
+// The backward is two launches of two jobs each, so that one's tiles fill the pairs that the other's last round
+// leaves idle: BWD1 = DACT, and dWd where that is shorter (it needs nothing of DACT's); BWD2 = DX and the other
+// weight gradients.  One job's tiles go round robin; the other's are shared out behind them so that all pairs end
+// as nearly together as whole tiles allow (make_plan).
 #include <initializer_list>
 
 #include "mok_ffn.cuh"
@@ -20,24 +24,36 @@ constexpr int kPairThreads = 64 + 32 * 8;
 constexpr uint32_t kPairTmemCols = 512;  // two accumulators, 256 columns apart
 constexpr int kGroupM = 4;  // M tiles of one band of the tile order
 
+// How a launch's tiles are dealt out to its `pairs` CTA pairs.  Job 0 is the row-tiled contraction, job 1 the weight
+// gradients.  The first job's units go round robin: pairs below `rem` get `quot` + 1, the rest `quot`.  Of the
+// second job's, every pair gets `each`, round robin, and the pairs from `rem` on `extra` before them.
+struct PairPlan {
+  int32_t pairs;
+  int32_t first;        // which job goes first
+  int32_t quot, rem;
+  int32_t each, extra;
+  int32_t units[2];
+};
+
 struct PairArgs {
-  FfnArgs f;
-  int32_t units;
-  // DW: units [0, u1) are dWg, [u1, u2) dWu, [u2, units) dWd, whose M and N are h and i
-  int32_t u1, u2;
-  int32_t m_tiles2, n_tiles2;  // dWd's tiles
+  FfnArgs f;            // job 0
+  PairPlan plan;
+  // job 1: units [0, u1) are dWg, [u1, 2 u1) dWu (I x H), the rest dWd (H x I)
+  int32_t H, I, u1;
+  int32_t m_tiles_i, n_tiles_h, m_tiles_h, n_tiles_i;
+  int32_t k_blocks1;
 };
 
 struct PairMaps {
-  CUtensorMap a[3], b[3], o[3];
+  CUtensorMap a[2], b[2], o[2];     // job 0
+  CUtensorMap a1[3], b1[2], o1[3];  // job 1
 };
 
-// What one launch computes: the four row-tiled contractions, or the three weight gradients together.
-enum PairVariant : int { P_GATEUP = 0, P_DOWN, P_DACT, P_DX, P_DW };
+enum PairVariant : int { P_GATEUP = 0, P_DOWN, P_BWD1, P_BWD2 };
 
 template <int VAR, int BN>
 struct PairCfg {
-  static constexpr bool kBmn = VAR >= P_DACT;
+  static constexpr bool kBmn = VAR >= P_BWD1;
   static constexpr uint32_t kABytes = 128 * 128;
   // an MN-major B half is whole 64-column boxes (the columns past BN / 2 of the last one are not used)
   static constexpr uint32_t kBBoxes = (BN / 2 + 63) / 64;
@@ -56,7 +72,9 @@ struct PairCfg {
 
 struct PairUnit {
   int m, n;      // tile of 256 rows x BN columns
-  int which;     // DW: 0 dWg, 1 dWu, 2 dWd
+  int job;       // 0, or 1: a weight gradient
+  int which;     // job 1: 0 dWg, 1 dWu, 2 dWd
+  int k_blocks;
 };
 
 // Tile u of an m_tiles x n_tiles output in bands of kGroupM M tiles, M fastest within a band.
@@ -67,23 +85,39 @@ __device__ __forceinline__ void ordered_tile(int u, int m_tiles, int n_tiles, in
   m = band * kGroupM + (r - n * rows);
 }
 
+// Units of pair `pair`, and its i-th one; false when that slot of the plan is empty.
 template <int VAR>
-__device__ __forceinline__ PairUnit pair_unit(const PairArgs& p, int u) {
-  PairUnit w;
-  w.which = 0;
-  if constexpr (VAR == P_DW) {
-    if (u >= p.u2) {
-      w.which = 2;
-      ordered_tile(u - p.u2, p.m_tiles2, p.n_tiles2, w.m, w.n);
-      return w;
-    }
-    if (u >= p.u1) {
-      w.which = 1;
-      u -= p.u1;
-    }
+__device__ __forceinline__ int pair_steps(const PairArgs& p, int pair) {
+  const PairPlan& g = p.plan;
+  return g.quot + (pair < g.rem ? 1 : 0) + g.each + (pair >= g.rem ? g.extra : 0);
+}
+template <int VAR>
+__device__ __forceinline__ bool pair_unit(const PairArgs& p, int pair, int i, PairUnit& w) {
+  const PairPlan& g = p.plan;
+  int u;
+  const int mine = g.quot + (pair < g.rem ? 1 : 0);
+  if (i < mine) {
+    u = i * g.pairs + pair;
+    w.job = g.first;
+  } else {
+    const int j = i - mine, e = pair >= g.rem ? g.extra : 0;
+    u = j < e ? g.each * g.pairs + j * (g.pairs - g.rem) + (pair - g.rem) : (j - e) * g.pairs + pair;
+    w.job = 1 - g.first;
+    if (u >= g.units[w.job]) return false;
   }
-  ordered_tile(u, p.f.m_tiles, p.f.n_tiles, w.m, w.n);
-  return w;
+  w.which = 0;
+  if (VAR < P_BWD1 || w.job == 0) {
+    w.job = 0;
+    w.k_blocks = p.f.k_blocks;
+    ordered_tile(u, p.f.m_tiles, p.f.n_tiles, w.m, w.n);
+  } else {
+    w.k_blocks = p.k_blocks1;
+    w.which = u >= 2 * p.u1 ? 2 : u >= p.u1 ? 1 : 0;
+    u -= w.which * p.u1;
+    if (w.which == 2) ordered_tile(u, p.m_tiles_h, p.n_tiles_i, w.m, w.n);
+    else ordered_tile(u, p.m_tiles_i, p.n_tiles_h, w.m, w.n);
+  }
+  return true;
 }
 
 // This CTA's loads of one K block: its 128 rows of A, and its half of B's columns.
@@ -91,11 +125,11 @@ template <int VAR>
 __device__ __forceinline__ void pair_load_a(const PairArgs& p, const PairMaps& t, const PairUnit& w, int kb,
                                             uint32_t sa, uint32_t bar, int rank) {
   const int k0 = kb * kFfnBK, m0 = w.m * 256 + rank * 128;
-  if constexpr (VAR == P_DW) {
-    const CUtensorMap* ta = &t.a[w.which];
+  if (VAR >= P_BWD1 && w.job) {
+    const CUtensorMap* ta = &t.a1[w.which];
     tma_load_2d_pair(sa, ta, bar, m0, k0);
     tma_load_2d_pair(sa + 8192, ta, bar, m0 + 64, k0);
-  } else if constexpr (VAR == P_DX) {
+  } else if constexpr (VAR == P_BWD2) {
     const int half = kb < p.f.kb_split ? 0 : 1;
     tma_load_2d_pair(sa, &t.a[half], bar, k0 - half * p.f.kb_split * kFfnBK, m0);
   } else {
@@ -112,8 +146,8 @@ __device__ __forceinline__ void pair_load_b(const PairArgs& p, const PairMaps& t
   } else if constexpr (VAR == P_DOWN) {
     tma_load_2d_pair(sb, &t.b[0], bar, k0, w.n * BN + rank * HB);
   } else {
-    const int half = VAR == P_DX && kb >= p.f.kb_split ? 1 : 0;
-    const CUtensorMap* tb = &t.b[VAR == P_DW ? (w.which == 2 ? 1 : 0) : half];
+    const int half = VAR == P_BWD2 && !w.job && kb >= p.f.kb_split ? 1 : 0;
+    const CUtensorMap* tb = w.job ? &t.b1[w.which == 2 ? 1 : 0] : &t.b[half];
     const int kr = k0 - half * p.f.kb_split * kFfnBK;
 #pragma unroll
     for (int j = 0; j < static_cast<int>(PairCfg<VAR, BN>::kBBoxes); ++j)
@@ -199,7 +233,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
                                               SavedChunk& pre) {
   const FfnArgs& f = p.f;
   const int r0 = w.m * 256 + rank * 128 + q * 32;  // the warp's first row
-  const bool rows = r0 < f.M;                       // (DWd: M below)
+  const bool rows = r0 < f.M;                       // (job 0)
   auto release = [&] {  // the accumulator's last column has been read
     tc_fence_before();
     __syncwarp();
@@ -226,7 +260,9 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
       for (int i = 0; i < 32; ++i) g[i] = act_fwd(g[i], f.act) * u[i];
       st.put_bf16(g, &t.o[0], c0 + c, r0);
     }
-  } else if constexpr (VAR == P_DACT) {
+    return;
+  }
+  if (VAR == P_BWD1 && !w.job) {  // DACT
     const int c0 = w.n * BN;
 #pragma unroll 1
     for (int c = c_beg; c < c_end; c += 32) {
@@ -263,16 +299,18 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
       st.put(du, &t.o[1], c0 + c, r0);
     }
   } else {
-    const int M = VAR == P_DW && w.which == 2 ? f.N : f.M, N = VAR == P_DW && w.which == 2 ? f.M : f.N;
-    const CUtensorMap* to = &t.o[VAR == P_DW ? w.which : 0];
+    const bool dw = VAR >= P_BWD1 && w.job;
+    const int M = !dw ? f.M : w.which == 2 ? p.H : p.I, N = !dw ? f.N : w.which == 2 ? p.I : p.H;
+    const CUtensorMap* to = dw ? &t.o1[w.which] : &t.o[0];
+    const uint16_t* add = dw ? nullptr : f.residual;
     const int c0 = w.n * BN;
 #pragma unroll 1
     for (int c = c_beg; c < c_end; c += 32) {
       const bool in = r0 < M && c0 + c < N;
       uint4 res[4];
-      if constexpr (VAR == P_DOWN || VAR == P_DX) {
-        if (f.residual && in && r0 + lane < M) {
-          const uint4* s = reinterpret_cast<const uint4*>(f.residual + static_cast<int64_t>(r0 + lane) * N + c0 + c);
+      if constexpr (VAR == P_DOWN || VAR == P_BWD2) {
+        if (add && in && r0 + lane < M) {
+          const uint4* s = reinterpret_cast<const uint4*>(add + static_cast<int64_t>(r0 + lane) * N + c0 + c);
 #pragma unroll
           for (int j = 0; j < 4; ++j) res[j] = c0 + c + 8 * j < N ? s[j] : make_uint4(0, 0, 0, 0);
         }
@@ -281,8 +319,8 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
       tmem_ld32(taddr + c, v);
       if (c + 32 >= c_end) release();
       if (!in) continue;
-      if constexpr (VAR == P_DOWN || VAR == P_DX) {
-        if (f.residual && r0 + lane < M) {
+      if constexpr (VAR == P_DOWN || VAR == P_BWD2) {
+        if (add && r0 + lane < M) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t r[4] = {res[j].x, res[j].y, res[j].z, res[j].w};
@@ -294,7 +332,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
           }
         }
       }
-      if (VAR == P_DW && f.out_f32) {
+      if (dw && f.out_f32) {
 #pragma unroll
         for (int k = 0; k < 32; k += 16) {
           uint4 ch[4];
@@ -316,8 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     ffn_pair_kernel(const __grid_constant__ PairMaps t, const PairArgs p) {
   using C = PairCfg<VAR, BN>;
   constexpr int S = C::kStages;
-  constexpr bool kAmn = VAR == P_DW, kBmn = C::kBmn;
-  constexpr uint32_t kIdesc = idesc_bf16(256, BN, kAmn, kBmn);
+  constexpr bool kBmn = C::kBmn;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms: 1024-byte aligned
@@ -334,7 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t drain = bar0 + 8u * (2 * S + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int u0 = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+  const int pair = static_cast<int>(blockIdx.x >> 1), steps = pair_steps<VAR>(p, pair);
   uint32_t* status = p.f.status;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -348,7 +385,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
-    if (VAR != P_DW) {  // (DW: only the maps of the gradients asked for are set)
+    if (p.plan.units[0]) {  // (a backward's launch may have weight gradients only)
       tma_prefetch_desc(&t.a[0]);
       tma_prefetch_desc(&t.b[0]);
       tma_prefetch_desc(&t.o[0]);
@@ -364,14 +401,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = *tmem_slot;
   // DOWN and DX always follow another kernel of this block, which runs once everything before it has ended:
   // their first weights are loaded before its end
-  constexpr bool kEarlyB = VAR == P_DOWN || VAR == P_DX;
+  constexpr bool kEarlyB = VAR == P_DOWN || VAR == P_BWD2;
 
   if (warp == 0) {
     int ahead = 0;
     if constexpr (kEarlyB) {
-      ahead = min(p.f.k_blocks, S);
-      if (u0 < p.units) {
-        const PairUnit w = pair_unit<VAR>(p, u0);
+      PairUnit w;
+      if (steps > 0 && pair_unit<VAR>(p, pair, 0, w) && !w.job) {
+        ahead = min(w.k_blocks, S);
         for (int kb = 0; kb < ahead; ++kb)
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(full(kb), C::kTxBytes);
@@ -384,9 +421,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int st = 0, issued = 0;
     uint32_t ph = 0;
     bool ok = true;
-    for (int u = u0; u < p.units && ok; u += step) {
-      const PairUnit w = pair_unit<VAR>(p, u);
-      for (int kb = 0; kb < p.f.k_blocks; ++kb) {
+    for (int i = 0; i < steps && ok; ++i) {
+      PairUnit w;
+      if (!pair_unit<VAR>(p, pair, i, w)) continue;
+      for (int kb = 0; kb < w.k_blocks; ++kb) {
         if (!warp_wait(empty(st), ph ^ 1u, abort_flag, status)) {
           ok = false;
           break;
@@ -415,24 +453,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int st = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      for (int u = u0; u < p.units && ok; u += step) {
+      for (int i = 0; i < steps && ok; ++i) {
+        PairUnit w;
+        if (!pair_unit<VAR>(p, pair, i, w)) continue;
+        const bool amn = VAR >= P_BWD1 && w.job;  // A's layout goes by the job
+        const uint32_t idesc = amn ? idesc_bf16(256, BN, true, kBmn) : idesc_bf16(256, BN, false, kBmn);
+        const uint32_t a_step = amn ? 128 : 2, a_lbo = amn ? 8192 : 16;  // steps count 16-byte units
         if (!__all_sync(0xffffffffu, mbar_wait<true>(tempty(acc), aph ^ 1u, abort_flag, status))) break;
         tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(acc) * 256u;
-        for (int kb = 0; kb < p.f.k_blocks; ++kb) {
+        for (int kb = 0; kb < w.k_blocks; ++kb) {
           if (!warp_wait(full(st), ph, abort_flag, status)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sa = base + st * C::kStageBytes, sb = sa + C::kABytes;
-          const uint64_t ad = kAmn ? sdesc_sw128(sa, 8192, 1024) : sdesc_sw128(sa, 16, 1024);
+          const uint64_t ad = sdesc_sw128(sa, a_lbo, 1024);
           const uint64_t bd = kBmn ? sdesc_sw128(sb, 8192, 1024) : sdesc_sw128(sb, 16, 1024);
           if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)  // descriptors count 16-byte units
-              umma_bf16_pair(d, ad + ks * (kAmn ? 128 : 2), bd + ks * (kBmn ? 128 : 2), kIdesc,
-                             (kb | ks) != 0 ? 1u : 0u);
+            for (int ks = 0; ks < 4; ++ks)
+              umma_bf16_pair(d, ad + ks * a_step, bd + ks * (kBmn ? 128 : 2), idesc, (kb | ks) != 0 ? 1u : 0u);
             umma_commit_pair(empty(st));
           }
           if (++st == S) {
@@ -459,10 +501,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     WarpStage st{base + C::kStagingOff + static_cast<uint32_t>(warp - 2) * 4096u, 0, lane};
     int acc = 0;
     uint32_t aph = 0;
-    for (int u = u0; u < p.units; u += step) {
-      const PairUnit w = pair_unit<VAR>(p, u);
+    for (int i = 0; i < steps; ++i) {
+      PairUnit w;
+      if (!pair_unit<VAR>(p, pair, i, w)) continue;
       SavedChunk pre;
-      if constexpr (VAR == P_DACT) {
+      if (VAR == P_BWD1 && !w.job) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           saved_fetch(p.f, w.m * 256 + rank * 128 + q * 32, lane, w.n * BN + (h ? (BN / 32 + 1) / 2 * 32 : 0), j, pre);
@@ -509,22 +552,80 @@ int launch_pair(const PairMaps& maps, const PairArgs& p, cudaStream_t stream) {
                           },
                           static_cast<int>(cudaErrorInvalidDevice));
   if (se) return se;
-  const int pairs = sm_count() / 2;
-  if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
-  const int grid = 2 * (p.units < pairs ? p.units : pairs);
-  constexpr int kKind = VAR == P_DW ? static_cast<int>(K_FFN_DW) : K_FFN_GATEUP + VAR;
+  constexpr int kKind = VAR == P_BWD1 ? static_cast<int>(K_FFN_BWD1)
+                        : VAR == P_BWD2 ? static_cast<int>(K_FFN_BWD2) : K_FFN_GATEUP + VAR;
   trace_begin(stream, kKind);
   const cudaError_t e =
-      launch_pdl(ffn_pair_kernel<VAR, BN>, dim3(grid), dim3(kPairThreads), C::kSmemBytes, stream, maps, p);
+      launch_pdl(ffn_pair_kernel<VAR, BN>, dim3(2 * p.plan.pairs), dim3(kPairThreads), C::kSmemBytes, stream, maps, p);
   trace_end(stream);
   return static_cast<int>(e);
 }
 
 int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
 
-// Row-tiled contraction over M rows, N output columns, K (of one half for DX).
+// The plan of a launch with units[j] tiles of k[j] K blocks of job j on at most `pairs` pairs, the job with the longer
+// K first unless `rows_first`; returns the K blocks of the pair that has the most.
+int64_t make_plan(const int64_t (&units)[2], const int64_t (&k)[2], bool rows_first, int pairs, PairPlan* g) {
+  const int first = units[0] && (!units[1] || rows_first || k[0] >= k[1]) ? 0 : 1, second = 1 - first;
+  const int64_t total = units[0] + units[1], n = total < pairs ? total : pairs;
+  g->pairs = static_cast<int32_t>(n);
+  g->first = first;
+  g->units[0] = static_cast<int32_t>(units[0]);
+  g->units[1] = static_cast<int32_t>(units[1]);
+  const int64_t quot = units[first] / n, rem = units[first] % n;
+  g->quot = static_cast<int32_t>(quot);
+  g->rem = static_cast<int32_t>(rem);
+  const int64_t ca = (quot + 1) * k[first], cb = quot * k[first];  // K blocks of a pair below rem, and of the rest
+  int64_t end = rem ? ca : cb;                                     // no pair ends before its first job
+  g->each = g->extra = 0;
+  if (units[second]) {
+    // the earliest end by which the pairs can have taken all of the second job: it is reached either by a whole
+    // number of units behind `ca` or behind `cb`
+    const int64_t ks = k[second];
+    auto room = [&](int64_t t) { return (rem ? rem * ((t - ca) / ks) : 0) + (n - rem) * ((t - cb) / ks); };
+    const int64_t share = (units[0] * k[0] + units[1] * k[1]) / n;  // none can end before an even share
+    const int64_t least = end > share ? end : share;
+    int64_t best = -1;
+    for (int64_t c : {rem ? ca : cb, cb}) {
+      int64_t t = c + (least > c ? (least - c + ks - 1) / ks * ks : 0);
+      while (room(t) < units[second]) t += ks;
+      if (best < 0 || t < best) best = t;
+    }
+    end = best;
+    const int64_t nb = (end - cb) / ks, na = rem ? (end - ca) / ks : nb;
+    g->each = static_cast<int32_t>(na);
+    g->extra = static_cast<int32_t>(nb - na);
+  }
+  return end;
+}
+
+// The tile width of the least cost, and that cost: the longest pair's K blocks x the columns of a tile and 16 more for
+// what a tile costs besides them (a K block measured 0.30 us at 256 columns, 0.23 to 0.25 at 192; 0.235 at 128, but
+// counting that at its time chose no better).  tiles(bn, units) gives each job's tiles.
+struct Width {
+  int bn;
+  int64_t cost;
+};
+template <class Tiles>
+Width best_width(std::initializer_list<int> widths, const int64_t (&k)[2], bool rows_first, int pairs, Tiles&& tiles) {
+  Width best{0, 0};
+  for (int bn : widths) {
+    int64_t units[2] = {0, 0};
+    PairPlan g;
+    tiles(bn, units);
+    if (!units[0] && !units[1]) return Width{0, 0};
+    const int64_t c = make_plan(units, k, rows_first, pairs, &g) * (bn + 16);
+    if (!best.bn || c < best.cost) best = Width{bn, c};
+  }
+  return best;
+}
+
+bool fits(const int64_t (&units)[2]) { return units[0] + units[1] < (int64_t{1} << 30); }
+
+// GATEUP or DOWN: M rows, N output columns, K.
 template <int VAR, int BN>
-int pair_rows(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& f, cudaStream_t stream) {
+int pair_fwd(int64_t M, int64_t N, int64_t K, int pairs, const FfnOperands& o, const FfnArgs& f,
+             cudaStream_t stream) {
   constexpr int kCols = VAR == P_GATEUP ? BN / 2 : BN;
   PairArgs p{};
   p.f = f;
@@ -532,123 +633,143 @@ int pair_rows(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnAr
   p.f.N = static_cast<int32_t>(N);
   p.f.m_tiles = static_cast<int32_t>(tiles_of(M, 256));
   p.f.n_tiles = static_cast<int32_t>(tiles_of(N, kCols));
-  p.f.kb_split = static_cast<int32_t>(tiles_of(K, kFfnBK));
-  p.f.k_blocks = p.f.kb_split * (VAR == P_DX ? 2 : 1);
-  const int64_t units = static_cast<int64_t>(p.f.m_tiles) * p.f.n_tiles;
-  if (units >= (int64_t{1} << 30)) return static_cast<int>(cudaErrorInvalidValue);
-  p.units = static_cast<int32_t>(units);
-  const uint64_t m = static_cast<uint64_t>(M), n = static_cast<uint64_t>(N), k = static_cast<uint64_t>(K);
-  PairMaps t;
-  bool good = make_tmap_bf16(&t.a[0], o.a, k, m, 64, 128);
-  if constexpr (VAR == P_DX) good = good && make_tmap_bf16(&t.a[1], o.a2, k, m, 64, 128);
-  if constexpr (VAR >= P_DACT) good = good && make_tmap_bf16(&t.b[0], o.b, n, k, 64, 64);
-  else good = good && make_tmap_bf16(&t.b[0], o.b, k, n, 64, BN / 2);
-  if constexpr (VAR == P_DX) good = good && make_tmap_bf16(&t.b[1], o.b2, n, k, 64, 64);
-  if constexpr (VAR == P_GATEUP) good = good && make_tmap_bf16(&t.b[1], o.b2, k, n, 64, BN / 2);
-  good = good && make_tmap_bf16_sw64(&t.o[0], f.out0, n, m, 32, 32);
-  if constexpr (VAR == P_DACT) good = good && make_tmap_bf16_sw64(&t.o[1], f.out1, n, m, 32, 32);
+  p.f.k_blocks = static_cast<int32_t>(tiles_of(K, kFfnBK));
+  const int64_t units[2] = {tiles_of(M, 256) * tiles_of(N, kCols), 0}, k[2] = {p.f.k_blocks, 0};
+  if (!fits(units)) return static_cast<int>(cudaErrorInvalidValue);
+  make_plan(units, k, true, pairs, &p.plan);
+  const uint64_t um = static_cast<uint64_t>(M), un = static_cast<uint64_t>(N), uk = static_cast<uint64_t>(K);
+  PairMaps t{};
+  bool good = make_tmap_bf16(&t.a[0], o.a, uk, um, 64, 128) && make_tmap_bf16(&t.b[0], o.b, uk, un, 64, BN / 2) &&
+              make_tmap_bf16_sw64(&t.o[0], f.out0, un, um, 32, 32);
+  if constexpr (VAR == P_GATEUP) good = good && make_tmap_bf16(&t.b[1], o.b2, uk, un, 64, BN / 2);
   if (!good) return static_cast<int>(cudaErrorInvalidValue);
   return launch_pair<VAR, BN>(t, p, stream);
 }
 
-}  // namespace
-
-namespace {
-
-// Cost of a launch of `units` tiles of bn columns, by rounds of pairs x columns per tile, 16 columns more for
-// what a tile costs besides them: the feed of its A rows.
-int64_t width_cost(int64_t units, int bn, int pairs) { return tiles_of(units, pairs) * (bn + 16); }
-
-// The tile width of the least cost; units(bn): tiles of that width.
-template <class Units>
-int best_width(std::initializer_list<int> widths, int pairs, Units&& units) {
-  int best = 0;
-  int64_t cost = 0;
-  for (int bn : widths) {
-    const int64_t c = width_cost(units(bn), bn, pairs);
-    if (!best || c < cost) best = bn, cost = c;
+template <int VAR>
+int pair_fwd_any(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& f, cudaStream_t stream) {
+  const int pairs = sm_count() / 2;
+  if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
+  const int64_t mt = tiles_of(M, 256), k[2] = {tiles_of(K, kFfnBK), 0};
+  const int64_t cols = VAR == P_GATEUP ? 2 * N : N;
+  auto tiles = [&](int w, int64_t* units) { units[0] = mt * tiles_of(cols, w); };
+  int bn;
+  if constexpr (VAR == P_GATEUP) {  // (half of the columns are gate columns, in whole 32-column chunks)
+    bn = best_width({256, 192, 128}, k, true, pairs, tiles).bn;
+  } else {
+    bn = best_width({256, 224, 192, 128}, k, true, pairs, tiles).bn;
+    if (bn == 224) return pair_fwd<VAR, 224>(M, N, K, pairs, o, f, stream);
   }
-  return best;
+  if (bn == 256) return pair_fwd<VAR, 256>(M, N, K, pairs, o, f, stream);
+  if (bn == 192) return pair_fwd<VAR, 192>(M, N, K, pairs, o, f, stream);
+  return pair_fwd<VAR, 128>(M, N, K, pairs, o, f, stream);
+}
+
+// What a launch of the backward does: its row-tiled contraction (DACT or DX), dWg and dWu, dWd.
+struct BwdJobs {
+  bool rows, gate_up, down;
+};
+template <int VAR>
+void bwd_tiles(const FfnBackward& b, const BwdJobs& j, int w, int64_t* units) {
+  units[0] = j.rows ? tiles_of(b.T, 256) * tiles_of(VAR == P_BWD1 ? b.I : b.H, w) : 0;
+  units[1] = (j.gate_up ? 2 * tiles_of(b.I, 256) * tiles_of(b.H, w) : 0) +
+             (j.down ? tiles_of(b.H, 256) * tiles_of(b.I, w) : 0);
+}
+// DACT's tiles go before dWd's, whose MMAs then hide its epilogue.
+template <int VAR>
+constexpr bool rows_first() { return VAR == P_BWD1; }
+
+template <int VAR>
+Width bwd_width(const FfnBackward& b, const BwdJobs& j, int pairs) {
+  const int64_t k[2] = {VAR == P_BWD1 ? tiles_of(b.H, kFfnBK) : 2 * tiles_of(b.I, kFfnBK), tiles_of(b.T, kFfnBK)};
+  return best_width({256, 224, 192, 128}, k, rows_first<VAR>(), pairs,
+                    [&](int w, int64_t* u) { bwd_tiles<VAR>(b, j, w, u); });
+}
+
+template <int VAR, int BN>
+int pair_bwd(const FfnBackward& b, const BwdJobs& j, int pairs, cudaStream_t stream) {
+  const int64_t cols = VAR == P_BWD1 ? b.I : b.H;
+  PairArgs p{};
+  p.f.M = static_cast<int32_t>(b.T);
+  p.f.N = static_cast<int32_t>(cols);
+  p.f.m_tiles = static_cast<int32_t>(tiles_of(b.T, 256));
+  p.f.n_tiles = static_cast<int32_t>(tiles_of(cols, BN));
+  p.f.kb_split = static_cast<int32_t>(tiles_of(VAR == P_BWD1 ? b.H : b.I, kFfnBK));
+  p.f.k_blocks = p.f.kb_split * (VAR == P_BWD2 ? 2 : 1);
+  p.f.act = b.act;
+  p.f.out_f32 = b.dw_f32;
+  p.f.status = b.status;
+  p.f.g = const_cast<float*>(b.g);
+  p.f.u = const_cast<float*>(b.u);
+  p.f.residual = static_cast<const uint16_t*>(b.dx_add);
+  p.H = static_cast<int32_t>(b.H);
+  p.I = static_cast<int32_t>(b.I);
+  p.m_tiles_i = static_cast<int32_t>(tiles_of(b.I, 256));
+  p.n_tiles_h = static_cast<int32_t>(tiles_of(b.H, BN));
+  p.m_tiles_h = static_cast<int32_t>(tiles_of(b.H, 256));
+  p.n_tiles_i = static_cast<int32_t>(tiles_of(b.I, BN));
+  p.u1 = j.gate_up ? p.m_tiles_i * p.n_tiles_h : 0;
+  p.k_blocks1 = static_cast<int32_t>(tiles_of(b.T, kFfnBK));
+  int64_t units[2];
+  bwd_tiles<VAR>(b, j, BN, units);
+  if (!fits(units)) return static_cast<int>(cudaErrorInvalidValue);
+  make_plan(units, {p.f.k_blocks, p.k_blocks1}, rows_first<VAR>(), pairs, &p.plan);
+  const uint64_t t = static_cast<uint64_t>(b.T), h = static_cast<uint64_t>(b.H), i = static_cast<uint64_t>(b.I);
+  PairMaps m{};
+  auto dw_map = [&](CUtensorMap* tm, void* d, uint64_t inner, uint64_t outer) {
+    return b.dw_f32 ? make_tmap_f32_sw64(tm, d, inner, outer, 16, 32)
+                    : make_tmap_bf16_sw64(tm, d, inner, outer, 32, 32);
+  };
+  bool good = true;
+  if (j.rows && VAR == P_BWD1)
+    good = make_tmap_bf16(&m.a[0], b.dy, h, t, 64, 128) && make_tmap_bf16(&m.b[0], b.w_down, i, h, 64, 64) &&
+           make_tmap_bf16_sw64(&m.o[0], b.dg, i, t, 32, 32) && make_tmap_bf16_sw64(&m.o[1], b.du, i, t, 32, 32);
+  else if (j.rows)
+    good = make_tmap_bf16(&m.a[0], b.dg, i, t, 64, 128) && make_tmap_bf16(&m.a[1], b.du, i, t, 64, 128) &&
+           make_tmap_bf16(&m.b[0], b.w_gate, h, i, 64, 64) && make_tmap_bf16(&m.b[1], b.w_up, h, i, 64, 64) &&
+           make_tmap_bf16_sw64(&m.o[0], b.dx, h, t, 32, 32);
+  if (good && j.gate_up)
+    good = make_tmap_bf16(&m.a1[0], b.dg, i, t, 64, 64) && make_tmap_bf16(&m.a1[1], b.du, i, t, 64, 64) &&
+           make_tmap_bf16(&m.b1[0], b.x, h, t, 64, 64) && dw_map(&m.o1[0], b.dw_gate, h, i) &&
+           dw_map(&m.o1[1], b.dw_up, h, i);
+  if (good && j.down)
+    good = make_tmap_bf16(&m.a1[2], b.dy, h, t, 64, 64) && make_tmap_bf16(&m.b1[1], b.a, i, t, 64, 64) &&
+           dw_map(&m.o1[2], b.dw_down, i, h);
+  if (!good) return static_cast<int>(cudaErrorInvalidValue);
+  return launch_pair<VAR, BN>(m, p, stream);
 }
 
 template <int VAR>
-int pair_rows_any(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& f, cudaStream_t stream) {
-  const int pairs = sm_count() / 2;
-  if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
-  const int64_t mt = tiles_of(M, 256);
-  int bn;
-  if constexpr (VAR == P_GATEUP) {  // (half of the columns are gate columns, in whole 32-column chunks)
-    bn = best_width({256, 192, 128}, pairs, [&](int w) { return mt * tiles_of(2 * N, w); });
-  } else {
-    bn = best_width({256, 224, 192, 128}, pairs, [&](int w) { return mt * tiles_of(N, w); });
-    if (bn == 224) return pair_rows<VAR, 224>(M, N, K, o, f, stream);
+int pair_bwd_any(const FfnBackward& b, const BwdJobs& j, int pairs, cudaStream_t stream) {
+  switch (bwd_width<VAR>(b, j, pairs).bn) {
+    case 0: return 0;
+    case 256: return pair_bwd<VAR, 256>(b, j, pairs, stream);
+    case 224: return pair_bwd<VAR, 224>(b, j, pairs, stream);
+    case 192: return pair_bwd<VAR, 192>(b, j, pairs, stream);
+    default: return pair_bwd<VAR, 128>(b, j, pairs, stream);
   }
-  if (bn == 256) return pair_rows<VAR, 256>(M, N, K, o, f, stream);
-  if (bn == 192) return pair_rows<VAR, 192>(M, N, K, o, f, stream);
-  return pair_rows<VAR, 128>(M, N, K, o, f, stream);
 }
 
 }  // namespace
 
-int launch_ffn_pair(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
-                    cudaStream_t stream) {
-  switch (var) {
-    case F_GATEUP: return pair_rows_any<P_GATEUP>(M, N, K, o, a, stream);
-    case F_DOWN: return pair_rows_any<P_DOWN>(M, N, K, o, a, stream);
-    case F_DACT: return pair_rows_any<P_DACT>(M, N, K, o, a, stream);
-    default: return pair_rows_any<P_DX>(M, N, K, o, a, stream);
-  }
+int launch_ffn_pair_fwd(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
+                        cudaStream_t stream) {
+  return var == F_GATEUP ? pair_fwd_any<P_GATEUP>(M, N, K, o, a, stream)
+                         : pair_fwd_any<P_DOWN>(M, N, K, o, a, stream);
 }
 
-namespace {
-
-template <int BN>
-int pair_dw(int64_t T, int64_t H, int64_t I, const FfnGradOperands& o, int out_f32, uint32_t* status,
-            cudaStream_t stream) {
-  PairArgs p{};
-  p.f.M = static_cast<int32_t>(I);
-  p.f.N = static_cast<int32_t>(H);
-  p.f.m_tiles = static_cast<int32_t>(tiles_of(I, 256));
-  p.f.n_tiles = static_cast<int32_t>(tiles_of(H, BN));
-  p.m_tiles2 = static_cast<int32_t>(tiles_of(H, 256));
-  p.n_tiles2 = static_cast<int32_t>(tiles_of(I, BN));
-  p.f.k_blocks = p.f.kb_split = static_cast<int32_t>(tiles_of(T, kFfnBK));
-  p.f.out_f32 = out_f32;
-  p.f.status = status;
-  const int gu = o.dw_gate ? p.f.m_tiles * p.f.n_tiles : 0;
-  p.u1 = gu;
-  p.u2 = 2 * gu;
-  p.units = 2 * gu + (o.dw_down ? p.m_tiles2 * p.n_tiles2 : 0);
-  if (p.units == 0) return 0;
-  const uint64_t t = static_cast<uint64_t>(T), h = static_cast<uint64_t>(H), i = static_cast<uint64_t>(I);
-  PairMaps m{};
-  auto out_map = [&](CUtensorMap* tm, void* d, uint64_t inner, uint64_t outer) {
-    return out_f32 ? make_tmap_f32_sw64(tm, d, inner, outer, 16, 32) : make_tmap_bf16_sw64(tm, d, inner, outer, 32, 32);
-  };
-  bool good = true;
-  if (o.dw_gate)
-    good = make_tmap_bf16(&m.a[0], o.dg, i, t, 64, 64) && make_tmap_bf16(&m.a[1], o.du, i, t, 64, 64) &&
-           make_tmap_bf16(&m.b[0], o.x, h, t, 64, 64) && out_map(&m.o[0], o.dw_gate, h, i) &&
-           out_map(&m.o[1], o.dw_up, h, i);
-  if (good && o.dw_down)
-    good = make_tmap_bf16(&m.a[2], o.dy, h, t, 64, 64) && make_tmap_bf16(&m.b[1], o.a, i, t, 64, 64) &&
-           out_map(&m.o[2], o.dw_down, i, h);
-  if (!good) return static_cast<int>(cudaErrorInvalidValue);
-  return launch_pair<P_DW, BN>(m, p, stream);
-}
-
-}  // namespace
-
-int launch_ffn_dw(int64_t T, int64_t H, int64_t I, const FfnGradOperands& o, int out_f32, uint32_t* status,
-                  cudaStream_t stream) {
+int launch_ffn_pair_bwd(int phase, const FfnBackward& b, cudaStream_t stream) {
   const int pairs = sm_count() / 2;
   if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
-  const int bn = best_width({256, 192, 128}, pairs, [&](int w) {
-    return (o.dw_gate ? 2 * tiles_of(I, 256) * tiles_of(H, w) : 0) + (o.dw_down ? tiles_of(H, 256) * tiles_of(I, w) : 0);
-  });
-  if (bn == 256) return pair_dw<256>(T, H, I, o, out_f32, status, stream);
-  if (bn == 192) return pair_dw<192>(T, H, I, o, out_f32, status, stream);
-  return pair_dw<128>(T, H, I, o, out_f32, status, stream);
+  // dWd goes with DACT where the two launches then cost less
+  BwdJobs one{b.dact, false, b.dw_down != nullptr}, two{b.dx_rows, b.dw_gate != nullptr, false};
+  BwdJobs one_x = one, two_x = two;
+  one_x.down = false;
+  two_x.down = one.down;
+  if (!b.dact || bwd_width<P_BWD1>(b, one_x, pairs).cost + bwd_width<P_BWD2>(b, two_x, pairs).cost <=
+                     bwd_width<P_BWD1>(b, one, pairs).cost + bwd_width<P_BWD2>(b, two, pairs).cost)
+    one = one_x, two = two_x;
+  return phase == 1 ? pair_bwd_any<P_BWD1>(b, one, pairs, stream) : pair_bwd_any<P_BWD2>(b, two, pairs, stream);
 }
 
 }  // namespace mok

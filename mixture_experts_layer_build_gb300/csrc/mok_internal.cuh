@@ -158,7 +158,8 @@ enum KernelKind : int {
   K_FFN_DOWN,
   K_FFN_DACT,
   K_FFN_DX,
-  K_FFN_DW,
+  K_FFN_BWD1,
+  K_FFN_BWD2,
   K_NUM_KINDS
 };
 void trace_begin(cudaStream_t s, int kind);  // no-ops unless a trace is set
