@@ -173,28 +173,38 @@ __device__ __forceinline__ void mx_store8(const Pair (&v)[4], uint8_t* q, uint8_
   if ((c & 31) == 0) s[soff + c / 32] = static_cast<uint8_t>(bad ? 0xFF : byte);
 }
 
+// Facts of one call that a kernel's type may hold.  kFull: every thread has V vectors of an existing row, no bounds to
+// test; kStream: every tensor of the residual stream is there (forward: residual and h; backward: dres, dh and dx);
+// kDrop: with dropout.
+enum { kFull = 1, kStream = 2, kDrop = 4 };
+template <int KNOWN>
+using Known = std::integral_constant<int, KNOWN>;
+
 // Block = blockDim.x / tpr rows of tpr threads; thread t of a row holds vectors t, t + tpr, ... of 8 values.
-// The draws need no data: they are made while the row's loads fly.
-template <int V, bool F32, int MAXT, int MINB>
+// The draws need no data: they are made while the row's loads fly.  What a call is known to have
+// is in the type: issue slots are what the MXFP8 output with dropout runs out of (at 8192 x 4096: 45.9 us with nothing
+// known, 42.4 with kFull and kDrop, 40.5 with all three).
+template <int V, bool F32, int MAXT, int MINB, int KNOWN>
 __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_fwd_kernel(const NormFwdArgs a) {
+  constexpr bool FULL = KNOWN & kFull, STREAM = KNOWN & kStream, DROP = KNOWN & kDrop;
   pdl_wait();
   __shared__ float buf[32];
   const int rows = static_cast<int>(blockDim.x) / a.tpr;
   const int rl = static_cast<int>(threadIdx.x) / a.tpr, t = static_cast<int>(threadIdx.x) - rl * a.tpr;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * rows + rl, off = row * a.H;
-  const bool live = row < a.T;
+  auto has = [&](int c) { return FULL || (row < a.T && c < a.H); };  // column c of this thread's row exists
   uint4 x[V];
   Vec8<F32> r[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * a.tpr + t) * 8;
-    if (live && c < a.H) {
+    if (has(c)) {
       x[j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + off + c));
-      if (a.residual) r[j].load(a.residual, off + c);
+      if (STREAM || a.residual) r[j].load(a.residual, off + c);
     }
   }
   uint32_t draws[V][4];
-  if (a.drop.rng) {
+  if constexpr (DROP) {
     DropState ds;
     ds.load(a.drop);
 #pragma unroll
@@ -208,12 +218,12 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_fwd_kernel(const NormFwdAr
     const int c = (j * a.tpr + t) * 8;
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[j][k] = 0;
-    if (live && c < a.H) {
+    if (has(c)) {
       uint32_t xb[8];
       bits_of(x[j], xb);
-      if (a.drop.rng) drop_bits(xb, a.drop, draws[j]);
+      if constexpr (DROP) drop_bits(xb, a.drop, draws[j]);
       Pair rr[4];
-      if (a.residual) {
+      if (STREAM || a.residual) {
         r[j].get(rr);
       } else {
 #pragma unroll
@@ -221,7 +231,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_fwd_kernel(const NormFwdAr
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[j][k] = fma2(pair_of(xb[2 * k], xb[2 * k + 1]), scale, rr[k]);
-      if (a.h) {
+      if (STREAM || a.h) {
         Vec8<F32>::store(a.h, off + c, v[j]);
         Vec8<F32>::round(v[j]);
       }
@@ -233,16 +243,16 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_fwd_kernel(const NormFwdAr
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * a.tpr + t) * 8;
-    wq[j] = c < a.H ? __ldg(reinterpret_cast<const uint4*>(a.w + c)) : make_uint4(0, 0, 0, 0);
+    wq[j] = FULL || c < a.H ? __ldg(reinterpret_cast<const uint4*>(a.w + c)) : make_uint4(0, 0, 0, 0);
   }
   const float2 s2 = floats_of(ss);
   const float rs = rsqrtf(row_sum(s2.x + s2.y, a.tpr, buf) / static_cast<float>(a.H) + a.eps);
-  if (live && t == 0 && a.rstd) a.rstd[row] = rs;
+  if (has(0) && t == 0 && a.rstd) a.rstd[row] = rs;
   const Pair rs2 = splat(rs);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * a.tpr + t) * 8;
-    const bool in = live && c < a.H;
+    const bool in = has(c);
     Pair w[4];
     pairs_of(wq[j], w);
 #pragma unroll
@@ -272,8 +282,11 @@ struct NormBwdArgs {
 // of a block are added in ascending order at the end: one partial row of dweight per block.  (Rows copied ahead into
 // shared memory by cp.async, for four blocks per SM instead of two, were slower: 59 against 57 us at
 // 8192 x 4096 bf16 with dropout, 375 against 230 at 16384 x 7168 with an fp32 stream.)
-template <int V, bool F32, int MAXT, int MINB>
+// KNOWN (see above) takes 4096 x 2048 bf16 with dropout from 19.2 to 17.1 us; with an fp32 stream or four vectors its
+// registers do not suffice (16384 x 7168: 322 us against 230), so those never have it.
+template <int V, bool F32, int MAXT, int MINB, int KNOWN>
 __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_bwd_kernel(const NormBwdArgs a) {
+  constexpr bool FULL = KNOWN & kFull, STREAM = KNOWN & kStream;
   pdl_wait();
   __shared__ float buf[2][32];
   extern __shared__ float group_dw[];  // [rows, H] when the block holds several rows
@@ -288,15 +301,15 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_bwd_kernel(const NormBwdAr
     float rs;
   } next;
   auto fetch = [&](int64_t at, int64_t rw) {
-    if (rw >= a.T) return;
+    if (rw >= a.T) return;  // past the end: nothing of it is used
     next.rs = __ldg(a.rstd + rw);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * a.tpr + t) * 8;
-      if (c < a.H) {
+      if (FULL || c < a.H) {
         next.h[j].load(a.h, at + c);
         next.dy[j] = __ldcs(reinterpret_cast<const uint4*>(a.dy + at + c));
-        if (a.dres) next.d[j].load(a.dres, at + c);
+        if (STREAM || a.dres) next.d[j].load(a.dres, at + c);
       }
     }
   };
@@ -308,14 +321,14 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_bwd_kernel(const NormBwdAr
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * a.tpr + t) * 8;
-    wq[j] = c < a.H ? __ldg(reinterpret_cast<const uint4*>(a.w + c)) : make_uint4(0, 0, 0, 0);
+    wq[j] = FULL || c < a.H ? __ldg(reinterpret_cast<const uint4*>(a.w + c)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int k = 0; k < 4; ++k) dw[j][k] = 0;
   }
   const Pair scale = splat(a.drop.scale);
   const float inv_h = 1.0f / static_cast<float>(a.H);
   for (int ph = 0; r0 < a.T; r0 += step, row += step, off += hop, ph ^= 1) {
-    const bool live = row < a.T;
+    const bool live = FULL || row < a.T;
     if constexpr (!kAhead) fetch(off, row);
     const Row cur = next;
     if constexpr (kAhead) fetch(off + hop, row + step);
@@ -324,7 +337,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_bwd_kernel(const NormBwdAr
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * a.tpr + t) * 8;
-      if (live && c < a.H) {
+      if (live && (FULL || c < a.H)) {
         Pair dy[4], xh[4], w[4];
         cur.h[j].get(xh);
         pairs_of(cur.dy[j], dy);
@@ -342,12 +355,12 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_bwd_kernel(const NormBwdAr
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * a.tpr + t) * 8;
-      if (live && c < a.H) {
+      if (live && (FULL || c < a.H)) {
         Pair g[4], xh[4], w[4], e[4];
         cur.h[j].get(xh);
         pairs_of(cur.dy[j], g);
         pairs_of(wq[j], w);
-        if (a.dres) {
+        if (STREAM || a.dres) {
           cur.d[j].get(e);
         } else {
 #pragma unroll
@@ -355,8 +368,8 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_bwd_kernel(const NormBwdAr
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) g[k] = fma2(fma2(mul2(xh[k], rs2), c2, mul2(g[k], w[k])), rs2, e[k]);
-        if (a.dh) Vec8<F32>::store(a.dh, off + c, g);
-        if (a.dx) {
+        if (STREAM || a.dh) Vec8<F32>::store(a.dh, off + c, g);
+        if (STREAM || a.dx) {
           if (a.drop.rng) {
             uint32_t b[8], dr[4];
 #pragma unroll
@@ -379,7 +392,7 @@ __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_bwd_kernel(const NormBwdAr
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int c = (j * a.tpr + t) * 8;
-    if (c < a.H) Vec8<true>::store(p, c, dw[j]);
+    if (FULL || c < a.H) Vec8<true>::store(p, c, dw[j]);
   }
   if (rows > 1) {
     __syncthreads();
@@ -489,6 +502,8 @@ struct RowPlan {
     if (need <= 16) tpr = need > 8 ? 16 : need > 4 ? 8 : 4;
     rows = tpr >= 256 ? 1 : 256 / tpr;
   }
+  // Every thread of every block has v vectors of an existing row.
+  bool full(const mok_norm_shape& s) const { return tpr * v * 8 == s.H && s.T % rows == 0; }
 };
 
 // Blocks of the backward, and partial rows of dweight: two 256-thread blocks' worth of threads per SM of 152 (a
@@ -587,11 +602,18 @@ mok_status mok_rmsnorm_forward(const mok_norm_shape* s, const void* x, const voi
   const int e = with_row_kernel(p, s->stream_type == MOK_DT_FP32, [&](auto v, auto f32) {
     constexpr int kV = decltype(v)::value;
     constexpr bool kF32 = decltype(f32)::value;
-    constexpr int kBlocks = kV == 4 ? 4 : 5;  // blocks of 256 threads per SM: as many as its registers hold
-    const dim3 grid(static_cast<unsigned>(blocks)), block(p.tpr * p.rows);
-    return static_cast<int>(p.tpr <= 256
-                                ? launch_pdl(rmsnorm_fwd_kernel<kV, kF32, 256, kBlocks>, grid, block, 0, st, a)
-                                : launch_pdl(rmsnorm_fwd_kernel<kV, kF32, 512, 2>, grid, block, 0, st, a));
+    auto run = [&](auto known) {
+      constexpr int kBlocks = kV == 4 ? 4 : 5;  // blocks of 256 threads per SM: as many as its registers hold
+      constexpr int kKnown = decltype(known)::value;
+      const dim3 grid(static_cast<unsigned>(blocks)), block(p.tpr * p.rows);
+      return static_cast<int>(p.tpr <= 256
+                                  ? launch_pdl(rmsnorm_fwd_kernel<kV, kF32, 256, kBlocks, kKnown>, grid, block, 0, st, a)
+                                  : launch_pdl(rmsnorm_fwd_kernel<kV, kF32, 512, 2, kKnown>, grid, block, 0, st, a));
+    };
+    const bool stream_there = residual && h;
+    if (!p.full(*s)) return a.drop.rng ? run(Known<kDrop>{}) : run(Known<0>{});
+    if (!stream_there) return a.drop.rng ? run(Known<kFull | kDrop>{}) : run(Known<kFull>{});
+    return a.drop.rng ? run(Known<kFull | kStream | kDrop>{}) : run(Known<kFull | kStream>{});
   });
   trace_end(st);
   return e ? MOK_ERR_CUDA : MOK_OK;
@@ -635,9 +657,16 @@ mok_status mok_rmsnorm_backward(const mok_norm_shape* s, const void* h, const fl
       constexpr bool kF32 = decltype(f32)::value;
       const dim3 grid(blocks), block(p.tpr * p.rows);
       const size_t smem = p.rows > 1 ? static_cast<size_t>(p.rows) * s->H * sizeof(float) : 0;
-      return static_cast<int>(p.tpr <= 256
-                                  ? launch_pdl(rmsnorm_bwd_kernel<kV, kF32, 256, 2>, grid, block, smem, st, a)
-                                  : launch_pdl(rmsnorm_bwd_kernel<kV, kF32, 512, 1>, grid, block, smem, st, a));
+      auto run = [&](auto known) {
+        constexpr int kKnown = decltype(known)::value;
+        return static_cast<int>(
+            p.tpr <= 256 ? launch_pdl(rmsnorm_bwd_kernel<kV, kF32, 256, 2, kKnown>, grid, block, smem, st, a)
+                         : launch_pdl(rmsnorm_bwd_kernel<kV, kF32, 512, 1, kKnown>, grid, block, smem, st, a));
+      };
+      if constexpr (!kF32 && kV <= 2) {
+        if (p.full(*s) && dres && dh && dx) return run(Known<kFull | kStream>{});
+      }
+      return run(Known<0>{});
     });
     trace_end(st);
     if (e) return MOK_ERR_CUDA;

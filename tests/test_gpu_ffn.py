@@ -161,11 +161,10 @@ def test_gradients_left_out(mok):
             assert torch.equal(got[k], want[k]) if k in keep else (got[k] == 0).all()
 
 
-# Sizes by the tile widths of the pair kernel: the width with the least rounds of 76 pairs x (columns + 16).  GATEUP
-# has 2 I columns, DOWN and DX H, DACT I; the weight gradients are (I x H) twice and (H x I).
+# Sizes by the tile widths of the pair kernel (forward and DX, DACT, DW).
 @pytest.mark.parametrize("T,H,I,widths", [
-    (512, 5000, 2600, "gate/up 192"), (1100, 2048, 1024, "128 columns"), (2048, 4096, 1536, "192, 224, 256"),
-    (700, 3400, 3400, "ragged 192 and 224"), (5120, 1792, 896, "224 and 256")])
+    (512, 5000, 2600, "192; DACT 128; DW 256"), (1100, 2048, 1024, "192; 128"), (2048, 4096, 1536, "192, 224, 256"),
+    (700, 3400, 3400, "192, ragged"), (5120, 1792, 896, "256; 128; 192")])
 def test_every_tile_width(mok, T, H, I, widths):
     check(mok, T, H, I, "silu" if T % 3 else "gelu")
 

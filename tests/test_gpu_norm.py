@@ -157,6 +157,35 @@ def test_no_rows(mok):
     assert mok.dropout_forward(e, mok.Dropout(0.5, state)).numel() == 0
 
 
+@pytest.mark.parametrize("T,H,stream,p", [(32, 128, BF, 0.1), (64, 512, F32, 0.0), (6, 1024, BF, 0.1), (34, 2048, BF, 0.1),
+                                          (5, 4096, BF, 0.1), (4, 2048, F32, 0.1), (3, 7168, BF, 0.0), (3, 8192, F32, 0.1)])
+def test_rows_do_not_depend_on_how_many_there_are(mok, T, H, stream, p):
+    """T rows that fill every block and T + 1 that do not give the first T the same bits; in place as well."""
+    d = draw(T + 1, H, stream, 3 * T + H)
+    c = {k: v.cuda() for k, v in d.items()}
+    state = rng_state()
+    drop = mok.Dropout(p, state) if p else None
+    o = mok.rmsnorm_forward(c["x"], c["w"], 1e-5, residual=c["res"], dropout=drop, mx=True)
+    g = mok.rmsnorm_backward(o.h, o.rstd, c["w"], c["dy"], dres=c["dres"], dropout=drop)
+    cut = {k: v[:T].clone() if v.dim() == 2 else v for k, v in c.items()}
+    a = mok.rmsnorm_forward(cut["x"], cut["w"], 1e-5, residual=cut["res"], dropout=drop, mx=True)
+    b = mok.rmsnorm_backward(a.h, a.rstd, cut["w"], cut["dy"], dres=cut["dres"], dropout=drop)
+    for k in "h", "rstd", "y", "q", "s":
+        assert torch.equal(getattr(a, k), getattr(o, k)[:T]), k
+    assert torch.equal(b.dh, g.dh[:T]) and torch.equal(b.dx, g.dx[:T])
+    h = a.h.cpu().double()
+    _, dw = ref.rmsnorm_grads(h, a.rstd.cpu().double(), d["w"].double(), d["dy"][:T].double(), None)
+    near(b.dweight, dw, (d["dy"][:T].double().abs() * (h * a.rstd.cpu().double()[:, None]).abs()).sum(0), "dweight")
+    import ctypes
+    shape = mok.mok_norm_shape(T, H, 0 if stream == BF else 1, 1e-5)
+    dh, dx, dweight = cut["dres"].clone(), cut["dy"].clone(), torch.empty(H, device="cuda")
+    ws = torch.empty(mok.mok_rmsnorm_workspace_bytes(shape), dtype=torch.uint8, device="cuda")
+    rc = mok._lib.mok_rmsnorm_backward(ctypes.byref(shape), a.h.data_ptr(), a.rstd.data_ptr(), c["w"].data_ptr(),
+                                       dx.data_ptr(), dh.data_ptr(), drop.ref if drop else None, dh.data_ptr(),
+                                       dx.data_ptr(), dweight.data_ptr(), ws.data_ptr(), ws.numel(), mok._stream(None))
+    assert rc == 0 and torch.equal(dh, b.dh) and torch.equal(dx, b.dx) and torch.equal(dweight, b.dweight)
+
+
 @pytest.mark.parametrize("n,stream,p", [(8, BF, 0.5), (8 * 511, F32, 0.1), (8 * 513, BF, 0.1), (8 * 40001, BF, 0.02),
                                         (8 * 1000, F32, 0.0), (8 * 1000, BF, 1.0)])
 def test_dropout(mok, n, stream, p):
