@@ -491,8 +491,8 @@ bool norm_shape_ok(const mok_norm_shape* s) {
 // Threads per row (a power of two of lanes up to a warp, then whole warps), vectors of 8 per thread, rows per
 // block of 256 threads or one row of more.  More values per thread mean fewer threads to reduce over and more
 // loads in flight each, as long as the registers hold them: forward, bf16, H = 2048 with dropout, 4096
-// rows: 14.1 us with one vector per thread, 11.8 with two; H = 7168, MXFP8, 16384 rows: 172 with two, 161 with
-// four; fp32 stream: 204 with two, 253 with four.
+// rows: 13.0 us with one vector per thread, 10.0 with two; H = 7168, MXFP8, 16384 rows: 158 with two, 140 with
+// four; H = 4096, 8192 rows: 40.4 with two, 41.1 with four; fp32 stream, H = 7168: 204 with two, 253 with four.
 struct RowPlan {
   int tpr, v, rows;
   RowPlan(int H, bool four) {  // four: four vectors already from H > 4096 on

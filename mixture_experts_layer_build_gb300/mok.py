@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -678,23 +679,30 @@ def mok_rmsnorm_workspace_bytes(shape: mok_norm_shape) -> int:
     return n
 
 
+@lru_cache(maxsize=256)
+def _norm_bwd_plan(T: int, H: int, stream_type: int):
+    """(reference to the shape, workspace bytes): 1.8 us of a call's 22 on the host."""
+    shape = mok_norm_shape(T, H, stream_type, 0.0)
+    return ctypes.byref(shape), mok_rmsnorm_workspace_bytes(shape)
+
+
 def rmsnorm_backward(h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
                      dres: torch.Tensor | None = None, dropout: Dropout | None = None, stream=None) -> NormGrads:
     """Gradients of rmsnorm_forward from dy [T, H] bf16 = dL/dy and dres = dL/dh from the stream's other
     uses (h's type, or None), under the forward's masks."""
     T, H = h.shape
     dev = h.device
-    shape = mok_norm_shape(T, H, _stream_type(h, "h"), 0.0)
+    shape, ws_bytes = _norm_bwd_plan(T, H, _stream_type(h, "h"))
     dh = torch.empty_like(h)
     own_dx = dropout is not None or h.dtype != torch.bfloat16
     dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if own_dx else None
     dw = torch.empty((H,), dtype=torch.float32, device=dev)
-    ws = torch.empty(mok_rmsnorm_workspace_bytes(shape), dtype=torch.uint8, device=dev)
-    _check(_lib.mok_rmsnorm_backward(ctypes.byref(shape), _ptr(h, None, "h"), _arg(rstd, (T,), torch.float32, "rstd"),
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    _check(_lib.mok_rmsnorm_backward(shape, _ptr(h, None, "h"), _arg(rstd, (T,), torch.float32, "rstd"),
                                      _arg(weight, (H,), torch.bfloat16, "weight"),
                                      _arg(dy, h.shape, torch.bfloat16, "dy"), _arg(dres, h.shape, h.dtype, "dres"),
                                      dropout.ref if dropout is not None else None, dh.data_ptr(),
-                                     None if dx is None else dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws.numel(),
+                                     None if dx is None else dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws_bytes,
                                      _stream(stream)), "mok_rmsnorm_backward")
     return NormGrads(dh, dh if dx is None else dx, dw)
 
