@@ -12,11 +12,11 @@ bool ffn_shape_ok(const mok_ffn_shape* s) {
          s->I <= 65536 && s->H % 8 == 0 && s->I % 8 == 0 && (s->act == MOK_ACT_SILU || s->act == MOK_ACT_GELU);
 }
 
-// The context: a [T, I] bf16, then (saved) g and u fp32 in the layout of ffn_saved_offset.
+// The context: a [T, I] bf16, then (saved) the factors u act'(g) and act(g) in fp32, in the layout of ffn_saved_offset.
 struct FfnCtx {
   uint16_t* a;
-  float* g;
-  float* u;
+  float* kg;
+  float* ku;
   size_t bytes;
   FfnCtx(const mok_ffn_shape& s, bool save, const void* p) {
     char* base = static_cast<char*>(const_cast<void*>(p));
@@ -24,8 +24,8 @@ struct FfnCtx {
     const size_t ns = (static_cast<size_t>(s.T) + 31) / 32 * 32 * s.I;
     const size_t og = up256(2 * n), ou = og + up256(4 * ns);
     a = reinterpret_cast<uint16_t*>(base);
-    g = save ? reinterpret_cast<float*>(base + og) : nullptr;
-    u = save ? reinterpret_cast<float*>(base + ou) : nullptr;
+    kg = save ? reinterpret_cast<float*>(base + og) : nullptr;
+    ku = save ? reinterpret_cast<float*>(base + ou) : nullptr;
     bytes = save ? ou + up256(4 * ns) : og;
     if (bytes < 256) bytes = 256;
   }
@@ -84,11 +84,11 @@ mok_status mok_ffn_forward(const mok_ffn_shape* s, const void* x, const void* w_
   a.act = s->act;
   a.status = status;
   a.out0 = c.a;
-  a.g = c.g;
-  a.u = c.u;
+  a.kg = c.kg;
+  a.ku = c.ku;
   if (launch_fwd(F_GATEUP, s->T, s->I, s->H, {x, nullptr, w_gate, w_up}, a, st)) return MOK_ERR_CUDA;
   a.out0 = out;
-  a.g = a.u = nullptr;
+  a.kg = a.ku = nullptr;
   a.residual = static_cast<const uint16_t*>(residual);
   return launch_fwd(F_DOWN, s->T, s->H, s->I, {c.a, nullptr, w_down, nullptr}, a, st) ? MOK_ERR_CUDA : MOK_OK;
 }
@@ -126,8 +126,8 @@ mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w
   b.w_up = w_up;
   b.w_down = w_down;
   b.a = c.a;
-  b.g = c.g;
-  b.u = c.u;
+  b.kg = c.kg;
+  b.ku = c.ku;
   b.dy = dy;
   b.dg = dg;
   b.du = du;
@@ -147,10 +147,10 @@ mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w
   if (dact && !b.dact) {
     a.out0 = dg;
     a.out1 = du;
-    a.g = c.g;
-    a.u = c.u;
+    a.kg = c.kg;
+    a.ku = c.ku;
     if (launch_ffn_tile(F_DACT, s->T, s->I, s->H, {dy, nullptr, w_down, nullptr}, a, st)) return MOK_ERR_CUDA;
-    a.g = a.u = nullptr;
+    a.kg = a.ku = nullptr;
   }
   if (launch_ffn_pair_bwd(1, b, st)) return MOK_ERR_CUDA;
   if (gr->dx && !b.dx_rows) {

@@ -6,6 +6,7 @@
 //   GATEUP  [g | u] = x [Wg | Wu]^T, epilogue a = act(g) u           M = T, N = I (twice), K = H
 //   DOWN    out = a Wd^T + residual                                  M = T, N = H, K = I
 //   DACT    da = dy Wd, epilogue dg = da u act'(g), du = da act(g)   M = T, N = I, K = H
+//           (both factors are made and saved by GATEUP's epilogue, where the sigmoid is at hand)
 //   DX      dx = dg Wg + du Wu + dx_add                              M = T, N = H, K = I twice
 //   DW      dWg = dg^T x, dWu = du^T x                               M = I, N = H, K = T
 //           dWd = dy^T a                                             M = H, N = I, K = T
@@ -35,13 +36,13 @@ struct FfnArgs {
   int32_t out_f32;      // weight gradients: fp32 instead of bf16
   void* out0;           // a | out | dg | dx
   void* out1;           // - | -   | du | -
-  float* g;             // GATEUP: saved when not null; DACT: read
-  float* u;
+  float* kg;            // u act'(g) and act(g), fp32.  GATEUP: saved when not null; DACT: read
+  float* ku;
   const uint16_t* residual;  // DOWN (the residual), DX (dx_add): added to the output, may be null
   uint32_t* status;
 };
 
-// Element offset of (row, column) of the saved g and u, columns a multiple of 4 wide: blocks of 32 rows x 4
+// Element offset of (row, column) of the saved factors, columns a multiple of 4 wide: blocks of 32 rows x 4
 // columns, so that a warp whose lanes hold 32 rows of an accumulator moves 512 contiguous bytes per
 // 4 columns straight from and to its registers.  Rows are padded to a multiple of 32.
 __host__ __device__ __forceinline__ int64_t ffn_saved_offset(int64_t row, int col, int I) {
@@ -91,6 +92,13 @@ __device__ __forceinline__ void act_bwd(float g, int act, float& f, float& df) {
     df = fmaf(f * (1.0f - s), 1.5957691216057308f * fmaf(3.0f * 0.044715f * g, g, 1.0f), s);
   }
 }
+// a = act(g) u, with the factors of dg and du.
+__device__ __forceinline__ float act_saved(float g, float u, int act, float& kg, float& ku) {
+  float df;
+  act_bwd(g, act, ku, df);
+  kg = u * df;
+  return ku * u;
+}
 #endif
 
 bool make_tmap_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
@@ -116,8 +124,8 @@ struct FfnBackward {
   const void* w_up;
   const void* w_down;
   const void* a;
-  const float* g;
-  const float* u;
+  const float* kg;
+  const float* ku;
   const void* dy;
   void* dg;
   void* du;

@@ -205,25 +205,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 32 columns of this lane's row of the saved g and u (ffn_saved_offset), 4 columns per entry.  DACT keeps one
+// 32 columns of this lane's row of the saved factors (ffn_saved_offset), 4 columns per entry.  DACT keeps one
 // chunk loaded ahead: its first one while the tile's MMAs run, the next one entry by entry as the current
 // one is used (a chunk's loads issued and awaited in place took 2.3 us, four of them per warp and tile).
 struct SavedChunk {
-  float4 g[8], u[8];
+  float4 kg[8], ku[8];
 };
 __device__ __forceinline__ void saved_fetch(const FfnArgs& f, int row0, int lane, int col, int j, SavedChunk& s) {
   if (row0 < f.M && col + 4 * j < f.N) {
     const int64_t off = ffn_saved_offset(row0 + lane, col, f.N);
-    s.g[j] = __ldcs(reinterpret_cast<const float4*>(f.g + off) + 32 * j);
-    s.u[j] = __ldcs(reinterpret_cast<const float4*>(f.u + off) + 32 * j);
+    s.kg[j] = __ldcs(reinterpret_cast<const float4*>(f.kg + off) + 32 * j);
+    s.ku[j] = __ldcs(reinterpret_cast<const float4*>(f.ku + off) + 32 * j);
   }
-}
-__device__ __forceinline__ void saved_store(float* p, int64_t off, int left, const float (&v)[32]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (4 * j < left)
-      __stcs(reinterpret_cast<float4*>(p + off) + 32 * j,
-             make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
 }
 
 // Epilogue of one tile for one warp: accumulator rows q * 32 ... (lane = row), column half h.
@@ -251,13 +244,22 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
       tmem_ld32(taddr + BN / 2 + c, u);
       if (c + 32 >= c_end) release();
       if (!rows || c0 + c >= f.N) continue;
-      if (f.g) {
+      if (f.kg) {
         const int64_t off = ffn_saved_offset(r0 + lane, c0 + c, f.N);
-        saved_store(f.g, off, f.N - c0 - c, g);
-        saved_store(f.u, off, f.N - c0 - c, u);
-      }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) g[i] = act_fwd(g[i], f.act) * u[i];
+        for (int j = 0; j < 8; ++j) {
+          float kg[4], ku[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) g[4 * j + k] = act_saved(g[4 * j + k], u[4 * j + k], f.act, kg[k], ku[k]);
+          if (c0 + c + 4 * j < f.N) {
+            __stcs(reinterpret_cast<float4*>(f.kg + off) + 32 * j, make_float4(kg[0], kg[1], kg[2], kg[3]));
+            __stcs(reinterpret_cast<float4*>(f.ku + off) + 32 * j, make_float4(ku[0], ku[1], ku[2], ku[3]));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) g[i] = act_fwd(g[i], f.act) * u[i];
+      }
       st.put_bf16(g, &t.o[0], c0 + c, r0);
     }
     return;
@@ -277,16 +279,13 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs& p, const PairMaps&
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
           const int j = i / 4 + jj;
-          const float g[4] = {pre.g[j].x, pre.g[j].y, pre.g[j].z, pre.g[j].w};
-          const float u[4] = {pre.u[j].x, pre.u[j].y, pre.u[j].z, pre.u[j].w};
+          float x[4] = {pre.kg[j].x, pre.kg[j].y, pre.kg[j].z, pre.kg[j].w};
+          float y[4] = {pre.ku[j].x, pre.ku[j].y, pre.ku[j].z, pre.ku[j].w};
           if (c + 32 < c_end) saved_fetch(f, r0, lane, c0 + c + 32, j, pre);
-          float x[4], y[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float a, da;
-            act_bwd(g[k], f.act, a, da);
-            x[k] = v[4 * jj + k] * u[k] * da;
-            y[k] = v[4 * jj + k] * a;
+            x[k] *= v[4 * jj + k];
+            y[k] *= v[4 * jj + k];
           }
           pg[2 * j] = pack_bf16x2(x[0], x[1]);
           pg[2 * j + 1] = pack_bf16x2(x[2], x[3]);
@@ -497,7 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else {
     const int q = warp & 3, h = (warp - 2) >> 2;
-    pdl_wait();  // the residual, the saved g and u, and outputs that an earlier kernel may still read
+    pdl_wait();  // the residual, the saved factors, and outputs that an earlier kernel may still read
     WarpStage st{base + C::kStagingOff + static_cast<uint32_t>(warp - 2) * 4096u, 0, lane};
     int acc = 0;
     uint32_t aph = 0;
@@ -699,8 +698,8 @@ int pair_bwd(const FfnBackward& b, const BwdJobs& j, int pairs, cudaStream_t str
   p.f.act = b.act;
   p.f.out_f32 = b.dw_f32;
   p.f.status = b.status;
-  p.f.g = const_cast<float*>(b.g);
-  p.f.u = const_cast<float*>(b.u);
+  p.f.kg = const_cast<float*>(b.kg);
+  p.f.ku = const_cast<float*>(b.ku);
   p.f.residual = static_cast<const uint16_t*>(b.dx_add);
   p.H = static_cast<int32_t>(b.H);
   p.I = static_cast<int32_t>(b.I);

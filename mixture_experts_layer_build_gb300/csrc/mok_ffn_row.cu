@@ -126,12 +126,12 @@ __global__ void __launch_bounds__(32 * kRowWarps) ffn_row_kernel(const RowArgs a
   float v;
   if constexpr (kGate) {
     const float g = sum(2 * j), u = sum(2 * j + 1);
-    if (a.f.g) {
+    if (a.f.kg) {
       const int64_t s = ffn_saved_offset(t, n, N);
-      a.f.g[s] = g;
-      a.f.u[s] = u;
+      v = act_saved(g, u, a.f.act, a.f.kg[s], a.f.ku[s]);
+    } else {
+      v = act_fwd(g, a.f.act) * u;
     }
-    v = act_fwd(g, a.f.act) * u;
   } else {
     v = sum(j);
     if (a.f.residual) v += bf16_lo(a.f.residual[o]);

@@ -67,7 +67,7 @@ __device__ __forceinline__ void store_bf16x8(void* p, int64_t i, const float (&v
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
       make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
-// 8 columns of a saved g or u: two blocks of 4 columns, 128 elements apart.
+// 8 columns of a saved factor: two blocks of 4 columns, 128 elements apart.
 __device__ __forceinline__ void saved_store8(float* p, int64_t off, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p + off) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + off + 128) = make_float4(v[4], v[5], v[6], v[7]);
@@ -110,12 +110,16 @@ template <int VAR>
 __device__ __forceinline__ void tile_epilogue8(const FfnArgs& f, int64_t m, int c, float (&v)[8], float (&w)[8]) {
   const int64_t i = m * f.N + c;
   if constexpr (VAR == F_GATEUP) {
-    if (f.g) {
-      saved_store8(f.g, ffn_saved_offset(m, c, f.N), v);
-      saved_store8(f.u, ffn_saved_offset(m, c, f.N), w);
-    }
+    if (f.kg) {
+      float kg[8], ku[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = act_fwd(v[k], f.act) * w[k];
+      for (int k = 0; k < 8; ++k) v[k] = act_saved(v[k], w[k], f.act, kg[k], ku[k]);
+      saved_store8(f.kg, ffn_saved_offset(m, c, f.N), kg);
+      saved_store8(f.ku, ffn_saved_offset(m, c, f.N), ku);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = act_fwd(v[k], f.act) * w[k];
+    }
     store_bf16x8(f.out0, i, v);
   } else if constexpr (VAR == F_DOWN || VAR == F_DX) {
     if (f.residual) {
@@ -126,14 +130,12 @@ __device__ __forceinline__ void tile_epilogue8(const FfnArgs& f, int64_t m, int 
     store_bf16x8(f.out0, i, v);
   } else if constexpr (VAR == F_DACT) {
     float g[8], u[8];
-    saved_load8(f.g, ffn_saved_offset(m, c, f.N), g);
-    saved_load8(f.u, ffn_saved_offset(m, c, f.N), u);
+    saved_load8(f.kg, ffn_saved_offset(m, c, f.N), g);
+    saved_load8(f.ku, ffn_saved_offset(m, c, f.N), u);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float a, da;
-      act_bwd(g[k], f.act, a, da);
-      g[k] = v[k] * u[k] * da;
-      u[k] = v[k] * a;
+      g[k] *= v[k];
+      u[k] *= v[k];
     }
     store_bf16x8(f.out0, i, g);
     store_bf16x8(f.out1, i, u);
