@@ -598,22 +598,29 @@ int64_t make_plan(const int64_t (&units)[2], const int64_t (&k)[2], bool rows_fi
   return end;
 }
 
-// The tile width of the least cost, and that cost: the longest pair's K blocks x the columns of a tile and 16 more for
-// what a tile costs besides them (a K block measured 0.30 us at 256 columns, 0.23 to 0.25 at 192; 0.235 at 128, but
-// counting that at its time chose no better).  tiles(bn, units) gives each job's tiles.
+// What a 64-wide K block takes on a pair, in ns: measured 300 at 256 columns, 270 and 240 at 224 and 192 (the loads
+// from L2 bound it: 128 + columns / 2 rows of 128 bytes per CTA), 205 to 285 at 128.
+constexpr int64_t block_ns(int bn) { return bn == 256 ? 300 : bn == 224 ? 270 : bn == 192 ? 240 : 220; }
+
+// The tile width of the least cost, and that cost: the longest pair's time, a tile counted as its K blocks and one more
+// for what it costs besides them, three for a row-tiled one where those go first (rows_first: an epilogue there stands
+// at the end of some pairs).  tiles(bn, units) gives each job's tiles.  Against counting K blocks x (columns + 16):
+// 41 training sizes 0.976 of the time on average, 0.82 to 1.03; T = 9602, H = 4024, I = 848 forward 205 -> 170 us,
+// T = 2675, H = 3992, I = 536 training 143 -> 132.
 struct Width {
   int bn;
   int64_t cost;
 };
 template <class Tiles>
 Width best_width(std::initializer_list<int> widths, const int64_t (&k)[2], bool rows_first, int pairs, Tiles&& tiles) {
+  const int64_t k1[2] = {k[0] + (rows_first ? 3 : 1), k[1] + 1};
   Width best{0, 0};
   for (int bn : widths) {
     int64_t units[2] = {0, 0};
     PairPlan g;
     tiles(bn, units);
     if (!units[0] && !units[1]) return Width{0, 0};
-    const int64_t c = make_plan(units, k, rows_first, pairs, &g) * (bn + 16);
+    const int64_t c = make_plan(units, k1, rows_first, pairs, &g) * block_ns(bn);
     if (!best.bn || c < best.cost) best = Width{bn, c};
   }
   return best;

@@ -161,10 +161,11 @@ def test_gradients_left_out(mok):
             assert torch.equal(got[k], want[k]) if k in keep else (got[k] == 0).all()
 
 
-# Sizes by the tile widths of the pair kernel (forward and DX, DACT, DW).
+# Sizes by the tile widths of the pair kernel: GATEUP, DOWN, the backward's two launches (- : on the tile kernel).
 @pytest.mark.parametrize("T,H,I,widths", [
-    (512, 5000, 2600, "192; DACT 128; DW 256"), (1100, 2048, 1024, "192; 128"), (2048, 4096, 1536, "192, 224, 256"),
-    (700, 3400, 3400, "192, ragged"), (5120, 1792, 896, "256; 128; 192")])
+    (512, 5000, 2600, "192 192 192 256"), (1100, 2048, 1024, "192 192 128 256"), (2048, 4096, 1536, "192 224 224 224"),
+    (700, 3400, 3400, "192 192 192 224"), (5120, 1792, 896, "256 256 128 224"), (396, 160, 1584, "128 - 128 128"),
+    (580, 1720, 128, "- 128 - 128"), (1662, 192, 2288, "256 - 256 128"), (372, 2792, 136, "- 128 - 192")])
 def test_every_tile_width(mok, T, H, I, widths):
     check(mok, T, H, I, "silu" if T % 3 else "gelu")
 
