@@ -170,6 +170,16 @@ def test_every_tile_width(mok, T, H, I, widths):
     check(mok, T, H, I, "silu" if T % 3 else "gelu")
 
 
+# Sizes whose GATEUP or DOWN takes two tile widths: the first M tiles in one, the last in the other.
+@pytest.mark.parametrize("T,H,I,widths", [
+    (1370, 80, 1768, "gate/up 192 128"), (2759, 104, 1272, "gate/up 256 128"), (2078, 88, 1624, "gate/up 256 192"),
+    (1300, 3344, 80, "down 192 128"), (3224, 3272, 80, "down 224 128"), (2349, 2968, 80, "down 224 192"),
+    (5592, 2944, 80, "down 256 128"), (4231, 1816, 80, "down 256 192"), (5699, 1448, 80, "down 256 224"),
+    (4096, 2048, 1024, "both 256 192")])
+def test_two_tile_widths(mok, T, H, I, widths):
+    check(mok, T, H, I, "silu" if T % 2 else "gelu")
+
+
 def test_dx_add(mok):
     for T, H, I in ((40, 136, 72), (900, 1032, 520)):  # tile kernel and pairs
         plan, d = check(mok, T, H, I, "silu", residual=False)
