@@ -3,8 +3,8 @@
 // A CTA computes a 128 x BN tile, or (split) one of S CTAs of a cluster computes a share of its K
 // range.  Warp 0 issues TMA loads into a ring of stages, warp 1 issues the tcgen05.mma (M = 128, N = BN,
 // K = 16) into one TMEM accumulator.  Then warps 2 to 5 push the accumulator, 8 columns of a row at a
-// time, into the shared memory of the CTA of the cluster that owns them (dealt out round robin), and after one
-// cluster barrier every owner adds its sources in ascending order, applies the epilogue and writes 16-byte
+// time, into the shared memory of the CTA of the cluster that owns them (dealt out round robin), and every owner
+// adds its sources in ascending order, applies the epilogue and writes 16-byte
 // vectors.  Every output has a fixed order of summation.
 //
 // With few tokens the weights' bytes bound it, and what stands in the way is latency: so the loops of
@@ -20,6 +20,11 @@ namespace {
 constexpr int kTileThreads = 192;
 constexpr int kTileMaxStages = 16;
 constexpr uint32_t kTileMaxSmem = 230400;  // what a launch may ask for
+// Tokens up to which the partials are counted on the owners' mbarriers, each CTA waiting for its own only; above, a
+// store that is counted costs more than the cluster barrier that orders plain ones: 16 tokens at H = 4096, I = 1536
+// 14.4 and 14.9 us, 48 tokens 15.0 and 15.3, 64 tokens 16.8 and 16.2, 128 tokens 25.2 and 22.5.  (Staged first and copied
+// in bulk: 14.7 and 23.3 for 16 and 128 tokens.)
+constexpr int64_t kTileCounted = 48;
 constexpr uint32_t kTileSmem = 116224;  // two CTAs per SM
 
 struct TileArgs {
@@ -61,6 +66,13 @@ __device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t* v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3])
+               : "memory");
+}
+// The same, counted on a barrier of that CTA when the bytes are there.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, const uint32_t* v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                   addr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
                : "memory");
 }
 __device__ __forceinline__ void store_bf16x8(void* p, int64_t i, const float (&v)[8]) {
@@ -142,7 +154,8 @@ __device__ __forceinline__ void tile_epilogue8(const FfnArgs& f, int64_t m, int 
   }
 }
 
-template <int VAR, int BN>
+// COUNTED (split): the pushed partials are counted on mbarriers; else a cluster barrier orders them.
+template <int VAR, int BN, bool COUNTED>
 __global__ void __launch_bounds__(kTileThreads)
     ffn_tile_kernel(const __grid_constant__ CUtensorMap tA, const __grid_constant__ CUtensorMap tA2,
                     const __grid_constant__ CUtensorMap tB, const __grid_constant__ CUtensorMap tB2,
@@ -150,14 +163,14 @@ __global__ void __launch_bounds__(kTileThreads)
   using C = TileCfg<VAR, BN>;
   constexpr uint32_t kIdesc = idesc_bf16(128, BN, false, ffn_b_mn(VAR));
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kTileMaxStages + 1];
+  __shared__ __align__(8) uint64_t bars[2 * kTileMaxStages + 2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;  // swizzle atoms: 1024-byte aligned
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (kTileMaxStages + s); };
-  const uint32_t done = bar0 + 8u * (2 * kTileMaxStages);
+  const uint32_t done = bar0 + 8u * (2 * kTileMaxStages), pushed = done + 8u;
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = t.split, rank = static_cast<int>(blockIdx.x) % S, tile = static_cast<int>(blockIdx.x) / S;
@@ -165,6 +178,7 @@ __global__ void __launch_bounds__(kTileThreads)
   const int kb0 = static_cast<int>(static_cast<int64_t>(t.f.k_blocks) * rank / S);
   const int count = static_cast<int>(static_cast<int64_t>(t.f.k_blocks) * (rank + 1) / S) - kb0;
   const uint32_t a_bytes = static_cast<uint32_t>(t.a_rows) * 128u;
+  const int rows = min(128, t.f.M - m * 128), items = rows * C::kChunks;  // chunks of the tile's valid rows
   if (warp == 0) {
     if (elect_one()) {
       for (int s = 0; s < t.stages; ++s) {
@@ -172,8 +186,11 @@ __global__ void __launch_bounds__(kTileThreads)
         mbar_init(empty(s), 1);
       }
       mbar_init(done, 1);
+      mbar_init(pushed, 1);
       abort_word = 0;
       fence_barrier_init();
+      const int mine = items > rank ? (items - rank + S - 1) / S : 0;  // this CTA's chunks, once from every source
+      mbar_arrive_expect_tx(pushed, COUNTED ? static_cast<uint32_t>(S * mine) * C::kChunkBytes : 0u);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -246,7 +263,6 @@ __global__ void __launch_bounds__(kTileThreads)
   tc_fence_after();
   // the accumulator's chunks to their owners: chunk j (row-major over the tile's valid rows) is slot j / S
   // of CTA j % S.  Without a split they are staged over the stages, every copy into which has been consumed.
-  const int rows = min(128, t.f.M - m * 128);
   const uint32_t push = S > 1 ? base + t.push_off : base;
   if (warp >= 2) {
     const int q = warp & 3, r = q * 32 + lane;  // this warp's TMEM lane quarter; the lane's row
@@ -264,8 +280,14 @@ __global__ void __launch_bounds__(kTileThreads)
           uint32_t slot = slot0, own = own0 + chunk;
           while (own >= static_cast<uint32_t>(S)) own -= S, ++slot;
           const uint32_t d = mapa_shared(src + C::slot_off(slot) + sub, own);
-          st_cluster_v4(d, v);
-          st_cluster_v4(d + 16, v + 4);
+          if constexpr (COUNTED) {
+            const uint32_t bar = mapa_shared(pushed, own);
+            st_async_v4(d, v, bar);
+            st_async_v4(d + 16, v + 4, bar);
+          } else {
+            st_cluster_v4(d, v);
+            st_cluster_v4(d + 16, v + 4);
+          }
         }
       };
 #pragma unroll 1
@@ -283,13 +305,15 @@ __global__ void __launch_bounds__(kTileThreads)
     }
   }
   tc_fence_before();
-  if (S > 1) cluster_sync();  // release / acquire: the pushed chunks are there
+  if (S > 1 && !COUNTED) cluster_sync();  // release / acquire: the pushed chunks are there
   else __syncthreads();
+  if constexpr (COUNTED) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has pushed
   if (warp == 1) tmem_dealloc(tmem, BN < 32 ? 32 : BN);
-  if (*abort_flag) return;  // the partials are not whole (recorded in the status word)
+  if constexpr (COUNTED) __all_sync(0xffffffffu, mbar_wait<true>(pushed, 0, abort_flag, t.f.status));
+  const bool whole = *abort_flag == 0;  // (else recorded in the status word)
   const int64_t m0 = static_cast<int64_t>(m) * 128;
-  const int c0 = n * C::kCols, items = rows * C::kChunks;
-  for (int slot = threadIdx.x; slot * S + rank < items; slot += kTileThreads) {
+  const int c0 = n * C::kCols;
+  for (int slot = threadIdx.x; whole && slot * S + rank < items; slot += kTileThreads) {
     const int j = slot * S + rank, r = j / C::kChunks, c = (j - r * C::kChunks) * 8;
     if (c0 + c >= t.f.N) continue;
     float v[8], w[8];
@@ -306,15 +330,24 @@ __global__ void __launch_bounds__(kTileThreads)
     }
     tile_epilogue8<VAR>(t.f, m0 + r, c0 + c, v, w);
   }
+  if constexpr (COUNTED) {
+    if (!whole) {  // failure path: a peer's chunks may still be under way
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < kWaitLimitNs / 100) {
+      }
+    }
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // no CTA leaves before every peer has pushed
+  }
 }
 
-template <int VAR, int BN>
+template <int VAR, int BN, bool COUNTED>
 int launch_tile(const TileMaps& maps, TileArgs t, cudaStream_t stream) {
   using C = TileCfg<VAR, BN>;
   static DeviceOnce once;
   const int se = once.run([](int* d) { return static_cast<int>(cudaGetDevice(d)); },
                           [] {
-                            return static_cast<int>(cudaFuncSetAttribute(ffn_tile_kernel<VAR, BN>,
+                            return static_cast<int>(cudaFuncSetAttribute(ffn_tile_kernel<VAR, BN, COUNTED>,
                                                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                                          static_cast<int>(kTileMaxSmem)));
                           },
@@ -360,7 +393,7 @@ int launch_tile(const TileMaps& maps, TileArgs t, cudaStream_t stream) {
   cfg.numAttrs = t.split > 1 ? 2 : 1;
   constexpr int kKind = K_FFN_GATEUP + VAR;
   trace_begin(stream, kKind);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_tile_kernel<VAR, BN>, maps.a, maps.a2, maps.b, maps.b2, t);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, ffn_tile_kernel<VAR, BN, COUNTED>, maps.a, maps.a2, maps.b, maps.b2, t);
   trace_end(stream);
   return static_cast<int>(e);
 }
@@ -393,7 +426,10 @@ int launch_var(int64_t M, int64_t N, int64_t K, int split, const FfnOperands& o,
   if constexpr (VAR == F_GATEUP) good = good && make_tmap_bf16(&p.b2, o.b2, uk, un, 64, kCols);
   if constexpr (VAR == F_DX) good = good && make_tmap_bf16(&p.b2, o.b2, un, uk, 64, 64);
   if (!good) return static_cast<int>(cudaErrorInvalidValue);
-  return launch_tile<VAR, BN>(p, t, stream);
+  if constexpr (BN == 64) {
+    if (split > 1 && M <= kTileCounted) return launch_tile<VAR, BN, true>(p, t, stream);
+  }
+  return launch_tile<VAR, BN, false>(p, t, stream);
 }
 
 // Columns of a tile and CTAs per tile.  64-column tiles, two CTAs resident per SM; with few tiles the K range is
