@@ -599,6 +599,13 @@ class Dropout:
         self.ref = ctypes.byref(self.c)
 
 
+def _on_stream(stream):
+    """Makes `stream` (torch.cuda.Stream or handle) current: what a call allocates then belongs to the stream that it
+    runs on, so that neither a workspace that it drops nor an output's earlier owner can still be in use there."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(_stream(stream)))
+
+
 def _stream_type(t: torch.Tensor, name: str) -> int:
     st = _STREAM_TYPES.get(t.dtype)
     if st is None:
@@ -610,23 +617,29 @@ def dropout_forward(x: torch.Tensor, dropout: Dropout, residual: torch.Tensor | 
                     out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """residual + dropout(x): x bf16, residual bf16 or fp32 of x's shape; out of the residual's type
     (bf16 without one).  The number of values is a multiple of 8."""
+    if stream is not None:
+        with _on_stream(stream):
+            return dropout_forward(x, dropout, residual, out)
     like = residual if residual is not None else x
     if out is None:
         out = torch.empty_like(like)
     st = _stream_type(like, "residual")
     _check(_lib.mok_dropout_forward(x.numel(), st, dropout.ref, _ptr(x, torch.bfloat16, "x"),
                                     _arg(residual, x.shape, like.dtype, "residual"),
-                                    _arg(out, x.shape, like.dtype, "out"), _stream(stream)), "mok_dropout_forward")
+                                    _arg(out, x.shape, like.dtype, "out"), _stream(None)), "mok_dropout_forward")
     return out
 
 
 def dropout_backward(dout: torch.Tensor, dropout: Dropout, dx: torch.Tensor | None = None,
                      stream=None) -> torch.Tensor:
     """The branch's gradient (bf16) for dout of the stream's type, under the forward's masks."""
+    if stream is not None:
+        with _on_stream(stream):
+            return dropout_backward(dout, dropout, dx)
     if dx is None:
         dx = torch.empty(dout.shape, dtype=torch.bfloat16, device=dout.device)
     _check(_lib.mok_dropout_backward(dout.numel(), _stream_type(dout, "dout"), dropout.ref, _ptr(dout, None, "dout"),
-                                     _arg(dx, dout.shape, torch.bfloat16, "dx"), _stream(stream)),
+                                     _arg(dx, dout.shape, torch.bfloat16, "dx"), _stream(None)),
            "mok_dropout_backward")
     return dx
 
@@ -645,6 +658,9 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
     """h = residual + dropout(x) and its root-mean-square norm times weight (mok_rmsnorm_forward):
     x [T, H] bf16, residual [T, H] bf16 or fp32 (the type of h), weight [H] bf16.  bf16 / mx choose the
     outputs.  Without residual and dropout h is x."""
+    if stream is not None:
+        with _on_stream(stream):
+            return rmsnorm_forward(x, weight, eps, residual, dropout, bf16, mx)
     T, H = x.shape
     like = residual if residual is not None else x
     st = _stream_type(like, "residual")
@@ -660,7 +676,7 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
                                     dropout.ref if dropout is not None else None,
                                     _arg(weight, (H,), torch.bfloat16, "weight"), None if h is None else h.data_ptr(),
                                     None if y is None else y.data_ptr(), None if q is None else q.data_ptr(),
-                                    None if s is None else s.data_ptr(), rstd.data_ptr(), _stream(stream)),
+                                    None if s is None else s.data_ptr(), rstd.data_ptr(), _stream(None)),
            "mok_rmsnorm_forward")
     return NormOut(x if h is None else h, y, q, s, rstd)
 
@@ -690,6 +706,9 @@ def rmsnorm_backward(h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, 
                      dres: torch.Tensor | None = None, dropout: Dropout | None = None, stream=None) -> NormGrads:
     """Gradients of rmsnorm_forward from dy [T, H] bf16 = dL/dy and dres = dL/dh from the stream's other
     uses (h's type, or None), under the forward's masks."""
+    if stream is not None:
+        with _on_stream(stream):
+            return rmsnorm_backward(h, rstd, weight, dy, dres, dropout)
     T, H = h.shape
     dev = h.device
     shape, ws_bytes = _norm_bwd_plan(T, H, _stream_type(h, "h"))
@@ -703,7 +722,7 @@ def rmsnorm_backward(h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, 
                                      _arg(dy, h.shape, torch.bfloat16, "dy"), _arg(dres, h.shape, h.dtype, "dres"),
                                      dropout.ref if dropout is not None else None, dh.data_ptr(),
                                      None if dx is None else dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws_bytes,
-                                     _stream(stream)), "mok_rmsnorm_backward")
+                                     _stream(None)), "mok_rmsnorm_backward")
     return NormGrads(dh, dh if dx is None else dx, dw)
 
 

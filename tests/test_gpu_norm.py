@@ -255,3 +255,30 @@ def test_side_stream_repeats_and_offsets_past_32_bits(mok):
     again = mok.rmsnorm_backward(o.h, o.rstd, w, x, dropout=drop)
     assert torch.equal(again.dweight, g.dweight) and torch.equal(again.dx, g.dx) and torch.equal(again.dh, g.dh)
     assert np.isfinite(g.dweight.double().sum().item())
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_a_given_stream_owns_what_the_call_allocates(mok, handle, monkeypatch):
+    d = draw(300, 1032, BF, 9)
+    c = {k: v.cuda() for k, v in d.items()}
+    drop = mok.Dropout(0.1, rng_state())
+    want = mok.rmsnorm_forward(c["x"], c["w"], 1e-6, residual=c["res"], dropout=drop)
+    wg = mok.rmsnorm_backward(want.h, want.rstd, c["w"], c["dy"], dres=c["dres"], dropout=drop)
+    wd, wb = mok.dropout_forward(c["x"], drop, residual=c["res"]), mok.dropout_backward(c["dres"], drop)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    seen = []
+    for name in ("empty", "empty_like"):
+        make = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, _make=make, **k: (
+            seen.append(torch.cuda.current_stream().cuda_stream), _make(*a, **k))[1])
+    s = side.cuda_stream if handle else side
+    o = mok.rmsnorm_forward(c["x"], c["w"], 1e-6, residual=c["res"], dropout=drop, stream=s)
+    g = mok.rmsnorm_backward(want.h, want.rstd, c["w"], c["dy"], dres=c["dres"], dropout=drop, stream=s)
+    f, b = mok.dropout_forward(c["x"], drop, residual=c["res"], stream=s), mok.dropout_backward(c["dres"], drop, stream=s)
+    assert len(seen) == 9 and set(seen) == {side.cuda_stream}  # h, y, rstd; dh, dx, dweight, workspace; out; dx
+    assert torch.cuda.current_stream() != side
+    torch.cuda.synchronize()
+    assert torch.equal(o.h, want.h) and torch.equal(o.y, want.y) and torch.equal(o.rstd, want.rstd)
+    assert torch.equal(g.dh, wg.dh) and torch.equal(g.dx, wg.dx) and torch.equal(g.dweight, wg.dweight)
+    assert torch.equal(f, wd) and torch.equal(b, wb)
