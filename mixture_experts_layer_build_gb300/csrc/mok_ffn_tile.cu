@@ -433,11 +433,12 @@ int launch_var(int64_t M, int64_t N, int64_t K, int split, const FfnOperands& o,
 }
 
 // Columns of a tile and CTAs per tile.  64-column tiles, two CTAs resident per SM; with few tiles the K range is
-// split over a cluster of 2, 4 or 8 while there are at most two CTAs per SM and each keeps four K blocks or
-// more; from six rounds of tiles on, 128 columns.  What a split costs is its partials, so with the rows: above 32
-// tokens clusters of four at most, above 64 eight K blocks at least.  Measured, both forward contractions: H =
-// 1000, I = 2000, 5 tokens: 9.7 us with clusters of eight allowed, 10.5 without; 128 tokens 19.8 and 18.1, and 13.6
-// with eight K blocks at least; H = 4096, I = 1536, 61 tokens 16.3 with four K blocks at least, 17.1 with eight.
+// split over a cluster of 2, 4 or 8 while there are at most two CTAs per SM; from six rounds of tiles on, 128
+// columns.  What a split costs is its partials, so with the rows: up to 24 tokens each CTA keeps two K blocks or more, up
+// to 64 four, above eight, and above 32 tokens clusters of four at most.  Measured, both forward contractions: H =
+// I = 640, 16 tokens 7.0 us with two K blocks at least, 8.0 with four; H = I = 1000, 32 tokens 9.0 and 8.5; H = 4096,
+// I = 1536, 61 tokens 16.3 with four at least, 17.1 with eight; H = 1000, I = 2000, 5 tokens 9.7 with clusters of
+// eight allowed, 10.5 without; 128 tokens 19.8 and 18.1, and 13.6 with eight K blocks at least.
 // (Clusters of 3, 5 or 6 leave SMs of a GPC without one.)
 template <int VAR>
 int launch_tiles(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& f, cudaStream_t stream) {
@@ -448,7 +449,8 @@ int launch_tiles(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const Ff
   if (tiles(64 / kPer) > 6 * sms) return launch_var<VAR, 128>(M, N, K, 1, o, f, stream);
   const int64_t kb = (K + kFfnBK - 1) / kFfnBK * (VAR == F_DX ? 2 : 1);
   int64_t split = 2 * sms / tiles(64 / kPer);
-  if (split > kb / (M > 64 ? 8 : 4)) split = kb / (M > 64 ? 8 : 4);
+  const int64_t least = M > 64 ? 8 : M > 24 ? 4 : 2;  // K blocks per CTA
+  if (split > kb / least) split = kb / least;
   split = split >= 8 && M <= 32 ? 8 : split >= 4 ? 4 : split >= 2 ? 2 : 1;
   return launch_var<VAR, 64>(M, N, K, static_cast<int>(split), o, f, stream);
 }
