@@ -1,4 +1,5 @@
-"""Build ``libmok.so`` in-tree with nvcc for sm_103a (one -gencode, translation units in parallel)."""
+"""Build ``libmok.so`` in-tree with nvcc for sm_103a (one -gencode, translation units in parallel), and the compiled
+part of the Python binding, ``_mok_bind.so``, with g++."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -12,6 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmok.so")
+BIND = os.path.join(HERE, "_mok_bind.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -28,6 +30,22 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _bind_commands() -> list:
+    """[compile, link] of _mok_bind.so against this machine's torch; it finds libmok.so beside it."""
+    import importlib.util
+    import sysconfig
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    obj = os.path.join(BUILD, "mok_bind.o")
+    inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    cxx = os.environ.get("CXX", "g++")
+    return [[cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{i}" for i in inc), "-c",
+             os.path.join(CSRC, "mok_bind.cpp"), "-o", obj],
+            [cxx, "-shared", obj, "-o", BIND + f".tmp{os.getpid()}", f"-L{HERE}", "-l:libmok.so", "-Wl,-rpath,$ORIGIN",
+             f"-L{os.path.join(torch, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]]
+
+
 def build(verbose: bool = False, extra=None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
@@ -38,6 +56,9 @@ def build(verbose: bool = False, extra=None) -> str:
         o = os.path.join(BUILD, src.replace(".cu", ".o"))
         if _stale(o, [s, *headers, __file__]):
             jobs.append([NVCC, *ARCH, *FLAGS, *(extra or []), "-c", s, "-o", o])
+    compile_bind, link_bind = _bind_commands()
+    if _stale(compile_bind[-1], [compile_bind[-3], headers[-1], __file__]):
+        jobs.append(compile_bind)
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
             res = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs))
@@ -45,7 +66,7 @@ def build(verbose: bool = False, extra=None) -> str:
             if verbose or r.returncode:
                 sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             if r.returncode:
-                raise RuntimeError(f"nvcc failed on {cmd[-3]}")
+                raise RuntimeError(f"the compiler failed on {cmd[-3]}")
     objs = [os.path.join(BUILD, s.replace(".cu", ".o")) for s in SOURCES]
     if jobs or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
@@ -56,6 +77,12 @@ def build(verbose: bool = False, extra=None) -> str:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of libmok.so failed")
         os.replace(tmp, LIB)
+    if _stale(BIND, [compile_bind[-1]]):
+        r = subprocess.run(link_bind, capture_output=True, text=True)
+        if r.returncode:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("link of _mok_bind.so failed")
+        os.replace(BIND + f".tmp{os.getpid()}", BIND)
     return LIB
 
 

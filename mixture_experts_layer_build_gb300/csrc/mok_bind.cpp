@@ -1,0 +1,196 @@
+// mok_bind.cpp -- the norm and dropout calls of the Python binding: checks, outputs and the C call in one step.
+//
+// These calls allocate what they return, and at small sizes the host is what bounds them: three tensors made one by
+// one from Python and a call with eleven arguments through ctypes took 15.3 us for a kernel of 1.6.  Each function
+// returns its tensors in a tuple; the mok_status as an int when the library refuses; None when a tensor is not what
+// it has to be, which the caller then names.
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "mok.h"
+
+namespace {
+
+using at::Tensor;
+
+// A tensor argument, or nullptr for None; false when it is neither.
+bool tensor_arg(PyObject* o, const Tensor** t) {
+  *t = nullptr;
+  if (o == Py_None) return true;
+  if (!THPVariable_Check(o)) return false;
+  *t = &THPVariable_Unpack(o);
+  return true;
+}
+
+bool plain(const Tensor& t) { return t.is_cuda() && t.is_contiguous(); }
+bool plain(const Tensor& t, at::ScalarType type) { return plain(t) && t.scalar_type() == type; }
+bool like(const Tensor& t, const Tensor& other, at::ScalarType type) {
+  return plain(t, type) && t.sizes() == other.sizes();
+}
+bool vec(const Tensor& t, int64_t n, at::ScalarType type) { return plain(t, type) && t.dim() == 1 && t.size(0) == n; }
+
+// mok_dtype of a residual stream, or -1.
+int stream_type(const Tensor& t) {
+  return t.scalar_type() == at::kBFloat16 ? MOK_DT_BF16 : t.scalar_type() == at::kFloat ? MOK_DT_FP32 : -1;
+}
+
+void* ptr(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
+void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+void* current_stream(const Tensor& t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
+Tensor make(at::IntArrayRef shape, const Tensor& on, at::ScalarType type) {
+  return at::empty(shape, on.options().dtype(type).requires_grad(false));
+}
+
+const mok_dropout* drop_arg(PyObject* o) {
+  return o == Py_None ? nullptr : static_cast<const mok_dropout*>(PyLong_AsVoidPtr(o));
+}
+
+PyObject* wrap(const Tensor& t) {
+  if (t.defined()) return THPVariable_Wrap(t);
+  Py_RETURN_NONE;
+}
+template <size_t N>
+PyObject* wrap_all(const Tensor (&t)[N]) {
+  PyObject* r = PyTuple_New(N);
+  for (size_t i = 0; r && i < N; ++i) {
+    PyObject* o = wrap(t[i]);
+    if (!o) {
+      Py_DECREF(r);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(r, i, o);
+  }
+  return r;
+}
+
+template <class F>
+PyObject* guarded(F&& f) {  // no C++ exception leaves (an allocation may fail)
+  try {
+    return f();
+  } catch (const c10::OutOfMemoryError& e) {
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    Py_XDECREF(torch);
+    if (type) PyErr_SetString(type, e.what());  // (else the lookup's error stands)
+    Py_XDECREF(type);
+  } catch (const std::exception& e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+// (x, weight, eps, residual, dropout, bf16, mx) -> (h or None: x, y, q, s, rstd)
+PyObject* rmsnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor *x, *w, *res;
+    if (n != 7 || !tensor_arg(a[0], &x) || !tensor_arg(a[1], &w) || !tensor_arg(a[3], &res) || !x || !w || x->dim() != 2)
+      Py_RETURN_NONE;
+    const int64_t T = x->size(0), H = x->size(1);
+    const Tensor& stream = res ? *res : *x;
+    const int st = stream_type(stream);
+    if (st < 0 || !plain(*x, at::kBFloat16) || !like(stream, *x, stream.scalar_type()) || !vec(*w, H, at::kBFloat16) ||
+        H > INT32_MAX)
+      Py_RETURN_NONE;
+    const double eps = PyFloat_AsDouble(a[2]);
+    const mok_dropout* drop = drop_arg(a[4]);
+    const int bf16 = PyObject_IsTrue(a[5]), mx = PyObject_IsTrue(a[6]);
+    if (PyErr_Occurred()) return nullptr;
+    const c10::cuda::CUDAGuard guard(x->device());
+    Tensor out[5];
+    if (res || drop) out[0] = make({T, H}, *x, stream.scalar_type());
+    if (bf16) out[1] = make({T, H}, *x, at::kBFloat16);
+    if (mx) {
+      out[2] = make({T, H}, *x, at::kByte);
+      out[3] = make({T, H / 32}, *x, at::kByte);
+    }
+    out[4] = make({T}, *x, at::kFloat);
+    const mok_norm_shape shape{T, static_cast<int32_t>(H), st, static_cast<float>(eps)};
+    const int rc = mok_rmsnorm_forward(&shape, x->data_ptr(), ptr(res), drop, w->data_ptr(), ptr(out[0]), ptr(out[1]),
+                                       static_cast<uint8_t*>(ptr(out[2])), static_cast<uint8_t*>(ptr(out[3])),
+                                       static_cast<float*>(ptr(out[4])), current_stream(*x));
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+// (h, rstd, weight, dy, dres, dropout) -> (dh, dx or None: dh, dweight)
+PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor *h, *rstd, *w, *dy, *dres;
+    if (n != 6 || !tensor_arg(a[0], &h) || !tensor_arg(a[1], &rstd) || !tensor_arg(a[2], &w) || !tensor_arg(a[3], &dy) ||
+        !tensor_arg(a[4], &dres) || !h || !rstd || !w || !dy || h->dim() != 2)
+      Py_RETURN_NONE;
+    const int64_t T = h->size(0), H = h->size(1);
+    const int st = stream_type(*h);
+    if (st < 0 || !plain(*h) || !vec(*rstd, T, at::kFloat) || !vec(*w, H, at::kBFloat16) ||
+        !like(*dy, *h, at::kBFloat16) || (dres && !like(*dres, *h, h->scalar_type())) || H > INT32_MAX)
+      Py_RETURN_NONE;
+    const mok_dropout* drop = drop_arg(a[5]);
+    if (PyErr_Occurred()) return nullptr;
+    const mok_norm_shape shape{T, static_cast<int32_t>(H), st, 0.0f};
+    const size_t bytes = mok_rmsnorm_workspace_bytes(&shape);
+    if (!bytes) return PyLong_FromLong(MOK_ERR_INVALID_ARG);
+    const c10::cuda::CUDAGuard guard(h->device());
+    Tensor out[3];
+    out[0] = make({T, H}, *h, h->scalar_type());
+    if (drop || st != MOK_DT_BF16) out[1] = make({T, H}, *h, at::kBFloat16);
+    out[2] = make({H}, *h, at::kFloat);
+    const Tensor ws = make({static_cast<int64_t>(bytes)}, *h, at::kByte);
+    const int rc = mok_rmsnorm_backward(&shape, h->data_ptr(), static_cast<const float*>(rstd->data_ptr()), w->data_ptr(),
+                                        dy->data_ptr(), ptr(dres), drop, ptr(out[0]), ptr(out[1]),
+                                        static_cast<float*>(ptr(out[2])), ws.data_ptr(), bytes, current_stream(*h));
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+// (x, dropout, residual, out) -> (out,)
+PyObject* dropout_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor *x, *res, *given;
+    if (n != 4 || !tensor_arg(a[0], &x) || !tensor_arg(a[2], &res) || !tensor_arg(a[3], &given) || !x) Py_RETURN_NONE;
+    const Tensor& stream = res ? *res : *x;
+    const int st = stream_type(stream);
+    if (st < 0 || !plain(*x, at::kBFloat16) || !like(stream, *x, stream.scalar_type()) ||
+        (given && !like(*given, *x, stream.scalar_type())))
+      Py_RETURN_NONE;
+    const mok_dropout* drop = drop_arg(a[1]);
+    if (PyErr_Occurred()) return nullptr;
+    const c10::cuda::CUDAGuard guard(x->device());
+    const Tensor out[1] = {given ? *given : make(x->sizes(), *x, stream.scalar_type())};
+    const int rc = mok_dropout_forward(x->numel(), st, drop, x->data_ptr(), ptr(res), ptr(out[0]), current_stream(*x));
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+// (dout, dropout, dx) -> (dx,)
+PyObject* dropout_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor *dout, *given;
+    if (n != 3 || !tensor_arg(a[0], &dout) || !tensor_arg(a[2], &given) || !dout) Py_RETURN_NONE;
+    const int st = stream_type(*dout);
+    if (st < 0 || !plain(*dout) || (given && !like(*given, *dout, at::kBFloat16))) Py_RETURN_NONE;
+    const mok_dropout* drop = drop_arg(a[1]);
+    if (PyErr_Occurred()) return nullptr;
+    const c10::cuda::CUDAGuard guard(dout->device());
+    const Tensor out[1] = {given ? *given : make(dout->sizes(), *dout, at::kBFloat16)};
+    const int rc = mok_dropout_backward(dout->numel(), st, drop, dout->data_ptr(), ptr(out[0]), current_stream(*dout));
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyMethodDef method(const char* name) {
+  return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
+}
+PyMethodDef methods[] = {method<rmsnorm_forward>("rmsnorm_forward"), method<rmsnorm_backward>("rmsnorm_backward"),
+                         method<dropout_forward>("dropout_forward"), method<dropout_backward>("dropout_backward"),
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_mok_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__mok_bind() { return PyModule_Create(&module_def); }

@@ -12,7 +12,6 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from functools import lru_cache
 
 import torch
 
@@ -23,6 +22,7 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libmok.so not found at {LIB_PATH}; build it with __graft_entry__.build() "
                       "(nvcc, sm_103a). There is no CPU fallback.")
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _mok_bind as _bind  # noqa: E402  (built beside libmok.so, which it calls)
 
 MOK_OK = 0
 MOK_ERR_INVALID_ARG = 1
@@ -597,6 +597,19 @@ class Dropout:
         self.rng = rng  # kept alive with the pointer
         self.c = mok_dropout(p, _arg(rng, (2,), torch.int64, "rng"))
         self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self.c)
+
+
+def _refused(result, where: str, *args):
+    """Raises for what a compiled call returned instead of its tensors: the library's status, or None for a tensor
+    that is not what it has to be.  args: (tensor, shape, dtype, name) in the order of the call's checks."""
+    if result is not None:
+        raise MokError(result, where)
+    for t, shape, dtype, name in args:
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
+        _arg(t, t.shape if shape is None else shape, dtype, name)
+    raise ValueError(f"{where}: unsupported arguments")
 
 
 def _on_stream(stream):
@@ -620,14 +633,13 @@ def dropout_forward(x: torch.Tensor, dropout: Dropout, residual: torch.Tensor | 
     if stream is not None:
         with _on_stream(stream):
             return dropout_forward(x, dropout, residual, out)
-    like = residual if residual is not None else x
-    if out is None:
-        out = torch.empty_like(like)
-    st = _stream_type(like, "residual")
-    _check(_lib.mok_dropout_forward(x.numel(), st, dropout.ref, _ptr(x, torch.bfloat16, "x"),
-                                    _arg(residual, x.shape, like.dtype, "residual"),
-                                    _arg(out, x.shape, like.dtype, "out"), _stream(None)), "mok_dropout_forward")
-    return out
+    r = _bind.dropout_forward(x, dropout.addr, residual, out)
+    if type(r) is not tuple:
+        like = x if residual is None else residual
+        _stream_type(like, "residual")
+        _refused(r, "mok_dropout_forward", (x, None, torch.bfloat16, "x"), (like, x.shape, None, "residual"),
+                 *(() if out is None else ((out, x.shape, like.dtype, "out"),)))
+    return r[0]
 
 
 def dropout_backward(dout: torch.Tensor, dropout: Dropout, dx: torch.Tensor | None = None,
@@ -636,12 +648,12 @@ def dropout_backward(dout: torch.Tensor, dropout: Dropout, dx: torch.Tensor | No
     if stream is not None:
         with _on_stream(stream):
             return dropout_backward(dout, dropout, dx)
-    if dx is None:
-        dx = torch.empty(dout.shape, dtype=torch.bfloat16, device=dout.device)
-    _check(_lib.mok_dropout_backward(dout.numel(), _stream_type(dout, "dout"), dropout.ref, _ptr(dout, None, "dout"),
-                                     _arg(dx, dout.shape, torch.bfloat16, "dx"), _stream(None)),
-           "mok_dropout_backward")
-    return dx
+    r = _bind.dropout_backward(dout, dropout.addr, dx)
+    if type(r) is not tuple:
+        _stream_type(dout, "dout")
+        _refused(r, "mok_dropout_backward", (dout, None, None, "dout"),
+                 *(() if dx is None else ((dx, dout.shape, torch.bfloat16, "dx"),)))
+    return r[0]
 
 
 @dataclass
@@ -661,23 +673,14 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
     if stream is not None:
         with _on_stream(stream):
             return rmsnorm_forward(x, weight, eps, residual, dropout, bf16, mx)
-    T, H = x.shape
-    like = residual if residual is not None else x
-    st = _stream_type(like, "residual")
-    dev = x.device
-    h = torch.empty_like(like) if residual is not None or dropout is not None else None
-    y = torch.empty_like(x) if bf16 else None
-    q = torch.empty((T, H), dtype=torch.uint8, device=dev) if mx else None
-    s = torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if mx else None
-    rstd = torch.empty((T,), dtype=torch.float32, device=dev)
-    shape = mok_norm_shape(T, H, st, eps)
-    _check(_lib.mok_rmsnorm_forward(ctypes.byref(shape), _ptr(x, torch.bfloat16, "x"),
-                                    _arg(residual, x.shape, like.dtype, "residual"),
-                                    dropout.ref if dropout is not None else None,
-                                    _arg(weight, (H,), torch.bfloat16, "weight"), None if h is None else h.data_ptr(),
-                                    None if y is None else y.data_ptr(), None if q is None else q.data_ptr(),
-                                    None if s is None else s.data_ptr(), rstd.data_ptr(), _stream(None)),
-           "mok_rmsnorm_forward")
+    r = _bind.rmsnorm_forward(x, weight, eps, residual, None if dropout is None else dropout.addr, bf16, mx)
+    if type(r) is not tuple:
+        like = x if residual is None else residual
+        _stream_type(like, "residual")
+        T, H = x.shape
+        _refused(r, "mok_rmsnorm_forward", (x, None, torch.bfloat16, "x"), (like, x.shape, None, "residual"),
+                 (weight, (H,), torch.bfloat16, "weight"))
+    h, y, q, s, rstd = r
     return NormOut(x if h is None else h, y, q, s, rstd)
 
 
@@ -695,13 +698,6 @@ def mok_rmsnorm_workspace_bytes(shape: mok_norm_shape) -> int:
     return n
 
 
-@lru_cache(maxsize=256)
-def _norm_bwd_plan(T: int, H: int, stream_type: int):
-    """(reference to the shape, workspace bytes): 1.8 us of a call's 22 on the host."""
-    shape = mok_norm_shape(T, H, stream_type, 0.0)
-    return ctypes.byref(shape), mok_rmsnorm_workspace_bytes(shape)
-
-
 def rmsnorm_backward(h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
                      dres: torch.Tensor | None = None, dropout: Dropout | None = None, stream=None) -> NormGrads:
     """Gradients of rmsnorm_forward from dy [T, H] bf16 = dL/dy and dres = dL/dh from the stream's other
@@ -709,20 +705,14 @@ def rmsnorm_backward(h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, 
     if stream is not None:
         with _on_stream(stream):
             return rmsnorm_backward(h, rstd, weight, dy, dres, dropout)
-    T, H = h.shape
-    dev = h.device
-    shape, ws_bytes = _norm_bwd_plan(T, H, _stream_type(h, "h"))
-    dh = torch.empty_like(h)
-    own_dx = dropout is not None or h.dtype != torch.bfloat16
-    dx = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if own_dx else None
-    dw = torch.empty((H,), dtype=torch.float32, device=dev)
-    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    _check(_lib.mok_rmsnorm_backward(shape, _ptr(h, None, "h"), _arg(rstd, (T,), torch.float32, "rstd"),
-                                     _arg(weight, (H,), torch.bfloat16, "weight"),
-                                     _arg(dy, h.shape, torch.bfloat16, "dy"), _arg(dres, h.shape, h.dtype, "dres"),
-                                     dropout.ref if dropout is not None else None, dh.data_ptr(),
-                                     None if dx is None else dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws_bytes,
-                                     _stream(None)), "mok_rmsnorm_backward")
+    r = _bind.rmsnorm_backward(h, rstd, weight, dy, dres, None if dropout is None else dropout.addr)
+    if type(r) is not tuple:
+        _stream_type(h, "h")
+        T, H = h.shape
+        _refused(r, "mok_rmsnorm_backward", (h, None, None, "h"), (rstd, (T,), torch.float32, "rstd"),
+                 (weight, (H,), torch.bfloat16, "weight"), (dy, h.shape, torch.bfloat16, "dy"),
+                 *(() if dres is None else ((dres, h.shape, h.dtype, "dres"),)))
+    dh, dx, dw = r
     return NormGrads(dh, dh if dx is None else dx, dw)
 
 

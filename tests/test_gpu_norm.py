@@ -258,7 +258,7 @@ def test_side_stream_repeats_and_offsets_past_32_bits(mok):
 
 
 @pytest.mark.parametrize("handle", [False, True])
-def test_a_given_stream_owns_what_the_call_allocates(mok, handle, monkeypatch):
+def test_a_given_stream_owns_what_the_call_allocates(mok, handle):
     d = draw(300, 1032, BF, 9)
     c = {k: v.cuda() for k, v in d.items()}
     drop = mok.Dropout(0.1, rng_state())
@@ -267,18 +267,50 @@ def test_a_given_stream_owns_what_the_call_allocates(mok, handle, monkeypatch):
     wd, wb = mok.dropout_forward(c["x"], drop, residual=c["res"]), mok.dropout_backward(c["dres"], drop)
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
-    seen = []
-    for name in ("empty", "empty_like"):
-        make = getattr(torch, name)
-        monkeypatch.setattr(torch, name, lambda *a, _make=make, **k: (
-            seen.append(torch.cuda.current_stream().cuda_stream), _make(*a, **k))[1])
     s = side.cuda_stream if handle else side
     o = mok.rmsnorm_forward(c["x"], c["w"], 1e-6, residual=c["res"], dropout=drop, stream=s)
     g = mok.rmsnorm_backward(want.h, want.rstd, c["w"], c["dy"], dres=c["dres"], dropout=drop, stream=s)
     f, b = mok.dropout_forward(c["x"], drop, residual=c["res"], stream=s), mok.dropout_backward(c["dres"], drop, stream=s)
-    assert len(seen) == 9 and set(seen) == {side.cuda_stream}  # h, y, rstd; dh, dx, dweight, workspace; out; dx
     assert torch.cuda.current_stream() != side
+    pools = torch.cuda.memory_snapshot()  # each segment with the stream that owns it
+    for t in (o.h, o.y, o.rstd, g.dh, g.dx, g.dweight, f, b):
+        owner = [p["stream"] for p in pools if p["address"] <= t.data_ptr() < p["address"] + p["total_size"]]
+        assert owner == [side.cuda_stream]
     torch.cuda.synchronize()
     assert torch.equal(o.h, want.h) and torch.equal(o.y, want.y) and torch.equal(o.rstd, want.rstd)
     assert torch.equal(g.dh, wg.dh) and torch.equal(g.dx, wg.dx) and torch.equal(g.dweight, wg.dweight)
     assert torch.equal(f, wd) and torch.equal(b, wb)
+
+
+def test_wrong_tensors_are_named(mok):
+    d = draw(16, 64, BF, 2)
+    c = {k: v.cuda() for k, v in d.items()}
+    x, res, w, dy = c["x"], c["res"], c["w"], c["dy"]
+    drop = mok.Dropout(0.1, rng_state())
+    rstd = torch.ones(16, device="cuda")
+    turned = x.t().contiguous().t()
+    for bad, name in ((dict(x=turned), "x"), (dict(x=x.float()), "x"), (dict(x=x.cpu()), "x"), (dict(weight=w[:32]), "weight"),
+                      (dict(weight=w.float()), "weight"), (dict(residual=res[:8]), "residual"),
+                      (dict(residual=res.half()), "residual"), (dict(residual=turned), "residual"), (dict(weight=None), "weight")):
+        with pytest.raises(ValueError, match=name):
+            mok.rmsnorm_forward(**{**dict(x=x, weight=w, eps=1e-6, residual=res), **bad})
+    for bad, name in ((dict(h=x.half()), "h"), (dict(rstd=rstd[:8]), "rstd"), (dict(rstd=rstd.double()), "rstd"),
+                      (dict(weight=w.float()), "weight"), (dict(dy=turned), "dy"), (dict(dy=dy.float()), "dy"),
+                      (dict(dres=dy.float()), "dres"), (dict(h=turned), "h")):
+        with pytest.raises(ValueError, match=name):
+            mok.rmsnorm_backward(**{**dict(h=x, rstd=rstd, weight=w, dy=dy, dres=res), **bad})
+    for call in (lambda: mok.dropout_forward(x.float(), drop), lambda: mok.dropout_forward(x, drop, residual=res[:8]),
+                 lambda: mok.dropout_forward(x, drop, out=torch.empty_like(x, dtype=F32)),
+                 lambda: mok.dropout_backward(x.half(), drop), lambda: mok.dropout_backward(x, drop, dx=res.float()),
+                 lambda: mok.rmsnorm_forward(x.view(-1), w, 1e-6)):
+        with pytest.raises(ValueError):
+            call()
+    odd = torch.zeros((4, 68), dtype=BF, device="cuda")
+    for call in (lambda: mok.rmsnorm_forward(odd, odd[0].clone(), 1e-6), lambda: mok.rmsnorm_forward(x, w, float("nan")),
+                 lambda: mok.rmsnorm_forward(c["x"][:, :40].contiguous(), w[:40].clone(), 1e-6, mx=True),
+                 lambda: mok.rmsnorm_backward(odd, rstd[:4].clone(), odd[0].clone(), odd),
+                 lambda: mok.dropout_forward(torch.zeros(12, dtype=BF, device="cuda"), drop)):
+        with pytest.raises(mok.MokError):
+            call()
+    with pytest.raises(TypeError):
+        mok.rmsnorm_forward(x, w, "eps")
