@@ -1,9 +1,10 @@
-// mok_bind.cpp -- the norm and dropout calls of the Python binding: checks, outputs and the C call in one step.
+// mok_bind.cpp -- the norm, dropout and feed-forward calls of the Python binding: checks, outputs and the C call in one
+// step.
 //
-// These calls allocate what they return, and at small sizes the host is what bounds them: three tensors made one by
-// one from Python and a call with eleven arguments through ctypes took 15.3 us for a kernel of 1.6.  Each function
-// returns its tensors in a tuple; the mok_status as an int when the library refuses; None when a tensor is not what
-// it has to be, which the caller then names.
+// At small sizes the host is what bounds these calls: three tensors made one by one from Python and a call with eleven
+// arguments through ctypes took 15.3 us for a norm kernel of 1.6, now 6.4.  Each function returns its tensors in a
+// tuple (feed-forward: an empty one); the mok_status as an int when the library refuses; None when a tensor is not
+// what it has to be, which the caller then names.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -182,12 +183,44 @@ PyObject* dropout_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+bool mat(const Tensor& t, int64_t rows, int64_t cols) {
+  return plain(t, at::kBFloat16) && t.dim() == 2 && t.size(0) == rows && t.size(1) == cols;
+}
+
+// (shape, out, ctx, ctx bytes, save, status: the plan's addresses and sizes, x, w_gate, w_up, w_down, residual, stream
+// or None: the current one) -> ()
+PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor *x, *wg, *wu, *wd, *res;
+    if (n != 12 || !tensor_arg(a[6], &x) || !tensor_arg(a[7], &wg) || !tensor_arg(a[8], &wu) || !tensor_arg(a[9], &wd) ||
+        !tensor_arg(a[10], &res) || !x || !wg || !wu || !wd)
+      Py_RETURN_NONE;
+    const mok_ffn_shape* s = static_cast<const mok_ffn_shape*>(PyLong_AsVoidPtr(a[0]));
+    void* out = PyLong_AsVoidPtr(a[1]);
+    void* ctx = PyLong_AsVoidPtr(a[2]);
+    const size_t bytes = PyLong_AsSize_t(a[3]);
+    const long save = PyLong_AsLong(a[4]);
+    uint32_t* status = static_cast<uint32_t*>(PyLong_AsVoidPtr(a[5]));
+    if (PyErr_Occurred()) return nullptr;
+    if (!mat(*x, s->T, s->H) || !mat(*wg, s->I, s->H) || !mat(*wu, s->I, s->H) || !mat(*wd, s->H, s->I) ||
+        (res && !mat(*res, s->T, s->H)))
+      Py_RETURN_NONE;
+    void* stream = a[11] == Py_None ? current_stream(*x) : PyLong_AsVoidPtr(a[11]);
+    if (PyErr_Occurred()) return nullptr;
+    const c10::cuda::CUDAGuard guard(x->device());
+    const int rc = mok_ffn_forward(s, x->data_ptr(), wg->data_ptr(), wu->data_ptr(), wd->data_ptr(), ptr(res), out, ctx,
+                                   bytes, static_cast<int32_t>(save), status, stream);
+    return rc ? PyLong_FromLong(rc) : PyTuple_New(0);
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {method<rmsnorm_forward>("rmsnorm_forward"), method<rmsnorm_backward>("rmsnorm_backward"),
                          method<dropout_forward>("dropout_forward"), method<dropout_backward>("dropout_backward"),
+                         method<ffn_forward>("ffn_forward"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_mok_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

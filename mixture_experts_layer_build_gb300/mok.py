@@ -757,8 +757,8 @@ class FFN:
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
         self.status = torch.zeros((1,), dtype=torch.int32, device=device)
         self._ref = ctypes.byref(self.shape)
-        self._fwd_ptrs = (self.out.data_ptr(), self.ctx.data_ptr(), self.ctx.numel(), 1 if train else 0,
-                          self.status.data_ptr())
+        self._fwd = (ctypes.addressof(self.shape), self.out.data_ptr(), self.ctx.data_ptr(), self.ctx.numel(),
+                     1 if train else 0, self.status.data_ptr())
         if train:
             e = lambda *s: torch.empty(s, dtype=dw_dtype, device=device)  # noqa: E731
             self.grads = FFNGrads(torch.empty_like(self.out), e(I, H), e(I, H), e(H, I))
@@ -774,10 +774,11 @@ class FFN:
 
     def forward(self, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                 residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-        out, ctx, n, save, status = self._fwd_ptrs
-        _check(_lib.mok_ffn_forward(self._ref, *self._in(x, w_gate, w_up, w_down),
-                                    _arg(residual, (self.T, self.H), torch.bfloat16, "residual"), out, ctx, n, save,
-                                    status, _stream(stream)), "mok_ffn_forward")
+        r = _bind.ffn_forward(*self._fwd, x, w_gate, w_up, w_down, residual, None if stream is None else _stream(stream))
+        if type(r) is not tuple:
+            self._in(x, w_gate, w_up, w_down)
+            _refused(r, "mok_ffn_forward",
+                     *(() if residual is None else ((residual, (self.T, self.H), torch.bfloat16, "residual"),)))
         return self.out
 
     def backward(self, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
