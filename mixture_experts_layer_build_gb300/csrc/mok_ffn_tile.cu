@@ -11,7 +11,9 @@
 // warps 0 and 1 are warp-uniform with one elected lane at each asynchronous instruction (issued from a
 // single-lane branch, a K block took 240 ns to issue whatever its size), the first loads are issued
 // before the CTA's set-up has finished, and the contractions that follow another of this block
-// load their weights before they wait for it.
+// load their weights before they wait for it.  Measured (both forward contractions, weights from HBM): 16 tokens at
+// H = 4096, I = 1536 14.3 us; 61 tokens at H = 7168, I = 2048 24.7 (13.0 of weights: gate/up streams at 7.1 TB/s; the rest
+// is first bytes, reductions and the launch between, when HBM idles).
 #include "mok_ffn.cuh"
 
 namespace mok {

