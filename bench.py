@@ -250,11 +250,12 @@ def _code_only(text: str) -> bytes:
 
 def src_hash() -> str:
     """Hash of the CUDA sources of the layer kernels and the ABI header (code only), keying the
-    stored ncu counters (all of them belong to layer kernels; the router's file is left out)."""
+    stored ncu counters (all of them belong to layer kernels; the router's and the dense operators' files are
+    left out)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "mixture_experts_layer_build_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.endswith((".cu", ".cuh")) and f != "mok_router.cu":
+        if f.endswith((".cu", ".cuh")) and not f.startswith(("mok_router", "mok_norm", "mok_philox", "mok_ffn")):
             h.update(_code_only(open(os.path.join(csrc, f)).read()))
     h.update(_code_only(open(os.path.join(ROOT, "include", "mok.h")).read()))
     return h.hexdigest()[:16]
