@@ -615,8 +615,10 @@ def _refused(result, where: str, *args):
 def _on_stream(stream):
     """Makes `stream` (torch.cuda.Stream or handle) current: what a call allocates then belongs to the stream that it
     runs on, so that neither a workspace that it drops nor an output's earlier owner can still be in use there."""
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
-                             torch.cuda.ExternalStream(_stream(stream)))
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # 0: the default stream, of which ExternalStream makes a new stream of torch's pool
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _stream_type(t: torch.Tensor, name: str) -> int:
