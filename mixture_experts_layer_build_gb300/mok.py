@@ -180,6 +180,15 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on_stream(stream):
+    """Makes `stream` (torch.cuda.Stream or handle) current: what a call allocates then belongs to the stream that it
+    runs on, so that neither a workspace that it drops nor an output's earlier owner can still be in use there."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # 0: the default stream, of which ExternalStream makes a new stream of torch's pool
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _ptr(t: torch.Tensor | None, dtype=None, name="tensor"):
     if t is None:
         return None
@@ -478,13 +487,16 @@ def mok_router_backward(sched: Schedule, x: torch.Tensor, w_router: torch.Tensor
 
 def router_forward(x: torch.Tensor, w_router: torch.Tensor, bias: torch.Tensor | None, K: int, stream=None):
     """Allocating form: returns (logits [T,E] fp32, topk_ids [T,K] int32, topk_weights [T,K] fp32)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return router_forward(x, w_router, bias, K)
     T, H = x.shape
     E = w_router.shape[1]
     shape = make_shape(T, H, 128, E, K)
     logits = torch.empty((T, E), dtype=torch.float32, device=x.device)
     ids = torch.empty((T, K), dtype=torch.int32, device=x.device)
     wts = torch.empty((T, K), dtype=torch.float32, device=x.device)
-    mok_router_forward(shape, x, w_router, bias, logits, ids, wts, stream)
+    mok_router_forward(shape, x, w_router, bias, logits, ids, wts)
     return logits, ids, wts
 
 
@@ -493,6 +505,9 @@ def router_backward(sched: Schedule, x: torch.Tensor, w_router: torch.Tensor, to
                     dx: torch.Tensor | None = None, stream=None):
     """Allocating form: returns (dw_router [H,E] fp32, d_bias [E] fp32 or None, dx [T,H] bf16).  A
     given dx receives the router's share added in place."""
+    if stream is not None:
+        with _on_stream(stream):
+            return router_backward(sched, x, w_router, topk_ids, topk_weights, d_topk_weights, with_bias, dx)
     H, E = w_router.shape
     dw = torch.empty((H, E), dtype=torch.float32, device=x.device)
     db = torch.empty((E,), dtype=torch.float32, device=x.device) if with_bias else None
@@ -500,7 +515,7 @@ def router_backward(sched: Schedule, x: torch.Tensor, w_router: torch.Tensor, to
     if dx is None:
         dx = torch.empty_like(x)
     ws = torch.empty(mok_router_workspace_bytes(sched.c.shape), dtype=torch.uint8, device=x.device)
-    mok_router_backward(sched, x, w_router, topk_ids, topk_weights, d_topk_weights, dw, db, dx, acc, ws, stream)
+    mok_router_backward(sched, x, w_router, topk_ids, topk_weights, d_topk_weights, dw, db, dx, acc, ws)
     return dw, db, dx
 
 
@@ -610,15 +625,6 @@ def _refused(result, where: str, *args):
             raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
         _arg(t, t.shape if shape is None else shape, dtype, name)
     raise ValueError(f"{where}: unsupported arguments")
-
-
-def _on_stream(stream):
-    """Makes `stream` (torch.cuda.Stream or handle) current: what a call allocates then belongs to the stream that it
-    runs on, so that neither a workspace that it drops nor an output's earlier owner can still be in use there."""
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream)  # 0: the default stream, of which ExternalStream makes a new stream of torch's pool
-        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
 
 
 def _stream_type(t: torch.Tensor, name: str) -> int:

@@ -50,6 +50,35 @@ def test_a_handle_stands_for_its_own_stream(mok, monkeypatch, handle):
         assert [s.cuda_stream for s in streams.current] == [handle]
 
 
+class _Recorder:
+    """Stands in for a library call, and notes the stream that is current at it and at each torch.empty before it."""
+
+    def __init__(self, monkeypatch, streams, module, name):
+        self.at = []
+        note = lambda: self.at.append(streams.current[-1].cuda_stream if streams.current else None)  # noqa: E731
+        empty = torch.empty
+
+        def allocate(*a, **k):
+            note()
+            return empty(*a, **k)
+        monkeypatch.setattr(torch, "empty", allocate)
+        monkeypatch.setattr(module, name, lambda *a, **k: note())
+
+
+def test_router_allocates_on_the_stream_it_runs_on(mok, monkeypatch):
+    streams = _Streams(monkeypatch)
+    x, w = torch.zeros((4, 128), dtype=BF), torch.zeros((128, 8), dtype=BF)
+    calls = _Recorder(monkeypatch, streams, mok, "mok_router_forward")
+    mok.router_forward(x, w, None, 2, stream=0x5550)
+    assert calls.at == [0x5550] * 4  # logits, ids, weights, the call
+    ids, s = torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2))
+    sched = mok.Schedule(mok.mok_schedule(), None, ids, s)
+    sched.c.shape = mok.make_shape(4, 128, 128, 8, 2)
+    calls = _Recorder(monkeypatch, streams, mok, "mok_router_backward")
+    mok.router_backward(sched, x, w, ids, s, s, with_bias=True, stream=0x5550)
+    assert calls.at[-4:] == [0x5550] * 4  # dw, db, ws, the call
+
+
 def owner(t):
     """Handle of the stream that owns t's memory, by the allocator's record."""
     return next(p["stream"] for p in torch.cuda.memory_snapshot()
@@ -69,3 +98,35 @@ def test_handle_of_the_default_stream(mok):
     torch.cuda.synchronize()
     assert owner(o.y) == 0 and owner(o.rstd) == 0
     assert torch.equal(o.y, want.y) and torch.equal(o.rstd, want.rstd)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [False, True])
+def test_sublayer_on_a_given_stream(mok, handle):
+    """Forward and backward of a sublayer on a stream that is not the current one: results as on the current stream, and
+    every tensor of the router and the norm owned by that stream."""
+    from mixture_experts_layer_build_gb300.sublayer import Params, Sublayer
+    T, H, I, E, K, Is = 300, 256, 128, 8, 2, 200
+    g = torch.Generator().manual_seed(4)
+    n = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    p = Params(**{k: (n(*s) * 1.5 / H**0.5).to(BF).cuda() for k, s in dict(
+        w_norm=(H,), w_router=(H, E), w_gate=(E, I, H), w_up=(E, I, H), w_down=(E, H, I), s_gate=(Is, H), s_up=(Is, H),
+        s_down=(H, Is)).items()})
+    branch, dout, res, dh = n(T, H).to(BF).cuda(), n(T, H).to(BF).cuda(), n(T, H).cuda(), n(T, H).cuda()
+    drop = mok.Dropout(0.1, torch.tensor([3, 4], device="cuda"))
+
+    def step(sub, stream):
+        out, h = sub.forward(branch, res, p, drop, stream=stream)
+        dbranch, dres, grads = sub.backward(dout, dh, p, drop, stream=stream)
+        return [out, h, dbranch, dres, *vars(grads).values()], grads
+    want, _ = step(Sublayer(T, H, I, E, K, Is), None)
+    sub = Sublayer(T, H, I, E, K, Is)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got, grads = step(sub, side.cuda_stream if handle else side)
+    assert torch.cuda.current_stream() != side
+    for t in (sub.norm.h, sub.norm.y, sub.norm.rstd, sub.ids, sub.weights, grads.w_router, grads.w_norm, got[2], got[3]):
+        assert owner(t) == side.cuda_stream
+    torch.cuda.synchronize()
+    assert sub.device_status() == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
