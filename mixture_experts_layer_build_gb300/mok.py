@@ -233,13 +233,16 @@ def mok_fwd_ctx_bytes(cfg: mok_config, shape: mok_shape) -> int:
 def mok_mxfp8_quantize(x: torch.Tensor, out_q: torch.Tensor | None = None, out_s: torch.Tensor | None = None,
                        stream=None):
     """MXFP8 of a 2-D bf16 tensor: (E4M3 bytes [rows, cols] uint8, E8M0 scales [rows, cols/32] uint8)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return mok_mxfp8_quantize(x, out_q, out_s)
     rows, cols = x.shape
     if out_q is None:
         out_q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
     if out_s is None:
         out_s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
     _check(_lib.mok_mxfp8_quantize(_ptr(x, torch.bfloat16, "x"), rows, cols, _ptr(out_q, torch.uint8, "out_q"),
-                                   _ptr(out_s, torch.uint8, "out_s"), _stream(stream)), "mok_mxfp8_quantize")
+                                   _ptr(out_s, torch.uint8, "out_s"), _stream(None)), "mok_mxfp8_quantize")
     return out_q, out_s
 
 
@@ -333,14 +336,17 @@ def weights_struct(Wg=None, Wu=None, Wd=None, mx: dict | None = None) -> mok_wei
 def quantize_weights(Wg: torch.Tensor, Wu: torch.Tensor, Wd: torch.Tensor, stream=None) -> dict:
     """The MXFP8 weight copies of mok_weights, made with mok_mxfp8_quantize on the device: forward
     copies along each GEMM's K and backward copies of the transposes."""
+    if stream is not None:  # the transposed copies below are made on it as well
+        with _on_stream(stream):
+            return quantize_weights(Wg, Wu, Wd)
     E, I, H = Wg.shape
     out = {}
-    out["q_gate"], out["s_gate"] = mok_mxfp8_quantize(Wg.reshape(E * I, H), stream=stream)
-    out["q_up"], out["s_up"] = mok_mxfp8_quantize(Wu.reshape(E * I, H), stream=stream)
-    out["q_down"], out["s_down"] = mok_mxfp8_quantize(Wd.reshape(E * H, I), stream=stream)
-    out["qt_gate"], out["st_gate"] = mok_mxfp8_quantize(Wg.transpose(1, 2).contiguous().reshape(E * H, I), stream=stream)
-    out["qt_up"], out["st_up"] = mok_mxfp8_quantize(Wu.transpose(1, 2).contiguous().reshape(E * H, I), stream=stream)
-    out["qt_down"], out["st_down"] = mok_mxfp8_quantize(Wd.transpose(1, 2).contiguous().reshape(E * I, H), stream=stream)
+    out["q_gate"], out["s_gate"] = mok_mxfp8_quantize(Wg.reshape(E * I, H))
+    out["q_up"], out["s_up"] = mok_mxfp8_quantize(Wu.reshape(E * I, H))
+    out["q_down"], out["s_down"] = mok_mxfp8_quantize(Wd.reshape(E * H, I))
+    out["qt_gate"], out["st_gate"] = mok_mxfp8_quantize(Wg.transpose(1, 2).contiguous().reshape(E * H, I))
+    out["qt_up"], out["st_up"] = mok_mxfp8_quantize(Wu.transpose(1, 2).contiguous().reshape(E * H, I))
+    out["qt_down"], out["st_down"] = mok_mxfp8_quantize(Wd.transpose(1, 2).contiguous().reshape(E * I, H))
     return out
 
 

@@ -79,6 +79,27 @@ def test_router_allocates_on_the_stream_it_runs_on(mok, monkeypatch):
     assert calls.at[-4:] == [0x5550] * 4  # dw, db, ws, the call
 
 
+def test_weight_copies_are_made_on_the_given_stream(mok, monkeypatch):
+    """Allocations and transposes of quantize_weights: a transposed copy is read by the kernel of the given stream and
+    dropped at once."""
+    streams = _Streams(monkeypatch)
+    at = []
+    note = lambda: at.append(streams.current[-1].cuda_stream if streams.current else None)  # noqa: E731
+    contiguous = torch.Tensor.contiguous
+    monkeypatch.setattr(torch.Tensor, "contiguous", lambda t: (note(), contiguous(t))[1])
+    monkeypatch.setattr(mok._lib, "mok_mxfp8_quantize", lambda *a: note() or 0)
+    monkeypatch.setattr(mok, "_ptr", lambda t, *a: t.data_ptr())
+    monkeypatch.setattr(mok, "_stream", lambda s: 0 if s is None else int(s))
+    w = torch.zeros((2, 64, 64), dtype=BF)
+    assert set(mok.quantize_weights(w, w, w, stream=0x5550)) == set(mok.MX_KEYS)
+    assert at == [0x5550] * 9  # six calls, three transposes
+    at.clear()
+    calls = _Recorder(monkeypatch, streams, mok._lib, "mok_mxfp8_quantize")
+    monkeypatch.setattr(mok, "_check", lambda rc, where: None)
+    mok.mok_mxfp8_quantize(w[0], stream=0x5550)
+    assert calls.at == [0x5550] * 3  # codes, scales, the call
+
+
 def owner(t):
     """Handle of the stream that owns t's memory, by the allocator's record."""
     return next(p["stream"] for p in torch.cuda.memory_snapshot()
@@ -130,3 +151,16 @@ def test_sublayer_on_a_given_stream(mok, handle):
     torch.cuda.synchronize()
     assert sub.device_status() == 0
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_weight_copies_on_a_given_stream(mok):
+    g = torch.Generator().manual_seed(6)
+    w = [torch.randn(s, generator=g).to(BF).cuda() for s in ((3, 128, 256), (3, 128, 256), (3, 256, 128))]
+    want = mok.quantize_weights(*w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = mok.quantize_weights(*w, stream=side)
+    assert all(owner(t) == side.cuda_stream for t in got.values())
+    torch.cuda.synchronize()
+    assert all(torch.equal(got[k], want[k]) for k in want)
