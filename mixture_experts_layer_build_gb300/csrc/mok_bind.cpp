@@ -188,7 +188,7 @@ bool mat(const Tensor& t, int64_t rows, int64_t cols) {
 }
 
 // (shape, out, ctx, ctx bytes, save, status: the plan's addresses and sizes, x, w_gate, w_up, w_down, residual, stream
-// or None: the current one) -> ()
+// or None: the current one of x's device) -> ()
 PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const Tensor *x, *wg, *wu, *wd, *res;
@@ -214,13 +214,43 @@ PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (shape, ctx, ctx bytes, gradients, ws, ws bytes, status: the plan's addresses and sizes, x, w_gate, w_up, w_down, dy,
+// dx_add, stream or None: the current one of x's device) -> ()
+PyObject* ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor *x, *wg, *wu, *wd, *dy, *add;
+    if (n != 14 || !tensor_arg(a[7], &x) || !tensor_arg(a[8], &wg) || !tensor_arg(a[9], &wu) || !tensor_arg(a[10], &wd) ||
+        !tensor_arg(a[11], &dy) || !tensor_arg(a[12], &add) || !x || !wg || !wu || !wd || !dy)
+      Py_RETURN_NONE;
+    const mok_ffn_shape* s = static_cast<const mok_ffn_shape*>(PyLong_AsVoidPtr(a[0]));
+    const void* ctx = PyLong_AsVoidPtr(a[1]);
+    const size_t ctx_bytes = PyLong_AsSize_t(a[2]);
+    const mok_ffn_grads* plan = static_cast<const mok_ffn_grads*>(PyLong_AsVoidPtr(a[3]));
+    void* ws = PyLong_AsVoidPtr(a[4]);
+    const size_t ws_bytes = PyLong_AsSize_t(a[5]);
+    uint32_t* status = static_cast<uint32_t*>(PyLong_AsVoidPtr(a[6]));
+    if (PyErr_Occurred()) return nullptr;
+    if (!mat(*x, s->T, s->H) || !mat(*wg, s->I, s->H) || !mat(*wu, s->I, s->H) || !mat(*wd, s->H, s->I) ||
+        !mat(*dy, s->T, s->H) || (add && !mat(*add, s->T, s->H)))
+      Py_RETURN_NONE;
+    void* stream = a[13] == Py_None ? current_stream(*x) : PyLong_AsVoidPtr(a[13]);
+    if (PyErr_Occurred()) return nullptr;
+    const c10::cuda::CUDAGuard guard(x->device());
+    mok_ffn_grads g = *plan;
+    g.dx_add = ptr(add);
+    const int rc = mok_ffn_backward(s, x->data_ptr(), wg->data_ptr(), wu->data_ptr(), wd->data_ptr(), ctx, ctx_bytes,
+                                    dy->data_ptr(), &g, ws, ws_bytes, status, stream);
+    return rc ? PyLong_FromLong(rc) : PyTuple_New(0);
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {method<rmsnorm_forward>("rmsnorm_forward"), method<rmsnorm_backward>("rmsnorm_backward"),
                          method<dropout_forward>("dropout_forward"), method<dropout_backward>("dropout_backward"),
-                         method<ffn_forward>("ffn_forward"),
+                         method<ffn_forward>("ffn_forward"), method<ffn_backward>("ffn_backward"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_mok_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -770,7 +770,6 @@ class FFN:
         self.ctx = torch.empty(mok_ffn_ctx_bytes(self.shape, train), dtype=torch.uint8, device=device)
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
         self.status = torch.zeros((1,), dtype=torch.int32, device=device)
-        self._ref = ctypes.byref(self.shape)
         self._fwd = (ctypes.addressof(self.shape), self.out.data_ptr(), self.ctx.data_ptr(), self.ctx.numel(),
                      1 if train else 0, self.status.data_ptr())
         if train:
@@ -780,18 +779,19 @@ class FFN:
             g = self.grads
             self._grads = mok_ffn_grads(g.dx.data_ptr(), g.dw_gate.data_ptr(), g.dw_up.data_ptr(),
                                         g.dw_down.data_ptr(), _STREAM_TYPES[dw_dtype])
+            self._bwd = (ctypes.addressof(self.shape), self.ctx.data_ptr(), self.ctx.numel(),
+                         ctypes.addressof(self._grads), self.ws.data_ptr(), self.ws.numel(), self.status.data_ptr())
 
     def _in(self, x, w_gate, w_up, w_down):
         xs, ws, bf = (self.T, self.H), (self.I, self.H), torch.bfloat16
-        return (_arg(x, xs, bf, "x"), _arg(w_gate, ws, bf, "w_gate"), _arg(w_up, ws, bf, "w_up"),
-                _arg(w_down, (self.H, self.I), bf, "w_down"))
+        return ((x, xs, bf, "x"), (w_gate, ws, bf, "w_gate"), (w_up, ws, bf, "w_up"),
+                (w_down, (self.H, self.I), bf, "w_down"))
 
     def forward(self, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                 residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         r = _bind.ffn_forward(*self._fwd, x, w_gate, w_up, w_down, residual, None if stream is None else _stream(stream))
         if type(r) is not tuple:
-            self._in(x, w_gate, w_up, w_down)
-            _refused(r, "mok_ffn_forward",
+            _refused(r, "mok_ffn_forward", *self._in(x, w_gate, w_up, w_down),
                      *(() if residual is None else ((residual, (self.T, self.H), torch.bfloat16, "residual"),)))
         return self.out
 
@@ -800,11 +800,11 @@ class FFN:
         """Gradients of the last forward; dx_add: x's gradient from its other uses, added to dx."""
         if not self.train:
             raise ValueError("backward needs a plan made with train=True")
-        self._grads.dx_add = _arg(dx_add, (self.T, self.H), torch.bfloat16, "dx_add")
-        _check(_lib.mok_ffn_backward(self._ref, *self._in(x, w_gate, w_up, w_down), self.ctx.data_ptr(),
-                                     self.ctx.numel(), _arg(dy, (self.T, self.H), torch.bfloat16, "dy"),
-                                     ctypes.byref(self._grads), self.ws.data_ptr(), self.ws.numel(),
-                                     self.status.data_ptr(), _stream(stream)), "mok_ffn_backward")
+        r = _bind.ffn_backward(*self._bwd, x, w_gate, w_up, w_down, dy, dx_add, None if stream is None else _stream(stream))
+        if type(r) is not tuple:
+            like = (self.T, self.H), torch.bfloat16
+            _refused(r, "mok_ffn_backward", *self._in(x, w_gate, w_up, w_down), (dy, *like, "dy"),
+                     *(() if dx_add is None else ((dx_add, *like, "dx_add"),)))
         return self.grads
 
     def device_status(self) -> int:
