@@ -7,6 +7,8 @@
 // what it has to be, which the caller then names.
 #include <Python.h>
 
+#include <initializer_list>
+
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
@@ -47,8 +49,26 @@ Tensor make(at::IntArrayRef shape, const Tensor& on, at::ScalarType type) {
   return at::empty(shape, on.options().dtype(type).requires_grad(false));
 }
 
-const mok_dropout* drop_arg(PyObject* o) {
-  return o == Py_None ? nullptr : static_cast<const mok_dropout*>(PyLong_AsVoidPtr(o));
+// Whether every tensor that is there is on `device`: its address goes to a kernel there.
+bool all_on(c10::Device device, std::initializer_list<const Tensor*> ts) {
+  for (const Tensor* t : ts)
+    if (t && t->device() != device) return false;
+  return true;
+}
+
+// Dropout's arguments, and the device that holds the generator's state.
+struct PlacedDropout {
+  mok_dropout d;
+  int32_t device;
+};
+// False when they are on another device than `device`.
+bool drop_arg(PyObject* o, c10::Device device, const mok_dropout** drop) {
+  *drop = nullptr;
+  if (o == Py_None) return true;
+  const PlacedDropout* p = static_cast<const PlacedDropout*>(PyLong_AsVoidPtr(o));
+  if (!p) return true;  // (the caller sees the error)
+  *drop = &p->d;
+  return p->device == device.index();
 }
 
 PyObject* wrap(const Tensor& t) {
@@ -95,10 +115,11 @@ PyObject* rmsnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& stream = res ? *res : *x;
     const int st = stream_type(stream);
     if (st < 0 || !plain(*x, at::kBFloat16) || !like(stream, *x, stream.scalar_type()) || !vec(*w, H, at::kBFloat16) ||
-        H > INT32_MAX)
+        !all_on(x->device(), {w, res}) || H > INT32_MAX)
       Py_RETURN_NONE;
     const double eps = PyFloat_AsDouble(a[2]);
-    const mok_dropout* drop = drop_arg(a[4]);
+    const mok_dropout* drop;
+    if (!drop_arg(a[4], x->device(), &drop)) Py_RETURN_NONE;
     const int bf16 = PyObject_IsTrue(a[5]), mx = PyObject_IsTrue(a[6]);
     if (PyErr_Occurred()) return nullptr;
     const c10::cuda::CUDAGuard guard(x->device());
@@ -128,9 +149,11 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t T = h->size(0), H = h->size(1);
     const int st = stream_type(*h);
     if (st < 0 || !plain(*h) || !vec(*rstd, T, at::kFloat) || !vec(*w, H, at::kBFloat16) ||
-        !like(*dy, *h, at::kBFloat16) || (dres && !like(*dres, *h, h->scalar_type())) || H > INT32_MAX)
+        !like(*dy, *h, at::kBFloat16) || (dres && !like(*dres, *h, h->scalar_type())) ||
+        !all_on(h->device(), {rstd, w, dy, dres}) || H > INT32_MAX)
       Py_RETURN_NONE;
-    const mok_dropout* drop = drop_arg(a[5]);
+    const mok_dropout* drop;
+    if (!drop_arg(a[5], h->device(), &drop)) Py_RETURN_NONE;
     if (PyErr_Occurred()) return nullptr;
     const mok_norm_shape shape{T, static_cast<int32_t>(H), st, 0.0f};
     const size_t bytes = mok_rmsnorm_workspace_bytes(&shape);
@@ -156,9 +179,10 @@ PyObject* dropout_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& stream = res ? *res : *x;
     const int st = stream_type(stream);
     if (st < 0 || !plain(*x, at::kBFloat16) || !like(stream, *x, stream.scalar_type()) ||
-        (given && !like(*given, *x, stream.scalar_type())))
+        (given && !like(*given, *x, stream.scalar_type())) || !all_on(x->device(), {res, given}))
       Py_RETURN_NONE;
-    const mok_dropout* drop = drop_arg(a[1]);
+    const mok_dropout* drop;
+    if (!drop_arg(a[1], x->device(), &drop)) Py_RETURN_NONE;
     if (PyErr_Occurred()) return nullptr;
     const c10::cuda::CUDAGuard guard(x->device());
     const Tensor out[1] = {given ? *given : make(x->sizes(), *x, stream.scalar_type())};
@@ -173,8 +197,11 @@ PyObject* dropout_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor *dout, *given;
     if (n != 3 || !tensor_arg(a[0], &dout) || !tensor_arg(a[2], &given) || !dout) Py_RETURN_NONE;
     const int st = stream_type(*dout);
-    if (st < 0 || !plain(*dout) || (given && !like(*given, *dout, at::kBFloat16))) Py_RETURN_NONE;
-    const mok_dropout* drop = drop_arg(a[1]);
+    if (st < 0 || !plain(*dout) || (given && !like(*given, *dout, at::kBFloat16)) ||
+        !all_on(dout->device(), {given}))
+      Py_RETURN_NONE;
+    const mok_dropout* drop;
+    if (!drop_arg(a[1], dout->device(), &drop)) Py_RETURN_NONE;
     if (PyErr_Occurred()) return nullptr;
     const c10::cuda::CUDAGuard guard(dout->device());
     const Tensor out[1] = {given ? *given : make(dout->sizes(), *dout, at::kBFloat16)};
@@ -187,25 +214,26 @@ bool mat(const Tensor& t, int64_t rows, int64_t cols) {
   return plain(t, at::kBFloat16) && t.dim() == 2 && t.size(0) == rows && t.size(1) == cols;
 }
 
-// (shape, out, ctx, ctx bytes, save, status: the plan's addresses and sizes, x, w_gate, w_up, w_down, residual, stream
+// (device, shape, out, ctx, ctx bytes, save, status: the plan's index, addresses and sizes, x, w_gate, w_up, w_down, residual, stream
 // or None: the current one of x's device) -> ()
 PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const Tensor *x, *wg, *wu, *wd, *res;
-    if (n != 12 || !tensor_arg(a[6], &x) || !tensor_arg(a[7], &wg) || !tensor_arg(a[8], &wu) || !tensor_arg(a[9], &wd) ||
-        !tensor_arg(a[10], &res) || !x || !wg || !wu || !wd)
+    if (n != 13 || !tensor_arg(a[7], &x) || !tensor_arg(a[8], &wg) || !tensor_arg(a[9], &wu) || !tensor_arg(a[10], &wd) ||
+        !tensor_arg(a[11], &res) || !x || !wg || !wu || !wd)
       Py_RETURN_NONE;
-    const mok_ffn_shape* s = static_cast<const mok_ffn_shape*>(PyLong_AsVoidPtr(a[0]));
-    void* out = PyLong_AsVoidPtr(a[1]);
-    void* ctx = PyLong_AsVoidPtr(a[2]);
-    const size_t bytes = PyLong_AsSize_t(a[3]);
-    const long save = PyLong_AsLong(a[4]);
-    uint32_t* status = static_cast<uint32_t*>(PyLong_AsVoidPtr(a[5]));
+    const long device = PyLong_AsLong(a[0]);
+    const mok_ffn_shape* s = static_cast<const mok_ffn_shape*>(PyLong_AsVoidPtr(a[1]));
+    void* out = PyLong_AsVoidPtr(a[2]);
+    void* ctx = PyLong_AsVoidPtr(a[3]);
+    const size_t bytes = PyLong_AsSize_t(a[4]);
+    const long save = PyLong_AsLong(a[5]);
+    uint32_t* status = static_cast<uint32_t*>(PyLong_AsVoidPtr(a[6]));
     if (PyErr_Occurred()) return nullptr;
     if (!mat(*x, s->T, s->H) || !mat(*wg, s->I, s->H) || !mat(*wu, s->I, s->H) || !mat(*wd, s->H, s->I) ||
-        (res && !mat(*res, s->T, s->H)))
+        (res && !mat(*res, s->T, s->H)) || x->device().index() != device || !all_on(x->device(), {wg, wu, wd, res}))
       Py_RETURN_NONE;
-    void* stream = a[11] == Py_None ? current_stream(*x) : PyLong_AsVoidPtr(a[11]);
+    void* stream = a[12] == Py_None ? current_stream(*x) : PyLong_AsVoidPtr(a[12]);
     if (PyErr_Occurred()) return nullptr;
     const c10::cuda::CUDAGuard guard(x->device());
     const int rc = mok_ffn_forward(s, x->data_ptr(), wg->data_ptr(), wu->data_ptr(), wd->data_ptr(), ptr(res), out, ctx,
@@ -214,26 +242,28 @@ PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (shape, ctx, ctx bytes, gradients, ws, ws bytes, status: the plan's addresses and sizes, x, w_gate, w_up, w_down, dy,
+// (device, shape, ctx, ctx bytes, gradients, ws, ws bytes, status: the plan's index, addresses and sizes, x, w_gate, w_up, w_down, dy,
 // dx_add, stream or None: the current one of x's device) -> ()
 PyObject* ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const Tensor *x, *wg, *wu, *wd, *dy, *add;
-    if (n != 14 || !tensor_arg(a[7], &x) || !tensor_arg(a[8], &wg) || !tensor_arg(a[9], &wu) || !tensor_arg(a[10], &wd) ||
-        !tensor_arg(a[11], &dy) || !tensor_arg(a[12], &add) || !x || !wg || !wu || !wd || !dy)
+    if (n != 15 || !tensor_arg(a[8], &x) || !tensor_arg(a[9], &wg) || !tensor_arg(a[10], &wu) || !tensor_arg(a[11], &wd) ||
+        !tensor_arg(a[12], &dy) || !tensor_arg(a[13], &add) || !x || !wg || !wu || !wd || !dy)
       Py_RETURN_NONE;
-    const mok_ffn_shape* s = static_cast<const mok_ffn_shape*>(PyLong_AsVoidPtr(a[0]));
-    const void* ctx = PyLong_AsVoidPtr(a[1]);
-    const size_t ctx_bytes = PyLong_AsSize_t(a[2]);
-    const mok_ffn_grads* plan = static_cast<const mok_ffn_grads*>(PyLong_AsVoidPtr(a[3]));
-    void* ws = PyLong_AsVoidPtr(a[4]);
-    const size_t ws_bytes = PyLong_AsSize_t(a[5]);
-    uint32_t* status = static_cast<uint32_t*>(PyLong_AsVoidPtr(a[6]));
+    const long device = PyLong_AsLong(a[0]);
+    const mok_ffn_shape* s = static_cast<const mok_ffn_shape*>(PyLong_AsVoidPtr(a[1]));
+    const void* ctx = PyLong_AsVoidPtr(a[2]);
+    const size_t ctx_bytes = PyLong_AsSize_t(a[3]);
+    const mok_ffn_grads* plan = static_cast<const mok_ffn_grads*>(PyLong_AsVoidPtr(a[4]));
+    void* ws = PyLong_AsVoidPtr(a[5]);
+    const size_t ws_bytes = PyLong_AsSize_t(a[6]);
+    uint32_t* status = static_cast<uint32_t*>(PyLong_AsVoidPtr(a[7]));
     if (PyErr_Occurred()) return nullptr;
     if (!mat(*x, s->T, s->H) || !mat(*wg, s->I, s->H) || !mat(*wu, s->I, s->H) || !mat(*wd, s->H, s->I) ||
-        !mat(*dy, s->T, s->H) || (add && !mat(*add, s->T, s->H)))
+        !mat(*dy, s->T, s->H) || (add && !mat(*add, s->T, s->H)) || x->device().index() != device ||
+        !all_on(x->device(), {wg, wu, wd, dy, add}))
       Py_RETURN_NONE;
-    void* stream = a[13] == Py_None ? current_stream(*x) : PyLong_AsVoidPtr(a[13]);
+    void* stream = a[14] == Py_None ? current_stream(*x) : PyLong_AsVoidPtr(a[14]);
     if (PyErr_Occurred()) return nullptr;
     const c10::cuda::CUDAGuard guard(x->device());
     mok_ffn_grads g = *plan;

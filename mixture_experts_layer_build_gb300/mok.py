@@ -180,12 +180,23 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _on_stream(stream):
-    """Makes `stream` (torch.cuda.Stream or handle) current: what a call allocates then belongs to the stream that it
-    runs on, so that neither a workspace that it drops nor an output's earlier owner can still be in use there."""
+def _check_stream(stream, x):
+    """Refuses a torch stream of another device than tensor x's (a bare handle does not say which it is of)."""
+    if isinstance(stream, torch.cuda.Stream) and isinstance(x, torch.Tensor) and x.is_cuda and stream.device != x.device:
+        raise ValueError(f"the stream must be on {x.device}, as the tensors are, got {stream.device}")
+
+
+def _on_stream(stream, x=None):
+    """Makes `stream` (torch.cuda.Stream, or a handle on x's device; None: that device's current one) current: what a call
+    allocates then belongs to the stream that it runs on, so that neither a workspace that it drops nor an output's
+    earlier owner can still be in use there.  Without x the device is the current one."""
+    device = x.device if isinstance(x, torch.Tensor) and x.is_cuda else None
+    if stream is None:
+        return torch.cuda.device(device)
+    _check_stream(stream, x)
     if not isinstance(stream, torch.cuda.Stream):
         handle = _stream(stream)  # 0: the default stream, of which ExternalStream makes a new stream of torch's pool
-        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
     return torch.cuda.stream(stream)
 
 
@@ -563,6 +574,10 @@ class mok_dropout(ctypes.Structure):
     _fields_ = [("p", ctypes.c_float), ("rng", _P)]
 
 
+class _placed_dropout(ctypes.Structure):  # with the index of the device that holds the state, for the compiled binding
+    _fields_ = [("d", mok_dropout), ("device", ctypes.c_int32)]
+
+
 class mok_norm_shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int32), ("stream_type", ctypes.c_int32), ("eps", ctypes.c_float)]
 
@@ -616,21 +631,31 @@ class Dropout:
 
     def __init__(self, p: float, rng: torch.Tensor):
         self.rng = rng  # kept alive with the pointer
-        self.c = mok_dropout(p, _arg(rng, (2,), torch.int64, "rng"))
+        ptr = _arg(rng, (2,), torch.int64, "rng")
+        self._placed = _placed_dropout(mok_dropout(p, ptr), rng.device.index)
+        self.c = self._placed.d
         self.ref = ctypes.byref(self.c)
-        self.addr = ctypes.addressof(self.c)
+        self.addr = ctypes.addressof(self._placed)
 
 
 def _refused(result, where: str, *args):
     """Raises for what a compiled call returned instead of its tensors: the library's status, or None for a tensor
-    that is not what it has to be.  args: (tensor, shape, dtype, name) in the order of the call's checks."""
+    that is not what or where it has to be.  args: (tensor, shape, dtype, name) in the order of the call's checks, the
+    first one's device being the call's."""
     if result is not None:
         raise MokError(result, where)
     for t, shape, dtype, name in args:
         if not isinstance(t, torch.Tensor):
             raise ValueError(f"{name} must be a tensor, got {type(t).__name__}")
         _arg(t, t.shape if shape is None else shape, dtype, name)
+        if t.device != args[0][0].device:
+            raise ValueError(f"{name} must be on {args[0][0].device}, as {args[0][3]} is, got {t.device}")
     raise ValueError(f"{where}: unsupported arguments")
+
+
+def _rng_of(dropout):
+    """The generator's state of an optional Dropout, as arguments of _refused."""
+    return () if dropout is None else ((dropout.rng, (2,), torch.int64, "dropout.rng"),)
 
 
 def _stream_type(t: torch.Tensor, name: str) -> int:
@@ -645,14 +670,14 @@ def dropout_forward(x: torch.Tensor, dropout: Dropout, residual: torch.Tensor | 
     """residual + dropout(x): x bf16, residual bf16 or fp32 of x's shape; out of the residual's type
     (bf16 without one).  The number of values is a multiple of 8."""
     if stream is not None:
-        with _on_stream(stream):
+        with _on_stream(stream, x):
             return dropout_forward(x, dropout, residual, out)
     r = _bind.dropout_forward(x, dropout.addr, residual, out)
     if type(r) is not tuple:
         like = x if residual is None else residual
         _stream_type(like, "residual")
         _refused(r, "mok_dropout_forward", (x, None, torch.bfloat16, "x"), (like, x.shape, None, "residual"),
-                 *(() if out is None else ((out, x.shape, like.dtype, "out"),)))
+                 *(() if out is None else ((out, x.shape, like.dtype, "out"),)), *_rng_of(dropout))
     return r[0]
 
 
@@ -660,13 +685,13 @@ def dropout_backward(dout: torch.Tensor, dropout: Dropout, dx: torch.Tensor | No
                      stream=None) -> torch.Tensor:
     """The branch's gradient (bf16) for dout of the stream's type, under the forward's masks."""
     if stream is not None:
-        with _on_stream(stream):
+        with _on_stream(stream, dout):
             return dropout_backward(dout, dropout, dx)
     r = _bind.dropout_backward(dout, dropout.addr, dx)
     if type(r) is not tuple:
         _stream_type(dout, "dout")
         _refused(r, "mok_dropout_backward", (dout, None, None, "dout"),
-                 *(() if dx is None else ((dx, dout.shape, torch.bfloat16, "dx"),)))
+                 *(() if dx is None else ((dx, dout.shape, torch.bfloat16, "dx"),)), *_rng_of(dropout))
     return r[0]
 
 
@@ -685,7 +710,7 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
     x [T, H] bf16, residual [T, H] bf16 or fp32 (the type of h), weight [H] bf16.  bf16 / mx choose the
     outputs.  Without residual and dropout h is x."""
     if stream is not None:
-        with _on_stream(stream):
+        with _on_stream(stream, x):
             return rmsnorm_forward(x, weight, eps, residual, dropout, bf16, mx)
     r = _bind.rmsnorm_forward(x, weight, eps, residual, None if dropout is None else dropout.addr, bf16, mx)
     if type(r) is not tuple:
@@ -693,7 +718,7 @@ def rmsnorm_forward(x: torch.Tensor, weight: torch.Tensor, eps: float, residual:
         _stream_type(like, "residual")
         T, H = x.shape
         _refused(r, "mok_rmsnorm_forward", (x, None, torch.bfloat16, "x"), (like, x.shape, None, "residual"),
-                 (weight, (H,), torch.bfloat16, "weight"))
+                 (weight, (H,), torch.bfloat16, "weight"), *_rng_of(dropout))
     h, y, q, s, rstd = r
     return NormOut(x if h is None else h, y, q, s, rstd)
 
@@ -717,7 +742,7 @@ def rmsnorm_backward(h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, 
     """Gradients of rmsnorm_forward from dy [T, H] bf16 = dL/dy and dres = dL/dh from the stream's other
     uses (h's type, or None), under the forward's masks."""
     if stream is not None:
-        with _on_stream(stream):
+        with _on_stream(stream, h):
             return rmsnorm_backward(h, rstd, weight, dy, dres, dropout)
     r = _bind.rmsnorm_backward(h, rstd, weight, dy, dres, None if dropout is None else dropout.addr)
     if type(r) is not tuple:
@@ -725,7 +750,7 @@ def rmsnorm_backward(h: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor, 
         T, H = h.shape
         _refused(r, "mok_rmsnorm_backward", (h, None, None, "h"), (rstd, (T,), torch.float32, "rstd"),
                  (weight, (H,), torch.bfloat16, "weight"), (dy, h.shape, torch.bfloat16, "dy"),
-                 *(() if dres is None else ((dres, h.shape, h.dtype, "dres"),)))
+                 *(() if dres is None else ((dres, h.shape, h.dtype, "dres"),)), *_rng_of(dropout))
     dh, dx, dw = r
     return NormGrads(dh, dh if dx is None else dx, dw)
 
@@ -770,7 +795,8 @@ class FFN:
         self.ctx = torch.empty(mok_ffn_ctx_bytes(self.shape, train), dtype=torch.uint8, device=device)
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
         self.status = torch.zeros((1,), dtype=torch.int32, device=device)
-        self._fwd = (ctypes.addressof(self.shape), self.out.data_ptr(), self.ctx.data_ptr(), self.ctx.numel(),
+        self._device = self.out.device.index if self.out.is_cuda else -1
+        self._fwd = (self._device, ctypes.addressof(self.shape), self.out.data_ptr(), self.ctx.data_ptr(), self.ctx.numel(),
                      1 if train else 0, self.status.data_ptr())
         if train:
             e = lambda *s: torch.empty(s, dtype=dw_dtype, device=device)  # noqa: E731
@@ -779,7 +805,7 @@ class FFN:
             g = self.grads
             self._grads = mok_ffn_grads(g.dx.data_ptr(), g.dw_gate.data_ptr(), g.dw_up.data_ptr(),
                                         g.dw_down.data_ptr(), _STREAM_TYPES[dw_dtype])
-            self._bwd = (ctypes.addressof(self.shape), self.ctx.data_ptr(), self.ctx.numel(),
+            self._bwd = (self._device, ctypes.addressof(self.shape), self.ctx.data_ptr(), self.ctx.numel(),
                          ctypes.addressof(self._grads), self.ws.data_ptr(), self.ws.numel(), self.status.data_ptr())
 
     def _in(self, x, w_gate, w_up, w_down):
@@ -789,10 +815,12 @@ class FFN:
 
     def forward(self, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                 residual: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        _check_stream(stream, x)
         r = _bind.ffn_forward(*self._fwd, x, w_gate, w_up, w_down, residual, None if stream is None else _stream(stream))
         if type(r) is not tuple:
             _refused(r, "mok_ffn_forward", *self._in(x, w_gate, w_up, w_down),
-                     *(() if residual is None else ((residual, (self.T, self.H), torch.bfloat16, "residual"),)))
+                     *(() if residual is None else ((residual, (self.T, self.H), torch.bfloat16, "residual"),)),
+                     (self.out, None, None, "the plan"))
         return self.out
 
     def backward(self, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
@@ -800,11 +828,12 @@ class FFN:
         """Gradients of the last forward; dx_add: x's gradient from its other uses, added to dx."""
         if not self.train:
             raise ValueError("backward needs a plan made with train=True")
+        _check_stream(stream, x)
         r = _bind.ffn_backward(*self._bwd, x, w_gate, w_up, w_down, dy, dx_add, None if stream is None else _stream(stream))
         if type(r) is not tuple:
             like = (self.T, self.H), torch.bfloat16
             _refused(r, "mok_ffn_backward", *self._in(x, w_gate, w_up, w_down), (dy, *like, "dy"),
-                     *(() if dx_add is None else ((dx_add, *like, "dx_add"),)))
+                     *(() if dx_add is None else ((dx_add, *like, "dx_add"),)), (self.out, None, None, "the plan"))
         return self.grads
 
     def device_status(self) -> int:

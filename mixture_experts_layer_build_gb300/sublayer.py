@@ -52,27 +52,37 @@ class Sublayer:
         self.layer = mok.Layer(T, H, I, E, K, cfg or mok.make_config(0, 0), device)
         self.ffn = mok.FFN(T, H, shared_I, act=act, train=True, dw_dtype=shared_dw_dtype, device=device)
 
+    def _here(self, x: torch.Tensor, name: str, p: Params):
+        """Refuses tensors on another device than the plans': the layer's calls take their addresses as they are."""
+        for k, t in ((name, x), *vars(p).items()):
+            if t.device != self.ffn.out.device:
+                raise ValueError(f"{k} must be on {self.ffn.out.device}, as the sublayer's buffers are, got {t.device}")
+
     def forward(self, branch: torch.Tensor, residual: torch.Tensor, p: Params, dropout: mok.Dropout | None = None,
                 stream=None):
         """(out, h): this sublayer's output [T, H] bf16 and the residual stream, of residual's type."""
-        self.norm = mok.rmsnorm_forward(branch, p.w_norm, self.eps, residual=residual, dropout=dropout, stream=stream)
-        y = self.norm.y
-        _, self.ids, self.weights = mok.router_forward(y, p.w_router, None, self.K, stream)
-        self.layer.schedule(self.ids, self.weights, stream)
-        routed = self.layer.forward(y, mok.weights_struct(p.w_gate, p.w_up, p.w_down), stream)
-        out = self.ffn.forward(y, p.s_gate, p.s_up, p.s_down, residual=routed, stream=stream)
+        self._here(branch, "branch", p)
+        with mok._on_stream(stream, branch):
+            self.norm = mok.rmsnorm_forward(branch, p.w_norm, self.eps, residual=residual, dropout=dropout)
+            y = self.norm.y
+            _, self.ids, self.weights = mok.router_forward(y, p.w_router, None, self.K)
+            self.layer.schedule(self.ids, self.weights)
+            routed = self.layer.forward(y, mok.weights_struct(p.w_gate, p.w_up, p.w_down))
+            out = self.ffn.forward(y, p.s_gate, p.s_up, p.s_down, residual=routed)
         return out, self.norm.h
 
     def backward(self, dout: torch.Tensor, dh: torch.Tensor | None, p: Params, dropout: mok.Dropout | None = None,
                  stream=None):
         """(dbranch, dresidual, ParamGrads) of the last forward, for dout [T, H] bf16 = dL/dout and dh = dL/dh
         from the stream's later uses (None: 0).  dropout: the forward's, with its generator state unchanged."""
-        y = self.norm.y
-        g = self.layer.backward(dout, mok.weights_struct(p.w_gate, p.w_up, p.w_down), stream)
-        dw_router, _, dy = mok.router_backward(self.layer.sched, y, p.w_router, self.ids, self.weights,
-                                               g.d_topk_weights, dx=g.dx, stream=stream)
-        f = self.ffn.backward(y, p.s_gate, p.s_up, p.s_down, dout, dx_add=dy, stream=stream)
-        n = mok.rmsnorm_backward(self.norm.h, self.norm.rstd, p.w_norm, f.dx, dres=dh, dropout=dropout, stream=stream)
+        self._here(dout, "dout", p)
+        with mok._on_stream(stream, dout):
+            y = self.norm.y
+            g = self.layer.backward(dout, mok.weights_struct(p.w_gate, p.w_up, p.w_down))
+            dw_router, _, dy = mok.router_backward(self.layer.sched, y, p.w_router, self.ids, self.weights,
+                                                   g.d_topk_weights, dx=g.dx)
+            f = self.ffn.backward(y, p.s_gate, p.s_up, p.s_down, dout, dx_add=dy)
+            n = mok.rmsnorm_backward(self.norm.h, self.norm.rstd, p.w_norm, f.dx, dres=dh, dropout=dropout)
         return n.dx, n.dh, ParamGrads(n.dweight, dw_router, g.dw_gate, g.dw_up, g.dw_down, f.dw_gate, f.dw_up,
                                       f.dw_down)
 
