@@ -48,6 +48,8 @@ class Sublayer:
 
     def __init__(self, T: int, H: int, I: int, E: int, K: int, shared_I: int, act: str = "silu", eps: float = 1e-6,
                  cfg: mok.mok_config | None = None, shared_dw_dtype=torch.float32, device="cuda"):
+        if cfg is not None and cfg.precision != mok.MOK_BF16:
+            raise ValueError("cfg must be of MOK_BF16 precision: the parameters are bf16")
         self.K, self.eps = K, eps
         self.layer = mok.Layer(T, H, I, E, K, cfg or mok.make_config(0, 0), device)
         self.ffn = mok.FFN(T, H, shared_I, act=act, train=True, dw_dtype=shared_dw_dtype, device=device)
