@@ -472,6 +472,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
+      pdl_wait();  // the kernel in front may take its time: no bounded wait starts before its end
       int st = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;

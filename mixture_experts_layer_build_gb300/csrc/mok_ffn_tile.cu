@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kTileThreads)
     int st = 0, i = 0;
     uint32_t ph = 1;  // parity of the empty barrier's phase to wait for: none in the first round
     for (; i < count; ++i) {
+      if (i == t.stages) pdl_wait();  // (weights: the stages filled early; see warp 1)
       if (i >= t.stages && !warp_wait(empty(st), ph, abort_flag, t.f.status)) {
         ok = false;
         break;
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kTileThreads)
     }
     __syncwarp();
   } else if (warp == 1) {
+    pdl_wait();  // the kernel in front may take its time: no bounded wait starts before its end
     int st = 0;
     uint32_t ph = 0;
     for (int i = 0; i < count; ++i) {
