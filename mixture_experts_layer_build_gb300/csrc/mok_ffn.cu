@@ -8,7 +8,7 @@ namespace {
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 bool ffn_shape_ok(const mok_ffn_shape* s) {
-  return s && s->T >= 0 && s->T < (int64_t{1} << 31) - 256 && s->H >= 8 && s->I >= 8 && s->H <= 65536 &&
+  return s && s->T >= 0 && s->T <= kFfnMaxTokens && s->H >= 8 && s->I >= 8 && s->H <= 65536 &&
          s->I <= 65536 && s->H % 8 == 0 && s->I % 8 == 0 && (s->act == MOK_ACT_SILU || s->act == MOK_ACT_GELU);
 }
 

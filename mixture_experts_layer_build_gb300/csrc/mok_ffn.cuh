@@ -15,6 +15,7 @@
 #pragma once
 #include <cuda.h>
 
+#include "mok_ffn_plan.h"
 #include "mok_internal.cuh"
 #include "mok_once.h"
 #include "mok_ptx.cuh"
@@ -55,6 +56,22 @@ __device__ __forceinline__ void wait_landed(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity) && global_timer_ns() - t0 < kWaitLimitNs / 4) {
   }
+}
+// mbar_wait for a barrier that completes when all k_blocks MMAs of a tile have: the tokens of a weight gradient may be
+// more K blocks than the limit of a single wait allows.
+__device__ __forceinline__ bool mbar_wait_tile(uint32_t bar, uint32_t parity, int k_blocks, volatile int* abort,
+                                               uint32_t* status) {
+  const uint64_t limit = tile_wait_ns(kWaitLimitNs, k_blocks), t0 = global_timer_ns();
+  for (uint32_t spins = 1; !mbar_try_wait(bar, parity); ++spins) {
+    if (spins & 63u) continue;
+    if (*abort) return false;
+    if (global_timer_ns() - t0 > limit) {
+      *abort = 1;
+      record_status(status, MOK_ERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {

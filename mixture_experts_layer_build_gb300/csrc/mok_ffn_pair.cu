@@ -536,7 +536,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           saved_fetch(p.f, w.m * 256 + rank * 128 + q * 32, lane, w.n * BN + (h ? (BN / 32 + 1) / 2 * 32 : 0), j, pre);
       }
       int ok = 0;
-      if (lane == 0) ok = mbar_wait(tfull(acc), aph, abort_flag, status) ? 1 : 0;
+      if (lane == 0) ok = mbar_wait_tile(tfull(acc), aph, w.k_blocks, abort_flag, status) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       tc_fence_after();
