@@ -4,8 +4,9 @@ Every step of the layer runs in the library's CUDA kernels; this module only che
 dtypes / devices / contiguity, passes ``data_ptr()``s and the current CUDA stream, and turns
 status codes into exceptions.  PyTorch provides device memory and streams.
 
-Importing this module loads the library and raises ``ImportError`` when it is missing: there is
-no fallback path.
+Importing this module loads the library and raises ``ImportError`` when it is missing; the norm,
+dropout and feed-forward calls go through a compiled module beside it and raise ``ImportError``
+without it.  There is no fallback path.
 """
 from __future__ import annotations
 
@@ -22,7 +23,23 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libmok.so not found at {LIB_PATH}; build it with __graft_entry__.build() "
                       "(nvcc, sm_103a). There is no CPU fallback.")
 _lib = ctypes.CDLL(LIB_PATH)
-from . import _mok_bind as _bind  # noqa: E402  (built beside libmok.so, which it calls)
+
+
+class _MissingBinding:
+    """In place of the compiled binding of the norm, dropout and feed-forward calls where it cannot be loaded: the routed
+    layer does without it, those calls raise."""
+
+    def __init__(self, why: Exception):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{name} needs _mok_bind.so beside libmok.so; build it with __graft_entry__.build()") from self._why
+
+
+try:
+    from . import _mok_bind as _bind  # built beside libmok.so, which it calls
+except ImportError as e:
+    _bind = _MissingBinding(e)
 
 MOK_OK = 0
 MOK_ERR_INVALID_ARG = 1
