@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import subprocess
 import sys
 
@@ -14,6 +15,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmok.so")
 BIND = os.path.join(HERE, "_mok_bind.so")
+BIND_TARGET = os.path.join(BUILD, "mok_bind.target")  # what BIND was built for
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -30,20 +32,40 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    import importlib.util
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def bind_target() -> str:
+    """What _mok_bind.so is built for: torch's inlined accessors and Python's ABI are in it.  (torch's version from its
+    own file: the build does not import torch.)"""
+    text = open(os.path.join(_torch_dir(), "version.py")).read()
+    version = re.search(r"^__version__ = ['\"](.+?)['\"]", text, re.M).group(1)
+    return f"torch {version}, python {sys.version_info.major}.{sys.version_info.minor}"
+
+
 def _bind_commands() -> list:
     """[compile, link] of _mok_bind.so against this machine's torch; it finds libmok.so beside it."""
-    import importlib.util
     import sysconfig
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(NVCC))
     obj = os.path.join(BUILD, "mok_bind.o")
     inc = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
     cxx = os.environ.get("CXX", "g++")
-    return [[cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{i}" for i in inc), "-c",
-             os.path.join(CSRC, "mok_bind.cpp"), "-o", obj],
+    return [[cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", *(f"-I{i}" for i in inc),
+             f'-DMOK_BUILT_FOR="{bind_target()}"', "-c", os.path.join(CSRC, "mok_bind.cpp"), "-o", obj],
             [cxx, "-shared", obj, "-o", BIND + f".tmp{os.getpid()}", f"-L{HERE}", "-l:libmok.so", "-Wl,-rpath,$ORIGIN",
              f"-L{os.path.join(torch, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]]
+
+
+def bind_stale() -> bool:
+    """Whether _mok_bind.so has to be compiled: sources that changed, or another torch or Python than it is for."""
+    compile_bind = _bind_commands()[0]
+    if _stale(compile_bind[-1], [compile_bind[-3], os.path.join(INCLUDE, "mok.h"), __file__]):
+        return True
+    return not os.path.exists(BIND_TARGET) or open(BIND_TARGET).read() != bind_target()
 
 
 def build(verbose: bool = False, extra=None) -> str:
@@ -57,7 +79,7 @@ def build(verbose: bool = False, extra=None) -> str:
         if _stale(o, [s, *headers, __file__]):
             jobs.append([NVCC, *ARCH, *FLAGS, *(extra or []), "-c", s, "-o", o])
     compile_bind, link_bind = _bind_commands()
-    if _stale(compile_bind[-1], [compile_bind[-3], headers[-1], __file__]):
+    if bind_stale():
         jobs.append(compile_bind)
     failed = []
     if jobs:
@@ -89,6 +111,8 @@ def build(verbose: bool = False, extra=None) -> str:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of _mok_bind.so failed")
         os.replace(BIND + f".tmp{os.getpid()}", BIND)
+        with open(BIND_TARGET, "w") as f:
+            f.write(bind_target())
     return LIB
 
 

@@ -286,4 +286,8 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_mok_bind", nullptr, -1, metho
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__mok_bind() { return PyModule_Create(&module_def); }
+PyMODINIT_FUNC PyInit__mok_bind() {
+  PyObject* m = PyModule_Create(&module_def);
+  if (m && PyModule_AddStringConstant(m, "built_for", MOK_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}

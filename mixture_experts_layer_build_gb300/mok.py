@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from dataclasses import dataclass
 
 import torch
@@ -38,6 +39,10 @@ class _MissingBinding:
 
 try:
     from . import _mok_bind as _bind  # built beside libmok.so, which it calls
+    _here = f"torch {torch.__version__}, python {sys.version_info.major}.{sys.version_info.minor}"
+    _for = getattr(_bind, "built_for", "another torch or Python")
+    if _for != _here:  # what it has inlined of torch may not match
+        raise ImportError(f"_mok_bind.so is built for {_for}, this is {_here}")
 except ImportError as e:
     _bind = _MissingBinding(e)
 

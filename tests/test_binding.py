@@ -66,3 +66,16 @@ def test_the_library_is_linked_when_the_binding_does_not_compile(monkeypatch, tm
     with pytest.raises(RuntimeError, match="mok_bind"):
         build.build()
     assert (tmp_path / "LIB").exists() and not (tmp_path / "BIND").exists()
+
+
+def test_a_binding_of_another_torch_is_not_used():
+    out = python("import torch\ntorch.__version__ = '0.0.1'" + USE).splitlines()
+    assert len(out) == 4 and all("0.0.1" in line.split("/", 1)[1] for line in out), out
+
+
+def test_the_binding_is_rebuilt_for_another_torch(monkeypatch):
+    from mixture_experts_layer_build_gb300 import build
+    import torch
+    assert not build.bind_stale() and torch.__version__ in build.bind_target()
+    monkeypatch.setattr(build, "bind_target", lambda: "torch 0.0.1, python 3.12")
+    assert build.bind_stale()
