@@ -34,20 +34,7 @@ struct FfnCtx {
 bool unaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 bool need16(const void* p) { return p && !unaligned(p, 16); }
 
-// Whether a row-tiled contraction runs on pairs of CTAs: where their narrowest tiles, 256 x 128, are enough for
-// half of the pairs, or a quarter up to 1024 tokens; below, the tile kernel, which can split K.  In the backward,
-// where weight gradients fill the other pairs, an eighth is enough from 384 tokens on, and a quarter below if three
-// quarters of the tiles' rows are tokens.  Measured at H = 4096, I = 1536, a training step with every contraction
-// on the tile kernel and on pairs: 67.6 and 74.9 us for 256 tokens, 151 and 96.7 for 1024; the quarter: T = 1000,
-// H = 1000, I = 512 16.1 -> 14.8 forward, but T = 1500, H = I = 640 12.9 -> 13.8; the backward's: 384 tokens at H =
-// 2048, I = 1024 49.6 -> 44.4, 1024 tokens 62.7 -> 52.3; 150 tokens at H = 4096, I = 1536 would lose 66.4 -> 70.4.
-bool on_pairs(int var, int64_t M, int64_t N) {
-  const int cols = var == F_GATEUP ? 64 : 128;
-  const int64_t mt = (M + 255) / 256, tiles = mt * ((N + cols - 1) / cols);
-  int part = M <= 1024 ? 4 : 2;  // of the pairs that has tiles
-  if (var >= F_DACT) part = M > 384 ? 8 : 4 * M >= 3 * 256 * mt ? 4 : 2;
-  return M > 128 && 2 * part * tiles >= sm_count();
-}
+bool on_pairs(int var, int64_t M, int64_t N) { return ffn_on_pairs(var, M, N, sm_count()); }
 
 int launch_fwd(int var, int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& a,
                cudaStream_t stream) {

@@ -22,11 +22,7 @@
 
 namespace mok {
 
-enum FfnVariant : int { F_GATEUP = 0, F_DOWN, F_DACT, F_DX };  // the row-tiled ones (M = T)
-
 __host__ __device__ constexpr bool ffn_b_mn(int v) { return v >= F_DACT; }
-
-constexpr int kFfnBK = 64;  // bf16 of K per block: one 128-byte swizzle row
 
 struct FfnArgs {
   int32_t M, N;         // rows and columns of the output

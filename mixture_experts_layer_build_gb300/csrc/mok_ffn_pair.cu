@@ -18,8 +18,6 @@
 // Measured: a training step of 8192 tokens at H = 4096, I = 1536 518 us, 1,790 TFLOP/s (1,930 for a plain library product
 // in bursts), 603 us in a sustained loop; a forward of 4096 tokens at H = 2048, I = 1024 38.3 us, 1,350 TFLOP/s; a
 // training step of 1003 tokens at H = 2056, I = 1000 61 us: its four launches cost 5 us each besides their tiles.
-#include <initializer_list>
-
 #include "mok_ffn.cuh"
 
 namespace mok {
@@ -27,20 +25,6 @@ namespace {
 
 constexpr int kPairThreads = 64 + 32 * 8;
 constexpr uint32_t kPairTmemCols = 512;  // two accumulators, 256 columns apart
-constexpr int kGroupM = 4;  // M tiles of one band of the tile order
-
-// How a launch's tiles are dealt out to its `pairs` CTA pairs.  Job 0 is the row-tiled contraction, job 1 the weight
-// gradients; in the forward, the same contraction's last rows in narrower tiles.  The first job's units go round
-// robin: pairs below `rem` get `quot` + 1, the rest `quot`.  Of the second job's, every pair gets `each`, round robin,
-// and the pairs from `rem` on `extra` before them.
-struct PairPlan {
-  int32_t pairs;
-  int32_t first;        // which job goes first
-  int32_t quot, rem;
-  int32_t each, extra;
-  int32_t units[2];
-};
-
 struct PairArgs {
   FfnArgs f;            // job 0
   PairPlan plan;
@@ -89,34 +73,11 @@ struct PairUnit {
   int k_blocks;
 };
 
-// Tile u of an m_tiles x n_tiles output in bands of kGroupM M tiles, M fastest within a band.
-__device__ __forceinline__ void ordered_tile(int u, int m_tiles, int n_tiles, int& m, int& n) {
-  const int band = u / (kGroupM * n_tiles), r = u - band * (kGroupM * n_tiles);
-  const int rows = min(kGroupM, m_tiles - band * kGroupM);
-  n = r / rows;
-  m = band * kGroupM + (r - n * rows);
-}
-
-// Units of pair `pair`, and its i-th one; false when that slot of the plan is empty.
-template <int VAR>
-__device__ __forceinline__ int pair_steps(const PairArgs& p, int pair) {
-  const PairPlan& g = p.plan;
-  return g.quot + (pair < g.rem ? 1 : 0) + g.each + (pair >= g.rem ? g.extra : 0);
-}
+// The i-th unit of pair `pair`; false when that slot of the plan is empty.
 template <int VAR, int BN, bool MIX>
 __device__ __forceinline__ bool pair_unit(const PairArgs& p, int pair, int i, PairUnit& w) {
-  const PairPlan& g = p.plan;
   int u;
-  const int mine = g.quot + (pair < g.rem ? 1 : 0);
-  if (i < mine) {
-    u = i * g.pairs + pair;
-    w.job = g.first;
-  } else {
-    const int j = i - mine, e = pair >= g.rem ? g.extra : 0;
-    u = j < e ? g.each * g.pairs + j * (g.pairs - g.rem) + (pair - g.rem) : (j - e) * g.pairs + pair;
-    w.job = 1 - g.first;
-    if (u >= g.units[w.job]) return false;
-  }
+  if (!plan_unit(p.plan, pair, i, w.job, u)) return false;
   w.which = 0;
   w.bn = BN;
   if constexpr (VAR < P_BWD1) {
@@ -393,7 +354,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const uint32_t drain = bar0 + 8u * (2 * S + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int pair = static_cast<int>(blockIdx.x >> 1), steps = pair_steps<VAR>(p, pair);
+  const int pair = static_cast<int>(blockIdx.x >> 1), steps = plan_steps(p.plan, pair);
   uint32_t* status = p.f.status;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -586,82 +547,9 @@ int launch_pair(const PairMaps& maps, const PairArgs& p, cudaStream_t stream) {
   return static_cast<int>(e);
 }
 
-int64_t tiles_of(int64_t n, int64_t tile) { return (n + tile - 1) / tile; }
-
-// The plan of a launch with units[j] tiles of k[j] K blocks of job j on at most `pairs` pairs, the job with the longer
-// K first unless `rows_first`; returns the K blocks of the pair that has the most.
-int64_t make_plan(const int64_t (&units)[2], const int64_t (&k)[2], bool rows_first, int pairs, PairPlan* g) {
-  const int first = units[0] && (!units[1] || rows_first || k[0] >= k[1]) ? 0 : 1, second = 1 - first;
-  const int64_t total = units[0] + units[1], n = total < pairs ? total : pairs;
-  g->pairs = static_cast<int32_t>(n);
-  g->first = first;
-  g->units[0] = static_cast<int32_t>(units[0]);
-  g->units[1] = static_cast<int32_t>(units[1]);
-  const int64_t quot = units[first] / n, rem = units[first] % n;
-  g->quot = static_cast<int32_t>(quot);
-  g->rem = static_cast<int32_t>(rem);
-  const int64_t ca = (quot + 1) * k[first], cb = quot * k[first];  // K blocks of a pair below rem, and of the rest
-  int64_t end = rem ? ca : cb;                                     // no pair ends before its first job
-  g->each = g->extra = 0;
-  if (units[second]) {
-    // the earliest end by which the pairs can have taken all of the second job: it is reached either by a whole
-    // number of units behind `ca` or behind `cb`
-    const int64_t ks = k[second];
-    auto room = [&](int64_t t) { return (rem ? rem * ((t - ca) / ks) : 0) + (n - rem) * ((t - cb) / ks); };
-    const int64_t share = (units[0] * k[0] + units[1] * k[1]) / n;  // none can end before an even share
-    const int64_t least = end > share ? end : share;
-    int64_t best = -1;
-    for (int64_t c : {rem ? ca : cb, cb}) {
-      int64_t t = c + (least > c ? (least - c + ks - 1) / ks * ks : 0);
-      while (room(t) < units[second]) t += ks;
-      if (best < 0 || t < best) best = t;
-    }
-    end = best;
-    const int64_t nb = (end - cb) / ks, na = rem ? (end - ca) / ks : nb;
-    g->each = static_cast<int32_t>(na);
-    g->extra = static_cast<int32_t>(nb - na);
-  }
-  return end;
-}
-
-// What a 64-wide K block takes on a pair, in ns: measured 300 at 256 columns, 270 and 240 at 224 and 192 (the loads
-// from L2 bound it: 128 + columns / 2 rows of 128 bytes per CTA), 205 to 285 at 128.
-constexpr int64_t block_ns(int bn) { return bn == 256 ? 300 : bn == 224 ? 270 : bn == 192 ? 240 : 220; }
-
-// The tile width of the least cost, and that cost: the longest pair's time, a tile counted as its K blocks and one more
-// for what it costs besides them, three for a row-tiled one where those go first (rows_first: an epilogue there stands
-// at the end of some pairs).  tiles(bn, units) gives each job's tiles.  Against counting K blocks x (columns + 16):
-// 41 training sizes 0.976 of the time on average, 0.82 to 1.03; T = 9602, H = 4024, I = 848 forward 205 -> 170 us,
-// T = 2675, H = 3992, I = 536 training 143 -> 132.
-struct Width {
-  int bn;
-  int64_t cost;
-};
-template <class Tiles>
-Width best_width(std::initializer_list<int> widths, const int64_t (&k)[2], bool rows_first, int pairs, Tiles&& tiles) {
-  const int64_t k1[2] = {k[0] + (rows_first ? 3 : 1), k[1] + 1};
-  Width best{0, 0};
-  for (int bn : widths) {
-    int64_t units[2] = {0, 0};
-    PairPlan g;
-    tiles(bn, units);
-    if (!units[0] && !units[1]) return Width{0, 0};
-    const int64_t c = make_plan(units, k1, rows_first, pairs, &g) * block_ns(bn);
-    if (!best.bn || c < best.cost) best = Width{bn, c};
-  }
-  return best;
-}
-
-// A forward tile's time: its K blocks and three more.
-constexpr int64_t fwd_cost(int64_t k_blocks, int bn) { return (k_blocks + 3) * block_ns(bn); }
-
 bool fits(const int64_t (&units)[2]) { return units[0] + units[1] < (int64_t{1} << 30); }
 
-// GATEUP or DOWN: M rows, N output columns, K.  The first m_split M tiles in tiles of BN columns, the others of bn1.
-struct FwdSplit {
-  int bn0, bn1;  // bn1 = 0: no others
-  int64_t m_split;
-};
+// GATEUP or DOWN: M rows, N output columns, K, in the widths of `d`.
 template <int VAR, int BN>
 int pair_fwd(int64_t M, int64_t N, int64_t K, const FwdSplit& d, int pairs, const FfnOperands& o, const FfnArgs& f,
              cudaStream_t stream) {
@@ -697,39 +585,11 @@ int pair_fwd(int64_t M, int64_t N, int64_t K, const FwdSplit& d, int pairs, cons
   return launch_pair<VAR, BN, false>(t, p, stream);
 }
 
-// The widths of least cost.  With up to four rounds of tiles, the M tiles that do not fill whole rounds may take a
-// narrower width, so that the last round is shorter rather than part empty: T = 4096, H = 2048, I = 1024 40.7 -> 38.3 us
-// (76 pairs; 256 columns in nine of 16 M tiles, 192 in seven), T = 700, H = I = 3400 66.4 -> 64.1.
-template <int VAR>
-FwdSplit fwd_split(int64_t M, int64_t N, int64_t K, int pairs) {
-  const int64_t mt = tiles_of(M, 256), kb = tiles_of(K, kFfnBK), cols = VAR == P_GATEUP ? 2 * N : N;
-  constexpr int kWidths[4] = {256, 224, 192, 128};
-  FwdSplit best{0, 0, mt};
-  int64_t cost = 0;
-  for (int w : kWidths) {
-    if (VAR == P_GATEUP && w == 224) continue;  // half of the columns are gate columns, in whole 32-column chunks
-    const int64_t c = (mt * tiles_of(cols, w) + pairs - 1) / pairs * fwd_cost(kb, w);
-    if (!best.bn0 || c < cost) best.bn0 = w, cost = c;
-  }
-  for (int w : kWidths) {
-    const int64_t n = tiles_of(cols, w), rounds = mt * n / pairs, m = rounds * pairs / n;
-    if ((VAR == P_GATEUP && w == 224) || rounds < 1 || rounds > 3 || m <= 0 || m >= mt) continue;
-    for (int v : kWidths) {
-      if (v >= w || (VAR == P_GATEUP && v == 224)) continue;
-      PairPlan g;
-      const int64_t units[2] = {m * n, (mt - m) * tiles_of(cols, v)};
-      const int64_t c = make_plan(units, {fwd_cost(kb, w), fwd_cost(kb, v)}, true, pairs, &g);
-      if (c < cost) best = FwdSplit{w, v, m}, cost = c;
-    }
-  }
-  return best;
-}
-
 template <int VAR>
 int pair_fwd_any(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const FfnArgs& f, cudaStream_t stream) {
   const int pairs = sm_count() / 2;
   if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
-  const FwdSplit d = fwd_split<VAR>(M, N, K, pairs);
+  const FwdSplit d = fwd_split(VAR == P_GATEUP, M, N, K, pairs);
   if constexpr (VAR == P_DOWN) {
     if (d.bn0 == 224) return pair_fwd<VAR, 224>(M, N, K, d, pairs, o, f, stream);
   }
@@ -738,26 +598,8 @@ int pair_fwd_any(int64_t M, int64_t N, int64_t K, const FfnOperands& o, const Ff
   return pair_fwd<VAR, 128>(M, N, K, d, pairs, o, f, stream);
 }
 
-// What a launch of the backward does: its row-tiled contraction (DACT or DX), dWg and dWu, dWd.
-struct BwdJobs {
-  bool rows, gate_up, down;
-};
 template <int VAR>
-void bwd_tiles(const FfnBackward& b, const BwdJobs& j, int w, int64_t* units) {
-  units[0] = j.rows ? tiles_of(b.T, 256) * tiles_of(VAR == P_BWD1 ? b.I : b.H, w) : 0;
-  units[1] = (j.gate_up ? 2 * tiles_of(b.I, 256) * tiles_of(b.H, w) : 0) +
-             (j.down ? tiles_of(b.H, 256) * tiles_of(b.I, w) : 0);
-}
-// DACT's tiles go before dWd's, whose MMAs then hide its epilogue.
-template <int VAR>
-constexpr bool rows_first() { return VAR == P_BWD1; }
-
-template <int VAR>
-Width bwd_width(const FfnBackward& b, const BwdJobs& j, int pairs) {
-  const int64_t k[2] = {VAR == P_BWD1 ? tiles_of(b.H, kFfnBK) : 2 * tiles_of(b.I, kFfnBK), tiles_of(b.T, kFfnBK)};
-  return best_width({256, 224, 192, 128}, k, rows_first<VAR>(), pairs,
-                    [&](int w, int64_t* u) { bwd_tiles<VAR>(b, j, w, u); });
-}
+constexpr int phase_of() { return VAR == P_BWD1 ? 1 : 2; }
 
 template <int VAR, int BN>
 int pair_bwd(const FfnBackward& b, const BwdJobs& j, int pairs, cudaStream_t stream) {
@@ -784,9 +626,9 @@ int pair_bwd(const FfnBackward& b, const BwdJobs& j, int pairs, cudaStream_t str
   p.u1 = j.gate_up ? p.m_tiles_i * p.n_tiles_h : 0;
   p.k_blocks1 = static_cast<int32_t>(tiles_of(b.T, kFfnBK));
   int64_t units[2];
-  bwd_tiles<VAR>(b, j, BN, units);
+  bwd_tiles(phase_of<VAR>(), b.T, b.H, b.I, j, BN, units);
   if (!fits(units)) return static_cast<int>(cudaErrorInvalidValue);
-  make_plan(units, {p.f.k_blocks, p.k_blocks1}, rows_first<VAR>(), pairs, &p.plan);
+  make_plan(units, {p.f.k_blocks, p.k_blocks1}, rows_first(phase_of<VAR>()), pairs, &p.plan);
   const uint64_t t = static_cast<uint64_t>(b.T), h = static_cast<uint64_t>(b.H), i = static_cast<uint64_t>(b.I);
   PairMaps m{};
   auto dw_map = [&](CUtensorMap* tm, void* d, uint64_t inner, uint64_t outer) {
@@ -814,7 +656,7 @@ int pair_bwd(const FfnBackward& b, const BwdJobs& j, int pairs, cudaStream_t str
 
 template <int VAR>
 int pair_bwd_any(const FfnBackward& b, const BwdJobs& j, int pairs, cudaStream_t stream) {
-  switch (bwd_width<VAR>(b, j, pairs).bn) {
+  switch (bwd_width(phase_of<VAR>(), b.T, b.H, b.I, j, pairs).bn) {
     case 0: return 0;
     case 256: return pair_bwd<VAR, 256>(b, j, pairs, stream);
     case 224: return pair_bwd<VAR, 224>(b, j, pairs, stream);
@@ -834,14 +676,8 @@ int launch_ffn_pair_fwd(int var, int64_t M, int64_t N, int64_t K, const FfnOpera
 int launch_ffn_pair_bwd(int phase, const FfnBackward& b, cudaStream_t stream) {
   const int pairs = sm_count() / 2;
   if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
-  // dWd goes with DACT where the two launches then cost less
-  BwdJobs one{b.dact, false, b.dw_down != nullptr}, two{b.dx_rows, b.dw_gate != nullptr, false};
-  BwdJobs one_x = one, two_x = two;
-  one_x.down = false;
-  two_x.down = one.down;
-  if (!b.dact || bwd_width<P_BWD1>(b, one_x, pairs).cost + bwd_width<P_BWD2>(b, two_x, pairs).cost <=
-                     bwd_width<P_BWD1>(b, one, pairs).cost + bwd_width<P_BWD2>(b, two, pairs).cost)
-    one = one_x, two = two_x;
+  BwdJobs one, two;
+  bwd_jobs(b.T, b.H, b.I, b.dact, b.dx_rows, b.dw_gate != nullptr, b.dw_down != nullptr, pairs, &one, &two);
   return phase == 1 ? pair_bwd_any<P_BWD1>(b, one, pairs, stream) : pair_bwd_any<P_BWD2>(b, two, pairs, stream);
 }
 
