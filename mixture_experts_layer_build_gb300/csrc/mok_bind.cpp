@@ -89,6 +89,19 @@ PyObject* wrap_all(const Tensor (&t)[N]) {
   return r;
 }
 
+// Runs f() with x's device current and Python's lock free: an allocation or a launch may wait for the GPU (memory to be
+// freed, a full queue), and what the GPU waits for may need another thread.
+template <class F>
+int on_device(const Tensor& x, F&& f) {
+  struct Unlocked {
+    PyThreadState* const state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+  };
+  const c10::cuda::CUDAGuard guard(x.device());
+  const Unlocked unlocked;
+  return f();
+}
+
 template <class F>
 PyObject* guarded(F&& f) {  // no C++ exception leaves (an allocation may fail)
   try {
@@ -122,19 +135,20 @@ PyObject* rmsnorm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!drop_arg(a[4], x->device(), &drop)) Py_RETURN_NONE;
     const int bf16 = PyObject_IsTrue(a[5]), mx = PyObject_IsTrue(a[6]);
     if (PyErr_Occurred()) return nullptr;
-    const c10::cuda::CUDAGuard guard(x->device());
     Tensor out[5];
-    if (res || drop) out[0] = make({T, H}, *x, stream.scalar_type());
-    if (bf16) out[1] = make({T, H}, *x, at::kBFloat16);
-    if (mx) {
-      out[2] = make({T, H}, *x, at::kByte);
-      out[3] = make({T, H / 32}, *x, at::kByte);
-    }
-    out[4] = make({T}, *x, at::kFloat);
-    const mok_norm_shape shape{T, static_cast<int32_t>(H), st, static_cast<float>(eps)};
-    const int rc = mok_rmsnorm_forward(&shape, x->data_ptr(), ptr(res), drop, w->data_ptr(), ptr(out[0]), ptr(out[1]),
-                                       static_cast<uint8_t*>(ptr(out[2])), static_cast<uint8_t*>(ptr(out[3])),
-                                       static_cast<float*>(ptr(out[4])), current_stream(*x));
+    const int rc = on_device(*x, [&] {
+      if (res || drop) out[0] = make({T, H}, *x, stream.scalar_type());
+      if (bf16) out[1] = make({T, H}, *x, at::kBFloat16);
+      if (mx) {
+        out[2] = make({T, H}, *x, at::kByte);
+        out[3] = make({T, H / 32}, *x, at::kByte);
+      }
+      out[4] = make({T}, *x, at::kFloat);
+      const mok_norm_shape shape{T, static_cast<int32_t>(H), st, static_cast<float>(eps)};
+      return mok_rmsnorm_forward(&shape, x->data_ptr(), ptr(res), drop, w->data_ptr(), ptr(out[0]), ptr(out[1]),
+                                 static_cast<uint8_t*>(ptr(out[2])), static_cast<uint8_t*>(ptr(out[3])),
+                                 static_cast<float*>(ptr(out[4])), current_stream(*x));
+    });
     return rc ? PyLong_FromLong(rc) : wrap_all(out);
   });
 }
@@ -158,15 +172,16 @@ PyObject* rmsnorm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const mok_norm_shape shape{T, static_cast<int32_t>(H), st, 0.0f};
     const size_t bytes = mok_rmsnorm_workspace_bytes(&shape);
     if (!bytes) return PyLong_FromLong(MOK_ERR_INVALID_ARG);
-    const c10::cuda::CUDAGuard guard(h->device());
     Tensor out[3];
-    out[0] = make({T, H}, *h, h->scalar_type());
-    if (drop || st != MOK_DT_BF16) out[1] = make({T, H}, *h, at::kBFloat16);
-    out[2] = make({H}, *h, at::kFloat);
-    const Tensor ws = make({static_cast<int64_t>(bytes)}, *h, at::kByte);
-    const int rc = mok_rmsnorm_backward(&shape, h->data_ptr(), static_cast<const float*>(rstd->data_ptr()), w->data_ptr(),
-                                        dy->data_ptr(), ptr(dres), drop, ptr(out[0]), ptr(out[1]),
-                                        static_cast<float*>(ptr(out[2])), ws.data_ptr(), bytes, current_stream(*h));
+    const int rc = on_device(*h, [&] {
+      out[0] = make({T, H}, *h, h->scalar_type());
+      if (drop || st != MOK_DT_BF16) out[1] = make({T, H}, *h, at::kBFloat16);
+      out[2] = make({H}, *h, at::kFloat);
+      const Tensor ws = make({static_cast<int64_t>(bytes)}, *h, at::kByte);
+      return mok_rmsnorm_backward(&shape, h->data_ptr(), static_cast<const float*>(rstd->data_ptr()), w->data_ptr(),
+                                  dy->data_ptr(), ptr(dres), drop, ptr(out[0]), ptr(out[1]),
+                                  static_cast<float*>(ptr(out[2])), ws.data_ptr(), bytes, current_stream(*h));
+    });
     return rc ? PyLong_FromLong(rc) : wrap_all(out);
   });
 }
@@ -184,9 +199,11 @@ PyObject* dropout_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const mok_dropout* drop;
     if (!drop_arg(a[1], x->device(), &drop)) Py_RETURN_NONE;
     if (PyErr_Occurred()) return nullptr;
-    const c10::cuda::CUDAGuard guard(x->device());
-    const Tensor out[1] = {given ? *given : make(x->sizes(), *x, stream.scalar_type())};
-    const int rc = mok_dropout_forward(x->numel(), st, drop, x->data_ptr(), ptr(res), ptr(out[0]), current_stream(*x));
+    Tensor out[1];
+    const int rc = on_device(*x, [&] {
+      out[0] = given ? *given : make(x->sizes(), *x, stream.scalar_type());
+      return mok_dropout_forward(x->numel(), st, drop, x->data_ptr(), ptr(res), ptr(out[0]), current_stream(*x));
+    });
     return rc ? PyLong_FromLong(rc) : wrap_all(out);
   });
 }
@@ -203,9 +220,11 @@ PyObject* dropout_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const mok_dropout* drop;
     if (!drop_arg(a[1], dout->device(), &drop)) Py_RETURN_NONE;
     if (PyErr_Occurred()) return nullptr;
-    const c10::cuda::CUDAGuard guard(dout->device());
-    const Tensor out[1] = {given ? *given : make(dout->sizes(), *dout, at::kBFloat16)};
-    const int rc = mok_dropout_backward(dout->numel(), st, drop, dout->data_ptr(), ptr(out[0]), current_stream(*dout));
+    Tensor out[1];
+    const int rc = on_device(*dout, [&] {
+      out[0] = given ? *given : make(dout->sizes(), *dout, at::kBFloat16);
+      return mok_dropout_backward(dout->numel(), st, drop, dout->data_ptr(), ptr(out[0]), current_stream(*dout));
+    });
     return rc ? PyLong_FromLong(rc) : wrap_all(out);
   });
 }
@@ -214,8 +233,8 @@ bool mat(const Tensor& t, int64_t rows, int64_t cols) {
   return plain(t, at::kBFloat16) && t.dim() == 2 && t.size(0) == rows && t.size(1) == cols;
 }
 
-// (device, shape, out, ctx, ctx bytes, save, status: the plan's index, addresses and sizes, x, w_gate, w_up, w_down, residual, stream
-// or None: the current one of x's device) -> ()
+// (device, shape, out, ctx, ctx bytes, save, status: the plan's index, addresses and sizes, x, w_gate, w_up, w_down,
+// residual, stream or None: the current one of x's device) -> ()
 PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const Tensor *x, *wg, *wu, *wd, *res;
@@ -235,15 +254,16 @@ PyObject* ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Py_RETURN_NONE;
     void* stream = a[12] == Py_None ? current_stream(*x) : PyLong_AsVoidPtr(a[12]);
     if (PyErr_Occurred()) return nullptr;
-    const c10::cuda::CUDAGuard guard(x->device());
-    const int rc = mok_ffn_forward(s, x->data_ptr(), wg->data_ptr(), wu->data_ptr(), wd->data_ptr(), ptr(res), out, ctx,
-                                   bytes, static_cast<int32_t>(save), status, stream);
+    const int rc = on_device(*x, [&] {
+      return mok_ffn_forward(s, x->data_ptr(), wg->data_ptr(), wu->data_ptr(), wd->data_ptr(), ptr(res), out, ctx, bytes,
+                             static_cast<int32_t>(save), status, stream);
+    });
     return rc ? PyLong_FromLong(rc) : PyTuple_New(0);
   });
 }
 
-// (device, shape, ctx, ctx bytes, gradients, ws, ws bytes, status: the plan's index, addresses and sizes, x, w_gate, w_up, w_down, dy,
-// dx_add, stream or None: the current one of x's device) -> ()
+// (device, shape, ctx, ctx bytes, gradients, ws, ws bytes, status: the plan's index, addresses and sizes, x, w_gate, w_up,
+// w_down, dy, dx_add, stream or None: the current one of x's device) -> ()
 PyObject* ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     const Tensor *x, *wg, *wu, *wd, *dy, *add;
@@ -265,11 +285,12 @@ PyObject* ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       Py_RETURN_NONE;
     void* stream = a[14] == Py_None ? current_stream(*x) : PyLong_AsVoidPtr(a[14]);
     if (PyErr_Occurred()) return nullptr;
-    const c10::cuda::CUDAGuard guard(x->device());
     mok_ffn_grads g = *plan;
     g.dx_add = ptr(add);
-    const int rc = mok_ffn_backward(s, x->data_ptr(), wg->data_ptr(), wu->data_ptr(), wd->data_ptr(), ctx, ctx_bytes,
-                                    dy->data_ptr(), &g, ws, ws_bytes, status, stream);
+    const int rc = on_device(*x, [&] {
+      return mok_ffn_backward(s, x->data_ptr(), wg->data_ptr(), wu->data_ptr(), wd->data_ptr(), ctx, ctx_bytes,
+                              dy->data_ptr(), &g, ws, ws_bytes, status, stream);
+    });
     return rc ? PyLong_FromLong(rc) : PyTuple_New(0);
   });
 }
