@@ -513,7 +513,8 @@ MOK_API mok_status mok_ffn_forward(const mok_ffn_shape* shape, const void* x, co
                                    int32_t save, uint32_t* status, void* stream);
 
 /* Gradients, overwritten: dx [T, H] bf16; dw_gate, dw_up [I, H] and dw_down [H, I] of dw_type (mok_dtype;
- * T = 0 gives zeros).  dx, dw_down, or dw_gate and dw_up together, may be NULL: not computed.
+ * T = 0 gives zeros).  dx, dw_down, or dw_gate and dw_up together, may be NULL: not computed.  dx is written while
+ * weight gradients read x and dy: it must not overlap dy where dw_down is wanted, nor x where dw_gate and dw_up are.
  *   dx_add   [T, H] bf16 or NULL (0), added to dx before its one rounding: x's gradient from its other uses (the
  *            routed layer's dx); may be dx's buffer. */
 typedef struct {

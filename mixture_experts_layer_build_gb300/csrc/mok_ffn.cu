@@ -32,6 +32,10 @@ struct FfnCtx {
 };
 
 bool unaligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+bool overlap(const void* a, const void* b, size_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < n : x - y < n;
+}
 bool need16(const void* p) { return p && !unaligned(p, 16); }
 
 bool on_pairs(int var, int64_t M, int64_t N) { return ffn_on_pairs(var, M, N, sm_count()); }
@@ -103,6 +107,10 @@ mok_status mok_ffn_backward(const mok_ffn_shape* s, const void* x, const void* w
     return MOK_OK;
   }
   if (!need16(x) || !need16(w_gate) || !need16(w_up) || !need16(w_down) || !need16(dy)) return MOK_ERR_INVALID_ARG;
+  // dx is written while the weight gradients read x and dy
+  const size_t tokens = static_cast<size_t>(s->T) * s->H * 2;
+  if (gr->dx && ((gr->dw_down && overlap(gr->dx, dy, tokens)) || (gr->dw_gate && overlap(gr->dx, x, tokens))))
+    return MOK_ERR_INVALID_ARG;
   uint16_t* dg = static_cast<uint16_t*>(ws);
   uint16_t* du = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + up256(static_cast<size_t>(s->T) * s->I * 2));
   FfnBackward b{};

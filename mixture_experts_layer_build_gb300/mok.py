@@ -847,13 +847,17 @@ class FFN:
 
     def backward(self, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor,
                  dy: torch.Tensor, dx_add: torch.Tensor | None = None, stream=None) -> FFNGrads:
-        """Gradients of the last forward; dx_add: x's gradient from its other uses, added to dx."""
+        """Gradients of the last forward; dx_add: x's gradient from its other uses, added to dx.  x and dy are not the
+        plan's own dx (of a backward before); dx_add may be."""
         if not self.train:
             raise ValueError("backward needs a plan made with train=True")
         _check_stream(stream, x)
         r = _bind.ffn_backward(*self._bwd, x, w_gate, w_up, w_down, dy, dx_add, None if stream is None else _stream(stream))
         if type(r) is not tuple:
             like = (self.T, self.H), torch.bfloat16
+            for t, name in ((x, "x"), (dy, "dy")):
+                if r == MOK_ERR_INVALID_ARG and t.data_ptr() == self.grads.dx.data_ptr():
+                    raise ValueError(f"{name} must not be the plan's dx, which is written while {name} is read")
             _refused(r, "mok_ffn_backward", *self._in(x, w_gate, w_up, w_down), (dy, *like, "dy"),
                      *(() if dx_add is None else ((dx_add, *like, "dx_add"),)), (self.out, None, None, "the plan"))
         return self.grads
