@@ -863,7 +863,10 @@ class FFN:
         return self.grads
 
     def device_status(self) -> int:
-        """The block's device status word, bits (1 << status code); synchronises."""
+        """The block's device status word, bits (1 << status code), after all work on its device, on whatever stream;
+        synchronises."""
+        if self.status.is_cuda:
+            torch.cuda.synchronize(self.status.device)
         return int(self.status.item())
 
 

@@ -89,5 +89,6 @@ class Sublayer:
                                       f.dw_down)
 
     def device_status(self) -> int:
-        """Bits (1 << status code) of the layer's and the shared expert's device status; synchronises."""
-        return mok.mok_read_device_status(self.layer.sched) | self.ffn.device_status()
+        """Bits (1 << status code) of the layer's and the shared expert's device status, after all work on their device,
+        on whatever stream; synchronises."""
+        return self.ffn.device_status() | mok.mok_read_device_status(self.layer.sched)

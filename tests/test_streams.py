@@ -164,3 +164,24 @@ def test_weight_copies_on_a_given_stream(mok):
     assert all(owner(t) == side.cuda_stream for t in got.values())
     torch.cuda.synchronize()
     assert all(torch.equal(got[k], want[k]) for k in want)
+
+
+@pytest.mark.gpu
+def test_device_status_waits_for_every_stream(mok):
+    from mixture_experts_layer_build_gb300.sublayer import Sublayer
+    sub = Sublayer(16, 128, 128, 4, 2, 64)
+    ids, w = torch.zeros((16, 2), dtype=torch.int32, device="cuda"), torch.ones((16, 2), device="cuda")
+    ids[:, 1] = 1
+    side = torch.cuda.Stream()
+
+    def later(read):  # a problem that a kernel on another stream finds in half a second
+        sub.ffn.status.zero_()
+        sub.layer.schedule(ids, w)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000_000)
+            sub.ffn.status.fill_(1 << mok.MOK_ERR_TIMEOUT)
+            sub.layer.sched._view("status", 1).fill_(1 << mok.MOK_ERR_BAD_EXPERT_ID)
+        return read()
+    assert later(sub.ffn.device_status) == 1 << mok.MOK_ERR_TIMEOUT
+    assert later(sub.device_status) == 1 << mok.MOK_ERR_TIMEOUT | 1 << mok.MOK_ERR_BAD_EXPERT_ID
