@@ -501,8 +501,9 @@ typedef struct {
   int32_t act; /* mok_activation */
 } mok_ffn_shape;
 
-/* Bytes of the block's context (256-byte aligned device buffer).  save = 0: what one forward needs (a);
- * save = 1: with the factors of dg and du in fp32 for mok_ffn_backward.  0 for an unsupported shape. */
+/* Bytes of the block's context (256-byte aligned device buffer).  save = 0: what one forward needs (a, 2 T I bytes);
+ * save = 1: with the factors of dg and du in fp32 for mok_ffn_backward, 8 T I bytes more.  0 for an unsupported
+ * shape. */
 MOK_API size_t mok_ffn_ctx_bytes(const mok_ffn_shape* shape, int32_t save);
 
 /* Forward.  x [T, H] bf16; residual [T, H] bf16 or NULL (0); out [T, H] bf16 (may be the residual's

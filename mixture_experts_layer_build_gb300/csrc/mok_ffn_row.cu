@@ -10,10 +10,10 @@
 // (fma.rn.f32x2): along each lane's columns, the even and the odd ones apart, then a butterfly over the
 // warp, then the warps in ascending order.
 //
-// Measured (H = 4096, I = 1536, weights from HBM, both contractions): 9.1 us for one token, 13.4 for four,
-// against 14.3 on the tensor cores (mok_ffn_tile.cu) for any of 1 to 32; at H = 2048, I = 1024 6.9 and 10.1 for
-// four; at H = 7168, I = 2048 16.4 (5.4 TB/s) for one, 22.7 for four against 22.1.  For eight tokens it took 22.8 and
-// 41.0 at the larger two: the tokens' loads and the arithmetic, once per four weight rows, then outweigh the weights.
+// Measured (H = 4096, I = 1536, weights from HBM, both contractions): 9.1 us for one token, 10.7 for two, 13.3 for four,
+// against 13.6 to 14.1 on the tensor cores (mok_ffn_tile.cu) for any of 5 to 32; at H = 7168, I = 2048 16.3 (5.4 TB/s) for
+// one, 22.2 for four against 21.7.  For eight tokens it took 22.6 and 41.1 at the two: the tokens' loads and the
+// arithmetic, once per four weight rows, then outweigh the weights.
 // Hence kFfnRowTokens.
 #include "mok_ffn.cuh"
 

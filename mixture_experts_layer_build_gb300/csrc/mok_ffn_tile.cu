@@ -12,7 +12,7 @@
 // single-lane branch, a K block took 240 ns to issue whatever its size), the first loads are issued
 // before the CTA's set-up has finished, and the contractions that follow another of this block
 // load their weights before they wait for it.  Measured (both forward contractions, weights from HBM): 16 tokens at
-// H = 4096, I = 1536 14.3 us; 61 tokens at H = 7168, I = 2048 24.7 (13.0 of weights: gate/up streams at 7.1 TB/s; the rest
+// H = 4096, I = 1536 14.0 us; 61 tokens at H = 7168, I = 2048 23.9, 25.0 with a residual (13.0 of weights: gate/up streams at 7.1 TB/s; the rest
 // is first bytes, reductions and the launch between, when HBM idles).
 #include "mok_ffn.cuh"
 
@@ -24,8 +24,9 @@ constexpr int kTileMaxStages = 16;
 constexpr uint32_t kTileMaxSmem = 230400;  // what a launch may ask for
 // Tokens up to which the partials are counted on the owners' mbarriers, each CTA waiting for its own only; above, a
 // store that is counted costs more than the cluster barrier that orders plain ones: 16 tokens at H = 4096, I = 1536
-// 14.4 and 14.9 us, 48 tokens 15.0 and 15.3, 64 tokens 16.8 and 16.2, 128 tokens 25.2 and 22.5.  (Staged first and copied
-// in bulk: 14.7 and 23.3 for 16 and 128 tokens.)
+// 14.0 and 14.5 us, 48 tokens 14.9 both, 64 tokens 16.8 and 16.0, 128 tokens 21.6 and 19.4; at H = 7168, I = 2048 48 tokens
+// 22.0 and 22.5, 61 tokens 22.9 and 23.5, 128 tokens 31.6 and 28.9.  (Staged first and copied in bulk: 14.7 and 23.3 for 16
+// and 128 tokens at the first, when counted ones took 14.4 and plain ones 22.5.)
 constexpr int64_t kTileCounted = 48;
 constexpr uint32_t kTileSmem = 116224;  // two CTAs per SM
 

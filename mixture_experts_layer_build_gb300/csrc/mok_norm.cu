@@ -9,9 +9,9 @@
 // threads' registers between the row reduction and the outputs.  fp32 arithmetic throughout, one
 // rounding per output.  No atomics: the row sums and dweight are reduced in fixed orders.
 //
-// Measured (of 6,784 GB/s copy): forward 8192 x 4096 bf16 40.6 us (6.6 TB/s), with dropout and an MXFP8 output 40.4
-// (5.8: issue slots); backward 41.0 (6.5), with dropout 51.2 (6.6), 16384 x 7168 with an fp32 stream 289 (6.5);
-// dropout 29.2 (6.9), its backward at 16384 x 7168 74.2 (6.3).
+// Measured, every operand in memory of its own (of 6,784 GB/s copy): forward 8192 x 4096 bf16 40.6 us (6.6 TB/s), with
+// dropout and an MXFP8 output 40.4 (5.8: issue slots); backward 47.6 (5.6), with dropout 57.3 (5.9), 16384 x 7168 with an
+// fp32 stream 289 (6.5); dropout 32.8 (6.1), its backward at 16384 x 7168 74.2 (6.3), with an fp32 stream 105 (6.7).
 #include <cmath>
 #include <type_traits>
 
@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kNormMaxH = 16384;
 constexpr int kNormThreads = 512;  // most threads of a block
-constexpr int kNormParts = 608;  // most partial dweight rows: four CTAs on each of 152 SMs
+constexpr int kNormParts = 304;  // most partial dweight rows: two blocks of 256 threads on each of 152 SMs
 
 // fp32 values in pairs: one instruction for two (add, mul, fma .f32x2), each rounded as the scalar one.
 using Pair = uint64_t;
@@ -285,9 +285,10 @@ struct NormBwdArgs {
 // reduction.  Every thread sums dy xh of its columns over its rows in ascending order, the row groups
 // of a block are added in ascending order at the end: one partial row of dweight per block.  (Rows copied ahead into
 // shared memory by cp.async, for four blocks per SM instead of two, were slower: 59 against 57 us at
-// 8192 x 4096 bf16 with dropout, 375 against 230 at 16384 x 7168 with an fp32 stream.)
-// KNOWN (see above) takes 4096 x 2048 bf16 with dropout from 19.2 to 17.1 us; with an fp32 stream or four vectors its
-// registers do not suffice (16384 x 7168: 322 us against 230), so those never have it.
+// 8192 x 4096 bf16 with dropout, 375 against 230 at 16384 x 7168 with an fp32 stream, both with dres in h's buffer.)
+// KNOWN (see above) takes 4096 x 2048 bf16 with dropout from 19.2 to 17.1 us (dres in h's buffer; in its own 17.5 to
+// 19.4 us, the more the further apart the calls' outputs are); with an fp32 stream or four vectors its registers do not
+// suffice (16384 x 7168: 357 us against 289), so those never have it.
 template <int V, bool F32, int MAXT, int MINB, int KNOWN>
 __global__ void __launch_bounds__(MAXT, MINB) rmsnorm_bwd_kernel(const NormBwdArgs a) {
   constexpr bool FULL = KNOWN & kFull, STREAM = KNOWN & kStream;
@@ -510,12 +511,12 @@ struct RowPlan {
   bool full(const mok_norm_shape& s) const { return tpr * v * 8 == s.H && s.T % rows == 0; }
 };
 
-// Blocks of the backward, and partial rows of dweight: two 256-thread blocks' worth of threads per SM of 152 (a
+// Blocks of the backward, and partial rows of dweight: at most two blocks of 256 threads, or one of more, per SM of 152 (a
 // function of the shape alone, which the workspace is sized by).
 int norm_bwd_blocks(const mok_norm_shape& s) {
   const RowPlan p(s.H, false);
   const int64_t need = (s.T + p.rows - 1) / p.rows;
-  const int64_t cap = p.tpr > 256 ? kNormParts / 4 : kNormParts / 2;
+  const int64_t cap = p.tpr > 256 ? kNormParts / 2 : kNormParts;
   return static_cast<int>(need < cap ? need : cap);
 }
 

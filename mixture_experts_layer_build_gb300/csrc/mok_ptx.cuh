@@ -35,7 +35,8 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // kernels do signal, pdl_trigger() in mok_ffn.cuh: theirs load weights while they wait.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Deadline of any single wait inside a kernel (ns).  Legitimate waits last microseconds.
+// Deadline of any single wait inside a kernel (ns).  Legitimate waits last microseconds; the one that need not, for a
+// whole tile of a feed-forward weight gradient, has a longer one (mbar_wait_tile in mok_ffn.cuh).
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 __device__ __forceinline__ void record_status(uint32_t* status, uint32_t code) {

@@ -801,10 +801,11 @@ class FFNGrads:
 
 class FFN:
     """Owner of the buffers of one dense gated feed-forward block (mok_ffn_forward / _backward):
-    act(x Wg^T) * (x Wu^T) Wd^T + residual for T tokens, w_gate, w_up [I, H] and w_down [H, I] bf16.  act:
-    "silu" or "gelu" (tanh form).  train: the forward saves what the backward reads.  dw_dtype: type
-    of the weight gradients, torch.bfloat16 or torch.float32.  Outputs are the plan's own buffers,
-    overwritten by the next call."""
+    act(x Wg^T) * (x Wu^T) Wd^T + residual for exactly T tokens (another number is another plan; the C calls take any),
+    w_gate, w_up [I, H] and w_down [H, I] bf16.  act: "silu" or "gelu" (tanh form).  train: the forward saves what the
+    backward reads, 8 T I bytes beside the 2 T I of a forward alone (126 MB in all at T = 8192, I = 1536), and the plan has
+    the backward's workspace, 4 T I bytes, and gradients.  dw_dtype: type of the weight gradients, torch.bfloat16 or
+    torch.float32.  Outputs are the plan's own buffers, overwritten by the next call."""
 
     def __init__(self, T: int, H: int, I: int, act: str = "silu", train: bool = True, dw_dtype=torch.bfloat16,
                  device="cuda"):
