@@ -659,6 +659,9 @@ class Dropout:
         self.ref = ctypes.byref(self.c)
         self.addr = ctypes.addressof(self._placed)
 
+    def __reduce__(self):  # a copy has addresses of its own
+        return Dropout, (self.c.p, self.rng)
+
 
 def _refused(result, where: str, *args):
     """Raises for what a compiled call returned instead of its tensors: the library's status, or None for a tensor
@@ -805,7 +808,8 @@ class FFN:
     w_gate, w_up [I, H] and w_down [H, I] bf16.  act: "silu" or "gelu" (tanh form).  train: the forward saves what the
     backward reads, 8 T I bytes beside the 2 T I of a forward alone (126 MB in all at T = 8192, I = 1536), and the plan has
     the backward's workspace, 4 T I bytes, and gradients.  dw_dtype: type of the weight gradients, torch.bfloat16 or
-    torch.float32.  Outputs are the plan's own buffers, overwritten by the next call."""
+    torch.float32.  Outputs are the plan's own buffers, overwritten by the next call.  A copy (copy, deepcopy, pickle) is
+    a new plan, whose buffers hold nothing yet."""
 
     def __init__(self, T: int, H: int, I: int, act: str = "silu", train: bool = True, dw_dtype=torch.bfloat16,
                  device="cuda"):
@@ -814,6 +818,7 @@ class FFN:
         if dw_dtype not in _STREAM_TYPES:
             raise ValueError(f"dw_dtype must be torch.bfloat16 or torch.float32, got {dw_dtype}")
         self.T, self.H, self.I, self.train = T, H, I, train
+        self._made_of = (T, H, I, act, train, dw_dtype)
         self.shape = mok_ffn_shape(T, H, I, _ACTS[act])
         self.ctx = torch.empty(mok_ffn_ctx_bytes(self.shape, train), dtype=torch.uint8, device=device)
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
@@ -830,6 +835,9 @@ class FFN:
                                         g.dw_down.data_ptr(), _STREAM_TYPES[dw_dtype])
             self._bwd = (self._device, ctypes.addressof(self.shape), self.ctx.data_ptr(), self.ctx.numel(),
                          ctypes.addressof(self._grads), self.ws.data_ptr(), self.ws.numel(), self.status.data_ptr())
+
+    def __reduce__(self):  # a copy has buffers, and addresses, of its own
+        return FFN, (*self._made_of, self.out.device)
 
     def _in(self, x, w_gate, w_up, w_down):
         xs, ws, bf = (self.T, self.H), (self.I, self.H), torch.bfloat16
