@@ -44,7 +44,8 @@ class ParamGrads:
 
 class Sublayer:
     """Buffers and plans for T tokens, E experts of [I, H] of which each token takes K, and a shared expert
-    of [shared_I, H].  cfg: the layer's configuration (bf16 precision)."""
+    of [shared_I, H].  cfg: the layer's configuration (bf16 precision).  out and the experts' gradients are the plans' own
+    buffers, overwritten by the next call."""
 
     def __init__(self, T: int, H: int, I: int, E: int, K: int, shared_I: int, act: str = "silu", eps: float = 1e-6,
                  cfg: mok.mok_config | None = None, shared_dw_dtype=torch.float32, device="cuda"):
