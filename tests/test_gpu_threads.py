@@ -46,4 +46,4 @@ def test_other_threads_run_while_a_launch_waits(call):
         other.join()
     torch.cuda.synchronize()
     assert longest > 0.4, longest  # a call did wait
-    assert max(gaps) < 0.2, max(gaps)
+    assert max(gaps) < longest / 2, (max(gaps), longest)  # the lock was not held while it did
