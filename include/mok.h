@@ -540,6 +540,114 @@ MOK_API mok_status mok_ffn_backward(const mok_ffn_shape* shape, const void* x, c
                                     const mok_ffn_grads* grads, void* ws, size_t ws_bytes, uint32_t* status,
                                     void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Routed rows as calls of their own: tokens sorted by expert and back, for experts that the caller
+ * computes (with the 8-bit products below, or with kernels of its own).  They work on any schedule of one
+ * rank's tokens: mok_build_schedule's, mok_build_schedule_noalloc's, or mok_build_routes'.
+ * A buffer of routed rows has sched->rpad_max rows in the schedule's layout: row inv[j] belongs to slot j,
+ * each expert's segment is padded to a multiple of 128 rows, the layout ends at row Rpad = meta[0], and
+ * rows from there on are neither read nor written.  Widths are multiples of 8 values up to 16384, of the caller's choice
+ * (not the shape's H); tensors start on a 16-byte boundary.  Slots whose id is invalid have no row: they
+ * contribute nothing and their gradients are 0.
+ * ------------------------------------------------------------------------------------------- */
+
+/* A schedule without the layer's staging buffers: the tables of mok_build_schedule for the same arguments (they
+ * do not depend on H, I or the precision), in a workspace of mok_routes_workspace_bytes bytes, 256-byte aligned.
+ * out->ws is NULL: mok_forward, mok_backward and mok_ep_* refuse it. */
+MOK_API size_t mok_routes_workspace_bytes(const mok_config* cfg, const mok_shape* shape);
+MOK_API mok_status mok_build_routes(const mok_config* cfg, const mok_shape* shape, const int32_t* topk_ids,
+                                    const float* topk_weights, void* ws, size_t ws_bytes, mok_schedule* out,
+                                    void* stream);
+
+/* rows[r] = x[token of r], zeros on padding rows.  x [T, width] bf16; rows [rpad_max, width] bf16. */
+MOK_API mok_status mok_dispatch(const mok_schedule* sched, const void* x, int32_t width, void* rows, void* stream);
+
+/* Its gradient: dx[t] = sum over k ascending of drows[inv[t,k]], fp32, rounded once.  dx [T, width] bf16. */
+MOK_API mok_status mok_dispatch_backward(const mok_schedule* sched, const void* drows, int32_t width, void* dx,
+                                         void* stream);
+
+/* out[t] = sum over k ascending of s[t,k] rows[inv[t,k]], fp32, rounded once, with the schedule's topk_weights
+ * (read now, not as they were when it was built).  out [T, width] bf16. */
+MOK_API mok_status mok_combine(const mok_schedule* sched, const void* rows, int32_t width, void* out, void* stream);
+
+/* Its gradients from dout [T, width] bf16:
+ *   drows[inv[t,k]] = s[t,k] dout[t], zeros on padding rows, bf16 [rpad_max, width]; may be rows' buffer;
+ *   d_topk_weights[t,k] = <dout[t], rows[inv[t,k]]>, fp32 [T, K], 0 for a slot without a row. */
+MOK_API mok_status mok_combine_backward(const mok_schedule* sched, const void* rows, const void* dout, int32_t width,
+                                        void* drows, float* d_topk_weights, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Products in 8-bit floating point with one fp32 scale per block of 128: E4M3 codes q, and
+ *   MOK_FP8_ROWS    a scale per row and 128 columns:  s [ceil(cols/128)][rows rounded up to 4], columns' blocks
+ *                   first (a tile's rows are read together); the value of (r, c) is q[r][c] s[c/128][r];
+ *   MOK_FP8_BLOCKS  a scale per 128 x 128 values, row-major: s [ceil(rows/128)][ceil(cols/128)].
+ * Codes are row-major, K (the summed index) along the row, `ld` bytes between rows: a multiple of 16, >= cols.
+ * Codes and scales start on a 16-byte boundary.  batch matrices of one shape follow one another: codes batch * rows * ld
+ * bytes, scales likewise; every matrix has its own blocks.
+ * Quantisation: t = max(amax of the block, 2^-50); scale = t / 448; code = E4M3(v * (448 / t)), round to nearest
+ * even; both divisions and the product are rounded to fp32.  A block that holds a NaN or an infinity gets a NaN scale
+ * and codes 0x7F (NaN).
+ * A product adds up each block of 128 exactly scaled: fp32 sums of a block's E4M3 products, each times the two scales'
+ * fp32 product, added in fp32 in ascending order of the blocks.  (Scales of 128 x 1e38 multiply to infinity: the two
+ * matrices' largest magnitudes may multiply to at most 6e43.)
+ * ------------------------------------------------------------------------------------------- */
+typedef enum { MOK_FP8_ROWS = 0, MOK_FP8_BLOCKS = 1 } mok_fp8_scaling;
+typedef struct {
+  const uint8_t* q;
+  const float* s;
+  int64_t rows, cols; /* of one matrix; cols is the summed index */
+  int64_t ld;
+  int32_t batch;      /* 1, or the number of experts */
+  int32_t scaling;    /* mok_fp8_scaling */
+} mok_fp8_matrix;
+
+/* Scales of x [rows, cols] bf16 per row (MOK_FP8_ROWS), of its rows and of the rows of its transpose:
+ *   q [rows][cols rounded up to 16], s [ceil(cols/128)][rows rounded up to 4]: x;
+ *   qt [cols][rows rounded up to 16], st [ceil(rows/128)][cols rounded up to 4]: x^T, for products that sum over x's rows.
+ * q and s, or qt and st, may be NULL.  rows >= 0 (below 2^31); cols a positive multiple of 8. */
+MOK_API mok_status mok_fp8_quantize(const void* x, int64_t rows, int32_t cols, uint8_t* q, float* s, uint8_t* qt,
+                                    float* st, void* stream);
+
+/* The same for routed rows (rows = rpad_max in the sizes above):
+ *   gather = 1: x [T, cols] holds tokens, the routed row r is x[token of r] (dispatch);
+ *   gather = 0: x [rpad_max, cols] holds routed rows.
+ * Padding rows count as zeros whatever x holds there; in q and s they are not written, in qt they are zeros.  Nothing
+ * from row Rpad on is written. */
+MOK_API mok_status mok_fp8_quantize_routed(const mok_schedule* sched, int32_t gather, const void* x, int32_t cols,
+                                           uint8_t* q, float* s, uint8_t* qt, float* st, void* stream);
+
+/* Scales per 128 x 128 values (MOK_FP8_BLOCKS) of `batch` matrices x [batch, rows, cols] bf16, and the same codes
+ * transposed: q [batch][rows][cols rounded up to 16], s [batch][ceil(rows/128)][ceil(cols/128)]; qt [batch][cols][rows
+ * rounded up to 16], st [batch][ceil(cols/128)][ceil(rows/128)].  q and s, or qt and st, may be NULL.  rows and cols
+ * positive multiples of 8. */
+MOK_API mok_status mok_fp8_quantize_blocks(const void* x, int32_t batch, int64_t rows, int32_t cols, uint8_t* q, float* s,
+                                           uint8_t* qt, float* st, void* stream);
+
+/* out [M, N] = a b^T; a [M, K] MOK_FP8_ROWS, b [N, K] of either scaling, batch 1.  out of out_type (mok_dtype), rounded
+ * once.  M, K >= 0 (K = 0 gives zeros), N a positive multiple of 8; each below 2^31.  status: device word (bit (1 << mok_status code) per problem
+ * seen, never cleared here) or NULL. */
+MOK_API mok_status mok_fp8_matmul(const mok_fp8_matrix* a, const mok_fp8_matrix* b, void* out, int32_t out_type,
+                                  uint32_t* status, void* stream);
+
+/* Bytes of device workspace (256-byte aligned) of mok_fp8_linear: x's codes and scales.  0 for an unsupported shape. */
+MOK_API size_t mok_fp8_linear_workspace_bytes(int64_t M, int64_t K);
+
+/* out [M, N] bf16 = x w^T for x [M, K] bf16, quantised on the way as by mok_fp8_quantize; w [N, K] MOK_FP8_BLOCKS, batch 1.
+ * K a positive multiple of 8. */
+MOK_API mok_status mok_fp8_linear(const void* x, int64_t M, const mok_fp8_matrix* w, void* out, void* ws, size_t ws_bytes,
+                                  uint32_t* status, void* stream);
+
+/* out[r] = a[r] w[expert of r]^T for every routed row: a [rpad_max, K] MOK_FP8_ROWS, w [E][N, K] MOK_FP8_BLOCKS (batch =
+ * E), out [rpad_max, N] bf16.  Padding rows of out are not written (nor what lies behind Rpad).  N a positive multiple of 8. */
+MOK_API mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matrix* a, const mok_fp8_matrix* w,
+                                          void* out, void* stream);
+
+/* dw[e] = sum over expert e's rows of a[:, r] b[:, r]^T: a [N, rpad_max], b [K, rpad_max] MOK_FP8_ROWS, transposed routed
+ * rows as mok_fp8_quantize_routed writes them; dw [E, N, K] of dw_type (an expert without rows gets zeros).  K = b's rows: a
+ * positive multiple of 8. */
+MOK_API mok_status mok_fp8_grouped_wgrad(const mok_schedule* sched, const mok_fp8_matrix* a, const mok_fp8_matrix* b,
+                                         void* dw, int32_t dw_type, void* stream);
+
 /* Copy the schedule's device status word to *out (host pointer) after synchronising the stream.
  * The only call that blocks. */
 MOK_API mok_status mok_read_device_status(const mok_schedule* sched, uint32_t* out, void* stream);

@@ -81,8 +81,9 @@ bool make_sizes(const mok_config* cfg, const mok_shape* shape, Sizes* s) {
   return true;
 }
 
-size_t carve_workspace(const Sizes& z, char* base, mok_schedule* s, Staging* st) {
-  Carver c{base};
+// The schedule's tables and the histogram that its build scratches in: what a routes workspace holds, and the
+// front of a layer's.
+static mok_schedule carve_tables(const Sizes& z, Carver& c, int32_t** chunk_hist) {
   mok_schedule d{};
   d.counts = c.take<int32_t>(z.E);
   d.offsets = c.take<int32_t>(z.E + 1);
@@ -95,8 +96,14 @@ size_t carve_workspace(const Sizes& z, char* base, mok_schedule* s, Staging* st)
   d.status = reinterpret_cast<uint32_t*>(d.meta ? d.meta + 15 : nullptr);
   d.row_weight = c.take<float>(z.rpad_max);
   d.row_token = c.take<int32_t>(z.rpad_max);
+  *chunk_hist = c.take<int32_t>(z.nchunks * (z.E + 1));
+  return d;
+}
+
+size_t carve_workspace(const Sizes& z, char* base, mok_schedule* s, Staging* st) {
+  Carver c{base};
   Staging t{};
-  t.chunk_hist = c.take<int32_t>(z.nchunks * (z.E + 1));
+  const mok_schedule d = carve_tables(z, c, &t.chunk_hist);
   t.ybuf = c.take<uint16_t>(z.rpad_max * z.H);
   if (!z.mx) {
     t.dyg = c.take<uint16_t>(z.rpad_max * z.H);
@@ -198,14 +205,15 @@ static EncodeTiledFn encode_fn() {
 }
 
 // 2-D tensor [outer, inner] (inner contiguous), 128-byte swizzled boxes [box_outer, box_inner].
+// pitch: bytes between rows, 0: rows follow one another.
 static bool make_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, uint32_t esize, const void* base, uint64_t inner,
                          uint64_t outer, uint32_t box_inner, uint32_t box_outer,
-                         CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B) {
+                         CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, uint64_t pitch = 0) {
   EncodeTiledFn fn = encode_fn();
   if (!fn || !base || !aligned16(base)) return false;
   if (outer == 0) outer = 1;
   const cuuint64_t dims[2] = {inner, outer};
-  const cuuint64_t strides[1] = {inner * esize};
+  const cuuint64_t strides[1] = {pitch ? pitch : inner * esize};
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -242,6 +250,11 @@ bool make_tmap_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t out
                                 : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                       : CU_TENSOR_MAP_SWIZZLE_NONE;
   return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, inner, outer, box_inner, box_outer, sw);
+}
+
+bool make_tmap_fp8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t pitch, uint32_t box_outer) {
+  return make_tmap_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, inner, outer, 128, box_outer,
+                      CU_TENSOR_MAP_SWIZZLE_128B, pitch);
 }
 
 // One thread waits on an mbarrier that nothing completes, through the bounded wait every GEMM role
@@ -337,6 +350,39 @@ mok_status mok_build_schedule(const mok_config* cfg, const mok_shape* shape, con
   s.topk_weights = topk_weights;
   s.ws = ws;
   s.ws_bytes = ws_bytes;
+  const int rc = launch_schedule(z, plain_route(topk_ids, topk_weights), s, st, as_stream(stream));
+  if (rc) return MOK_ERR_CUDA;
+  *out = s;
+  return MOK_OK;
+}
+
+size_t mok_routes_workspace_bytes(const mok_config* cfg, const mok_shape* shape) {
+  Sizes z;
+  if (!make_sizes(cfg, shape, &z)) return 0;
+  Carver c{nullptr};
+  int32_t* hist;
+  carve_tables(z, c, &hist);
+  return align_up(c.off);
+}
+
+mok_status mok_build_routes(const mok_config* cfg, const mok_shape* shape, const int32_t* topk_ids,
+                            const float* topk_weights, void* ws, size_t ws_bytes, mok_schedule* out, void* stream) {
+  Sizes z;
+  if (!out || !make_sizes(cfg, shape, &z)) return MOK_ERR_INVALID_ARG;
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) % kAlign) != 0) return MOK_ERR_INVALID_ARG;
+  if (z.R > 0 && (!topk_ids || !topk_weights)) return MOK_ERR_INVALID_ARG;
+  if (ws_bytes < mok_routes_workspace_bytes(cfg, shape)) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  Carver c{static_cast<char*>(ws)};
+  Staging st{};
+  mok_schedule s = carve_tables(z, c, &st.chunk_hist);
+  s.shape = *shape;
+  s.config = *cfg;
+  s.config.minibatch_rows = z.mb;
+  s.config.macrobatch_rows = z.MB;
+  s.rpad_max = z.rpad_max;
+  s.tiles_max = z.tiles_max;
+  s.mblocks_max = z.mblocks_max;
+  s.topk_weights = topk_weights;  // (ws stays NULL: there is no staging for the layer's calls)
   const int rc = launch_schedule(z, plain_route(topk_ids, topk_weights), s, st, as_stream(stream));
   if (rc) return MOK_ERR_CUDA;
   *out = s;
@@ -626,7 +672,9 @@ const char* mok_kernel_name(int32_t kind) {
       "router_dw",       "selftest_wait", "push_y",        "push_dx",        "ep_combine",
       "ep_dx_reduce",    "ds_push",       "rmsnorm_fwd",   "rmsnorm_bwd",    "rmsnorm_dw",
       "dropout_fwd",     "dropout_bwd",   "ffn_gateup",    "ffn_down",      "ffn_dact",
-      "ffn_dx",          "ffn_bwd1",      "ffn_bwd2"};
+      "ffn_dx",          "ffn_bwd1",      "ffn_bwd2",      "dispatch",      "dispatch_bwd",
+      "route_combine",   "combine_bwd",   "fp8_quantize",  "fp8_dispatch",  "fp8_weight",
+      "fp8_tile",        "fp8_pair",      "fp8_grouped_tile", "fp8_grouped_pair", "fp8_wgrad"};
   return (kind >= 0 && kind < K_NUM_KINDS) ? names[kind] : "?";
 }
 

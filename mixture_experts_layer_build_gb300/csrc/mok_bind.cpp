@@ -1,5 +1,5 @@
-// mok_bind.cpp -- the norm, dropout and feed-forward calls of the Python binding: checks, outputs and the C call in one
-// step.
+// mok_bind.cpp -- the norm, dropout, feed-forward, routed-row and 8-bit calls of the Python binding: checks, outputs and
+// the C call in one step.
 //
 // At small sizes the host is what bounds these calls: three tensors made one by one from Python and a call with eleven
 // arguments through ctypes took 15.3 us for a norm kernel of 1.6, now 6.4.  Each function returns its tensors in a
@@ -295,6 +295,267 @@ PyObject* ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ---- routed rows and 8-bit products ----
+
+// The address of a mok_schedule and the index of the device that holds its tables; nullptr (with an error set) when it
+// is none.
+struct PlacedSchedule {
+  const mok_schedule* s;
+  long device;
+};
+bool sched_arg(PyObject* addr, PyObject* device, PlacedSchedule* p) {
+  p->s = static_cast<const mok_schedule*>(PyLong_AsVoidPtr(addr));
+  p->device = PyLong_AsLong(device);
+  return p->s && !PyErr_Occurred();
+}
+bool rows_of(const Tensor& t, int64_t rows, int64_t cols, at::ScalarType type) {
+  return plain(t, type) && t.dim() == 2 && t.size(0) == rows && t.size(1) == cols;
+}
+
+int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+// Codes [.., rows, ld] and scales as one matrix; false where they do not go together.
+bool fp8_arg(PyObject* q, PyObject* s, PyObject* cols, bool block, int batch_dims, const Tensor** tq, const Tensor** ts,
+             mok_fp8_matrix* m) {
+  if (!tensor_arg(q, tq) || !tensor_arg(s, ts) || !*tq || !*ts) return false;
+  const Tensor &c = **tq, &f = **ts;
+  m->cols = PyLong_AsLongLong(cols);
+  if (PyErr_Occurred()) return false;
+  const int d = 2 + batch_dims;
+  if (c.dim() != d || f.dim() != d || !plain(c) || !plain(f, at::kFloat) || f.device() != c.device()) return false;
+  if (c.scalar_type() != at::kByte && c.scalar_type() != at::kFloat8_e4m3fn) return false;
+  m->rows = c.size(d - 2);
+  m->ld = c.size(d - 1);
+  m->batch = batch_dims ? static_cast<int32_t>(c.size(0)) : 1;
+  m->scaling = block ? MOK_FP8_BLOCKS : MOK_FP8_ROWS;
+  if (batch_dims && f.size(0) != c.size(0)) return false;
+  const int64_t r = block ? blocks(m->rows) : blocks(m->cols), k = block ? blocks(m->cols) : up_to(m->rows, 4);
+  if (f.size(d - 2) != r || f.size(d - 1) != k) return false;
+  m->q = static_cast<const uint8_t*>(c.data_ptr());
+  m->s = static_cast<const float*>(f.data_ptr());
+  return true;
+}
+
+// (schedule, device, x, out) -> (out,): one row per routed row from one per token (`to_rows`), or the other way
+template <mok_status (*CALL)(const mok_schedule*, const void*, int32_t, void*, void*), bool TO_ROWS>
+PyObject* move_rows(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    PlacedSchedule p;
+    const Tensor *x, *given;
+    if (n != 4 || !sched_arg(a[0], a[1], &p) || !tensor_arg(a[2], &x) || !tensor_arg(a[3], &given) || !x || x->dim() != 2) {
+      if (PyErr_Occurred()) return nullptr;
+      Py_RETURN_NONE;
+    }
+    const int64_t W = x->size(1), from = TO_ROWS ? p.s->shape.T : p.s->rpad_max, to = TO_ROWS ? p.s->rpad_max : p.s->shape.T;
+    if (!rows_of(*x, from, W, at::kBFloat16) || (given && !rows_of(*given, to, W, at::kBFloat16)) ||
+        x->device().index() != p.device || !all_on(x->device(), {given}) || W > INT32_MAX)
+      Py_RETURN_NONE;
+    Tensor out[1];
+    const int rc = on_device(*x, [&] {
+      out[0] = given ? *given : make({to, W}, *x, at::kBFloat16);
+      return CALL(p.s, x->data_ptr(), static_cast<int32_t>(W), ptr(out[0]), current_stream(*x));
+    });
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+// (schedule, device, rows, dout, drows) -> (drows, dweights)
+PyObject* combine_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    PlacedSchedule p;
+    const Tensor *rows, *dout, *given;
+    if (n != 5 || !sched_arg(a[0], a[1], &p) || !tensor_arg(a[2], &rows) || !tensor_arg(a[3], &dout) ||
+        !tensor_arg(a[4], &given) || !rows || !dout || rows->dim() != 2) {
+      if (PyErr_Occurred()) return nullptr;
+      Py_RETURN_NONE;
+    }
+    const int64_t W = rows->size(1), R = p.s->rpad_max;
+    if (!rows_of(*rows, R, W, at::kBFloat16) || !rows_of(*dout, p.s->shape.T, W, at::kBFloat16) ||
+        (given && !rows_of(*given, R, W, at::kBFloat16)) || rows->device().index() != p.device ||
+        !all_on(rows->device(), {dout, given}) || W > INT32_MAX)
+      Py_RETURN_NONE;
+    Tensor out[2];
+    const int rc = on_device(*rows, [&] {
+      out[0] = given ? *given : make({R, W}, *rows, at::kBFloat16);
+      out[1] = make({p.s->shape.T, p.s->shape.K}, *rows, at::kFloat);
+      return mok_combine_backward(p.s, rows->data_ptr(), dout->data_ptr(), static_cast<int32_t>(W), ptr(out[0]),
+                                  static_cast<float*>(ptr(out[1])), current_stream(*rows));
+    });
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+// (x, rows, transposed, schedule or 0, device, gather) -> (q, s, qt, st)
+PyObject* fp8_quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor* x;
+    if (n != 6 || !tensor_arg(a[0], &x) || !x || x->dim() != 2) Py_RETURN_NONE;
+    const int rows = PyObject_IsTrue(a[1]), cols = PyObject_IsTrue(a[2]);
+    const mok_schedule* s = static_cast<const mok_schedule*>(PyLong_AsVoidPtr(a[3]));
+    const long device = PyLong_AsLong(a[4]), gather = PyLong_AsLong(a[5]);
+    if (PyErr_Occurred()) return nullptr;
+    const int64_t C = x->size(1), R = s ? s->rpad_max : x->size(0);
+    if (!rows_of(*x, s && gather ? s->shape.T : R, C, at::kBFloat16) || (s && x->device().index() != device) ||
+        C > INT32_MAX)
+      Py_RETURN_NONE;
+    Tensor out[4];
+    const int rc = on_device(*x, [&] {
+      if (rows) {
+        out[0] = make({R, up_to(C, 16)}, *x, at::kByte);
+        out[1] = make({blocks(C), up_to(R, 4)}, *x, at::kFloat);
+      }
+      if (cols) {
+        out[2] = make({C, up_to(R, 16)}, *x, at::kByte);
+        out[3] = make({blocks(R), up_to(C, 4)}, *x, at::kFloat);
+      }
+      uint8_t *q = static_cast<uint8_t*>(ptr(out[0])), *qt = static_cast<uint8_t*>(ptr(out[2]));
+      float *f = static_cast<float*>(ptr(out[1])), *ft = static_cast<float*>(ptr(out[3]));
+      if (s)
+        return mok_fp8_quantize_routed(s, static_cast<int32_t>(gather), x->data_ptr(), static_cast<int32_t>(C), q, f, qt, ft,
+                                       current_stream(*x));
+      return mok_fp8_quantize(x->data_ptr(), R, static_cast<int32_t>(C), q, f, qt, ft, current_stream(*x));
+    });
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+// (w, rows, transposed) -> (q, s, qt, st)
+PyObject* fp8_quantize_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor* x;
+    if (n != 3 || !tensor_arg(a[0], &x) || !x || !plain(*x, at::kBFloat16) || (x->dim() != 2 && x->dim() != 3)) Py_RETURN_NONE;
+    const int rows = PyObject_IsTrue(a[1]), cols = PyObject_IsTrue(a[2]);
+    if (PyErr_Occurred()) return nullptr;
+    const bool many = x->dim() == 3;
+    const int64_t B = many ? x->size(0) : 1, R = x->size(many), C = x->size(many + 1);
+    if (C > INT32_MAX || B > INT32_MAX) Py_RETURN_NONE;
+    auto shaped = [&](int64_t r, int64_t c, at::ScalarType type) {
+      return many ? make({B, r, c}, *x, type) : make({r, c}, *x, type);
+    };
+    Tensor out[4];
+    const int rc = on_device(*x, [&] {
+      if (rows) {
+        out[0] = shaped(R, up_to(C, 16), at::kByte);
+        out[1] = shaped(blocks(R), blocks(C), at::kFloat);
+      }
+      if (cols) {
+        out[2] = shaped(C, up_to(R, 16), at::kByte);
+        out[3] = shaped(blocks(C), blocks(R), at::kFloat);
+      }
+      return mok_fp8_quantize_blocks(x->data_ptr(), static_cast<int32_t>(B), R, static_cast<int32_t>(C),
+                                     static_cast<uint8_t*>(ptr(out[0])), static_cast<float*>(ptr(out[1])),
+                                     static_cast<uint8_t*>(ptr(out[2])), static_cast<float*>(ptr(out[3])),
+                                     current_stream(*x));
+    });
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+bool status_arg(PyObject* o, const Tensor** t) {
+  return tensor_arg(o, t) && (!*t || (plain(**t, at::kInt) && (*t)->numel() == 1));
+}
+
+// (a.q, a.s, a.cols, b.q, b.s, b.cols, b.block, out, f32, status) -> (out,)
+PyObject* fp8_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor *aq, *as, *bq, *bs, *given, *status;
+    mok_fp8_matrix ma{}, mb{};
+    if (n != 10 || !fp8_arg(a[0], a[1], a[2], false, 0, &aq, &as, &ma) ||
+        !fp8_arg(a[3], a[4], a[5], PyObject_IsTrue(a[6]), 0, &bq, &bs, &mb) || !tensor_arg(a[7], &given) ||
+        !status_arg(a[9], &status)) {
+      if (PyErr_Occurred()) return nullptr;
+      Py_RETURN_NONE;
+    }
+    const at::ScalarType type = PyObject_IsTrue(a[8]) ? at::kFloat : at::kBFloat16;
+    if ((given && !rows_of(*given, ma.rows, mb.rows, type)) || !all_on(aq->device(), {bq, given, status})) Py_RETURN_NONE;
+    Tensor out[1];
+    const int rc = on_device(*aq, [&] {
+      out[0] = given ? *given : make({ma.rows, mb.rows}, *aq, type);
+      return mok_fp8_matmul(&ma, &mb, ptr(out[0]), type == at::kFloat ? MOK_DT_FP32 : MOK_DT_BF16,
+                            static_cast<uint32_t*>(ptr(status)), current_stream(*aq));
+    });
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+// (x, w.q, w.s, w.cols, out, status) -> (out,)
+PyObject* fp8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const Tensor *x, *wq, *ws, *given, *status;
+    mok_fp8_matrix w{};
+    if (n != 6 || !tensor_arg(a[0], &x) || !x || x->dim() != 2 || !fp8_arg(a[1], a[2], a[3], true, 0, &wq, &ws, &w) ||
+        !tensor_arg(a[4], &given) || !status_arg(a[5], &status)) {
+      if (PyErr_Occurred()) return nullptr;
+      Py_RETURN_NONE;
+    }
+    const int64_t M = x->size(0);
+    if (!rows_of(*x, M, w.cols, at::kBFloat16) || (given && !rows_of(*given, M, w.rows, at::kBFloat16)) ||
+        !all_on(x->device(), {wq, given, status}))
+      Py_RETURN_NONE;
+    const size_t bytes = mok_fp8_linear_workspace_bytes(M, w.cols);
+    if (!bytes) return PyLong_FromLong(MOK_ERR_INVALID_ARG);
+    Tensor out[1];
+    const int rc = on_device(*x, [&] {
+      out[0] = given ? *given : make({M, w.rows}, *x, at::kBFloat16);
+      const Tensor scratch = make({static_cast<int64_t>(bytes)}, *x, at::kByte);
+      return mok_fp8_linear(x->data_ptr(), M, &w, ptr(out[0]), scratch.data_ptr(), bytes,
+                            static_cast<uint32_t*>(ptr(status)), current_stream(*x));
+    });
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+// (schedule, device, a.q, a.s, a.cols, w.q, w.s, w.cols, out) -> (out,)
+PyObject* fp8_grouped_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    PlacedSchedule p;
+    const Tensor *aq, *as, *wq, *ws, *given;
+    mok_fp8_matrix ma{}, w{};
+    if (n != 9 || !sched_arg(a[0], a[1], &p) || !fp8_arg(a[2], a[3], a[4], false, 0, &aq, &as, &ma) ||
+        !fp8_arg(a[5], a[6], a[7], true, 1, &wq, &ws, &w) || !tensor_arg(a[8], &given)) {
+      if (PyErr_Occurred()) return nullptr;
+      Py_RETURN_NONE;
+    }
+    if (ma.rows != p.s->rpad_max || w.batch != p.s->shape.E || (given && !rows_of(*given, ma.rows, w.rows, at::kBFloat16)) ||
+        aq->device().index() != p.device || !all_on(aq->device(), {wq, given}))
+      Py_RETURN_NONE;
+    Tensor out[1];
+    const int rc = on_device(*aq, [&] {
+      out[0] = given ? *given : make({ma.rows, w.rows}, *aq, at::kBFloat16);
+      return mok_fp8_grouped_matmul(p.s, &ma, &w, ptr(out[0]), current_stream(*aq));
+    });
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
+// (schedule, device, a.q, a.s, a.cols, b.q, b.s, b.cols, out, f32) -> (out,)
+PyObject* fp8_grouped_wgrad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    PlacedSchedule p;
+    const Tensor *aq, *as, *bq, *bs, *given;
+    mok_fp8_matrix ma{}, mb{};
+    if (n != 10 || !sched_arg(a[0], a[1], &p) || !fp8_arg(a[2], a[3], a[4], false, 0, &aq, &as, &ma) ||
+        !fp8_arg(a[5], a[6], a[7], false, 0, &bq, &bs, &mb) || !tensor_arg(a[8], &given)) {
+      if (PyErr_Occurred()) return nullptr;
+      Py_RETURN_NONE;
+    }
+    const at::ScalarType type = PyObject_IsTrue(a[9]) ? at::kFloat : at::kBFloat16;
+    const int64_t E = p.s->shape.E;
+    if (aq->device().index() != p.device || !all_on(aq->device(), {bq, given}) ||
+        (given && (!plain(*given, type) || given->dim() != 3 || given->size(0) != E || given->size(1) != ma.rows ||
+                   given->size(2) != mb.rows)))
+      Py_RETURN_NONE;
+    Tensor out[1];
+    const int rc = on_device(*aq, [&] {
+      out[0] = given ? *given : make({E, ma.rows, mb.rows}, *aq, type);
+      return mok_fp8_grouped_wgrad(p.s, &ma, &mb, ptr(out[0]), type == at::kFloat ? MOK_DT_FP32 : MOK_DT_BF16,
+                                   current_stream(*aq));
+    });
+    return rc ? PyLong_FromLong(rc) : wrap_all(out);
+  });
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
@@ -302,6 +563,12 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {method<rmsnorm_forward>("rmsnorm_forward"), method<rmsnorm_backward>("rmsnorm_backward"),
                          method<dropout_forward>("dropout_forward"), method<dropout_backward>("dropout_backward"),
                          method<ffn_forward>("ffn_forward"), method<ffn_backward>("ffn_backward"),
+                         method<move_rows<mok_dispatch, true>>("dispatch"),
+                         method<move_rows<mok_dispatch_backward, false>>("dispatch_backward"),
+                         method<move_rows<mok_combine, false>>("combine"), method<combine_backward>("combine_backward"),
+                         method<fp8_quantize>("fp8_quantize"), method<fp8_quantize_blocks>("fp8_quantize_blocks"),
+                         method<fp8_matmul>("fp8_matmul"), method<fp8_linear>("fp8_linear"),
+                         method<fp8_grouped_matmul>("fp8_grouped_matmul"), method<fp8_grouped_wgrad>("fp8_grouped_wgrad"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_mok_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,143 @@
+// mok_fp8.cu -- the C ABI of the 8-bit products: checks, and which kernel a product runs on.
+#include "mok_fp8_gemm.cuh"
+
+namespace mok {
+namespace {
+
+constexpr int64_t kMax = (int64_t{1} << 31) - 1;
+
+bool ok16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+mok_status from_cuda(int rc) { return rc == 0 ? MOK_OK : MOK_ERR_CUDA; }
+
+// A matrix that a product can read (rows * cols may be 0: then nothing is).
+bool matrix_ok(const mok_fp8_matrix* m, int32_t batch) {
+  if (!m || m->rows < 0 || m->cols < 0 || m->rows > kMax || m->cols > kMax || m->batch != batch || batch < 1) return false;
+  if (m->scaling != MOK_FP8_ROWS && m->scaling != MOK_FP8_BLOCKS) return false;
+  if (m->ld < m->cols || m->ld % 16 != 0 || m->ld > kMax) return false;
+  if (m->rows * static_cast<int64_t>(batch) > kMax) return false;  // TMA coordinates
+  return m->rows == 0 || m->cols == 0 || (ok16(m->q) && ok16(m->s));
+}
+
+Fp8Operand operand(const mok_fp8_matrix& m) {
+  return {m.q, m.s, m.rows, m.cols, m.ld, m.batch, m.scaling == MOK_FP8_ROWS};
+}
+
+// out [M, N]: see mok_fp8_matmul.
+mok_status product(const mok_fp8_matrix& a, const mok_fp8_matrix& b, void* out, int32_t out_type, bool early,
+                   uint32_t* status, cudaStream_t stream) {
+  Fp8Problem g{};
+  g.mode = FP8_DENSE;
+  g.k_blocks = static_cast<int32_t>(fp8_blocks(a.cols));
+  g.out = out;
+  g.ldo = b.rows;
+  g.out_f32 = out_type == MOK_DT_FP32;
+  g.early_p = early;
+  g.status = status;
+  return from_cuda(launch_fp8_tile(operand(a), operand(b), g, a.rows, 0, K_FP8_TILE, stream));
+}
+
+}  // namespace
+}  // namespace mok
+
+using namespace mok;
+
+extern "C" {
+
+mok_status mok_fp8_matmul(const mok_fp8_matrix* a, const mok_fp8_matrix* b, void* out, int32_t out_type,
+                          uint32_t* status, void* stream) {
+  if (!matrix_ok(a, 1) || !matrix_ok(b, 1) || a->scaling != MOK_FP8_ROWS || a->cols != b->cols) return MOK_ERR_INVALID_ARG;
+  if (b->rows < 8 || b->rows % 8 != 0 || (out_type != MOK_DT_BF16 && out_type != MOK_DT_FP32)) return MOK_ERR_INVALID_ARG;
+  if (a->rows == 0) return MOK_OK;
+  if (!ok16(out)) return MOK_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (a->cols == 0)
+    return from_cuda(static_cast<int>(cudaMemsetAsync(
+        out, 0, static_cast<size_t>(a->rows) * b->rows * (out_type == MOK_DT_FP32 ? 4 : 2), s)));
+  return product(*a, *b, out, out_type, false, status, s);
+}
+
+size_t mok_fp8_linear_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 0 || M > kMax || K < 8 || K % 8 != 0 || K > kMax) return 0;
+  const int64_t codes = (M * fp8_ld(K) + 255) / 256 * 256, scales = fp8_blocks(K) * fp8_pitch(M) * 4;
+  return static_cast<size_t>((codes + scales + 255) / 256 * 256 + 256);
+}
+
+mok_status mok_fp8_linear(const void* x, int64_t M, const mok_fp8_matrix* w, void* out, void* ws, size_t ws_bytes,
+                          uint32_t* status, void* stream) {
+  if (M < 0 || M > kMax || !matrix_ok(w, 1) || w->scaling != MOK_FP8_BLOCKS) return MOK_ERR_INVALID_ARG;
+  if (w->rows < 8 || w->rows % 8 != 0 || w->cols < 8 || w->cols % 8 != 0) return MOK_ERR_INVALID_ARG;
+  if (M == 0) return MOK_OK;
+  if (!ok16(x) || !ok16(out) || !ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MOK_ERR_INVALID_ARG;
+  if (ws_bytes < mok_fp8_linear_workspace_bytes(M, w->cols)) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  mok_fp8_matrix a{};
+  uint8_t* q = static_cast<uint8_t*>(ws);
+  float* s = reinterpret_cast<float*>(q + (M * fp8_ld(w->cols) + 255) / 256 * 256);
+  const mok_status rc = mok_fp8_quantize(x, M, static_cast<int32_t>(w->cols), q, s, nullptr, nullptr, stream);
+  if (rc != MOK_OK) return rc;
+  a.q = q;
+  a.s = s;
+  a.rows = M;
+  a.cols = w->cols;
+  a.ld = fp8_ld(w->cols);
+  a.batch = 1;
+  a.scaling = MOK_FP8_ROWS;
+  return product(a, *w, out, MOK_DT_BF16, true, status, static_cast<cudaStream_t>(stream));
+}
+
+mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matrix* a, const mok_fp8_matrix* w, void* out,
+                                  void* stream) {
+  Sizes z;
+  const mok_status rc = routed_sizes(sched, &z);
+  if (rc != MOK_OK) return rc;
+  if (!matrix_ok(a, 1) || !matrix_ok(w, z.E) || a->scaling != MOK_FP8_ROWS || w->scaling != MOK_FP8_BLOCKS)
+    return MOK_ERR_INVALID_ARG;
+  if (a->rows != z.rpad_max || a->cols != w->cols || w->cols < 8 || w->rows < 8 || w->rows % 8 != 0)
+    return MOK_ERR_INVALID_ARG;
+  if (z.T == 0) return MOK_OK;
+  if (!ok16(out)) return MOK_ERR_INVALID_ARG;
+  Fp8Problem g{};
+  g.mode = FP8_GROUPED;
+  g.k_blocks = static_cast<int32_t>(fp8_blocks(a->cols));
+  g.out = out;
+  g.ldo = w->rows;
+  g.experts = z.E;
+  g.mblocks = sched->mblocks;
+  g.poff = sched->poff;
+  g.meta = sched->meta;
+  g.status = sched->status;
+  // an expert with rows has one block that is not full at most
+  const int64_t blocks = (z.R < z.E ? z.R : z.E) + z.R / 128;
+  return from_cuda(launch_fp8_tile(operand(*a), operand(*w), g, z.R, blocks < z.mblocks_max ? blocks : z.mblocks_max,
+                                   K_FP8_GROUPED_TILE, static_cast<cudaStream_t>(stream)));
+}
+
+mok_status mok_fp8_grouped_wgrad(const mok_schedule* sched, const mok_fp8_matrix* a, const mok_fp8_matrix* b, void* dw,
+                                 int32_t dw_type, void* stream) {
+  Sizes z;
+  const mok_status rc = routed_sizes(sched, &z);
+  if (rc != MOK_OK) return rc;
+  if (!matrix_ok(a, 1) || !matrix_ok(b, 1) || a->scaling != MOK_FP8_ROWS || b->scaling != MOK_FP8_ROWS)
+    return MOK_ERR_INVALID_ARG;
+  if (a->cols != z.rpad_max || b->cols != z.rpad_max || a->rows < 8 || b->rows < 8 || b->rows % 8 != 0)
+    return MOK_ERR_INVALID_ARG;
+  if ((dw_type != MOK_DT_BF16 && dw_type != MOK_DT_FP32) || !ok16(dw)) return MOK_ERR_INVALID_ARG;
+  if (a->rows * b->rows > kMax) return MOK_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (z.T == 0)
+    return from_cuda(static_cast<int>(cudaMemsetAsync(
+        dw, 0, static_cast<size_t>(z.E) * a->rows * b->rows * (dw_type == MOK_DT_FP32 ? 4 : 2), s)));
+  Fp8Problem g{};
+  g.mode = FP8_WGRAD;
+  g.k_blocks = static_cast<int32_t>(fp8_blocks(z.rpad_max));
+  g.out = dw;
+  g.ldo = b->rows;
+  g.out_f32 = dw_type == MOK_DT_FP32;
+  g.experts = z.E;
+  g.mblocks = sched->mblocks;
+  g.poff = sched->poff;
+  g.meta = sched->meta;
+  g.status = sched->status;
+  return from_cuda(launch_fp8_tile(operand(*a), operand(*b), g, z.R, 0, K_FP8_WGRAD, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,295 @@
+// mok_fp8_quant.cu -- quantisation to E4M3 with one fp32 scale per block of 128 (mok_fp8.cuh).
+//
+// One kernel makes every form from tiles of 128 x 128 bf16 values that stay in registers: 256 threads, each with
+// 8 rows x 8 columns as packed pairs.  16 neighbouring lanes hold a row's 128 columns: its maximum is four shuffles.
+// A column's maximum is a lane's own over its 8 rows, one shuffle, and one exchange over the warps in shared memory; a
+// 128 x 128 block's comes from the row maxima.  Each form then converts from the same registers: row codes leave as 8
+// bytes per lane, 128 contiguous ones per row; transposed codes go through shared memory (8 rows of a column are
+// 8 bytes of a transposed row) and leave as 16-byte vectors.
+//
+// Bound by HBM: 2 bytes read, 1 written per value and form.
+#include "mok_fp8.cuh"
+
+namespace mok {
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr int kQStride = 128 + 16;  // bytes between the transposed rows of the staged tile (16-byte vectors)
+
+enum QuantForm : int { Q_ROWS = 1, Q_COLS = 2, Q_BLOCKS = 4 };
+
+struct QuantArgs {
+  Fp8Source src;
+  int64_t rows;
+  int32_t cols;
+  uint8_t* q;
+  float* s;
+  uint8_t* qt;
+  float* st;
+  int64_t ld, ldt, pitch, pitch_t;
+  int64_t src_batch, q_batch, s_batch, qt_batch, st_batch;  // Q_BLOCKS: elements between matrices
+};
+
+__device__ __forceinline__ uint32_t absmax_word(uint32_t m) { return absmax2(m, m >> 16) & 0x7FFFu; }
+
+// FORM: Q_ROWS | Q_COLS for 1 x 128 scales of rows and of columns, or Q_BLOCKS (q, qt as they are not null).
+template <int FORM, bool GATHER>
+__global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs p) {
+  pdl_wait();
+  __shared__ uint32_t wmax[8][64];                                // per warp, packed column maxima
+  __shared__ __align__(16) uint8_t tile[FORM == Q_ROWS ? 16 : 128 * kQStride];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, cg = t & 15, rg = t >> 4;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 128;
+  const int c0 = static_cast<int>(blockIdx.x) * 128, c = c0 + cg * 8;
+  const bool routed = p.src.row_token != nullptr;
+  if (routed && r0 >= p.src.meta[0]) return;  // (segments, and so the layout's end, are multiples of 128 rows)
+  const uint16_t* x = p.src.x + (FORM == Q_BLOCKS ? blockIdx.z * p.src_batch : 0);
+  uint4 v[8];
+  uint32_t live = 0;  // rows that are there, and no padding
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t r = r0 + rg * 8 + i;
+    int64_t from = r;
+    bool in = r < p.rows;
+    if (routed && in) {
+      const int token = __ldg(p.src.row_token + r);
+      in = token >= 0;
+      if (GATHER) from = token;
+    }
+    live |= in ? 1u << i : 0u;
+    v[i] = in && c < p.cols ? *reinterpret_cast<const uint4*>(x + from * p.cols + c) : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t rmax[8];  // of the row's 128 columns, in all 16 lanes
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t m = absmax2(absmax2(v[i].x, v[i].y), absmax2(v[i].z, v[i].w));
+#pragma unroll
+    for (int d = 8; d >= 1; d >>= 1) m = absmax2(m, __shfl_xor_sync(0xffffffffu, m, d));
+    rmax[i] = absmax_word(m);
+  }
+  float up = 0.0f;
+  bool bad = false;
+  if constexpr (FORM == Q_BLOCKS) {
+    uint32_t m = rmax[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max(m, rmax[i]);  // (magnitudes' bits order as they do, NaN above all)
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    if (lane == 0) wmax[warp][0] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) m = max(m, wmax[w][0]);
+    const float sc = fp8_scale(m, up);
+    bad = m >= 0x7F80u;
+    if (t == 0) {
+      if (p.q) p.s[blockIdx.z * p.s_batch + static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = sc;
+      if (p.qt) p.st[blockIdx.z * p.st_batch + static_cast<int64_t>(blockIdx.x) * gridDim.y + blockIdx.y] = sc;
+    }
+  }
+  auto row_codes = [&](int i, float f, bool nan) {
+    uint2 o = make_uint2(fp8_codes(v[i].x, f) | fp8_codes(v[i].y, f) << 16, fp8_codes(v[i].z, f) | fp8_codes(v[i].w, f) << 16);
+    if (nan) o = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+    return o;
+  };
+  if ((FORM & Q_ROWS) || (FORM == Q_BLOCKS && p.q)) {
+    uint8_t* q = p.q + (FORM == Q_BLOCKS ? blockIdx.z * p.q_batch : 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t r = r0 + rg * 8 + i;
+      if (FORM == Q_BLOCKS ? r >= p.rows : !(live >> i & 1u)) continue;
+      float f = up;
+      bool nan = bad;
+      if constexpr (FORM != Q_BLOCKS) {
+        const float sc = fp8_scale(rmax[i], f);
+        nan = rmax[i] >= 0x7F80u;
+        if (cg == 0) p.s[static_cast<int64_t>(blockIdx.x) * p.pitch + r] = sc;
+      }
+      if (c < p.cols) *reinterpret_cast<uint2*>(q + r * p.ld + c) = row_codes(i, f, nan);
+      else if (c < p.ld) *reinterpret_cast<uint2*>(q + r * p.ld + c) = make_uint2(0, 0);  // up to the pitch
+    }
+  }
+  if constexpr (FORM != Q_ROWS) {
+    if (FORM == Q_BLOCKS && !p.qt) return;
+    float f[8];
+    uint32_t nan = 0;
+    if constexpr (FORM & Q_COLS) {
+      uint32_t m[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 1; i < 8; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = absmax2(m[j], w[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        m[j] = absmax2(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
+        if (lane < 16) wmax[warp][cg * 4 + j] = m[j];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a = wmax[0][cg * 4 + j];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) a = absmax2(a, wmax[w][cg * 4 + j]);
+        a &= 0x7FFF7FFFu;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t am = h ? a >> 16 : a & 0xFFFFu;
+          const float sc = fp8_scale(am, f[2 * j + h]);
+          if (am >= 0x7F80u) nan |= 1u << (2 * j + h);
+          const int cc = c + 2 * j + h;
+          if (rg == 0 && cc < p.cols) p.st[static_cast<int64_t>(blockIdx.y) * p.pitch_t + cc] = sc;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = up;
+      nan = bad ? 0xFFu : 0u;
+    }
+    // column j's codes over the thread's 8 rows: 8 bytes of a transposed row.  In a bad block they are NaN on the rows that
+    // are there: bit i of `live` to byte i
+    const uint32_t nan_codes[2] = {((live & 15u) * 0x00204081u & 0x01010101u) * 0x7Fu,
+                                   ((live >> 4) * 0x00204081u & 0x01010101u) * 0x7Fu};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = j == 0 ? v[i].x : j == 1 ? v[i].y : j == 2 ? v[i].z : v[i].w;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t o[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t a = 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w0 = w[4 * i + 2 * k], w1 = w[4 * i + 2 * k + 1];
+            const uint32_t pair = h ? (w0 >> 16 | (w1 & 0xFFFF0000u)) : (w0 & 0xFFFFu) | w1 << 16;
+            a |= fp8_codes(pair, f[2 * j + h]) << (16 * k);
+          }
+          o[i] = nan >> (2 * j + h) & 1u ? nan_codes[i] : a;
+        }
+        *reinterpret_cast<uint2*>(tile + (cg * 8 + 2 * j + h) * kQStride + rg * 8) = make_uint2(o[0], o[1]);
+      }
+    }
+    __syncthreads();
+    uint8_t* qt = p.qt + (FORM == Q_BLOCKS ? blockIdx.z * p.qt_batch : 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // 8 vectors of 16 rows per transposed row
+      const int item = t + i * kQThreads, col = item >> 3, r16 = (item & 7) * 16;
+      if (c0 + col < p.cols && r0 + r16 < p.ldt)
+        *reinterpret_cast<uint4*>(qt + static_cast<int64_t>(c0 + col) * p.ldt + r0 + r16) =
+            *reinterpret_cast<const uint4*>(tile + col * kQStride + r16);
+    }
+  }
+}
+
+bool ok16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Row tiles are the grid's y: 65535 of them per launch, the rest in further launches of plain rows.
+template <int FORM, bool GATHER>
+int launch_form(const QuantArgs& p, int batch, int kind, cudaStream_t stream) {
+  const int64_t ty = fp8_blocks(p.rows), tx = fp8_blocks(p.cols);
+  trace_begin(stream, kind);
+  const cudaError_t e = launch_pdl(fp8_quantize_kernel<FORM, GATHER>, dim3(static_cast<unsigned>(tx), static_cast<unsigned>(ty), batch),
+                                   dim3(kQThreads), 0, stream, p);
+  trace_end(stream);
+  return static_cast<int>(e);
+}
+
+}  // namespace
+
+int launch_fp8_quantize(const Fp8Source& src, int64_t rows, int32_t cols, uint8_t* q, float* s, uint8_t* qt, float* st,
+                        int kind, cudaStream_t stream) {
+  QuantArgs p{};
+  p.src = src;
+  p.rows = rows;
+  p.cols = cols;
+  p.q = q;
+  p.s = s;
+  p.qt = qt;
+  p.st = st;
+  p.ld = fp8_ld(cols);
+  p.ldt = fp8_ld(rows);
+  p.pitch = fp8_pitch(rows);
+  p.pitch_t = fp8_pitch(cols);
+  auto run = [&](auto gather) {
+    constexpr bool G = decltype(gather)::value;
+    if (q && qt) return launch_form<Q_ROWS | Q_COLS, G>(p, 1, kind, stream);
+    return q ? launch_form<Q_ROWS, G>(p, 1, kind, stream) : launch_form<Q_COLS, G>(p, 1, kind, stream);
+  };
+  return src.gather ? run(std::true_type{}) : run(std::false_type{});
+}
+
+}  // namespace mok
+
+using namespace mok;
+
+namespace {
+constexpr int64_t kMaxRows = int64_t{65535} * 128;  // row tiles in a grid's y
+
+mok_status outputs_ok(const void* q, const void* s, const void* qt, const void* st) {
+  if ((!q && !qt) || (q != nullptr) != (s != nullptr) || (qt != nullptr) != (st != nullptr)) return MOK_ERR_INVALID_ARG;
+  if ((q && (!ok16(q) || !ok16(s))) || (qt && (!ok16(qt) || !ok16(st)))) return MOK_ERR_INVALID_ARG;
+  return MOK_OK;
+}
+}  // namespace
+
+extern "C" {
+
+mok_status mok_fp8_quantize(const void* x, int64_t rows, int32_t cols, uint8_t* q, float* s, uint8_t* qt, float* st,
+                            void* stream) {
+  if (rows < 0 || cols < 8 || cols % 8 != 0) return MOK_ERR_INVALID_ARG;
+  if (rows > kMaxRows) return MOK_ERR_UNSUPPORTED;
+  if (rows == 0) return MOK_OK;
+  if (!ok16(x)) return MOK_ERR_INVALID_ARG;
+  const mok_status rc = outputs_ok(q, s, qt, st);
+  if (rc != MOK_OK) return rc;
+  const Fp8Source src{static_cast<const uint16_t*>(x), nullptr, nullptr, 0};
+  return launch_fp8_quantize(src, rows, cols, q, s, qt, st, K_FP8_QUANTIZE, static_cast<cudaStream_t>(stream)) ? MOK_ERR_CUDA
+                                                                                                             : MOK_OK;
+}
+
+mok_status mok_fp8_quantize_routed(const mok_schedule* sched, int32_t gather, const void* x, int32_t cols, uint8_t* q,
+                                   float* s, uint8_t* qt, float* st, void* stream) {
+  Sizes z;
+  mok_status rc = routed_sizes(sched, &z);
+  if (rc != MOK_OK) return rc;
+  if (cols < 8 || cols % 8 != 0 || (gather != 0 && gather != 1)) return MOK_ERR_INVALID_ARG;
+  if (z.rpad_max > kMaxRows) return MOK_ERR_UNSUPPORTED;
+  if (z.T == 0) return MOK_OK;
+  if (!ok16(x)) return MOK_ERR_INVALID_ARG;
+  rc = outputs_ok(q, s, qt, st);
+  if (rc != MOK_OK) return rc;
+  const Fp8Source src{static_cast<const uint16_t*>(x), sched->row_token, sched->meta, gather};
+  return launch_fp8_quantize(src, z.rpad_max, cols, q, s, qt, st, gather ? K_FP8_DISPATCH : K_FP8_QUANTIZE,
+                             static_cast<cudaStream_t>(stream))
+             ? MOK_ERR_CUDA
+             : MOK_OK;
+}
+
+mok_status mok_fp8_quantize_blocks(const void* x, int32_t batch, int64_t rows, int32_t cols, uint8_t* q, float* s,
+                                   uint8_t* qt, float* st, void* stream) {
+  if (batch < 1 || rows < 8 || rows % 8 != 0 || cols < 8 || cols % 8 != 0) return MOK_ERR_INVALID_ARG;
+  if (rows > kMaxRows || batch > 65535) return MOK_ERR_UNSUPPORTED;
+  if (!ok16(x)) return MOK_ERR_INVALID_ARG;
+  if ((!q && !qt) || (q != nullptr) != (s != nullptr) || (qt != nullptr) != (st != nullptr)) return MOK_ERR_INVALID_ARG;
+  const mok_status rc = outputs_ok(q, s, qt, st);
+  if (rc != MOK_OK) return rc;
+  QuantArgs p{};
+  p.src.x = static_cast<const uint16_t*>(x);
+  p.rows = rows;
+  p.cols = cols;
+  p.q = q;
+  p.s = s;
+  p.qt = qt;
+  p.st = st;
+  p.ld = fp8_ld(cols);
+  p.ldt = fp8_ld(rows);
+  p.src_batch = rows * cols;
+  p.q_batch = rows * p.ld;
+  p.qt_batch = cols * p.ldt;
+  p.s_batch = p.st_batch = fp8_blocks(rows) * fp8_blocks(cols);
+  return launch_form<Q_BLOCKS, false>(p, batch, K_FP8_WEIGHT, static_cast<cudaStream_t>(stream)) ? MOK_ERR_CUDA : MOK_OK;
+}
+
+}  // extern "C"

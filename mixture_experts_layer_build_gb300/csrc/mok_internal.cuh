@@ -160,6 +160,18 @@ enum KernelKind : int {
   K_FFN_DX,
   K_FFN_BWD1,
   K_FFN_BWD2,
+  K_DISPATCH,
+  K_DISPATCH_BWD,
+  K_ROUTE_COMBINE,
+  K_COMBINE_BWD,
+  K_FP8_QUANTIZE,
+  K_FP8_DISPATCH,
+  K_FP8_WEIGHT,
+  K_FP8_TILE,
+  K_FP8_PAIR,
+  K_FP8_GROUPED_TILE,
+  K_FP8_GROUPED_PAIR,
+  K_FP8_WGRAD,
   K_NUM_KINDS
 };
 void trace_begin(cudaStream_t s, int kind);  // no-ops unless a trace is set

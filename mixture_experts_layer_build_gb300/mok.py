@@ -149,7 +149,10 @@ EXPORTED = ("mok_version", "mok_status_string", "mok_workspace_bytes", "mok_fwd_
             "mok_router_forward", "mok_router_backward", "mok_selftest_wait_timeout", "mok_ep_build_schedule",
             "mok_ep_forward", "mok_ep_backward", "mok_ep_combine", "mok_dropout_forward", "mok_dropout_backward",
             "mok_rmsnorm_forward", "mok_rmsnorm_workspace_bytes", "mok_rmsnorm_backward", "mok_ffn_ctx_bytes",
-            "mok_ffn_forward", "mok_ffn_workspace_bytes", "mok_ffn_backward")
+            "mok_ffn_forward", "mok_ffn_workspace_bytes", "mok_ffn_backward", "mok_routes_workspace_bytes",
+            "mok_build_routes", "mok_dispatch", "mok_dispatch_backward", "mok_combine", "mok_combine_backward",
+            "mok_fp8_quantize", "mok_fp8_quantize_routed", "mok_fp8_quantize_blocks", "mok_fp8_matmul",
+            "mok_fp8_linear_workspace_bytes", "mok_fp8_linear", "mok_fp8_grouped_matmul", "mok_fp8_grouped_wgrad")
 _lib.mok_router_workspace_bytes.restype = ctypes.c_size_t
 _lib.mok_router_workspace_bytes.argtypes = [ctypes.POINTER(mok_shape)]
 _lib.mok_router_forward.restype = ctypes.c_int
@@ -877,6 +880,331 @@ class FFN:
         if self.status.is_cuda:
             torch.cuda.synchronize(self.status.device)
         return int(self.status.item())
+
+
+# ---------------------------------------------------------------------------------------------
+# routed rows: tokens sorted by expert and back
+# ---------------------------------------------------------------------------------------------
+_SHAPE, _SCHED = ctypes.POINTER(mok_shape), ctypes.POINTER(mok_schedule)
+_lib.mok_routes_workspace_bytes.restype = ctypes.c_size_t
+_lib.mok_routes_workspace_bytes.argtypes = [ctypes.POINTER(mok_config), _SHAPE]
+_lib.mok_build_routes.restype = ctypes.c_int
+_lib.mok_build_routes.argtypes = [ctypes.POINTER(mok_config), _SHAPE, _P, _P, _P, ctypes.c_size_t, _SCHED, _P]
+for _f in (_lib.mok_dispatch, _lib.mok_dispatch_backward, _lib.mok_combine):
+    _f.restype = ctypes.c_int
+    _f.argtypes = [_SCHED, _P, ctypes.c_int32, _P, _P]
+_lib.mok_combine_backward.restype = ctypes.c_int
+_lib.mok_combine_backward.argtypes = [_SCHED, _P, _P, ctypes.c_int32, _P, _P, _P]
+
+
+def mok_routes_workspace_bytes(cfg: mok_config, shape: mok_shape) -> int:
+    n = _lib.mok_routes_workspace_bytes(ctypes.byref(cfg), ctypes.byref(shape))
+    if n == 0:
+        raise MokError(MOK_ERR_INVALID_ARG, "mok_routes_workspace_bytes")
+    return n
+
+
+def mok_build_routes(cfg: mok_config, shape: mok_shape, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                     ws: torch.Tensor, stream=None) -> Schedule:
+    """mok_build_schedule's tables without the layer's staging buffers, for the calls on routed rows alone."""
+    s = mok_schedule()
+    _check(_lib.mok_build_routes(ctypes.byref(cfg), ctypes.byref(shape), _ptr(topk_ids, torch.int32, "topk_ids"),
+                                 _ptr(topk_weights, torch.float32, "topk_weights"), _ptr(ws, None, "ws"),
+                                 ws.numel() * ws.element_size(), ctypes.byref(s), _stream(stream)), "mok_build_routes")
+    return Schedule(s, ws, topk_ids, topk_weights)
+
+
+class Routes:
+    """Owner of the workspace of a schedule of T tokens, K of E experts each, for the calls on routed rows (dispatch,
+    combine, the grouped products): the layer's own schedule serves them as well.  `rows`: rows of a buffer of routed
+    rows.  A schedule is valid until the next build on the same Routes."""
+
+    def __init__(self, T: int, E: int, K: int, cfg: mok_config | None = None, device="cuda"):
+        self.cfg, self.shape = cfg or make_config(0, 0), make_shape(T, 128, 128, E, K)
+        self.ws = torch.empty(mok_routes_workspace_bytes(self.cfg, self.shape), dtype=torch.uint8, device=device)
+        self.rows = T * K + E * 127
+
+    def build(self, topk_ids: torch.Tensor, topk_weights: torch.Tensor, stream=None) -> Schedule:
+        """topk_ids [T, K] int32, topk_weights [T, K] fp32 (read by combine when it runs)."""
+        for t, dt, name in ((topk_ids, torch.int32, "topk_ids"), (topk_weights, torch.float32, "topk_weights")):
+            _arg(t, (self.shape.T, self.shape.K), dt, name)
+            if t.device != self.ws.device:
+                raise ValueError(f"{name} must be on {self.ws.device}, as the workspace is, got {t.device}")
+        with _on_stream(stream, topk_ids):
+            return mok_build_routes(self.cfg, self.shape, topk_ids, topk_weights, self.ws)
+
+
+def _placed(sched: Schedule):
+    """A schedule's address and the index of its device, for the compiled binding."""
+    return ctypes.addressof(sched.c), sched.ws.device.index if sched.ws.is_cuda else -1
+
+
+def _sched_refused(result, where: str, sched: Schedule, *args):
+    """_refused for calls on a schedule's device, which no argument but the schedule fixes."""
+    if result is None:
+        for t, _, _, name in args:
+            if isinstance(t, torch.Tensor) and t.is_cuda and t.device != sched.ws.device:
+                raise ValueError(f"{name} must be on {sched.ws.device}, as the schedule is, got {t.device}")
+    _refused(result, where, *args)
+
+
+def _width(t) -> int:
+    return t.shape[1] if isinstance(t, torch.Tensor) and t.dim() == 2 else -1
+
+
+def _moved(call, where, sched, x, name, rows, out_rows, out):
+    r = call(*_placed(sched), x, out)
+    if type(r) is not tuple:
+        w = _width(x)
+        _sched_refused(r, where, sched, (x, (rows, w), torch.bfloat16, name),
+                       *(() if out is None else ((out, (out_rows, w), torch.bfloat16, "out"),)))
+    return r[0]
+
+
+def dispatch(sched: Schedule, x: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Tokens sorted by expert: rows [rpad_max, W] bf16 in the schedule's layout from x [T, W] bf16, zeros on padding
+    rows; what lies behind the layout's last row is left as it is."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return dispatch(sched, x, out)
+    return _moved(_bind.dispatch, "mok_dispatch", sched, x, "x", sched.c.shape.T, sched.c.rpad_max, out)
+
+
+def dispatch_backward(sched: Schedule, drows: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dispatch's gradient: dx [T, W] bf16, the fp32 sum of each token's rows of drows [rpad_max, W] bf16."""
+    if stream is not None:
+        with _on_stream(stream, drows):
+            return dispatch_backward(sched, drows, out)
+    return _moved(_bind.dispatch_backward, "mok_dispatch_backward", sched, drows, "drows", sched.c.rpad_max,
+                  sched.c.shape.T, out)
+
+
+def combine(sched: Schedule, rows: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Routed rows back to tokens: out [T, W] bf16, the fp32 sum of each token's rows of rows [rpad_max, W] bf16 times the
+    schedule's router weights."""
+    if stream is not None:
+        with _on_stream(stream, rows):
+            return combine(sched, rows, out)
+    return _moved(_bind.combine, "mok_combine", sched, rows, "rows", sched.c.rpad_max, sched.c.shape.T, out)
+
+
+def combine_backward(sched: Schedule, rows: torch.Tensor, dout: torch.Tensor, drows: torch.Tensor | None = None,
+                     stream=None):
+    """combine's gradients (drows [rpad_max, W] bf16 with zeros on padding rows, dweights [T, K] fp32) for dout [T, W] bf16.
+    drows, where given, receives the rows' gradient and may be rows itself."""
+    if stream is not None:
+        with _on_stream(stream, rows):
+            return combine_backward(sched, rows, dout, drows)
+    r = _bind.combine_backward(*_placed(sched), rows, dout, drows)
+    if type(r) is not tuple:
+        w, R = _width(rows), sched.c.rpad_max
+        _sched_refused(r, "mok_combine_backward", sched, (rows, (R, w), torch.bfloat16, "rows"),
+                       (dout, (sched.c.shape.T, w), torch.bfloat16, "dout"),
+                       *(() if drows is None else ((drows, (R, w), torch.bfloat16, "drows"),)))
+    return r
+
+
+# ---------------------------------------------------------------------------------------------
+# products in 8-bit floating point with one fp32 scale per block of 128
+# ---------------------------------------------------------------------------------------------
+MOK_FP8_ROWS = 0
+MOK_FP8_BLOCKS = 1
+
+
+class mok_fp8_matrix(ctypes.Structure):
+    _fields_ = [("q", _P), ("s", _P), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("batch", ctypes.c_int32), ("scaling", ctypes.c_int32)]
+
+
+_FP8 = ctypes.POINTER(mok_fp8_matrix)
+_lib.mok_fp8_quantize.restype = ctypes.c_int
+_lib.mok_fp8_quantize.argtypes = [_P, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, _P, _P]
+_lib.mok_fp8_quantize_routed.restype = ctypes.c_int
+_lib.mok_fp8_quantize_routed.argtypes = [_SCHED, ctypes.c_int32, _P, ctypes.c_int32, _P, _P, _P, _P, _P]
+_lib.mok_fp8_quantize_blocks.restype = ctypes.c_int
+_lib.mok_fp8_quantize_blocks.argtypes = [_P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, _P, _P]
+_lib.mok_fp8_matmul.restype = ctypes.c_int
+_lib.mok_fp8_matmul.argtypes = [_FP8, _FP8, _P, ctypes.c_int32, _P, _P]
+_lib.mok_fp8_linear_workspace_bytes.restype = ctypes.c_size_t
+_lib.mok_fp8_linear_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64]
+_lib.mok_fp8_linear.restype = ctypes.c_int
+_lib.mok_fp8_linear.argtypes = [_P, ctypes.c_int64, _FP8, _P, _P, ctypes.c_size_t, _P, _P]
+_lib.mok_fp8_grouped_matmul.restype = ctypes.c_int
+_lib.mok_fp8_grouped_matmul.argtypes = [_SCHED, _FP8, _FP8, _P, _P]
+_lib.mok_fp8_grouped_wgrad.restype = ctypes.c_int
+_lib.mok_fp8_grouped_wgrad.argtypes = [_SCHED, _FP8, _FP8, _P, ctypes.c_int32, _P]
+
+
+@dataclass
+class Fp8:
+    """An 8-bit matrix with one fp32 scale per block of 128, its summed axis along the rows.
+    q [rows, ld] or (block) [E, rows, ld]: E4M3 codes, uint8 or float8_e4m3fn; ld a multiple of 16, the first `cols` of a
+    row count.  s, fp32: [ceil(cols / 128), rows rounded up to 4], a scale per row and 128 columns, or (block)
+    [.., ceil(rows / 128), ceil(cols / 128)], one per 128 x 128 values."""
+    q: torch.Tensor
+    s: torch.Tensor
+    cols: int
+    block: bool = False
+
+    @property
+    def rows(self) -> int:
+        return self.q.shape[-2]
+
+
+def _fp8_named(m, name: str, batch: bool = False):
+    """Raises for what is wrong with an Fp8, by name; then its tensors as arguments of _refused."""
+    for t, part in ((m.q, "q"), (m.s, "s")):
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name}.{part} must be a tensor, got {type(t).__name__}")
+    if m.q.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise ValueError(f"{name}.q must be torch.uint8 or torch.float8_e4m3fn, got {m.q.dtype}")
+    if m.q.dim() != 2 + batch:
+        raise ValueError(f"{name}.q must have {2 + batch} dimensions, got shape {tuple(m.q.shape)}")
+    if not 0 <= m.cols <= m.q.shape[-1] or m.q.shape[-1] % 16:
+        raise ValueError(f"{name}.q's rows must be a multiple of 16 bytes and hold its {m.cols} columns, got {m.q.shape[-1]}")
+    b = lambda n: (n + 127) // 128  # noqa: E731
+    s = (b(m.rows), b(m.cols)) if m.block else (b(m.cols), (m.rows + 3) // 4 * 4)
+    return (m.q, m.q.shape, m.q.dtype, f"{name}.q"), (m.s, (*m.q.shape[:-2], *s), torch.float32, f"{name}.s")
+
+
+def _fp8(m, name: str, block: bool | None = None):
+    """Refuses what is no Fp8, or one of the other scaling (None: either)."""
+    if not isinstance(m, Fp8):
+        raise ValueError(f"{name} must be an Fp8, got {type(m).__name__}")
+    if block is not None and m.block != block:
+        raise ValueError(f"{name} must have scales per {'128 x 128 values' if block else 'row and 128 columns'}")
+
+
+def _opt(t, shape, dtype, name: str):
+    return () if t is None else ((t, shape, dtype, name),)
+
+
+def _pair_of(r, cols: int, rows: int, block: bool = False):
+    q, s, qt, st = r
+    return None if q is None else Fp8(q, s, cols, block), None if qt is None else Fp8(qt, st, rows, block)
+
+
+def fp8_quantize(x: torch.Tensor, transposed: bool = False, rows: bool = True, sched: Schedule | None = None, stream=None):
+    """(x, x^T) in 8 bits with a scale per row and 128 columns, either None if not asked for: x [R, C] bf16; x^T is for products
+    that sum over x's rows (weight gradients).  With a schedule x holds its routed rows [rpad_max, C]; padding rows
+    count as zeros."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return fp8_quantize(x, transposed, rows, sched)
+    return _quantized(x, transposed, rows, sched, 0)
+
+
+def dispatch_fp8(sched: Schedule, x: torch.Tensor, transposed: bool = False, rows: bool = True, stream=None):
+    """fp8_quantize of dispatch(sched, x), from the tokens x [T, C] bf16 in one step.  Padding rows of the first are not
+    written (the products do not use them)."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return dispatch_fp8(sched, x, transposed, rows)
+    return _quantized(x, transposed, rows, sched, 1)
+
+
+def _quantized(x, transposed, rows, sched, gather):
+    at = (0, -1) if sched is None else _placed(sched)
+    r = _bind.fp8_quantize(x, rows, transposed, *at, gather)
+    if type(r) is not tuple:
+        if sched is None:
+            _refused(r, "mok_fp8_quantize", (x, None, torch.bfloat16, "x"))
+        n = sched.c.shape.T if gather else sched.c.rpad_max
+        _sched_refused(r, "mok_fp8_quantize_routed", sched, (x, (n, _width(x)), torch.bfloat16, "x"))
+    return _pair_of(r, x.shape[1], x.shape[0] if sched is None else sched.c.rpad_max)
+
+
+def fp8_quantize_weight(w: torch.Tensor, transposed: bool = False, rows: bool = True, stream=None):
+    """(w, w^T) in 8 bits with a scale per 128 x 128 values, the same codes in both: w [N, K] or, one matrix per expert,
+    [E, N, K] bf16; w^T is for the data gradient."""
+    if stream is not None:
+        with _on_stream(stream, w):
+            return fp8_quantize_weight(w, transposed, rows)
+    r = _bind.fp8_quantize_blocks(w, rows, transposed)
+    if type(r) is not tuple:
+        _refused(r, "mok_fp8_quantize_blocks", (w, None, torch.bfloat16, "w"))
+    return _pair_of(r, w.shape[-1], w.shape[-2], True)
+
+
+def fp8_matmul(a: Fp8, b: Fp8, out_dtype=torch.bfloat16, out: torch.Tensor | None = None,
+               status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """a b^T for a [M, K] with scales per row and 128 columns and b [N, K] of either kind: [M, N] of out_dtype
+    (torch.bfloat16 or torch.float32).  status: one int32 on the device, bits (1 << status code) of what went wrong there."""
+    _fp8(a, "a", False)
+    _fp8(b, "b")
+    if stream is not None:
+        with _on_stream(stream, a.q):
+            return fp8_matmul(a, b, out_dtype, out, status)
+    if out_dtype not in _STREAM_TYPES:
+        raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    r = _bind.fp8_matmul(a.q, a.s, a.cols, b.q, b.s, b.cols, b.block, out, out_dtype is torch.float32, status)
+    if type(r) is not tuple:
+        named = _fp8_named(a, "a"), _fp8_named(b, "b")
+        if a.cols != b.cols:
+            raise ValueError(f"a and b must have the same columns, got {a.cols} and {b.cols}")
+        _refused(r, "mok_fp8_matmul", *named[0], *named[1], *_opt(out, (a.rows, b.rows), out_dtype, "out"),
+                 *_opt(status, (1,), torch.int32, "status"))
+    return r[0]
+
+
+def fp8_linear(x: torch.Tensor, w: Fp8, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """x w^T [M, N] bf16 for x [M, K] bf16, quantised on the way as by fp8_quantize, and w [N, K] with scales per
+    128 x 128 values.  status as in fp8_matmul."""
+    if stream is not None:
+        with _on_stream(stream, x):
+            return fp8_linear(x, w, out, status)
+    _fp8(w, "w", True)
+    r = _bind.fp8_linear(x, w.q, w.s, w.cols, out, status)
+    if type(r) is not tuple:
+        named = _fp8_named(w, "w")
+        M = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() else -1
+        _refused(r, "mok_fp8_linear", (x, (M, w.cols), torch.bfloat16, "x"), *named,
+                 *_opt(out, (M, w.rows), torch.bfloat16, "out"), *_opt(status, (1,), torch.int32, "status"))
+    return r[0]
+
+
+def fp8_grouped_matmul(sched: Schedule, a: Fp8, w: Fp8, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Every routed row times its expert's matrix: out [rpad_max, N] bf16 from a [rpad_max, K] (dispatch_fp8's, or routed rows
+    through fp8_quantize) and w [E, N, K] with scales per 128 x 128 values.  Padding rows of out are not written.  What goes
+    wrong on the device is in the schedule's status."""
+    _fp8(a, "a", False)
+    _fp8(w, "w", True)
+    if stream is not None:
+        with _on_stream(stream, a.q):
+            return fp8_grouped_matmul(sched, a, w, out)
+    r = _bind.fp8_grouped_matmul(*_placed(sched), a.q, a.s, a.cols, w.q, w.s, w.cols, out)
+    if type(r) is not tuple:
+        R = sched.c.rpad_max
+        named = _fp8_named(a, "a"), _fp8_named(w, "w", True)
+        if a.cols != w.cols:
+            raise ValueError(f"a and w must have the same columns, got {a.cols} and {w.cols}")
+        _sched_refused(r, "mok_fp8_grouped_matmul", sched, (a.q, (R, a.q.shape[1]), a.q.dtype, "a.q"), named[0][1],
+                       (w.q, (sched.c.shape.E, *w.q.shape[1:]), w.q.dtype, "w.q"), named[1][1],
+                       *_opt(out, (R, w.rows), torch.bfloat16, "out"))
+    return r[0]
+
+
+def fp8_grouped_wgrad(sched: Schedule, a: Fp8, b: Fp8, out_dtype=torch.float32, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """Weight gradients [E, N, K] of out_dtype: per expert the sum over its routed rows of a's times b's, for the transposed rows
+    a [N, rpad_max] and b [K, rpad_max] of fp8_quantize or dispatch_fp8.  An expert without rows gets zeros."""
+    _fp8(a, "a", False)
+    _fp8(b, "b", False)
+    if stream is not None:
+        with _on_stream(stream, a.q):
+            return fp8_grouped_wgrad(sched, a, b, out_dtype, out)
+    if out_dtype not in _STREAM_TYPES:
+        raise ValueError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    r = _bind.fp8_grouped_wgrad(*_placed(sched), a.q, a.s, a.cols, b.q, b.s, b.cols, out, out_dtype is torch.float32)
+    if type(r) is not tuple:
+        named = *_fp8_named(a, "a"), *_fp8_named(b, "b")
+        for m, name in ((a, "a"), (b, "b")):
+            if m.cols != sched.c.rpad_max:
+                raise ValueError(f"{name} must have the layout's {sched.c.rpad_max} rows as columns, got {m.cols}")
+        _sched_refused(r, "mok_fp8_grouped_wgrad", sched, *named,
+                       *_opt(out, (sched.c.shape.E, a.rows, b.rows), out_dtype, "out"))
+    return r[0]
 
 
 def mok_kernel_name(kind: int) -> str:
