@@ -19,6 +19,7 @@
 // in bursts), 603 us in a sustained loop; a forward of 4096 tokens at H = 2048, I = 1024 38.3 us, 1,350 TFLOP/s; a
 // training step of 1003 tokens at H = 2056, I = 1000 61 us: its four launches cost 5 us each besides their tiles.
 #include "mok_ffn.cuh"
+#include "mok_stage.cuh"
 
 namespace mok {
 namespace {
@@ -137,56 +138,6 @@ __device__ __forceinline__ void pair_load_b(const PairArgs& p, const PairMaps& t
     for (int j = 0; j < static_cast<int>(PairCfg<VAR, BN>::kBBoxes); ++j)
       tma_load_2d_pair(sb + j * 8192, tb, bar, w.n * BN + rank * HB + j * 64, kr);
   }
-}
-
-// One epilogue warp's output staging: two shared tiles of 32 rows x 64 bytes in the 64-byte TMA swizzle
-// (chunk j of row r at j ^ ((r >> 1) & 3)), each stored by one TMA store that clips at the tensor's
-// edges; a tile is refilled once its previous store has read it.
-struct WarpStage {
-  uint32_t base;
-  int cur, lane;
-  __device__ __forceinline__ void put(const uint4 (&ch)[4], const CUtensorMap* tm, int c0, int r0) {
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
-    const uint32_t b = base + static_cast<uint32_t>(cur) * 2048u;
-    cur ^= 1;
-    const uint32_t row = b + static_cast<uint32_t>(lane) * 64u;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) st_shared_v4(row + (static_cast<uint32_t>(j ^ ((lane >> 1) & 3)) << 4), ch[j]);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      tma_store_2d(tm, b, c0, r0);
-      bulk_commit();
-    }
-  }
-  __device__ __forceinline__ void put_bf16(const float (&v)[32], const CUtensorMap* tm, int c0, int r0) {
-    uint4 ch[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      ch[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                         pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-    put(ch, tm, c0, r0);
-  }
-};
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  tmem_ld_32x32b_x32(taddr, r);
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 32 columns of this lane's row of the saved factors (ffn_saved_offset), 4 columns per entry.  DACT keeps one

@@ -31,8 +31,10 @@ mok_status product(const mok_fp8_matrix& a, const mok_fp8_matrix& b, void* out, 
   g.out = out;
   g.ldo = b.rows;
   g.out_f32 = out_type == MOK_DT_FP32;
-  g.early_p = early;
+  g.early_p = g.early_q = early;
   g.status = status;
+  if (a.rows > 128 && fp8_blocks(a.rows) * fp8_blocks(b.rows) >= sm_count() / 2)
+    return from_cuda(launch_fp8_pair(operand(a), operand(b), g, 0, K_FP8_PAIR, stream));
   return from_cuda(launch_fp8_tile(operand(a), operand(b), g, a.rows, 0, K_FP8_TILE, stream));
 }
 
@@ -103,10 +105,14 @@ mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matri
   g.experts = z.E;
   g.mblocks = sched->mblocks;
   g.poff = sched->poff;
+  g.counts = sched->counts;
   g.meta = sched->meta;
   g.status = sched->status;
   // an expert with rows has one block that is not full at most
   const int64_t blocks = (z.R < z.E ? z.R : z.E) + z.R / 128;
+  if (z.R >= 64 * static_cast<int64_t>(z.E))
+    return from_cuda(launch_fp8_pair(operand(*a), operand(*w), g, (z.R < z.E ? z.R : z.E) + z.R / 256, K_FP8_GROUPED_PAIR,
+                                     static_cast<cudaStream_t>(stream)));
   return from_cuda(launch_fp8_tile(operand(*a), operand(*w), g, z.R, blocks < z.mblocks_max ? blocks : z.mblocks_max,
                                    K_FP8_GROUPED_TILE, static_cast<cudaStream_t>(stream)));
 }
@@ -135,9 +141,10 @@ mok_status mok_fp8_grouped_wgrad(const mok_schedule* sched, const mok_fp8_matrix
   g.experts = z.E;
   g.mblocks = sched->mblocks;
   g.poff = sched->poff;
+  g.counts = sched->counts;
   g.meta = sched->meta;
   g.status = sched->status;
-  return from_cuda(launch_fp8_tile(operand(*a), operand(*b), g, z.R, 0, K_FP8_WGRAD, s));
+  return from_cuda(launch_fp8_pair(operand(*a), operand(*b), g, 0, K_FP8_WGRAD, s));
 }
 
 }  // extern "C"

@@ -33,10 +33,11 @@ struct Fp8Problem {
   void* out;
   int64_t ldo;
   int32_t out_f32;
-  int32_t early_p;           // P (weights) may be read before the previous kernel of the stream ends
+  int32_t early_p, early_q;  // P or Q (weights) may be read before the previous kernel of the stream ends
   int32_t experts;
   const int32_t* mblocks;    // of the schedule
   const int32_t* poff;
+  const int32_t* counts;
   const int32_t* meta;
   uint32_t* status;
 };
@@ -44,5 +45,11 @@ struct Fp8Problem {
 // rows: of a that hold values; row_blocks: (FP8_GROUPED) 128-row blocks of the layout at most.
 int launch_fp8_tile(const Fp8Operand& a, const Fp8Operand& b, Fp8Problem g, int64_t rows, int64_t row_blocks, int kind,
                     cudaStream_t stream);
+
+bool make_tmap_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
+                   uint32_t box_outer);
+
+// p: rows of the output, with a scale per row; q: its columns.  row_units: (FP8_GROUPED) 256-row units at most.
+int launch_fp8_pair(const Fp8Operand& p, const Fp8Operand& q, Fp8Problem g, int64_t row_units, int kind, cudaStream_t stream);
 
 }  // namespace mok

@@ -1,0 +1,486 @@
+// mok_fp8_pair.cu -- 8-bit products with a scale per 128 values for many rows: persistent CTA pairs.
+//
+// A cluster of two CTAs computes 256 x BN tiles with tcgen05.mma.cta_group::2: each CTA loads its own 128 rows of P and half
+// of Q's rows, 32 KB per K block of 128 of a 256 x 256 tile.  The scales belong to whole K blocks, so every block's
+// products go to a TMEM accumulator of their own, one of 512 / BN in turn; eight warps per CTA drain it, two per TMEM lane
+// quarter with half of the columns each, times the block's scales into fp32 registers (BN / 2 per thread), while the
+// MMAs fill the next one.  A tile's output goes through shared memory and leaves by TMA while the next tile's blocks are in
+// the tensor cores.
+//
+// (Measured and not taken: 256-column tiles on four accumulators of 128 columns, two MMA groups per K block, 8192 x 8192 x
+// 8192 504 us against 400: A is read from shared memory twice.)
+//
+// Modes: dense rows; a schedule's rows against one matrix per expert (the units of 256 rows are counted from the
+// expert counts on the device, by every CTA for itself); weight gradients, whose K blocks are the 128-row blocks
+// of an expert's rows.
+#include "mok_ffn.cuh"  // warp_wait, wait_landed, elect_one, ordered_tile
+#include "mok_fp8_gemm.cuh"
+#include "mok_stage.cuh"
+
+namespace mok {
+namespace {
+
+// Warpgroup 0: warp 0 loads, warp 1 issues MMAs; warpgroups 1 and 2 drain.  A drain thread of a 256-column tile needs more
+// registers than a third of the SM's: the first group gives up of its own.  128 x 40 + 256 x 232 (and 128 x 72 + 256 x
+// 216) are the 384 x 168 that a launch has.
+constexpr int kThreads = 384;
+constexpr int kDrain = 4;  // the first drain warp
+constexpr int kMaxExperts = 1024;
+
+struct PairArgs {
+  Fp8Problem g;
+  int32_t pairs;
+  int32_t units;  // dense, weight gradients; a schedule's are counted on the device
+};
+struct PairMaps {
+  CUtensorMap p, q, out;
+};
+
+template <int BN, bool COLVEC>
+struct Cfg {
+  static constexpr int kLow = BN == 256 ? 40 : 72, kHigh = BN == 256 ? 232 : 216;  // registers per thread
+  static constexpr int HB = BN / 2;      // columns of a drain thread
+  static constexpr int kAccs = 512 / BN; // accumulators in TMEM
+  static constexpr uint32_t kQBytes = HB * 128, kStage = 16384 + kQBytes, kTx = 2 * kStage;
+  static constexpr uint32_t kStaging = 4096;     // per drain warp: a box of 32 rows x 128 bytes
+  // scales of a K block: the CTA's 128 rows', and (COLVEC) the tile's columns'.  A slot is filled again once the MMAs of
+  // kStages blocks before have ended, that is once the blocks two accumulators further back have been drained.
+  static constexpr int kSlots = BN == 256 ? 8 : 12;
+  static constexpr uint32_t kScales = 512 + (COLVEC ? BN * 4 : 0);
+  static constexpr uint32_t kMost = 227328;      // 5 KB of 227 are static
+  static constexpr uint32_t kFixed = 1024 + 8 * kStaging + kSlots * kScales + 512;
+  static constexpr int kStages = (kMost - kFixed) / kStage < 8 ? (kMost - kFixed) / kStage : 8;
+  static constexpr uint32_t kStagingOff = kStages * kStage;
+  static constexpr uint32_t kScaleOff = kStagingOff + 8 * kStaging;
+  static constexpr uint32_t kBarOff = kScaleOff + kSlots * kScales;
+  static constexpr uint32_t kSmem = 1024 + kBarOff + 512;
+  static_assert(2 * kStages + 2 * kAccs + 1 + kSlots <= 48, "barriers fit");
+  static_assert(kSlots > kStages + kAccs, "scales stay until they are used");
+};
+
+struct Unit {
+  int32_t p0, q0;           // first rows of the pair's tile in the operands' tensor maps
+  int32_t row0, row_end;    // output rows: row0 + r for tile row r, below row_end
+  int32_t j0;
+  int32_t kb0, count;
+  int32_t batch;
+};
+
+// Unit u: p0 is the pair's first row of P, rank adds 128.  `prefix`: (grouped) units of 256 rows before each expert.
+__device__ __forceinline__ void pair_unit(const Fp8Problem& g, const int* prefix, int u, int bn, Unit& w) {
+  w.kb0 = 0;
+  w.count = g.k_blocks;
+  w.batch = 0;
+  if (g.mode == FP8_DENSE) {
+    int m, n;
+    ordered_tile(u, g.p_tiles, g.q_tiles, m, n);
+    w.p0 = w.row0 = m * 256;
+    w.row_end = g.p_rows;
+    w.j0 = w.q0 = n * bn;
+  } else if (g.mode == FP8_WGRAD) {
+    const int per = g.p_tiles * g.q_tiles, e = u / per;
+    int m, n;
+    ordered_tile(u - e * per, g.p_tiles, g.q_tiles, m, n);
+    w.batch = e;
+    w.kb0 = __ldg(g.poff + e) / 128;
+    w.count = __ldg(g.poff + e + 1) / 128 - w.kb0;
+    w.p0 = m * 256;
+    w.row0 = e * g.p_rows + w.p0;
+    w.row_end = (e + 1) * g.p_rows;
+    w.j0 = w.q0 = n * bn;
+  } else {
+    const int mu = u / g.q_tiles, n = u - mu * g.q_tiles;
+    int lo = 0, hi = g.experts - 1;  // the last expert whose units begin at or before mu
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (prefix[mid] <= mu) lo = mid;
+      else hi = mid - 1;
+    }
+    const int first = __ldg(g.poff + lo);
+    w.batch = lo;
+    w.p0 = w.row0 = first + (mu - prefix[lo]) * 256;
+    w.row_end = first + __ldg(g.counts + lo);
+    w.j0 = n * bn;
+    w.q0 = lo * g.q_rows + w.j0;
+  }
+}
+
+// prefix[e] = units of 256 rows of the experts before e; returns their number.  All threads.
+__device__ __forceinline__ int count_units(const Fp8Problem& g, int* prefix, int* wsum) {
+  constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = threadIdx.x * kPer;
+  int v[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    v[i] = e0 + i < g.experts ? (__ldg(g.counts + e0 + i) + 255) / 256 : 0;
+    sum += v[i];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  int at = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) at += wsum[w];
+    total += wsum[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (e0 + i < g.experts) prefix[e0 + i] = at;
+    at += v[i];
+  }
+  __syncthreads();
+  return total;
+}
+
+template <int BN, bool COLVEC>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ PairMaps t, const PairArgs a) {
+  using C = Cfg<BN, COLVEC>;
+  constexpr int S = C::kStages, HB = C::HB, kAccs = C::kAccs;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int prefix[kMaxExperts];
+  __shared__ int wsum[kThreads / 32];
+  const Fp8Problem& g = a.g;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;  // swizzle atoms: 1024-byte aligned
+  uint8_t* smem = smem_raw + (base - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 48);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t bar0 = smem_u32(bars);
+  // the pair counts loads and drained accumulators on the first CTA's full / tempty barriers; each CTA has its own
+  // empty, tfull and drain barriers, on which the first CTA's commits arrive
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+  auto tfull = [&](int b) { return bar0 + 8u * (2 * S + b); };
+  auto tempty = [&](int b) { return bar0 + 8u * (2 * S + kAccs + b); };
+  const uint32_t drain = bar0 + 8u * (2 * S + 2 * kAccs);
+  auto sfull = [&](int i) { return drain + 8u * (1 + i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < kAccs; ++b) {
+      mbar_init(tfull(b), 1);
+      mbar_init(tempty(b), 16);  // eight warps of each CTA
+    }
+    mbar_init(drain, 1);
+    for (int i = 0; i < C::kSlots; ++i) mbar_init(sfull(i), 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&t.p);
+    tma_prefetch_desc(&t.q);
+    tma_prefetch_desc(&t.out);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  int units = a.units;
+  if (g.mode != FP8_DENSE) pdl_wait();  // the schedule's tables
+  if (g.mode == FP8_GROUPED) units = count_units(g, prefix, wsum) * g.q_tiles;
+  tc_fence_before();
+  cluster_sync();  // the peer's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp < kDrain) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLow));
+  if (warp == 0) {
+    int ahead = 0;
+    auto load_q = [&](const Unit& w, int kb, int st) {
+      tma_load_2d_pair(base + st * C::kStage + 16384, &t.q, mapa_shared(full(st), 0), (w.kb0 + kb) * 128, w.q0 + rank * HB);
+    };
+    if (g.early_q && pair < units) {  // weights: nothing that still runs writes them
+      Unit w;
+      pair_unit(g, prefix, pair, BN, w);
+      ahead = min(w.count, S);
+      for (int kb = 0; kb < ahead; ++kb)
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(full(kb), C::kTx);
+          load_q(w, kb, kb);
+        }
+    }
+    pdl_wait();
+    int st = 0, issued = 0, slot = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int u = pair; u < units && ok; u += a.pairs) {
+      Unit w;
+      pair_unit(g, prefix, u, BN, w);
+      // the scales that go with a block: this CTA's rows' and all columns', as many as there are (rounded up to four)
+      const int row = w.p0 + rank * 128;
+      const int64_t rows = g.p_pitch - row, cols = g.q_pitch - w.j0;
+      const uint32_t pb = rows <= 0 ? 0u : rows < 128 ? static_cast<uint32_t>(rows) * 4u : 512u;
+      const uint32_t qb = !COLVEC ? 0u : cols < BN ? static_cast<uint32_t>(cols) * 4u : BN * 4u;
+      for (int kb = 0; kb < w.count; ++kb) {
+        if (!warp_wait(empty(st), ph ^ 1u, abort_flag, g.status)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          if (issued >= ahead) {
+            if (rank == 0) mbar_arrive_expect_tx(full(st), C::kTx);
+            load_q(w, kb, st);
+          }
+          tma_load_2d_pair(base + st * C::kStage, &t.p, mapa_shared(full(st), 0), (w.kb0 + kb) * 128, row);
+          const uint32_t to = base + C::kScaleOff + slot * C::kScales;
+          const int64_t k = w.kb0 + kb;
+          mbar_arrive_expect_tx(sfull(slot), pb + qb);
+          if (pb) bulk_load(to, g.sp + k * g.p_pitch + row, pb, sfull(slot));
+          if (qb) bulk_load(to + 512, g.sq + k * g.q_pitch + w.j0, qb, sfull(slot));
+        }
+        ++issued;
+        if (++slot == C::kSlots) slot = 0;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    if (!ok && rank == 0 && lane == 0)  // let the copies in flight land: the last one of each stage
+      for (int b = issued > S ? issued - S : 0; b < issued; ++b) wait_landed(full(b % S), static_cast<uint32_t>(b / S) & 1u);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      pdl_wait();  // the kernel in front may take its time: no bounded wait starts before its end
+      int st = 0, n = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = pair; u < units && ok; u += a.pairs) {
+        Unit w;
+        pair_unit(g, prefix, u, BN, w);
+        for (int kb = 0; kb < w.count; ++kb, ++n) {
+          const int b = n % kAccs;
+          const uint32_t read = static_cast<uint32_t>(n / kAccs - 1) & 1u;  // parity of that accumulator's last drain
+          ok = (n < kAccs || warp_wait(tempty(b), read, abort_flag, g.status)) && warp_wait(full(st), ph, abort_flag, g.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sp = base + st * C::kStage;
+          const uint64_t pd = sdesc_sw128(sp, 16, 1024), qd = sdesc_sw128(sp + 16384, 16, 1024);
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)  // 32 bytes of K; descriptors count 16-byte units
+              umma_fp8_pair(tmem + b * BN, pd + ks * 2, qd + ks * 2, idesc_fp8(256, BN), ks > 0 ? 1u : 0u);
+            umma_commit_pair(tfull(b));
+            umma_commit_pair(empty(st));
+          }
+          if (++st == S) {
+            st = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (elect_one()) umma_commit_pair(drain);  // every MMA issued has ended before TMEM is freed, in both CTAs
+    }
+    __syncwarp();
+    if (lane == 0) wait_landed(drain, 0);
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kHigh));
+    const int q = warp & 3, dw = warp - kDrain, h = dw >> 2;
+    pdl_wait();
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * HB;
+    const uint32_t stage = base + C::kStagingOff + static_cast<uint32_t>(dw) * C::kStaging;
+    int n = 0;
+    bool ok = true;
+    for (int u = pair; u < units; u += a.pairs) {
+      Unit w;
+      pair_unit(g, prefix, u, BN, w);
+      const int j0 = w.j0 + h * HB;
+      float acc[HB];
+#pragma unroll
+      for (int j = 0; j < HB; ++j) acc[j] = 0.0f;
+      // the tile's column blocks' scales (one per thread's columns), 32 K blocks at a time and one lot ahead, a lane each
+      const float* qs = g.sq + w.batch * g.q_batch + static_cast<int64_t>(min(j0, g.q_rows - 1) / 128) * g.k_blocks;
+      float q_now = 0.0f, q_next = !COLVEC && lane < w.count ? __ldg(qs + lane) : 0.0f;
+      for (int kb = 0; kb < w.count; ++kb, ++n) {
+        if (!COLVEC && kb % 32 == 0) {
+          q_now = q_next;
+          if (kb + 32 + lane < w.count) q_next = __ldg(qs + kb + 32 + lane);
+        }
+        const int slot = n % C::kSlots;
+        ok = warp_wait(sfull(slot), static_cast<uint32_t>(n / C::kSlots) & 1u, abort_flag, g.status);
+        if (!ok) break;
+        const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff + slot * C::kScales);
+        const float* cs = sc + 128 + h * HB;
+        float s = sc[q * 32 + lane];
+        if constexpr (!COLVEC) s *= __shfl_sync(0xffffffffu, q_now, kb % 32);
+        const int b = n % kAccs;
+        ok = warp_wait(tfull(b), static_cast<uint32_t>(n / kAccs) & 1u, abort_flag, g.status);
+        if (!ok) break;
+        tc_fence_after();
+        // chunks of 32 columns, the next one on its way while this one is added
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(lanes + b * BN, v[0]);
+#pragma unroll
+        for (int c = 0; c < HB; c += 32) {
+          uint32_t(&x)[32] = v[c / 32 & 1];
+          tmem_ld_wait_for(x);
+          if (c + 32 < HB) {
+            tmem_ld_32x32b_x32(lanes + b * BN + c + 32, v[(c / 32 + 1) & 1]);
+          } else {  // read whole: the MMAs may write it again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty(b), 0));
+          }
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            float f0 = s, f1 = s, f2 = s, f3 = s;
+            if constexpr (COLVEC) {
+              const float4 y = *reinterpret_cast<const float4*>(cs + c + j);
+              mul_f32x2(f0, f1, s, s, y.x, y.y);
+              mul_f32x2(f2, f3, s, s, y.z, y.w);
+            }
+            fma_f32x2(acc[c + j], acc[c + j + 1], __uint_as_float(x[j]), __uint_as_float(x[j + 1]), f0, f1, acc[c + j],
+                      acc[c + j + 1]);
+            fma_f32x2(acc[c + j + 2], acc[c + j + 3], __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]), f2, f3,
+                      acc[c + j + 2], acc[c + j + 3]);
+          }
+        }
+      }
+      if (!ok) break;
+      // The tile's 32 rows of this warp.  Where all of them are there: through shared memory, a box of 32 rows x 128 bytes
+      // at a time (in the 128-byte TMA swizzle: 16-byte chunk k of row r at k ^ (r & 7)); else row by row.
+      const int row0 = w.row0 + rank * 128 + q * 32;
+      if (row0 >= w.row_end) continue;
+      if (row0 + 32 <= w.row_end) {
+        auto box = [&](const uint32_t (&x)[32], int c0) {
+          if (c0 >= g.q_rows) return;
+          if (lane == 0) bulk_wait_read<0>();  // what was stored from here before has been read
+          __syncwarp();
+          const uint32_t at = stage + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            st_shared_v4(at + (static_cast<uint32_t>(k ^ (lane & 7)) << 4), make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&t.out, stage, c0, row0);
+            bulk_commit();
+          }
+        };
+        uint32_t x[32];
+        if (!g.out_f32) {
+#pragma unroll
+          for (int c = 0; c < HB; c += 64) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = pack_bf16x2(acc[c + 2 * k], acc[c + 2 * k + 1]);
+            box(x, j0 + c);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < HB; c += 32) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(acc[c + k]);
+            box(x, j0 + c);
+          }
+        }
+      } else if (row0 + lane < w.row_end) {
+        const int64_t at = static_cast<int64_t>(row0 + lane) * g.ldo + j0;
+        if (g.out_f32) {
+          float* o = static_cast<float*>(g.out) + at;
+#pragma unroll
+          for (int j = 0; j < HB; j += 4)
+            if (j0 + j < g.q_rows) *reinterpret_cast<float4*>(o + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(g.out) + at;
+#pragma unroll
+          for (int j = 0; j < HB; j += 8)
+            if (j0 + j < g.q_rows)
+              *reinterpret_cast<uint4*>(o + j) =
+                  make_uint4(pack_bf16x2(acc[j], acc[j + 1]), pack_bf16x2(acc[j + 2], acc[j + 3]),
+                             pack_bf16x2(acc[j + 4], acc[j + 5]), pack_bf16x2(acc[j + 6], acc[j + 7]));
+        }
+      }
+      __syncwarp();
+    }
+    if (lane == 0) bulk_wait_read<0>();  // the staging has been read; the grid's end waits for the writes
+    __syncwarp();
+  }
+  if (*abort_flag) {  // failure path: copies or arrivals of the peer may still be in flight
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < kWaitLimitNs / 100) {
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the other may still address it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int BN, bool COLVEC>
+int launch_pair(const PairMaps& maps, const PairArgs& a, int kind, cudaStream_t stream) {
+  using C = Cfg<BN, COLVEC>;
+  static DeviceOnce once;
+  const int se = once.run([](int* d) { return static_cast<int>(cudaGetDevice(d)); },
+                          [] {
+                            return static_cast<int>(cudaFuncSetAttribute(fp8_pair_kernel<BN, COLVEC>,
+                                                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                                         static_cast<int>(C::kSmem)));
+                          },
+                          static_cast<int>(cudaErrorInvalidDevice));
+  if (se) return se;
+  trace_begin(stream, kind);
+  const cudaError_t e = launch_pdl(fp8_pair_kernel<BN, COLVEC>, dim3(2 * a.pairs), dim3(kThreads), C::kSmem, stream, maps, a);
+  trace_end(stream);
+  return static_cast<int>(e);
+}
+
+template <int BN>
+int pair_width(const Fp8Operand& p, const Fp8Operand& q, PairArgs a, int64_t out_rows, int kind, cudaStream_t stream) {
+  Fp8Problem& g = a.g;
+  g.q_tiles = static_cast<int32_t>((q.rows + BN - 1) / BN);
+  int64_t units = static_cast<int64_t>(g.p_tiles) * g.q_tiles * (g.mode == FP8_WGRAD ? g.experts : 1);
+  if (units == 0) return 0;
+  if (units >= (int64_t{1} << 30)) return static_cast<int>(cudaErrorInvalidValue);
+  a.units = static_cast<int32_t>(units);
+  if (units < a.pairs) a.pairs = static_cast<int32_t>(units);
+  PairMaps m;
+  const uint64_t N = static_cast<uint64_t>(q.rows), R = static_cast<uint64_t>(out_rows);
+  const bool good =
+      make_tmap_fp8(&m.p, p.q, static_cast<uint64_t>(p.cols), static_cast<uint64_t>(p.rows), static_cast<uint64_t>(p.ld), 128) &&
+      make_tmap_fp8(&m.q, q.q, static_cast<uint64_t>(q.cols), static_cast<uint64_t>(q.rows) * q.batch,
+                    static_cast<uint64_t>(q.ld), BN / 2) &&
+      (g.out_f32 ? make_tmap_f32(&m.out, g.out, N, R, 32, 32) : make_tmap_bf16(&m.out, g.out, N, R, 64, 32));
+  if (!good) return static_cast<int>(cudaErrorInvalidValue);
+  return q.row_scales ? launch_pair<BN, true>(m, a, kind, stream) : launch_pair<BN, false>(m, a, kind, stream);
+}
+
+}  // namespace
+
+int launch_fp8_pair(const Fp8Operand& p, const Fp8Operand& q, Fp8Problem g, int64_t row_units, int kind, cudaStream_t stream) {
+  const int pairs = sm_count() / 2;
+  if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
+  g.sp = p.s;
+  g.p_vec = 1;
+  g.p_pitch = fp8_pitch(p.rows);
+  g.p_rows = static_cast<int32_t>(p.rows);
+  g.sq = q.s;
+  g.q_pitch = fp8_pitch(q.rows);
+  g.q_batch = fp8_blocks(q.rows) * g.k_blocks;
+  g.q_rows = static_cast<int32_t>(q.rows);
+  g.p_tiles = static_cast<int32_t>(g.mode == FP8_GROUPED ? row_units : (p.rows + 255) / 256);
+  PairArgs a{};
+  a.g = g;
+  a.pairs = pairs;
+  const int64_t mats = g.mode == FP8_WGRAD ? g.experts : 1;
+  const int64_t out_rows = p.rows * mats;
+  if (g.p_tiles * ((q.rows + 255) / 256) * mats >= pairs) return pair_width<256>(p, q, a, out_rows, kind, stream);
+  return pair_width<128>(p, q, a, out_rows, kind, stream);
+}
+
+}  // namespace mok

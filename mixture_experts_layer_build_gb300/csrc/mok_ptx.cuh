@@ -129,6 +129,12 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same without a fence: for arrivals that publish no memory, such as "this accumulator has been read" behind
+// tcgen05.wait::ld and tcgen05.fence::before_thread_sync.  (A release at cluster scope waits for all of the thread's
+// memory operations.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 
 // ------------------------------------------------------------------------------------------------
 // cluster launch control: a running CTA takes over the work of a CTA that has not started yet
