@@ -33,7 +33,10 @@ mok_status product(const mok_fp8_matrix& a, const mok_fp8_matrix& b, void* out, 
   g.out_f32 = out_type == MOK_DT_FP32;
   g.early_p = g.early_q = early;
   g.status = status;
-  if (a.rows > 128 && fp8_blocks(a.rows) * fp8_blocks(b.rows) >= sm_count() / 2)
+  // Pairs from about a quarter of the SMs' worth of 128 x 128 tiles on, or where K is short; below, tiles, which can split K.
+  // Measured, tiles and pairs: 129 x 2048 x 7168 12.3 and 20.2 us, 512 x 1536 x 4096 13.0 and 13.4, 1003 x 1000 x 2056 10.2 and 9.7,
+  // 256 x 1024 x 1024 7.0 and 6.6, 1024 x 2048 x 2048 13.7 and 9.5; both row-scaled 512 x 512 x 2048 7.8 and 10.6.
+  if (a.rows > 128 && (4 * fp8_blocks(a.rows) * fp8_blocks(b.rows) >= sm_count() || g.k_blocks <= 8))
     return from_cuda(launch_fp8_pair(operand(a), operand(b), g, 0, K_FP8_PAIR, stream));
   return from_cuda(launch_fp8_tile(operand(a), operand(b), g, a.rows, 0, K_FP8_TILE, stream));
 }

@@ -51,6 +51,9 @@ struct Fp8Source {
   const uint16_t* x;
   const int32_t* row_token;  // null: plain rows
   const int32_t* meta;
+  const int32_t* inv;        // the row of each token's slots
+  int64_t tokens;
+  int32_t K;
   int32_t gather;
 };
 int launch_fp8_quantize(const Fp8Source& src, int64_t rows, int32_t cols, uint8_t* q, float* s, uint8_t* qt, float* st,

@@ -18,8 +18,8 @@ struct Fp8Operand {
   bool row_scales;
 };
 
-// P: the operand whose rows are an accumulator's lanes, Q: its columns.  Scales of K block kb: a scale per row (P:
-// p_vec) at s[kb * pitch + row], one per 128 rows at s[matrix * batch + row / 128 * k_blocks + kb].
+// P: the operand whose rows are an accumulator's lanes, Q: its columns (the tile kernel has P = b, the pairs P = a).  Scales
+// of K block kb: a scale per row at s[kb * pitch + row], one per 128 rows at s[matrix * batch + row / 128 * k_blocks + kb].
 struct Fp8Problem {
   int32_t mode;
   int32_t p_rows, q_rows;    // of one matrix
@@ -27,7 +27,6 @@ struct Fp8Problem {
   int32_t k_blocks;
   const float* sp;
   const float* sq;
-  int32_t p_vec;
   int64_t p_pitch, q_pitch;
   int64_t p_batch, q_batch;
   void* out;
@@ -42,7 +41,7 @@ struct Fp8Problem {
   uint32_t* status;
 };
 
-// rows: of a that hold values; row_blocks: (FP8_GROUPED) 128-row blocks of the layout at most.
+// out [rows of a, rows of b].  rows: of a that hold values; row_blocks: (FP8_GROUPED) 128-row blocks of the layout at most.
 int launch_fp8_tile(const Fp8Operand& a, const Fp8Operand& b, Fp8Problem g, int64_t rows, int64_t row_blocks, int kind,
                     cudaStream_t stream);
 

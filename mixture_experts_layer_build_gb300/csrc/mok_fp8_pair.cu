@@ -466,7 +466,6 @@ int launch_fp8_pair(const Fp8Operand& p, const Fp8Operand& q, Fp8Problem g, int6
   const int pairs = sm_count() / 2;
   if (pairs <= 0) return static_cast<int>(cudaErrorInvalidDevice);
   g.sp = p.s;
-  g.p_vec = 1;
   g.p_pitch = fp8_pitch(p.rows);
   g.p_rows = static_cast<int32_t>(p.rows);
   g.sq = q.s;
@@ -479,7 +478,14 @@ int launch_fp8_pair(const Fp8Operand& p, const Fp8Operand& q, Fp8Problem g, int6
   a.pairs = pairs;
   const int64_t mats = g.mode == FP8_WGRAD ? g.experts : 1;
   const int64_t out_rows = p.rows * mats;
-  if (g.p_tiles * ((q.rows + 255) / 256) * mats >= pairs) return pair_width<256>(p, q, a, out_rows, kind, stream);
+  // The tile width of fewer rounds of tiles, a round as long as its K blocks (440 ns of 256 columns, 310 of 128) and 1 us
+  // besides.  A schedule's rows count as spread evenly, a weight gradient's K likewise.
+  const int64_t k = g.mode == FP8_WGRAD ? (g.k_blocks + g.experts - 1) / g.experts : g.k_blocks;
+  auto cost = [&](int bn, int64_t ns) {
+    const int64_t tiles = static_cast<int64_t>(g.p_tiles) * ((q.rows + bn - 1) / bn) * mats;
+    return (tiles + pairs - 1) / pairs * (k * ns + 1000);
+  };
+  if (cost(256, 440) <= cost(128, 310)) return pair_width<256>(p, q, a, out_rows, kind, stream);
   return pair_width<128>(p, q, a, out_rows, kind, stream);
 }
 

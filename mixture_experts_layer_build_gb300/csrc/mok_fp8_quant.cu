@@ -8,6 +8,7 @@
 // 8 bytes of a transposed row) and leave as 16-byte vectors.
 //
 // Bound by HBM: 2 bytes read, 1 written per value and form.
+#include "mok_ffn.cuh"  // pdl_trigger
 #include "mok_fp8.cuh"
 
 namespace mok {
@@ -36,6 +37,7 @@ __device__ __forceinline__ uint32_t absmax_word(uint32_t m) { return absmax2(m, 
 template <int FORM, bool GATHER>
 __global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs p) {
   pdl_wait();
+  pdl_trigger();  // a product that follows sets itself up, and loads weights, meanwhile
   __shared__ uint32_t wmax[8][64];                                // per warp, packed column maxima
   __shared__ __align__(16) uint8_t tile[FORM == Q_ROWS ? 16 : 128 * kQStride];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, cg = t & 15, rg = t >> 4;
@@ -183,9 +185,69 @@ __global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs
   }
 }
 
+// Rows alone, on the dispatch gather: in token order, each token's row read and quantised once and written to the rows of its K
+// slots (the tile kernel above reads it K times).  A warp takes 1024 columns of a token, a lane 16 contiguous ones of
+// each of two 512-column pieces: 8 lanes hold a block of 128, codes leave as 16 bytes per lane.  Measured at T = 8192, H =
+// 4096, K = 8 (E = 128): see the product's header for what follows it.
+__global__ void __launch_bounds__(kQThreads) fp8_dispatch_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ inv,
+                                                                 int64_t T, int K, int cols, int64_t ld, int64_t pitch,
+                                                                 uint8_t* __restrict__ q, float* __restrict__ s) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = static_cast<int64_t>(blockIdx.x) * (kQThreads / 32) + (threadIdx.x >> 5);
+  const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kQThreads / 32);
+  const int64_t chunks = (cols + 1023) / 1024;
+  for (int64_t item = warp; item < T * chunks; item += nwarps) {
+    const int64_t t = item / chunks;
+    const int c0 = static_cast<int>(item - t * chunks) * 1024 + lane * 16;
+    uint4 v[2][2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = c0 + 512 * u + 8 * h;
+        v[u][h] = c < cols ? __ldcs(reinterpret_cast<const uint4*>(x + t * cols + c)) : make_uint4(0, 0, 0, 0);
+      }
+    uint4 codes[2];
+    float scale[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t m = absmax2(absmax2(absmax2(v[u][0].x, v[u][0].y), absmax2(v[u][0].z, v[u][0].w)),
+                           absmax2(absmax2(v[u][1].x, v[u][1].y), absmax2(v[u][1].z, v[u][1].w)));
+#pragma unroll
+      for (int d = 4; d >= 1; d >>= 1) m = absmax2(m, __shfl_xor_sync(0xffffffffu, m, d));
+      m = absmax_word(m);
+      float up;
+      scale[u] = fp8_scale(m, up);
+      codes[u] = make_uint4(fp8_codes(v[u][0].x, up) | fp8_codes(v[u][0].y, up) << 16,
+                            fp8_codes(v[u][0].z, up) | fp8_codes(v[u][0].w, up) << 16,
+                            fp8_codes(v[u][1].x, up) | fp8_codes(v[u][1].y, up) << 16,
+                            fp8_codes(v[u][1].z, up) | fp8_codes(v[u][1].w, up) << 16);
+      if (m >= 0x7F80u) {
+        const uint32_t second = c0 + 512 * u + 8 < cols ? 0x7F7F7F7Fu : 0u;  // (past the columns: zeros up to the pitch)
+        codes[u] = make_uint4(0x7F7F7F7Fu, 0x7F7F7F7Fu, second, second);
+      }
+    }
+    for (int k0 = 0; k0 < K; k0 += 32) {
+      const int row = k0 + lane < K ? __ldg(inv + t * K + k0 + lane) : -1;
+      for (unsigned live = __ballot_sync(0xffffffffu, row >= 0); live; live &= live - 1) {
+        const int64_t r = __shfl_sync(0xffffffffu, row, __ffs(live) - 1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = c0 + 512 * u;
+          if (c >= cols) continue;
+          __stcs(reinterpret_cast<uint4*>(q + r * ld + c), codes[u]);
+          if ((lane & 7) == 0) s[(c >> 7) * pitch + r] = scale[u];
+        }
+      }
+    }
+  }
+}
+
 bool ok16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Row tiles are the grid's y: 65535 of them per launch, the rest in further launches of plain rows.
+// Row tiles are the grid's y.
 template <int FORM, bool GATHER>
 int launch_form(const QuantArgs& p, int batch, int kind, cudaStream_t stream) {
   const int64_t ty = fp8_blocks(p.rows), tx = fp8_blocks(p.cols);
@@ -212,10 +274,23 @@ int launch_fp8_quantize(const Fp8Source& src, int64_t rows, int32_t cols, uint8_
   p.ldt = fp8_ld(rows);
   p.pitch = fp8_pitch(rows);
   p.pitch_t = fp8_pitch(cols);
+  if (src.gather && !qt) {
+    const int64_t want = (src.tokens * ((cols + 1023) / 1024) + kQThreads / 32 - 1) / (kQThreads / 32);
+    const int64_t most = static_cast<int64_t>(sm_count()) * 16;
+    if (most <= 0) return static_cast<int>(cudaErrorInvalidDevice);
+    trace_begin(stream, kind);
+    const cudaError_t e = launch_pdl(fp8_dispatch_kernel, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kQThreads),
+                                     0, stream, src.x, src.inv, src.tokens, src.K, static_cast<int>(cols), p.ld, p.pitch, q, s);
+    trace_end(stream);
+    return static_cast<int>(e);
+  }
   auto run = [&](auto gather) {
     constexpr bool G = decltype(gather)::value;
     if (q && qt) return launch_form<Q_ROWS | Q_COLS, G>(p, 1, kind, stream);
-    return q ? launch_form<Q_ROWS, G>(p, 1, kind, stream) : launch_form<Q_COLS, G>(p, 1, kind, stream);
+    if constexpr (!G) {
+      if (q) return launch_form<Q_ROWS, G>(p, 1, kind, stream);
+    }
+    return launch_form<Q_COLS, G>(p, 1, kind, stream);
   };
   return src.gather ? run(std::true_type{}) : run(std::false_type{});
 }
@@ -244,7 +319,7 @@ mok_status mok_fp8_quantize(const void* x, int64_t rows, int32_t cols, uint8_t* 
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
   const mok_status rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
-  const Fp8Source src{static_cast<const uint16_t*>(x), nullptr, nullptr, 0};
+  const Fp8Source src{static_cast<const uint16_t*>(x), nullptr, nullptr, nullptr, rows, 1, 0};
   return launch_fp8_quantize(src, rows, cols, q, s, qt, st, K_FP8_QUANTIZE, static_cast<cudaStream_t>(stream)) ? MOK_ERR_CUDA
                                                                                                              : MOK_OK;
 }
@@ -260,7 +335,7 @@ mok_status mok_fp8_quantize_routed(const mok_schedule* sched, int32_t gather, co
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
   rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
-  const Fp8Source src{static_cast<const uint16_t*>(x), sched->row_token, sched->meta, gather};
+  const Fp8Source src{static_cast<const uint16_t*>(x), sched->row_token, sched->meta, sched->inv, z.T, z.K, gather};
   return launch_fp8_quantize(src, z.rpad_max, cols, q, s, qt, st, gather ? K_FP8_DISPATCH : K_FP8_QUANTIZE,
                              static_cast<cudaStream_t>(stream))
              ? MOK_ERR_CUDA

@@ -1,13 +1,15 @@
 // mok_fp8_tile.cu -- 8-bit products with a scale per 128 values, one 128 x BN tile per CTA.
 //
-// With P the operand whose rows are the accumulator's 128 lanes and Q the one whose rows are its BN columns, a CTA
-// computes D[i, j] = sum over K blocks of sp[i] sq[j] (P[i, :] . Q[j, :]).  A K block is 128 bytes of a row, one
-// swizzle atom: four tcgen05.mma (M = 128, K = 32) into one of two TMEM accumulators, which four warps then drain,
-// scale and add into their registers while the next block's MMAs run into the other one.
+// With P = b, whose rows are the accumulator's 128 lanes, and Q = a, whose rows are its BN columns, a CTA computes out[j, i] =
+// sum over K blocks of sq[j] sp[i] (Q[j, :] . P[i, :]): few rows of a take few columns, and the weights' bytes bound it.  A
+// K block is 128 bytes of a row, one
+// swizzle atom: four tcgen05.mma (M = 128, K = 32) into a TMEM accumulator of its own, one of four or eight in turn, which four
+// warps then drain, scale and add into their registers.  Row scales come to shared memory in lots of 16 K blocks, the next
+// lot on its way while one is used (fetched block by block, their latency set the pace: 1.6 us per block, one row at N =
+// 2048, K = 7168 14 us).
 //
-// SWAP: P holds the weights and Q the tokens, whose number picks BN: few tokens take few columns, and the weights'
-// bytes bound it.  Their K range is then split over a cluster, whose CTAs add up their partials through shared memory
-// in rank order.
+// With few tiles their K range is split over a cluster, whose CTAs add up their partials through shared memory in rank
+// order.
 #include "mok_ffn.cuh"  // warp_wait, wait_landed, elect_one
 #include "mok_fp8.cuh"
 #include "mok_fp8_gemm.cuh"
@@ -17,13 +19,25 @@ namespace {
 
 constexpr int kThreads = 192;
 constexpr int kMaxStages = 12;
+constexpr uint32_t kHalfSmem = 114688;  // two CTAs
 constexpr uint32_t kMaxSmem = 227328;  // dynamic: 5 KB of 227 KB are left for what is static
+
+constexpr int kLot = 16;  // K blocks whose scales are fetched together
 
 struct TileArgs {
   Fp8Problem g;
-  int32_t split;   // CTAs of a cluster that share a tile's K range (SWAP)
+  int32_t split;   // CTAs of a cluster that share a tile's K range 
   int32_t stages;
-  uint32_t push_off;
+  uint32_t scale_off, push_off;
+};
+
+template <int BN, bool PVEC>
+struct Cfg {
+  static constexpr uint32_t kStage = 16384 + BN * 128;
+  static constexpr int kAccs = BN <= 32 ? 8 : 4;
+  static constexpr int kPerSm = BN <= 32 ? 2 : 1;  // CTAs of an SM
+  static constexpr uint32_t kRows = PVEC ? 128 : 0;  // of P with a scale each
+  static constexpr uint32_t kLotBytes = kLot * (kRows + BN) * 4;
 };
 
 // 32 or 16 columns of this lane's accumulator row.
@@ -43,20 +57,17 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[W]) {
 // A tile: where its operands' rows start, the output's rows and columns it holds, its K blocks.
 struct Tile {
   int32_t p0, q0;        // rows of P and Q in their tensor maps
-  int32_t i0, j0;        // output position (SWAP: i is the output's column)
+  int32_t i0, j0;        // output column and row
   int32_t i_end, j_end;
-  int32_t kb0, count;    // K blocks
-  int64_t out;           // element offset of the matrix written
+  int32_t count;         // K blocks
   int32_t batch;         // of BLOCKS-scaled operands
 };
 
-__device__ __forceinline__ bool fp8_tile(const Fp8Problem& g, int u, bool swap, int bn, Tile& t) {
-  t.kb0 = 0;
+__device__ __forceinline__ bool fp8_tile(const Fp8Problem& g, int u, int bn, Tile& t) {
   t.count = g.k_blocks;
-  t.out = 0;
   t.batch = 0;
   const int pt = u % g.p_tiles;
-  int rest = u / g.p_tiles;
+  const int rest = u / g.p_tiles;
   if (g.mode == FP8_DENSE) {
     t.p0 = t.i0 = pt * 128;
     t.q0 = t.j0 = rest * bn;
@@ -64,81 +75,68 @@ __device__ __forceinline__ bool fp8_tile(const Fp8Problem& g, int u, bool swap, 
     t.j_end = g.q_rows;
     return true;
   }
-  if (g.mode == FP8_WGRAD) {
-    const int qt = rest % g.q_tiles;
-    t.batch = rest / g.q_tiles;
-    t.kb0 = __ldg(g.poff + t.batch) / 128;
-    t.count = __ldg(g.poff + t.batch + 1) / 128 - t.kb0;
-    t.p0 = t.i0 = pt * 128;
-    t.q0 = t.j0 = qt * bn;
-    t.i_end = g.p_rows;
-    t.j_end = g.q_rows;
-    t.out = static_cast<int64_t>(t.batch) * g.p_rows * g.q_rows;
-    return true;
-  }
   // one 128-row block of an expert's rows, against a tile of its weights
-  int wt = pt, blk = rest;
-  if (!swap) {
-    wt = u % g.q_tiles;
-    blk = u / g.q_tiles;
-  }
-  if (blk >= __ldg(g.meta + 2)) return false;
-  const int4 b = __ldg(reinterpret_cast<const int4*>(g.mblocks) + blk);  // {expert, first row, valid rows, tile}
+  if (rest >= __ldg(g.meta + 2)) return false;
+  const int4 b = __ldg(reinterpret_cast<const int4*>(g.mblocks) + rest);  // {expert, first row, valid rows, tile}
   t.batch = b.x;
-  if (swap) {
-    t.i0 = wt * 128;
-    t.p0 = b.x * g.p_rows + t.i0;
-    t.i_end = g.p_rows;
-    t.q0 = t.j0 = b.y;
-    t.j_end = b.y + b.z;
-  } else {
-    t.p0 = t.i0 = b.y;
-    t.i_end = b.y + b.z;
-    t.j0 = wt * bn;
-    t.q0 = b.x * g.q_rows + t.j0;
-    t.j_end = g.q_rows;
-  }
+  t.i0 = pt * 128;
+  t.p0 = b.x * g.p_rows + t.i0;
+  t.i_end = g.p_rows;
+  t.q0 = t.j0 = b.y;
+  t.j_end = b.y + b.z;
   return true;
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// This thread's row r of the accumulator to the CTAs of a cluster of S that own its columns.
+template <int BN, int S>
+__device__ __forceinline__ void push_partials(uint32_t push, const float (&acc)[BN], int rank, int r) {
+  constexpr int kPer = BN / S;
+#pragma unroll
+  for (int own = 0; own < S; ++own) {
+    const uint32_t local = push + static_cast<uint32_t>(rank * kPer * 128 + r) * 4u;
+    const uint32_t to = S > 1 ? mapa_shared(local, own) : local;
+#pragma unroll
+    for (int jj = 0; jj < kPer; ++jj) {
+      if constexpr (S > 1)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + jj * 512), "f"(acc[own * kPer + jj]) : "memory");
+      else
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + jj * 512), "f"(acc[jj]) : "memory");
+    }
+  }
 }
 
-template <int BN, bool COLVEC, bool SWAP>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int BN, bool PVEC>
+__global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
     fp8_tile_kernel(const __grid_constant__ CUtensorMap tP, const __grid_constant__ CUtensorMap tQ, const TileArgs a) {
-  constexpr uint32_t kQBytes = BN * 128, kStage = 16384 + (kQBytes < 1024 ? 1024 : kQBytes);
-  constexpr uint32_t kCols = BN <= 16 ? 32 : 2 * BN;  // two accumulators
+  using C = Cfg<BN, PVEC>;
+  constexpr uint32_t kQBytes = BN * 128, kStage = C::kStage, kCols = C::kAccs * BN;
+  constexpr int kAccs = C::kAccs;
   constexpr int W = BN < 32 ? 16 : 32;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 5];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 17];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
-  __shared__ __align__(16) float colbuf[COLVEC ? 4 : 1][2][COLVEC ? BN : 4];  // per warp, of the current and next block
   const Fp8Problem& g = a.g;
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_u32(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
   auto tfull = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
-  auto tempty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + 2 + b); };
-  const uint32_t done = bar0 + 8u * (2 * kMaxStages + 4);
+  auto tempty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + kAccs + b); };
+  const uint32_t done = bar0 + 8u * (2 * kMaxStages + 2 * kAccs);
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = SWAP ? a.split : 1;
-  const int rank = SWAP ? static_cast<int>(blockIdx.x) % S : 0, unit = static_cast<int>(blockIdx.x) / S;
+  const int S = a.split;
+  const int rank = static_cast<int>(blockIdx.x) % S, unit = static_cast<int>(blockIdx.x) / S;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kAccs; ++b) {
       mbar_init(tfull(b), 1);
       mbar_init(tempty(b), 4);
     }
@@ -154,16 +152,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  if (SWAP && S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has started
+  if (S > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // this CTA has started
   if (g.mode != FP8_DENSE) pdl_wait();  // the schedule's tables
   Tile t;
-  const bool have = fp8_tile(g, unit, SWAP, BN, t);
-  const int subs = !have ? 0 : SWAP ? (min(t.j_end - t.j0, g.mode == FP8_DENSE ? BN : 128) + BN - 1) / BN : 1;
+  const bool have = fp8_tile(g, unit, BN, t);
+  const int subs = !have ? 0 : (min(t.j_end - t.j0, g.mode == FP8_DENSE ? BN : 128) + BN - 1) / BN;
   // this CTA's share of the K blocks
-  const int kb0 = t.kb0 + static_cast<int>(static_cast<int64_t>(t.count) * rank / S);
-  const int count = t.kb0 + static_cast<int>(static_cast<int64_t>(t.count) * (rank + 1) / S) - kb0;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(t.count) * rank / S);
+  const int count = static_cast<int>(static_cast<int64_t>(t.count) * (rank + 1) / S) - kb0;
   const int total = subs * count;  // K blocks that pass through the stages
-  if (SWAP && S > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (S > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   bool ok = true;
   int ahead = 0;  // (warp 0) K blocks of P that were loaded early
   if (warp == 0 && g.early_p) {  // weights: nothing that still runs writes them
@@ -205,8 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == 1) {
       for (int kb = 0; kb < count && ok; ++kb, ++n) {
-        const int b = n & 1;
-        ok = (n < 2 || warp_wait(tempty(b), static_cast<uint32_t>(n / 2 - 1) & 1u, abort_flag, g.status)) &&
+        const int b = n % kAccs;
+        ok = (n < kAccs || warp_wait(tempty(b), static_cast<uint32_t>(n / kAccs - 1) & 1u, abort_flag, g.status)) &&
              warp_wait(full(st), ph, abort_flag, g.status);
         if (!ok) break;
         tc_fence_after();
@@ -227,39 +225,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
 #pragma unroll
       for (int j = 0; j < BN; ++j) acc[j] = 0.0f;
-      const int i = min(t.i0 + r, t.i_end - 1), j0 = t.j0 + sub * BN;
-      const float* ps = g.p_vec ? g.sp + i : g.sp + t.batch * g.p_batch + static_cast<int64_t>(i / 128) * g.k_blocks;
-      const float* qs = COLVEC ? g.sq : g.sq + t.batch * g.q_batch + static_cast<int64_t>(j0 / 128) * g.k_blocks;
-      const int64_t p_step = g.p_vec ? g.p_pitch : 1;
-      float p_next = count > 0 ? __ldg(ps + kb0 * p_step) : 0.0f;
-      // column scales: each lane its share of the warp's BN, four at a time (rows of scales are padded to four)
-      float4 q_next = make_float4(0, 0, 0, 0);
-      const int cq = lane * 4;
-      auto fetch_q = [&](int kb) {
-        if constexpr (COLVEC) {
-          if (cq < BN && j0 + cq < g.q_pitch)
-            q_next = __ldg(reinterpret_cast<const float4*>(qs + static_cast<int64_t>(kb) * g.q_pitch + j0 + cq));
-        } else {
-          q_next.x = __ldg(qs + kb);
+      const int j0 = t.j0 + sub * BN;
+      // 16-byte pieces of a lot's row scales (their rows are padded to four); what lies past the matrix is not used
+      const int tid = static_cast<int>(threadIdx.x) - 64;
+      auto fetch = [&](int lot) {
+        const uint32_t to = base + a.scale_off + (lot & 1) * C::kLotBytes;
+        const int k0 = kb0 + lot * kLot, blocks = min(kLot, count - lot * kLot);
+        if constexpr (PVEC) {
+          for (int x = tid; x < blocks * 32; x += 128) {
+            const int k = x >> 5, i = (x & 31) * 4;
+            if (t.i0 + i < g.p_pitch)
+              cp_async16(to + (k * 128 + i) * 4, g.sp + static_cast<int64_t>(k0 + k) * g.p_pitch + t.i0 + i);
+          }
         }
+        for (int x = tid; x < blocks * (BN / 4); x += 128) {
+          const int k = x / (BN / 4), j = (x % (BN / 4)) * 4;
+          if (j0 + j < g.q_pitch)
+            cp_async16(to + kLot * C::kRows * 4 + (k * BN + j) * 4, g.sq + static_cast<int64_t>(k0 + k) * g.q_pitch + j0 + j);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      if (count > 0) fetch_q(kb0);
-      for (int kb = 0; kb < count && ok; ++kb, ++n) {
-        const int b = n & 1;
-        float s = p_next;
-        const float* cs = colbuf[COLVEC ? warp - 2 : 0][COLVEC ? b : 0];
-        if constexpr (COLVEC) {
-          if (cq < BN) *reinterpret_cast<float4*>(&colbuf[warp - 2][b][cq]) = q_next;
-          __syncwarp();
-        } else {
-          s *= q_next.x;
+      // scales of 128 x 128 values: a lot's, a lane each
+      const float* ps = g.sp + t.batch * g.p_batch + static_cast<int64_t>(t.i0 / 128) * g.k_blocks + kb0;
+      auto block_scales = [&](int lot) {
+        const int k = lot * kLot + (lane & (kLot - 1));
+        return k < count ? __ldg(ps + k) : 0.0f;
+      };
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // the lots of the sub-tile before have been used
+      if (count > 0) fetch(0);
+      float s_now = 0.0f, s_next = PVEC ? 0.0f : block_scales(0);
+      for (int kb = 0; kb < count; ++kb, ++n) {  // (also after a failed wait: the barriers count every warp)
+        const int b = n % kAccs, lot = kb / kLot, in = kb % kLot;
+        if (in == 0) {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          asm volatile("bar.sync 1, 128;" ::: "memory");  // everybody's pieces are there, and the other lot has been used
+          if (kb + kLot < count) fetch(lot + 1);
+          s_now = s_next;
+          if (!PVEC) s_next = block_scales(lot + 1);
         }
-        if (kb + 1 < count) {
-          p_next = __ldg(ps + (kb0 + kb + 1) * p_step);
-          fetch_q(kb0 + kb + 1);
-        }
-        ok = warp_wait(tfull(b), static_cast<uint32_t>(n / 2) & 1u, abort_flag, g.status);
-        if (!ok) break;
+        const float* lots = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + a.scale_off + (lot & 1) * C::kLotBytes);
+        const float* cs = lots + kLot * C::kRows + in * BN;
+        const float s = PVEC ? lots[in * 128 + r] : __shfl_sync(0xffffffffu, s_now, in);
+        ok = ok && warp_wait(tfull(b), static_cast<uint32_t>(n / kAccs) & 1u, abort_flag, g.status);
+        if (!ok) continue;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < BN; c += W) {
@@ -273,12 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int j = 0; j < W; j += 4) {
-            float f0 = s, f1 = s, f2 = s, f3 = s;
-            if constexpr (COLVEC) {
-              const float4 x = *reinterpret_cast<const float4*>(cs + c + j);
-              mul_f32x2(f0, f1, s, s, x.x, x.y);
-              mul_f32x2(f2, f3, s, s, x.z, x.w);
-            }
+            const float4 x = *reinterpret_cast<const float4*>(cs + c + j);
+            float f0, f1, f2, f3;
+            mul_f32x2(f0, f1, s, s, x.x, x.y);
+            mul_f32x2(f2, f3, s, s, x.z, x.w);
             fma_f32x2(acc[c + j], acc[c + j + 1], __uint_as_float(v[j]), __uint_as_float(v[j + 1]), f0, f1, acc[c + j],
                       acc[c + j + 1]);
             fma_f32x2(acc[c + j + 2], acc[c + j + 3], __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]), f2, f3,
@@ -288,61 +294,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     const int j0 = t.j0 + sub * BN;
-    if constexpr (SWAP) {
-      uint16_t* out = static_cast<uint16_t*>(g.out) + t.i0 + r;
-      const bool mine = warp >= 2 && t.i0 + r < t.i_end;
-      if (S == 1) {
-        if (mine && ok) {
-#pragma unroll
-          for (int j = 0; j < BN; ++j)
-            if (j0 + j < t.j_end) {
-              if (g.out_f32) static_cast<float*>(g.out)[static_cast<int64_t>(j0 + j) * g.ldo + t.i0 + r] = acc[j];
-              else out[static_cast<int64_t>(j0 + j) * g.ldo] = static_cast<uint16_t>(pack_bf16x2(acc[j], 0.0f));
-            }
+    // Column j belongs to CTA j / (BN / S) of the cluster: each sends it its partials, [source][column][row], and the owner
+    // adds them in rank order, 8 rows of a column per thread: 16 bytes of a row of the output.
+    const uint32_t push = base + a.push_off;
+    if (warp >= 2) {
+      if (S == 1) push_partials<BN, 1>(push, acc, rank, r);
+      else if (S == 2) push_partials<BN, 2>(push, acc, rank, r);
+      else if (S == 4) push_partials<BN, 4>(push, acc, rank, r);
+      else push_partials<BN, 8>(push, acc, rank, r);
+    }
+    __syncwarp();
+    if (S > 1) cluster_sync();
+    else if (warp >= 2) asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (warp >= 2 && *abort_flag == 0) {
+      const int per = BN / S;
+      const float* parts = reinterpret_cast<const float*>(smem_raw + (push - smem_u32(smem_raw)));
+      for (int x = static_cast<int>(threadIdx.x) - 64; x < per * 16; x += 128) {
+        const int jj = x >> 4, i = (x & 15) * 8, j = j0 + rank * per + jj;
+        if (t.i0 + i >= t.i_end || j >= t.j_end) continue;
+        float4 lo = make_float4(0, 0, 0, 0), hi = lo;
+        for (int c = 0; c < S; ++c) {
+          const float4* p = reinterpret_cast<const float4*>(parts + (c * per + jj) * 128 + i);
+          const float4 y = p[0], z = p[1];
+          lo.x += y.x, lo.y += y.y, lo.z += y.z, lo.w += y.w, hi.x += z.x, hi.y += z.y, hi.z += z.z, hi.w += z.w;
         }
-      } else {
-        // column j belongs to CTA j / per of the cluster: each sends it its partial, the owner adds them in rank order
-        const int per = BN / S;
-        const uint32_t push = base + a.push_off;
-        if (warp >= 2) {
-#pragma unroll
-          for (int j = 0; j < BN; ++j) {
-            const int own = j / per, jj = j - own * per;
-            st_cluster_f32(mapa_shared(push + static_cast<uint32_t>((rank * per + jj) * 128 + r) * 4u, own), acc[j]);
-          }
+        const int64_t at = static_cast<int64_t>(j) * g.ldo + t.i0 + i;
+        if (g.out_f32) {
+          float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.out) + at);
+          o[0] = lo;
+          o[1] = hi;
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.out) + at) =
+              make_uint4(pack_bf16x2(lo.x, lo.y), pack_bf16x2(lo.z, lo.w), pack_bf16x2(hi.x, hi.y), pack_bf16x2(hi.z, hi.w));
         }
-        __syncwarp();
-        cluster_sync();
-        if (mine && *abort_flag == 0)
-          for (int jj = 0; jj < per; ++jj) {
-            const int j = j0 + rank * per + jj;
-            float v = 0.0f;
-            for (int c = 0; c < S; ++c) v += ld_shared_f32(push + static_cast<uint32_t>((c * per + jj) * 128 + r) * 4u);
-            if (j < t.j_end) {
-              if (g.out_f32) static_cast<float*>(g.out)[static_cast<int64_t>(j) * g.ldo + t.i0 + r] = v;
-              else out[static_cast<int64_t>(j) * g.ldo] = static_cast<uint16_t>(pack_bf16x2(v, 0.0f));
-            }
-          }
-        __syncwarp();
-        if (sub + 1 < subs) cluster_sync();  // the partials have been read
-      }
-    } else if (warp >= 2 && ok && t.i0 + r < t.i_end) {
-      const int64_t at = t.out + static_cast<int64_t>(t.i0 + r) * g.ldo + j0;
-      if (g.out_f32) {
-        float* o = static_cast<float*>(g.out) + at;
-#pragma unroll
-        for (int j = 0; j < BN; j += 4)
-          if (j0 + j < t.j_end) *reinterpret_cast<float4*>(o + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-      } else {
-        uint16_t* o = static_cast<uint16_t*>(g.out) + at;
-#pragma unroll
-        for (int j = 0; j < BN; j += 8)
-          if (j0 + j < t.j_end)
-            *reinterpret_cast<uint4*>(o + j) =
-                make_uint4(pack_bf16x2(acc[j], acc[j + 1]), pack_bf16x2(acc[j + 2], acc[j + 3]),
-                           pack_bf16x2(acc[j + 4], acc[j + 5]), pack_bf16x2(acc[j + 6], acc[j + 7]));
       }
     }
+    __syncwarp();
+    if (S > 1 && sub + 1 < subs) cluster_sync();  // the partials have been read (without a split: bar.sync above)
   }
   __syncwarp();
   if (warp == 0 && *abort_flag && lane == 0)  // let the copies in flight land: the last one of each stage
@@ -362,28 +350,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BN, bool COLVEC, bool SWAP>
+template <int BN, bool PVEC>
 int launch_tile(const CUtensorMap& tP, const CUtensorMap& tQ, const Fp8Problem& g, int64_t units, int split, int kind,
                 cudaStream_t stream) {
   static DeviceOnce once;
   const int se = once.run([](int* d) { return static_cast<int>(cudaGetDevice(d)); },
                           [] {
-                            return static_cast<int>(cudaFuncSetAttribute(fp8_tile_kernel<BN, COLVEC, SWAP>,
+                            return static_cast<int>(cudaFuncSetAttribute(fp8_tile_kernel<BN, PVEC>,
                                                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                                          static_cast<int>(kMaxSmem)));
                           },
                           static_cast<int>(cudaErrorInvalidDevice));
   if (se) return se;
   if (units * split >= (int64_t{1} << 31)) return static_cast<int>(cudaErrorInvalidValue);
-  constexpr uint32_t kStage = 16384 + (BN * 128 < 1024 ? 1024 : BN * 128);
+  using C = Cfg<BN, PVEC>;
+  constexpr uint32_t kStage = C::kStage;
   TileArgs a{};
   a.g = g;
   a.split = split;
-  const uint32_t push = split > 1 ? BN * 512u : 0u;
-  const uint32_t fixed = 1024u + push;  // alignment; partials
-  a.stages = static_cast<int32_t>((kMaxSmem - fixed) / kStage);
+  constexpr uint32_t push = BN * 512u;
+  constexpr uint32_t fixed = 1024u + 2 * C::kLotBytes + push;  // alignment; scales; partials
+  a.stages = static_cast<int32_t>(((C::kPerSm == 2 ? kHalfSmem : kMaxSmem) - fixed) / kStage);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
-  a.push_off = static_cast<uint32_t>(a.stages) * kStage;
+  a.scale_off = static_cast<uint32_t>(a.stages) * kStage;
+  a.push_off = a.scale_off + 2 * C::kLotBytes;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * split));
   cfg.blockDim = dim3(kThreads);
@@ -399,7 +389,7 @@ int launch_tile(const CUtensorMap& tP, const CUtensorMap& tQ, const Fp8Problem& 
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 2 : 1;
   trace_begin(stream, kind);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, COLVEC, SWAP>, tP, tQ, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, PVEC>, tP, tQ, a);
   trace_end(stream);
   return static_cast<int>(e);
 }
@@ -410,55 +400,40 @@ int launch_fp8_tile(const Fp8Operand& a, const Fp8Operand& b, Fp8Problem g, int6
                     cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return static_cast<int>(cudaErrorInvalidDevice);
-  const int64_t N = b.rows;
-  auto maps = [&](const Fp8Operand& p, const Fp8Operand& q, int bn, CUtensorMap* tp, CUtensorMap* tq) {
-    return make_tmap_fp8(tp, p.q, static_cast<uint64_t>(p.cols), static_cast<uint64_t>(p.rows) * p.batch,
-                         static_cast<uint64_t>(p.ld), 128) &&
-           make_tmap_fp8(tq, q.q, static_cast<uint64_t>(q.cols), static_cast<uint64_t>(q.rows) * q.batch,
-                         static_cast<uint64_t>(q.ld), static_cast<uint32_t>(bn));
-  };
-  auto sides = [&](const Fp8Operand& p, const Fp8Operand& q) {
-    g.sp = p.s;
-    g.p_vec = p.row_scales;
-    g.p_pitch = fp8_pitch(p.rows);
-    g.p_batch = fp8_blocks(p.rows) * g.k_blocks;
-    g.p_rows = static_cast<int32_t>(p.rows);
-    g.sq = q.s;
-    g.q_pitch = fp8_pitch(q.rows);
-    g.q_batch = fp8_blocks(q.rows) * g.k_blocks;
-    g.q_rows = static_cast<int32_t>(q.rows);
-  };
-  CUtensorMap tp, tq;
-  const bool swap = !b.row_scales && rows <= 128 * (g.mode == FP8_GROUPED ? row_blocks : 1);
-  if (swap) {
-    sides(b, a);
-    g.p_tiles = static_cast<int32_t>(fp8_blocks(N));
-    const int64_t per = g.mode == FP8_GROUPED ? (rows + row_blocks - 1) / (row_blocks > 0 ? row_blocks : 1) : rows;
-    const int bn = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
-    g.q_tiles = static_cast<int32_t>(g.mode == FP8_GROUPED ? row_blocks : (rows + bn - 1) / bn);
-    const int64_t units = static_cast<int64_t>(g.p_tiles) * g.q_tiles;
-    int64_t split = sms / (units > 0 ? units : 1);
-    if (split > g.k_blocks / 2) split = g.k_blocks / 2;
-    split = split >= 8 ? 8 : split >= 4 ? 4 : split >= 2 ? 2 : 1;
-    if (units == 0) return 0;
-    if (!maps(b, a, bn, &tp, &tq)) return static_cast<int>(cudaErrorInvalidValue);
-    const int s = static_cast<int>(split);
-    switch (bn) {
-      case 16: return launch_tile<16, true, true>(tp, tq, g, units, s, kind, stream);
-      case 32: return launch_tile<32, true, true>(tp, tq, g, units, s, kind, stream);
-      case 64: return launch_tile<64, true, true>(tp, tq, g, units, s, kind, stream);
-      default: return launch_tile<128, true, true>(tp, tq, g, units, s, kind, stream);
-    }
-  }
-  sides(a, b);
-  g.early_p = 0;
-  g.q_tiles = static_cast<int32_t>(fp8_blocks(N));
-  g.p_tiles = static_cast<int32_t>(g.mode == FP8_GROUPED ? row_blocks : fp8_blocks(a.rows));
-  const int64_t units = static_cast<int64_t>(g.p_tiles) * g.q_tiles * (g.mode == FP8_WGRAD ? g.experts : 1);
+  const bool grouped = g.mode == FP8_GROUPED;
+  g.sp = b.s;
+  g.p_pitch = fp8_pitch(b.rows);
+  g.p_batch = fp8_blocks(b.rows) * g.k_blocks;
+  g.p_rows = static_cast<int32_t>(b.rows);
+  g.sq = a.s;
+  g.q_pitch = fp8_pitch(a.rows);
+  g.q_rows = static_cast<int32_t>(a.rows);
+  const int64_t per = grouped ? (rows + row_blocks - 1) / (row_blocks > 0 ? row_blocks : 1) : rows;  // rows of a block
+  const int bn = per <= 16 ? 16 : per <= 32 ? 32 : per <= 64 ? 64 : 128;
+  g.p_tiles = static_cast<int32_t>(fp8_blocks(b.rows));
+  g.q_tiles = static_cast<int32_t>(grouped ? row_blocks : (rows + bn - 1) / bn);
+  const int64_t units = static_cast<int64_t>(g.p_tiles) * g.q_tiles;
   if (units == 0) return 0;
-  if (!maps(a, b, 128, &tp, &tq)) return static_cast<int>(cudaErrorInvalidValue);
-  return b.row_scales ? launch_tile<128, true, false>(tp, tq, g, units, 1, kind, stream)
-                      : launch_tile<128, false, false>(tp, tq, g, units, 1, kind, stream);
+  int64_t split = (bn <= 32 ? 2 : 1) * sms / units;
+  if (split > g.k_blocks / 2) split = g.k_blocks / 2;
+  split = split >= 8 && bn <= 32 ? 8 : split >= 4 ? 4 : split >= 2 ? 2 : 1;
+  CUtensorMap tp, tq;
+  if (!make_tmap_fp8(&tp, b.q, static_cast<uint64_t>(b.cols), static_cast<uint64_t>(b.rows) * b.batch,
+                     static_cast<uint64_t>(b.ld), 128) ||
+      !make_tmap_fp8(&tq, a.q, static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.rows), static_cast<uint64_t>(a.ld),
+                     static_cast<uint32_t>(bn)))
+    return static_cast<int>(cudaErrorInvalidValue);
+  const int s = static_cast<int>(split);
+  auto width = [&](auto vec) {
+    constexpr bool V = decltype(vec)::value;
+    switch (bn) {
+      case 16: return launch_tile<16, V>(tp, tq, g, units, s, kind, stream);
+      case 32: return launch_tile<32, V>(tp, tq, g, units, s, kind, stream);
+      case 64: return launch_tile<64, V>(tp, tq, g, units, s, kind, stream);
+      default: return launch_tile<128, V>(tp, tq, g, units, s, kind, stream);
+    }
+  };
+  return b.row_scales ? width(std::true_type{}) : width(std::false_type{});
 }
 
 }  // namespace mok
