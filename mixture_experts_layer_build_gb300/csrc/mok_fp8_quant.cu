@@ -15,7 +15,6 @@ namespace mok {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kQStride = 128 + 16;  // bytes between the transposed rows of the staged tile (16-byte vectors)
 
 enum QuantForm : int { Q_ROWS = 1, Q_COLS = 2, Q_BLOCKS = 4 };
 
@@ -39,7 +38,8 @@ __global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs
   pdl_wait();
   pdl_trigger();  // a product that follows sets itself up, and loads weights, meanwhile
   __shared__ uint32_t wmax[8][64];                                // per warp, packed column maxima
-  __shared__ __align__(16) uint8_t tile[FORM == Q_ROWS ? 16 : 128 * kQStride];
+  __shared__ __align__(16) float col_up[FORM & Q_COLS ? 128 : 4];
+  __shared__ __align__(16) uint8_t tile[FORM == Q_ROWS ? 16 : 128 * 128];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, cg = t & 15, rg = t >> 4;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * 128;
   const int c0 = static_cast<int>(blockIdx.x) * 128, c = c0 + cg * 8;
@@ -61,21 +61,27 @@ __global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs
     live |= in ? 1u << i : 0u;
     v[i] = in && c < p.cols ? *reinterpret_cast<const uint4*>(x + from * p.cols + c) : make_uint4(0, 0, 0, 0);
   }
-  uint32_t rmax[8];  // of the row's 128 columns, in all 16 lanes
+  // The rows' maxima over the 16 lanes that hold a row, halving the rows that a lane keeps at each exchange: lanes 2 i and
+  // 2 i + 1 of the 16 end with row i's.
+  uint32_t rmax = 0;
+  if constexpr (FORM != Q_COLS) {
+    uint32_t m[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t m = absmax2(absmax2(v[i].x, v[i].y), absmax2(v[i].z, v[i].w));
+    for (int i = 0; i < 8; ++i) m[i] = absmax2(absmax2(v[i].x, v[i].y), absmax2(v[i].z, v[i].w));
 #pragma unroll
-    for (int d = 8; d >= 1; d >>= 1) m = absmax2(m, __shfl_xor_sync(0xffffffffu, m, d));
-    rmax[i] = absmax_word(m);
+    for (int d = 8, h = 4; d >= 2; d >>= 1, h >>= 1) {
+      const bool hi = cg & d;
+#pragma unroll
+      for (int i = 0; i < h; ++i) m[i] = absmax2(hi ? m[i + h] : m[i], __shfl_xor_sync(0xffffffffu, hi ? m[i] : m[i + h], d));
+    }
+    rmax = absmax_word(absmax2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1)));
   }
   float up = 0.0f;
   bool bad = false;
   if constexpr (FORM == Q_BLOCKS) {
-    uint32_t m = rmax[0];
+    uint32_t m = rmax;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = max(m, rmax[i]);  // (magnitudes' bits order as they do, NaN above all)
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    for (int d = 16; d >= 2; d >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));  // (magnitudes' bits order as they do)
     if (lane == 0) wmax[warp][0] = m;
     __syncthreads();
 #pragma unroll
@@ -94,17 +100,22 @@ __global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs
   };
   if ((FORM & Q_ROWS) || (FORM == Q_BLOCKS && p.q)) {
     uint8_t* q = p.q + (FORM == Q_BLOCKS ? blockIdx.z * p.q_batch : 0);
+    float row_up = 0.0f;  // of row cg / 2, negative where the block is bad
+    if constexpr (FORM != Q_BLOCKS) {
+      const float sc = fp8_scale(rmax, row_up);
+      if (rmax >= 0x7F80u) row_up = -1.0f;
+      if (!(cg & 1) && (live >> (cg >> 1) & 1u)) p.s[static_cast<int64_t>(blockIdx.x) * p.pitch + r0 + rg * 8 + (cg >> 1)] = sc;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t r = r0 + rg * 8 + i;
-      if (FORM == Q_BLOCKS ? r >= p.rows : !(live >> i & 1u)) continue;
       float f = up;
       bool nan = bad;
       if constexpr (FORM != Q_BLOCKS) {
-        const float sc = fp8_scale(rmax[i], f);
-        nan = rmax[i] >= 0x7F80u;
-        if (cg == 0) p.s[static_cast<int64_t>(blockIdx.x) * p.pitch + r] = sc;
+        f = __shfl_sync(0xffffffffu, row_up, (lane & 16) | 2 * i);
+        nan = f < 0.0f;
       }
+      if (FORM == Q_BLOCKS ? r >= p.rows : !(live >> i & 1u)) continue;
       if (c < p.cols) *reinterpret_cast<uint2*>(q + r * p.ld + c) = row_codes(i, f, nan);
       else if (c < p.ld) *reinterpret_cast<uint2*>(q + r * p.ld + c) = make_uint2(0, 0);  // up to the pitch
     }
@@ -127,21 +138,24 @@ __global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs
         if (lane < 16) wmax[warp][cg * 4 + j] = m[j];
       }
       __syncthreads();
+      if (t < 128) {  // a column each: its maximum over the warps, scale and multiplier (negative: a bad block)
+        const uint16_t* halves = reinterpret_cast<const uint16_t*>(wmax);
+        uint32_t a = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t a = wmax[0][cg * 4 + j];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) a = absmax2(a, wmax[w][cg * 4 + j]);
-        a &= 0x7FFF7FFFu;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t am = h ? a >> 16 : a & 0xFFFFu;
-          const float sc = fp8_scale(am, f[2 * j + h]);
-          if (am >= 0x7F80u) nan |= 1u << (2 * j + h);
-          const int cc = c + 2 * j + h;
-          if (rg == 0 && cc < p.cols) p.st[static_cast<int64_t>(blockIdx.y) * p.pitch_t + cc] = sc;
-        }
+        for (int w = 0; w < 8; ++w) a = max(a, halves[w * 128 + t] & 0x7FFFu);
+        float m;
+        const float sc = fp8_scale(a, m);
+        col_up[t] = a >= 0x7F80u ? -1.0f : m;
+        if (c0 + t < p.cols) p.st[static_cast<int64_t>(blockIdx.y) * p.pitch_t + c0 + t] = sc;
       }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(col_up + cg * 8 + j);
+        f[j] = x.x, f[j + 1] = x.y, f[j + 2] = x.z, f[j + 3] = x.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) nan |= f[j] < 0.0f ? 1u << j : 0u;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = up;
@@ -170,7 +184,8 @@ __global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs
           }
           o[i] = nan >> (2 * j + h) & 1u ? nan_codes[i] : a;
         }
-        *reinterpret_cast<uint2*>(tile + (cg * 8 + 2 * j + h) * kQStride + rg * 8) = make_uint2(o[0], o[1]);
+        // (8-byte unit rg of the column at rg ^ cg: the lanes of a store fall into different banks)
+        *reinterpret_cast<uint2*>(tile + (cg * 8 + 2 * j + h) * 128 + (rg ^ cg) * 8) = make_uint2(o[0], o[1]);
       }
     }
     __syncthreads();
@@ -178,9 +193,11 @@ __global__ void __launch_bounds__(kQThreads) fp8_quantize_kernel(const QuantArgs
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // 8 vectors of 16 rows per transposed row
       const int item = t + i * kQThreads, col = item >> 3, r16 = (item & 7) * 16;
+      const int k = col >> 3;  // the column's swizzle: units 2 n and 2 n + 1 at 2 (n ^ k / 2), the other way round where k is odd
+      uint4 o = *reinterpret_cast<const uint4*>(tile + col * 128 + (r16 ^ (k >> 1) * 16));
+      if (k & 1) o = make_uint4(o.z, o.w, o.x, o.y);
       if (c0 + col < p.cols && r0 + r16 < p.ldt)
-        *reinterpret_cast<uint4*>(qt + static_cast<int64_t>(c0 + col) * p.ldt + r0 + r16) =
-            *reinterpret_cast<const uint4*>(tile + col * kQStride + r16);
+        *reinterpret_cast<uint4*>(qt + static_cast<int64_t>(c0 + col) * p.ldt + r0 + r16) = o;
     }
   }
 }
