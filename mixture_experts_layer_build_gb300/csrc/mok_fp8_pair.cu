@@ -21,7 +21,7 @@ namespace mok {
 namespace {
 
 // Warpgroup 0: warp 0 loads, warp 1 issues MMAs; warpgroups 1 and 2 drain.  A drain thread of a 256-column tile needs more
-// registers than a third of the SM's: the first group gives up of its own.  128 x 40 + 256 x 232 (and 128 x 72 + 256 x
+// registers than a third of the SM's: the first group gives up of its own.  128 x 56 + 256 x 224 (and 128 x 72 + 256 x
 // 216) are the 384 x 168 that a launch has.
 constexpr int kThreads = 384;
 constexpr int kDrain = 4;  // the first drain warp
@@ -36,9 +36,22 @@ struct PairMaps {
   CUtensorMap p, q, out;
 };
 
+// 16 TMEM lanes x 64 columns: register 4 n + k of thread t holds lane t / 4 + 8 (k / 2), column 8 n + 2 (t % 4) + k % 2.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
 template <int BN, bool COLVEC>
 struct Cfg {
-  static constexpr int kLow = BN == 256 ? 40 : 72, kHigh = BN == 256 ? 232 : 216;  // registers per thread
+  static constexpr int kLow = BN == 256 ? 56 : 72, kHigh = BN == 256 ? 224 : 216;  // registers per thread
   static constexpr int HB = BN / 2;      // columns of a drain thread
   static constexpr int kAccs = 512 / BN; // accumulators in TMEM
   static constexpr uint32_t kQBytes = HB * 128, kStage = 16384 + kQBytes, kTx = 2 * kStage;
@@ -211,6 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     pdl_wait();
+    pdl_trigger();
     int st = 0, issued = 0, slot = 0;
     uint32_t ph = 0;
     bool ok = true;
@@ -313,62 +327,145 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = warp_wait(sfull(slot), static_cast<uint32_t>(n / C::kSlots) & 1u, abort_flag, g.status);
         if (!ok) break;
         const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff + slot * C::kScales);
-        const float* cs = sc + 128 + h * HB;
-        float s = sc[q * 32 + lane];
-        if constexpr (!COLVEC) s *= __shfl_sync(0xffffffffu, q_now, kb % 32);
         const int b = n % kAccs;
         ok = warp_wait(tfull(b), static_cast<uint32_t>(n / kAccs) & 1u, abort_flag, g.status);
         if (!ok) break;
         tc_fence_after();
-        // chunks of 32 columns, the next one on its way while this one is added
+        auto release = [&] {  // the accumulator has been read whole: the MMAs may write it again
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty(b), 0));
+        };
+        // chunks of 32 registers, the next one on its way while this one is added
         uint32_t v[2][32];
-        tmem_ld_32x32b_x32(lanes + b * BN, v[0]);
+        if constexpr (COLVEC) {
+          // a thread holds 4 rows x HB / 4 columns, so that it needs few of the column scales (all of them, for a row per
+          // thread, are 1024 cycles of shared memory per block: 8192 x 8192 x 8192 588 us)
+          const float* cs = sc + 128 + h * HB + (lane & 3) * 2;
+          float rs[4];
 #pragma unroll
-        for (int c = 0; c < HB; c += 32) {
-          uint32_t(&x)[32] = v[c / 32 & 1];
-          tmem_ld_wait_for(x);
-          if (c + 32 < HB) {
-            tmem_ld_32x32b_x32(lanes + b * BN + c + 32, v[(c / 32 + 1) & 1]);
-          } else {  // read whole: the MMAs may write it again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty(b), 0));
-          }
+          for (int i = 0; i < 4; ++i) rs[i] = sc[q * 32 + (lane >> 2) + 8 * i];
+          constexpr int kChunks = HB / 32;  // 16 lanes x 64 columns, lanes first
+          auto load = [&](int i, uint32_t(&x)[32]) {
+            tmem_ld_16x256b_x8(lanes + (static_cast<uint32_t>(i & 1) * 16u << 16) + b * BN + (i >> 1) * 64, x);
+          };
+          load(0, v[0]);
+          float2 y[8];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            float f0 = s, f1 = s, f2 = s, f3 = s;
-            if constexpr (COLVEC) {
-              const float4 y = *reinterpret_cast<const float4*>(cs + c + j);
-              mul_f32x2(f0, f1, s, s, y.x, y.y);
-              mul_f32x2(f2, f3, s, s, y.z, y.w);
+          for (int i = 0; i < kChunks; ++i) {
+            if (!(i & 1)) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = *reinterpret_cast<const float2*>(cs + (i >> 1) * 64 + k * 8);
             }
-            fma_f32x2(acc[c + j], acc[c + j + 1], __uint_as_float(x[j]), __uint_as_float(x[j + 1]), f0, f1, acc[c + j],
-                      acc[c + j + 1]);
-            fma_f32x2(acc[c + j + 2], acc[c + j + 3], __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]), f2, f3,
-                      acc[c + j + 2], acc[c + j + 3]);
+            uint32_t(&x)[32] = v[i & 1];
+            tmem_ld_wait_for(x);
+            if (i + 1 < kChunks) load(i + 1, v[(i + 1) & 1]);
+            else release();
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+              for (int o = 0; o < 2; ++o) {
+                float f0, f1;
+                const float s = rs[(i & 1) * 2 + o];
+                mul_f32x2(f0, f1, s, s, y[k].x, y[k].y);
+                float(&to)[HB] = acc;
+                const int at = i * 32 + k * 4 + o * 2;
+                fma_f32x2(to[at], to[at + 1], __uint_as_float(x[k * 4 + o * 2]), __uint_as_float(x[k * 4 + o * 2 + 1]), f0, f1,
+                          to[at], to[at + 1]);
+              }
+          }
+        } else {
+          const float s = sc[q * 32 + lane] * __shfl_sync(0xffffffffu, q_now, kb % 32);
+          tmem_ld_32x32b_x32(lanes + b * BN, v[0]);
+#pragma unroll
+          for (int c = 0; c < HB; c += 32) {
+            uint32_t(&x)[32] = v[c / 32 & 1];
+            tmem_ld_wait_for(x);
+            if (c + 32 < HB) tmem_ld_32x32b_x32(lanes + b * BN + c + 32, v[(c / 32 + 1) & 1]);
+            else release();
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              fma_f32x2(acc[c + j], acc[c + j + 1], __uint_as_float(x[j]), __uint_as_float(x[j + 1]), s, s, acc[c + j],
+                        acc[c + j + 1]);
           }
         }
       }
       if (!ok) break;
       // The tile's 32 rows of this warp.  Where all of them are there: through shared memory, a box of 32 rows x 128 bytes
-      // at a time (in the 128-byte TMA swizzle: 16-byte chunk k of row r at k ^ (r & 7)); else row by row.
+      // at a time (in the 128-byte TMA swizzle: 16-byte chunk k of row r at k ^ (r & 7)); else straight from the registers.
       const int row0 = w.row0 + rank * 128 + q * 32;
       if (row0 >= w.row_end) continue;
-      if (row0 + 32 <= w.row_end) {
-        auto box = [&](const uint32_t (&x)[32], int c0) {
+      const bool boxes = row0 + 32 <= w.row_end;
+      auto begin = [&] {
+        if (lane == 0) bulk_wait_read<0>();  // what was stored from here before has been read
+        __syncwarp();
+      };
+      auto send = [&](int c0) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&t.out, stage, c0, row0);
+          bulk_commit();
+        }
+      };
+      if constexpr (COLVEC) {
+        const int fr = lane >> 2, fc = lane & 3;  // row of the thread's first; its pair of columns in 8
+        if (boxes) {
+          constexpr int kPairs = 8;  // groups of 8 columns in 64
+#pragma unroll
+          for (int i = 0; i < HB; i += 64) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {  // fp32: two boxes of 32 columns
+              if (half && !g.out_f32) continue;
+              const int c0 = j0 + i + half * 32;
+              if (c0 >= g.q_rows) continue;
+              begin();
+#pragma unroll
+              for (int o = 0; o < 4; ++o) {  // rows fr + 8 o
+                const int r = fr + 8 * o;
+                const uint32_t at = stage + static_cast<uint32_t>(r) * 128u;
+#pragma unroll
+                for (int k = 0; k < kPairs; ++k) {
+                  const float* x = &acc[(i / 32 + (o >> 1)) * 32 + k * 4 + (o & 1) * 2];
+                  if (!g.out_f32) {
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + static_cast<uint32_t>((k ^ (r & 7)) * 16 + fc * 4)),
+                                 "r"(pack_bf16x2(x[0], x[1]))
+                                 : "memory");
+                  } else if ((k >= 4) == (half == 1)) {
+                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(
+                                     at + static_cast<uint32_t>((((k & 3) * 2 + (fc >> 1)) ^ (r & 7)) * 16 + (fc & 1) * 8)),
+                                 "f"(x[0]), "f"(x[1])
+                                 : "memory");
+                  }
+                }
+              }
+              send(c0);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < HB; i += 64)
+#pragma unroll
+            for (int o = 0; o < 4; ++o)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int row = row0 + fr + 8 * o, col = j0 + i + k * 8 + fc * 2;
+                if (row >= w.row_end || col >= g.q_rows) continue;
+                const float* x = &acc[(i / 32 + (o >> 1)) * 32 + k * 4 + (o & 1) * 2];
+                const int64_t at = static_cast<int64_t>(row) * g.ldo + col;
+                if (g.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(g.out) + at) = make_float2(x[0], x[1]);
+                else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(g.out) + at) = pack_bf16x2(x[0], x[1]);
+              }
+        }
+      } else if (boxes) {
+        const uint32_t at = stage + static_cast<uint32_t>(lane) * 128u;
+        auto box = [&](const uint32_t(&x)[32], int c0) {
           if (c0 >= g.q_rows) return;
-          if (lane == 0) bulk_wait_read<0>();  // what was stored from here before has been read
-          __syncwarp();
-          const uint32_t at = stage + static_cast<uint32_t>(lane) * 128u;
+          begin();
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             st_shared_v4(at + (static_cast<uint32_t>(k ^ (lane & 7)) << 4), make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&t.out, stage, c0, row0);
-            bulk_commit();
-          }
+          send(c0);
         };
         uint32_t x[32];
         if (!g.out_f32) {

@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
       }
   }
   pdl_wait();  // (the kernel in front may take its time: no bounded wait starts before its end)
+  pdl_trigger();
   const int q = warp & 3, r = q * 32 + lane;  // (warps 2 to 5) TMEM lane quarter; the lane's row
   const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
   int n = 0, st = 0;     // K blocks so far; (warps 0 and 1) the next one's stage

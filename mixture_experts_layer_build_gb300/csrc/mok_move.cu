@@ -94,20 +94,23 @@ __global__ void __launch_bounds__(kMoveThreads) gather_tokens_kernel(const RowSr
 // parallelism) and a slot counts when its id lies in [0, e_total).  Each
 // lane keeps eight 16-byte row loads in flight: U column vectors x (8 / U) of the K rows, issued
 // together before the fixed-order FMA chains (U = 8 for top-1 ... U = 1 for K >= 8).  Rows are
-// read once and written once: both streams are marked evict-first.
-template <int U, bool ONE>
+// read once and written once: both streams are marked evict-first.  `parts` warps share a token's columns: with few tokens
+// a warp each leaves SMs idle (T = 1003, K = 5, H = 2056 10.9 us with one, 4.9 with nine).  SPLIT:
+// whether there are parts (the indexing costs the other form registers).
+template <int U, bool ONE, bool SPLIT>
 __global__ void __launch_bounds__(kMoveThreads, 4) combine_kernel(const uint4* __restrict__ y,
                                                               const int32_t* __restrict__ inv,
                                                               const int32_t* __restrict__ ids, int e_total,
-                                                              const float* __restrict__ w, int64_t T, int K,
+                                                              const float* __restrict__ w, int64_t T, int K, int parts,
                                                               int64_t vecs, uint4* __restrict__ out) {
   pdl_wait();
   constexpr int kBatch = 8 / U;
   const int lane = threadIdx.x & 31;
   const int64_t nwarps = static_cast<int64_t>(gridDim.x) * (kMoveThreads / 32);
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); t < T;
-       t += nwarps) {
-    for (int64_t c0 = lane; c0 < vecs; c0 += 32 * U) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5); i < (SPLIT ? T * parts : T);
+       i += nwarps) {
+    const int64_t t = SPLIT ? i / parts : i;
+    for (int64_t c0 = SPLIT ? lane + (i - t * parts) * 32 * U : lane; c0 < vecs; c0 += SPLIT ? 32 * U * parts : 32 * U) {
       if constexpr (ONE) {
         // all K slots in one batch (K <= 8 / U): each column vector is reduced and stored as soon
         // as its loads land, so no U x 8 accumulator array stays live across a runtime k loop (the
@@ -607,21 +610,26 @@ int launch_mx_scale_atoms(const ScaleJob* jobs, int njobs, cudaStream_t stream) 
   return static_cast<int>(cudaGetLastError());
 }
 
+template <int U, bool ONE>
+static void combine_launch(const uint16_t* y, const int32_t* inv, const int32_t* ids, int32_t e_total, const float* s,
+                           int64_t T, int32_t K, int32_t H, uint16_t* out, cudaStream_t stream) {
+  // warps of a token: as many as it takes to have 32 per SM, and as it has pieces of 32 U vectors
+  const int64_t pieces = (H / 8 + 32 * U - 1) / (32 * U), want = (static_cast<int64_t>(sm_count()) * 32 + T - 1) / T;
+  const int parts = static_cast<int>(want < pieces ? (want > 0 ? want : 1) : pieces);
+  launch_pdl(parts > 1 ? combine_kernel<U, ONE, true> : combine_kernel<U, ONE, false>,
+             dim3(grid_for(T * parts, kMoveThreads / 32)), dim3(kMoveThreads), 0, stream, reinterpret_cast<const uint4*>(y),
+             inv, ids, e_total, s, T, K, parts, H / 8, reinterpret_cast<uint4*>(out));
+}
+
 static int combine_any(const uint16_t* y, const int32_t* inv, const int32_t* ids, int32_t e_total, const float* s,
                        int64_t T, int32_t K, int32_t H, uint16_t* out, int kind, cudaStream_t stream) {
   if (T <= 0) return 0;
-  const int grid = grid_for(T, kMoveThreads / 32);
   trace_begin(stream, kind);
-  const uint4* yv = reinterpret_cast<const uint4*>(y);
-  uint4* ov = reinterpret_cast<uint4*>(out);
-  if (K == 1)
-    launch_pdl(combine_kernel<8, true>, dim3(grid), dim3(kMoveThreads), 0, stream, yv, inv, ids, e_total, s, T, K, H / 8, ov);
-  else if (K == 2)
-    launch_pdl(combine_kernel<4, true>, dim3(grid), dim3(kMoveThreads), 0, stream, yv, inv, ids, e_total, s, T, K, H / 8, ov);
-  else if (K <= 4)
-    launch_pdl(combine_kernel<2, true>, dim3(grid), dim3(kMoveThreads), 0, stream, yv, inv, ids, e_total, s, T, K, H / 8, ov);
+  if (K == 1) combine_launch<8, true>(y, inv, ids, e_total, s, T, K, H, out, stream);
+  else if (K == 2) combine_launch<4, true>(y, inv, ids, e_total, s, T, K, H, out, stream);
+  else if (K <= 4) combine_launch<2, true>(y, inv, ids, e_total, s, T, K, H, out, stream);
   else  // one column vector, up to eight rows per batch (64 registers as it is)
-    launch_pdl(combine_kernel<1, false>, dim3(grid), dim3(kMoveThreads), 0, stream, yv, inv, ids, e_total, s, T, K, H / 8, ov);
+    combine_launch<1, false>(y, inv, ids, e_total, s, T, K, H, out, stream);
   trace_end(stream);
   return static_cast<int>(cudaGetLastError());
 }
