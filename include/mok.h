@@ -629,7 +629,8 @@ MOK_API mok_status mok_fp8_quantize_blocks(const void* x, int32_t batch, int64_t
 MOK_API mok_status mok_fp8_matmul(const mok_fp8_matrix* a, const mok_fp8_matrix* b, void* out, int32_t out_type,
                                   uint32_t* status, void* stream);
 
-/* Bytes of device workspace (256-byte aligned) of mok_fp8_linear: x's codes and scales.  0 for an unsupported shape. */
+/* Bytes of device workspace (256-byte aligned) of mok_fp8_linear: x's codes and scales; 256 where it needs none (few rows: ws
+ * may then be NULL).  0 for an unsupported shape. */
 MOK_API size_t mok_fp8_linear_workspace_bytes(int64_t M, int64_t K);
 
 /* out [M, N] bf16 = x w^T for x [M, K] bf16, quantised on the way as by mok_fp8_quantize; w [N, K] MOK_FP8_BLOCKS, batch 1.

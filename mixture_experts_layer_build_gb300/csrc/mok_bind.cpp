@@ -498,8 +498,8 @@ PyObject* fp8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor out[1];
     const int rc = on_device(*x, [&] {
       out[0] = given ? *given : make({M, w.rows}, *x, at::kBFloat16);
-      const Tensor scratch = make({static_cast<int64_t>(bytes)}, *x, at::kByte);
-      return mok_fp8_linear(x->data_ptr(), M, &w, ptr(out[0]), scratch.data_ptr(), bytes,
+      const Tensor scratch = bytes > 256 ? make({static_cast<int64_t>(bytes)}, *x, at::kByte) : Tensor();  // else not used
+      return mok_fp8_linear(x->data_ptr(), M, &w, ptr(out[0]), ptr(scratch), bytes,
                             static_cast<uint32_t*>(ptr(status)), current_stream(*x));
     });
     return rc ? PyLong_FromLong(rc) : wrap_all(out);

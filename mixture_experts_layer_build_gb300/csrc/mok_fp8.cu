@@ -22,8 +22,9 @@ Fp8Operand operand(const mok_fp8_matrix& m) {
   return {m.q, m.s, m.rows, m.cols, m.ld, m.batch, m.scaling == MOK_FP8_ROWS};
 }
 
-// out [M, N]: see mok_fp8_matmul.
-mok_status product(const mok_fp8_matrix& a, const mok_fp8_matrix& b, void* out, int32_t out_type, bool early,
+// out [M, N]: see mok_fp8_matmul.  x: a's values where the product quantises them itself, or null; early: b may be read before
+// the previous kernel of the stream has ended.
+mok_status product(const mok_fp8_matrix& a, const void* x, const mok_fp8_matrix& b, void* out, int32_t out_type, bool early,
                    uint32_t* status, cudaStream_t stream) {
   Fp8Problem g{};
   g.mode = FP8_DENSE;
@@ -38,7 +39,7 @@ mok_status product(const mok_fp8_matrix& a, const mok_fp8_matrix& b, void* out, 
   // 256 x 1024 x 1024 7.0 and 6.6, 1024 x 2048 x 2048 13.7 and 9.5; both row-scaled 512 x 512 x 2048 7.8 and 10.6.
   if (a.rows > 128 && (4 * fp8_blocks(a.rows) * fp8_blocks(b.rows) >= sm_count() || g.k_blocks <= 8))
     return from_cuda(launch_fp8_pair(operand(a), operand(b), g, 0, K_FP8_PAIR, stream));
-  return from_cuda(launch_fp8_tile(operand(a), operand(b), g, a.rows, 0, K_FP8_TILE, stream));
+  return from_cuda(launch_fp8_tile(operand(a), x, operand(b), g, a.rows, 0, K_FP8_TILE, stream));
 }
 
 }  // namespace
@@ -58,11 +59,12 @@ mok_status mok_fp8_matmul(const mok_fp8_matrix* a, const mok_fp8_matrix* b, void
   if (a->cols == 0)
     return from_cuda(static_cast<int>(cudaMemsetAsync(
         out, 0, static_cast<size_t>(a->rows) * b->rows * (out_type == MOK_DT_FP32 ? 4 : 2), s)));
-  return product(*a, *b, out, out_type, false, status, s);
+  return product(*a, nullptr, *b, out, out_type, false, status, s);
 }
 
 size_t mok_fp8_linear_workspace_bytes(int64_t M, int64_t K) {
   if (M < 0 || M > kMax || K < 8 || K % 8 != 0 || K > kMax) return 0;
+  if (M <= kFp8XqRows) return 256;  // none is used
   const int64_t codes = (M * fp8_ld(K) + 255) / 256 * 256, scales = fp8_blocks(K) * fp8_pitch(M) * 4;
   return static_cast<size_t>((codes + scales + 255) / 256 * 256 + 256);
 }
@@ -72,21 +74,26 @@ mok_status mok_fp8_linear(const void* x, int64_t M, const mok_fp8_matrix* w, voi
   if (M < 0 || M > kMax || !matrix_ok(w, 1) || w->scaling != MOK_FP8_BLOCKS) return MOK_ERR_INVALID_ARG;
   if (w->rows < 8 || w->rows % 8 != 0 || w->cols < 8 || w->cols % 8 != 0) return MOK_ERR_INVALID_ARG;
   if (M == 0) return MOK_OK;
-  if (!ok16(x) || !ok16(out) || !ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MOK_ERR_INVALID_ARG;
-  if (ws_bytes < mok_fp8_linear_workspace_bytes(M, w->cols)) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  if (!ok16(x) || !ok16(out)) return MOK_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   mok_fp8_matrix a{};
+  a.rows = M;
+  a.cols = w->cols;
+  a.ld = fp8_ld(w->cols);
+  a.batch = 1;
+  a.scaling = MOK_FP8_ROWS;
+  // (w is read no earlier than the previous kernel's end: it may be what wrote it)
+  if (M <= kFp8XqRows) return product(a, x, *w, out, MOK_DT_BF16, false, status, st);
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MOK_ERR_INVALID_ARG;
+  if (ws_bytes < mok_fp8_linear_workspace_bytes(M, w->cols)) return MOK_ERR_WORKSPACE_TOO_SMALL;
   uint8_t* q = static_cast<uint8_t*>(ws);
   float* s = reinterpret_cast<float*>(q + (M * fp8_ld(w->cols) + 255) / 256 * 256);
   const mok_status rc = mok_fp8_quantize(x, M, static_cast<int32_t>(w->cols), q, s, nullptr, nullptr, stream);
   if (rc != MOK_OK) return rc;
   a.q = q;
   a.s = s;
-  a.rows = M;
-  a.cols = w->cols;
-  a.ld = fp8_ld(w->cols);
-  a.batch = 1;
-  a.scaling = MOK_FP8_ROWS;
-  return product(a, *w, out, MOK_DT_BF16, true, status, static_cast<cudaStream_t>(stream));
+  // the quantisation has waited for all before it, and does not write w
+  return product(a, nullptr, *w, out, MOK_DT_BF16, true, status, st);
 }
 
 mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matrix* a, const mok_fp8_matrix* w, void* out,
@@ -116,7 +123,7 @@ mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matri
   if (z.R >= 64 * static_cast<int64_t>(z.E))
     return from_cuda(launch_fp8_pair(operand(*a), operand(*w), g, (z.R < z.E ? z.R : z.E) + z.R / 256, K_FP8_GROUPED_PAIR,
                                      static_cast<cudaStream_t>(stream)));
-  return from_cuda(launch_fp8_tile(operand(*a), operand(*w), g, z.R, blocks < z.mblocks_max ? blocks : z.mblocks_max,
+  return from_cuda(launch_fp8_tile(operand(*a), nullptr, operand(*w), g, z.R, blocks < z.mblocks_max ? blocks : z.mblocks_max,
                                    K_FP8_GROUPED_TILE, static_cast<cudaStream_t>(stream)));
 }
 

@@ -41,9 +41,11 @@ struct Fp8Problem {
   uint32_t* status;
 };
 
-// out [rows of a, rows of b].  rows: of a that hold values; row_blocks: (FP8_GROUPED) 128-row blocks of the layout at most.
-int launch_fp8_tile(const Fp8Operand& a, const Fp8Operand& b, Fp8Problem g, int64_t rows, int64_t row_blocks, int kind,
-                    cudaStream_t stream);
+// out [rows of a, rows of b].  x: a's bf16 values, quantised on the way (dense, at most kFp8XqRows rows; a's codes and scales
+// are not read then), or null.  rows: of a that hold values; row_blocks: (FP8_GROUPED) 128-row blocks of the layout at most.
+constexpr int kFp8XqRows = 8;
+int launch_fp8_tile(const Fp8Operand& a, const void* x, const Fp8Operand& b, Fp8Problem g, int64_t rows, int64_t row_blocks,
+                    int kind, cudaStream_t stream);
 
 bool make_tmap_f32(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_inner,
                    uint32_t box_outer);

@@ -8,6 +8,9 @@
 // lot on its way while one is used (fetched block by block, their latency set the pace: 1.6 us per block, one row at N =
 // 2048, K = 7168 14 us).
 //
+// XQ: a is bf16 and quantised on the way, by four more warps, each K block's rows by one of them, straight into the stage's
+// swizzled shared memory: a launch less, and its latency under the weights'.
+//
 // With few tiles their K range is split over a cluster, whose CTAs add up their partials through shared memory in rank
 // order.
 #include "mok_ffn.cuh"  // warp_wait, wait_landed, elect_one
@@ -17,7 +20,8 @@
 namespace mok {
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 192, kThreadsXq = 320;
+constexpr int kSlots = 24;  // (XQ) K blocks whose column scales are kept: stages + accumulators + 1 at least
 constexpr int kMaxStages = 12;
 constexpr uint32_t kHalfSmem = 114688;  // two CTAs
 constexpr uint32_t kMaxSmem = 227328;  // dynamic: 5 KB of 227 KB are left for what is static
@@ -29,15 +33,19 @@ struct TileArgs {
   int32_t split;   // CTAs of a cluster that share a tile's K range 
   int32_t stages;
   uint32_t scale_off, push_off;
+  const uint16_t* x;  // (XQ) a's values
+  int32_t K;
 };
 
-template <int BN, bool PVEC>
+template <int BN, bool PVEC, bool XQ>
 struct Cfg {
+  static_assert(!(PVEC && XQ), "a forward's weights have scales per 128 x 128 values");
   static constexpr uint32_t kStage = 16384 + BN * 128;
   static constexpr int kAccs = BN <= 32 ? 8 : 4;
   static constexpr int kPerSm = BN <= 32 ? 2 : 1;  // CTAs of an SM
   static constexpr uint32_t kRows = PVEC ? 128 : 0;  // of P with a scale each
   static constexpr uint32_t kLotBytes = kLot * (kRows + BN) * 4;
+  static constexpr uint32_t kScaleBytes = XQ ? kSlots * BN * 4 : 2 * kLotBytes;
 };
 
 // 32 or 16 columns of this lane's accumulator row.
@@ -108,15 +116,15 @@ __device__ __forceinline__ void push_partials(uint32_t push, const float (&acc)[
   }
 }
 
-template <int BN, bool PVEC>
-__global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
+template <int BN, bool PVEC, bool XQ>
+__global__ void __launch_bounds__(XQ ? kThreadsXq : kThreads, Cfg<BN, PVEC, XQ>::kPerSm)
     fp8_tile_kernel(const __grid_constant__ CUtensorMap tP, const __grid_constant__ CUtensorMap tQ, const TileArgs a) {
-  using C = Cfg<BN, PVEC>;
-  constexpr uint32_t kQBytes = BN * 128, kStage = C::kStage, kCols = C::kAccs * BN;
+  using C = Cfg<BN, PVEC, XQ>;
+  constexpr uint32_t kTx = 16384 + (XQ ? 0 : BN * 128), kStage = C::kStage, kCols = C::kAccs * BN;
   constexpr int kAccs = C::kAccs;
   constexpr int W = BN < 32 ? 16 : 32;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 17];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 17 + (XQ ? kSlots : 0)];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
   const Fp8Problem& g = a.g;
@@ -127,15 +135,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
   auto tfull = [&](int b) { return bar0 + 8u * (2 * kMaxStages + b); };
   auto tempty = [&](int b) { return bar0 + 8u * (2 * kMaxStages + kAccs + b); };
   const uint32_t done = bar0 + 8u * (2 * kMaxStages + 2 * kAccs);
+  auto qfull = [&](int i) { return done + 8u * (1 + i); };  // (XQ) the block's column scales are there
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = a.split;
   const int rank = static_cast<int>(blockIdx.x) % S, unit = static_cast<int>(blockIdx.x) / S;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
-      mbar_init(full(s), 1);
+      mbar_init(full(s), XQ ? 2 : 1);  // the loads; (XQ) the warp that quantised the block
       mbar_init(empty(s), 1);
     }
+    if (XQ)
+      for (int i = 0; i < kSlots; ++i) mbar_init(qfull(i), 1);
     for (int b = 0; b < kAccs; ++b) {
       mbar_init(tfull(b), 1);
       mbar_init(tempty(b), 4);
@@ -168,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
     ahead = min(total, a.stages);
     for (int n = 0; n < ahead; ++n)
       if (elect_one()) {
-        mbar_arrive_expect_tx(full(n), 16384 + kQBytes);
+        mbar_arrive_expect_tx(full(n), kTx);
         tma_load_2d(base + n * kStage, &tP, full(n), (kb0 + n % count) * 128, t.p0);
       }
   }
@@ -191,10 +202,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
         const uint32_t sp = base + st * kStage;
         if (elect_one()) {
           if (n >= ahead) {
-            mbar_arrive_expect_tx(full(st), 16384 + kQBytes);
+            mbar_arrive_expect_tx(full(st), kTx);
             tma_load_2d(sp, &tP, full(st), (kb0 + kb) * 128, t.p0);
           }
-          tma_load_2d(sp + 16384, &tQ, full(st), (kb0 + kb) * 128, t.q0 + sub * BN);
+          if (!XQ) tma_load_2d(sp + 16384, &tQ, full(st), (kb0 + kb) * 128, t.q0 + sub * BN);
         }
         ++n;
         if (++st == a.stages) {
@@ -223,13 +234,59 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
           ph ^= 1u;
         }
       }
+    } else if (XQ && warp >= 6) {
+      // K blocks warp - 6, + 4, ...: two rows at a time, 16 lanes x 8 columns each, the next rows on their way
+      const int rows = t.j_end - t.j0, half = lane >> 4, c = (lane & 15) * 8;
+      for (int kb = warp - 6; kb < count && ok; kb += 4) {
+        const int slot = kb % kSlots, at = kb % a.stages, col = (kb0 + kb) * 128 + c;
+        auto load = [&](int r) {
+          return r < rows && col < a.K
+                     ? __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<int64_t>(t.j0 + r) * a.K + col))
+                     : make_uint4(0, 0, 0, 0);
+        };
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = load(2 * i + half);
+        if (kb >= a.stages) ok = warp_wait(empty(at), static_cast<uint32_t>(kb / a.stages - 1) & 1u, abort_flag, g.status);
+        if (!ok) break;
+        const uint32_t to = base + at * kStage + 16384;
+        float* sc = reinterpret_cast<float*>(smem_raw + (base - smem_u32(smem_raw)) + a.scale_off) + slot * BN;
+        for (int r0 = 0; r0 < rows; r0 += 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = r0 + 2 * i + half;
+            const uint4 w = v[i];
+            v[i] = load(r + 8);
+            uint32_t m = absmax2(absmax2(w.x, w.y), absmax2(w.z, w.w));
+#pragma unroll
+            for (int d = 8; d >= 1; d >>= 1) m = absmax2(m, __shfl_xor_sync(0xffffffffu, m, d));
+            m = absmax2(m, m >> 16) & 0x7FFFu;
+            float up;
+            const float scale = fp8_scale(m, up);
+            uint2 o = make_uint2(fp8_codes(w.x, up) | fp8_codes(w.y, up) << 16, fp8_codes(w.z, up) | fp8_codes(w.w, up) << 16);
+            if (m >= 0x7F80u) o = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            if (r < rows) {  // 16-byte chunk k of row r at k ^ (r & 7); the rows past the last one's columns are not stored
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + static_cast<uint32_t>(r * 128 + (((c >> 4) ^ (r & 7)) << 4) + (c & 8))),
+                           "r"(o.x), "r"(o.y)
+                           : "memory");
+              if ((lane & 15) == 0) sc[r] = scale;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(full(at));
+          mbar_arrive(qfull(slot));
+        }
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < BN; ++j) acc[j] = 0.0f;
       const int j0 = t.j0 + sub * BN;
       // 16-byte pieces of a lot's row scales (their rows are padded to four); what lies past the matrix is not used
       const int tid = static_cast<int>(threadIdx.x) - 64;
-      auto fetch = [&](int lot) {
+      [[maybe_unused]] auto fetch = [&](int lot) {
         const uint32_t to = base + a.scale_off + (lot & 1) * C::kLotBytes;
         const int k0 = kb0 + lot * kLot, blocks = min(kLot, count - lot * kLot);
         if constexpr (PVEC) {
@@ -252,21 +309,27 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
         const int k = lot * kLot + (lane & (kLot - 1));
         return k < count ? __ldg(ps + k) : 0.0f;
       };
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // the lots of the sub-tile before have been used
-      if (count > 0) fetch(0);
+      if constexpr (!XQ) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");  // the lots of the sub-tile before have been used
+        if (count > 0) fetch(0);
+      }
       float s_now = 0.0f, s_next = PVEC ? 0.0f : block_scales(0);
       for (int kb = 0; kb < count; ++kb, ++n) {  // (also after a failed wait: the barriers count every warp)
         const int b = n % kAccs, lot = kb / kLot, in = kb % kLot;
         if (in == 0) {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
-          asm volatile("bar.sync 1, 128;" ::: "memory");  // everybody's pieces are there, and the other lot has been used
-          if (kb + kLot < count) fetch(lot + 1);
+          if constexpr (!XQ) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // everybody's pieces are there, and the other lot has been used
+            if (kb + kLot < count) fetch(lot + 1);
+          }
           s_now = s_next;
           if (!PVEC) s_next = block_scales(lot + 1);
         }
-        const float* lots = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + a.scale_off + (lot & 1) * C::kLotBytes);
-        const float* cs = lots + kLot * C::kRows + in * BN;
+        const float* lots = reinterpret_cast<const float*>(smem_raw + (base - smem_u32(smem_raw)) + a.scale_off);
+        if constexpr (!XQ) lots += (lot & 1) * (C::kLotBytes / 4);
+        const float* cs = XQ ? lots + kb % kSlots * BN : lots + kLot * C::kRows + in * BN;
         const float s = PVEC ? lots[in * 128 + r] : __shfl_sync(0xffffffffu, s_now, in);
+        if constexpr (XQ) ok = ok && warp_wait(qfull(kb % kSlots), static_cast<uint32_t>(kb / kSlots) & 1u, abort_flag, g.status);
         ok = ok && warp_wait(tfull(b), static_cast<uint32_t>(n / kAccs) & 1u, abort_flag, g.status);
         if (!ok) continue;
         tc_fence_after();
@@ -294,11 +357,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
         }
       }
     }
+    const bool drains = warp >= 2 && warp < 6;
     const int j0 = t.j0 + sub * BN;
     // Column j belongs to CTA j / (BN / S) of the cluster: each sends it its partials, [source][column][row], and the owner
     // adds them in rank order, 8 rows of a column per thread: 16 bytes of a row of the output.
     const uint32_t push = base + a.push_off;
-    if (warp >= 2) {
+    if (drains) {
       if (S == 1) push_partials<BN, 1>(push, acc, rank, r);
       else if (S == 2) push_partials<BN, 2>(push, acc, rank, r);
       else if (S == 4) push_partials<BN, 4>(push, acc, rank, r);
@@ -306,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
     }
     __syncwarp();
     if (S > 1) cluster_sync();
-    else if (warp >= 2) asm volatile("bar.sync 1, 128;" ::: "memory");
-    if (warp >= 2 && *abort_flag == 0) {
+    else if (drains) asm volatile("bar.sync 1, 128;" ::: "memory");
+    if (drains && *abort_flag == 0) {
       const int per = BN / S;
       const float* parts = reinterpret_cast<const float*>(smem_raw + (push - smem_u32(smem_raw)));
       for (int x = static_cast<int>(threadIdx.x) - 64; x < per * 16; x += 128) {
@@ -351,33 +415,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<BN, PVEC>::kPerSm)
   }
 }
 
-template <int BN, bool PVEC>
-int launch_tile(const CUtensorMap& tP, const CUtensorMap& tQ, const Fp8Problem& g, int64_t units, int split, int kind,
-                cudaStream_t stream) {
+template <int BN, bool PVEC, bool XQ>
+int launch_tile(const CUtensorMap& tP, const CUtensorMap& tQ, const Fp8Problem& g, int64_t units, int split, const void* x,
+                int64_t K, int kind, cudaStream_t stream) {
   static DeviceOnce once;
   const int se = once.run([](int* d) { return static_cast<int>(cudaGetDevice(d)); },
                           [] {
-                            return static_cast<int>(cudaFuncSetAttribute(fp8_tile_kernel<BN, PVEC>,
+                            return static_cast<int>(cudaFuncSetAttribute(fp8_tile_kernel<BN, PVEC, XQ>,
                                                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                                          static_cast<int>(kMaxSmem)));
                           },
                           static_cast<int>(cudaErrorInvalidDevice));
   if (se) return se;
   if (units * split >= (int64_t{1} << 31)) return static_cast<int>(cudaErrorInvalidValue);
-  using C = Cfg<BN, PVEC>;
+  using C = Cfg<BN, PVEC, XQ>;
   constexpr uint32_t kStage = C::kStage;
   TileArgs a{};
   a.g = g;
+  a.x = static_cast<const uint16_t*>(x);
+  a.K = static_cast<int32_t>(K);
   a.split = split;
   constexpr uint32_t push = BN * 512u;
-  constexpr uint32_t fixed = 1024u + 2 * C::kLotBytes + push;  // alignment; scales; partials
+  static_assert(!XQ || kSlots > kMaxStages + C::kAccs, "scales stay until they are used");
+  constexpr uint32_t fixed = 1024u + C::kScaleBytes + push;  // alignment; scales; partials
   a.stages = static_cast<int32_t>(((C::kPerSm == 2 ? kHalfSmem : kMaxSmem) - fixed) / kStage);
   if (a.stages > kMaxStages) a.stages = kMaxStages;
   a.scale_off = static_cast<uint32_t>(a.stages) * kStage;
-  a.push_off = a.scale_off + 2 * C::kLotBytes;
+  a.push_off = a.scale_off + C::kScaleBytes;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(units * split));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(XQ ? kThreadsXq : kThreads);
   cfg.dynamicSmemBytes = a.push_off + push + 1024u;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -390,15 +457,15 @@ int launch_tile(const CUtensorMap& tP, const CUtensorMap& tQ, const Fp8Problem& 
   cfg.attrs = attr;
   cfg.numAttrs = split > 1 ? 2 : 1;
   trace_begin(stream, kind);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, PVEC>, tP, tQ, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_tile_kernel<BN, PVEC, XQ>, tP, tQ, a);
   trace_end(stream);
   return static_cast<int>(e);
 }
 
 }  // namespace
 
-int launch_fp8_tile(const Fp8Operand& a, const Fp8Operand& b, Fp8Problem g, int64_t rows, int64_t row_blocks, int kind,
-                    cudaStream_t stream) {
+int launch_fp8_tile(const Fp8Operand& a, const void* x, const Fp8Operand& b, Fp8Problem g, int64_t rows, int64_t row_blocks,
+                    int kind, cudaStream_t stream) {
   const int sms = sm_count();
   if (sms <= 0) return static_cast<int>(cudaErrorInvalidDevice);
   const bool grouped = g.mode == FP8_GROUPED;
@@ -420,20 +487,23 @@ int launch_fp8_tile(const Fp8Operand& a, const Fp8Operand& b, Fp8Problem g, int6
   split = split >= 8 && bn <= 32 ? 8 : split >= 4 ? 4 : split >= 2 ? 2 : 1;
   CUtensorMap tp, tq;
   if (!make_tmap_fp8(&tp, b.q, static_cast<uint64_t>(b.cols), static_cast<uint64_t>(b.rows) * b.batch,
-                     static_cast<uint64_t>(b.ld), 128) ||
-      !make_tmap_fp8(&tq, a.q, static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.rows), static_cast<uint64_t>(a.ld),
-                     static_cast<uint32_t>(bn)))
+                     static_cast<uint64_t>(b.ld), 128))
+    return static_cast<int>(cudaErrorInvalidValue);
+  if (x) tq = tp;
+  else if (!make_tmap_fp8(&tq, a.q, static_cast<uint64_t>(a.cols), static_cast<uint64_t>(a.rows), static_cast<uint64_t>(a.ld),
+                          static_cast<uint32_t>(bn)))
     return static_cast<int>(cudaErrorInvalidValue);
   const int s = static_cast<int>(split);
   auto width = [&](auto vec) {
     constexpr bool V = decltype(vec)::value;
     switch (bn) {
-      case 16: return launch_tile<16, V>(tp, tq, g, units, s, kind, stream);
-      case 32: return launch_tile<32, V>(tp, tq, g, units, s, kind, stream);
-      case 64: return launch_tile<64, V>(tp, tq, g, units, s, kind, stream);
-      default: return launch_tile<128, V>(tp, tq, g, units, s, kind, stream);
+      case 16: return launch_tile<16, V, false>(tp, tq, g, units, s, nullptr, 0, kind, stream);
+      case 32: return launch_tile<32, V, false>(tp, tq, g, units, s, nullptr, 0, kind, stream);
+      case 64: return launch_tile<64, V, false>(tp, tq, g, units, s, nullptr, 0, kind, stream);
+      default: return launch_tile<128, V, false>(tp, tq, g, units, s, nullptr, 0, kind, stream);
     }
   };
+  if (x) return launch_tile<16, false, true>(tp, tq, g, units, s, x, a.cols, kind, stream);
   return b.row_scales ? width(std::true_type{}) : width(std::false_type{});
 }
 
