@@ -547,7 +547,7 @@ MOK_API mok_status mok_ffn_backward(const mok_ffn_shape* shape, const void* x, c
  * A buffer of routed rows has sched->rpad_max rows in the schedule's layout: row inv[j] belongs to slot j,
  * each expert's segment is padded to a multiple of 128 rows, the layout ends at row Rpad = meta[0], and
  * rows from there on are neither read nor written.  Widths are multiples of 8 values up to 16384, of the caller's choice
- * (not the shape's H); tensors start on a 16-byte boundary.  Slots whose id is invalid have no row: they
+ * (not the shape's H); tensors start on a 16-byte boundary; outputs do not overlap inputs but where a call says so.  Slots whose id is invalid have no row: they
  * contribute nothing and their gradients are 0.
  * ------------------------------------------------------------------------------------------- */
 
@@ -604,7 +604,7 @@ typedef struct {
 /* Scales of x [rows, cols] bf16 per row (MOK_FP8_ROWS), of its rows and of the rows of its transpose:
  *   q [rows][cols rounded up to 16], s [ceil(cols/128)][rows rounded up to 4]: x;
  *   qt [cols][rows rounded up to 16], st [ceil(rows/128)][cols rounded up to 4]: x^T, for products that sum over x's rows.
- * q and s, or qt and st, may be NULL.  rows >= 0 (below 2^31); cols a positive multiple of 8. */
+ * q and s, or qt and st, may be NULL.  0 <= rows <= 8,388,480; cols a positive multiple of 8. */
 MOK_API mok_status mok_fp8_quantize(const void* x, int64_t rows, int32_t cols, uint8_t* q, float* s, uint8_t* qt,
                                     float* st, void* stream);
 
@@ -624,8 +624,8 @@ MOK_API mok_status mok_fp8_quantize_blocks(const void* x, int32_t batch, int64_t
                                            uint8_t* qt, float* st, void* stream);
 
 /* out [M, N] = a b^T; a [M, K] MOK_FP8_ROWS, b [N, K] of either scaling, batch 1.  out of out_type (mok_dtype), rounded
- * once.  M, K >= 0 (K = 0 gives zeros), N a positive multiple of 8; each below 2^31.  status: device word (bit (1 << mok_status code) per problem
- * seen, never cleared here) or NULL. */
+ * once.  M, K >= 0 (K = 0 gives zeros), N a positive multiple of 8; each below 2^31 - 1024.  status: device word (bit
+ * (1 << mok_status code) per problem seen, never cleared here) or NULL. */
 MOK_API mok_status mok_fp8_matmul(const mok_fp8_matrix* a, const mok_fp8_matrix* b, void* out, int32_t out_type,
                                   uint32_t* status, void* stream);
 

@@ -4,7 +4,7 @@
 namespace mok {
 namespace {
 
-constexpr int64_t kMax = (int64_t{1} << 31) - 1;
+constexpr int64_t kMax = (int64_t{1} << 31) - 1024;  // rows and columns: indices of padded tiles stay within 31 bits
 
 bool ok16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 mok_status from_cuda(int rc) { return rc == 0 ? MOK_OK : MOK_ERR_CUDA; }
@@ -137,7 +137,7 @@ mok_status mok_fp8_grouped_wgrad(const mok_schedule* sched, const mok_fp8_matrix
   if (a->cols != z.rpad_max || b->cols != z.rpad_max || a->rows < 8 || b->rows < 8 || b->rows % 8 != 0)
     return MOK_ERR_INVALID_ARG;
   if ((dw_type != MOK_DT_BF16 && dw_type != MOK_DT_FP32) || !ok16(dw)) return MOK_ERR_INVALID_ARG;
-  if (a->rows * b->rows > kMax) return MOK_ERR_UNSUPPORTED;
+  if (a->rows * z.E > kMax) return MOK_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (z.T == 0)
     return from_cuda(static_cast<int>(cudaMemsetAsync(
