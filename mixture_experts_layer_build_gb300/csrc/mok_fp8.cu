@@ -120,7 +120,9 @@ mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matri
   g.status = sched->status;
   // an expert with rows has one block that is not full at most
   const int64_t blocks = (z.R < z.E ? z.R : z.E) + z.R / 128;
-  if (z.R >= 64 * static_cast<int64_t>(z.E))
+  // Pairs from about 48 rows per expert on.  Measured, tiles and pairs: 128 experts, K = 4096, N = 1536, 32 rows each 187 and 190
+  // us, 64 rows 243 and 192; 64 experts, K = 2048, N = 1024, 24 rows 35.2 and 45.1, 48 rows 45.3 and 45.1.
+  if (z.R >= 48 * static_cast<int64_t>(z.E))
     return from_cuda(launch_fp8_pair(operand(*a), operand(*w), g, (z.R < z.E ? z.R : z.E) + z.R / 256, K_FP8_GROUPED_PAIR,
                                      static_cast<cudaStream_t>(stream)));
   return from_cuda(launch_fp8_tile(operand(*a), nullptr, operand(*w), g, z.R, blocks < z.mblocks_max ? blocks : z.mblocks_max,

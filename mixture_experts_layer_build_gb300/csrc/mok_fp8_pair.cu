@@ -206,6 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();  // the peer's barriers exist before anything arrives on them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // (roles in one branch with their setmaxnreg: only then does the compiler give the drain code its registers)
   if (warp < kDrain) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kLow));
   if (warp == 0) {
@@ -525,6 +526,12 @@ int launch_pair(const PairMaps& maps, const PairArgs& a, int kind, cudaStream_t 
   static DeviceOnce once;
   const int se = once.run([](int* d) { return static_cast<int>(cudaGetDevice(d)); },
                           [] {
+                            // what setmaxnreg hands round must be what the launch has: a wait for more would not end
+                            cudaFuncAttributes f;
+                            const cudaError_t e = cudaFuncGetAttributes(&f, fp8_pair_kernel<BN, COLVEC>);
+                            if (e != cudaSuccess) return static_cast<int>(e);
+                            if (f.numRegs * kThreads < 128 * C::kLow + 256 * C::kHigh)
+                              return static_cast<int>(cudaErrorInvalidConfiguration);
                             return static_cast<int>(cudaFuncSetAttribute(fp8_pair_kernel<BN, COLVEC>,
                                                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                                          static_cast<int>(C::kSmem)));
