@@ -225,7 +225,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     pdl_wait();
-    pdl_trigger();
     int st = 0, issued = 0, slot = 0;
     uint32_t ph = 0;
     bool ok = true;
