@@ -250,12 +250,13 @@ def _code_only(text: str) -> bytes:
 
 def src_hash() -> str:
     """Hash of the CUDA sources of the layer kernels and the ABI header (code only), keying the
-    stored ncu counters (all of them belong to layer kernels; the router's and the dense operators' files are
-    left out)."""
+    stored ncu counters (all of them belong to layer kernels; the files of the router, the dense operators, the routed
+    rows and the 8-bit products are left out)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "mixture_experts_layer_build_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.endswith((".cu", ".cuh")) and not f.startswith(("mok_router", "mok_norm", "mok_philox", "mok_ffn")):
+        if f.endswith((".cu", ".cuh")) and not f.startswith(
+                ("mok_router", "mok_norm", "mok_philox", "mok_ffn", "mok_stage", "mok_route", "mok_fp8")):
             h.update(_code_only(open(os.path.join(csrc, f)).read()))
     h.update(_code_only(open(os.path.join(ROOT, "include", "mok.h")).read()))
     return h.hexdigest()[:16]
