@@ -587,9 +587,9 @@ MOK_API mok_status mok_combine_backward(const mok_schedule* sched, const void* r
  * Quantisation: t = max(amax of the block, 2^-50); scale = t / 448; code = E4M3(v * (448 / t)), round to nearest
  * even; both divisions and the product are rounded to fp32.  A block that holds a NaN or an infinity gets a NaN scale
  * and codes 0x7F (NaN).
- * A product adds up each block of 128 exactly scaled: fp32 sums of a block's E4M3 products, each times the two scales'
- * fp32 product, added in fp32 in ascending order of the blocks.  (Scales of 128 x 1e38 multiply to infinity: the two
- * matrices' largest magnitudes may multiply to at most 6e43.)
+ * A product takes the fp32 sum of each K block's E4M3 products times the two scales' fp32 product, and adds these up in
+ * fp32 in ascending order of the blocks; where there are few tiles, in up to 8 runs of consecutive blocks that are then added
+ * in order.  (The product of two blocks' scales has to be in fp32's range: their largest magnitudes may multiply to 6e43.)
  * ------------------------------------------------------------------------------------------- */
 typedef enum { MOK_FP8_ROWS = 0, MOK_FP8_BLOCKS = 1 } mok_fp8_scaling;
 typedef struct {

@@ -12,7 +12,11 @@
 // swizzled shared memory: a launch less, and its latency under the weights'.
 //
 // With few tiles their K range is split over a cluster, whose CTAs add up their partials through shared memory in rank
-// order.
+// order.  Up to 32 columns two CTAs share an SM: clusters of eight, of which 15 fit at one CTA per SM, then fit twice as often.
+//
+// The weights' bytes and the latencies of a start, a load, a chain of K blocks and a reduction bound it.  Measured: one row at
+// N = 2048, K = 7168 6.1 us with its quantisation (14.7 MB: 2.2), 61 rows at N = 7168, K = 2048 7.0, 128 rows 8.9; one token's eight
+// experts of 1536 x 4096 9.2 us (50 MB: 7.4); 128 experts of them with 8 rows each 125 (119).
 #include "mok_ffn.cuh"  // warp_wait, wait_landed, elect_one
 #include "mok_fp8.cuh"
 #include "mok_fp8_gemm.cuh"

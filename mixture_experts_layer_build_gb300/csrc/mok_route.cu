@@ -5,7 +5,9 @@
 //   combine             out[t] = sum_k s[t,k] rows[inv[t,k]]                  (the layer's combine kernel)
 //   combine, backward   drows[inv[t,k]] = s[t,k] dout[t], 0 on padding; ds[t,k] = <dout[t], rows[inv[t,k]]>
 //
-// All of them move each row once: bound by HBM.
+// All of them move each row once: bound by HBM.  Measured at T = 8192, K = 8, E = 128, width 4096: combine 101 us (5,950 GB/s),
+// its backward 202 (1.14 GB that it cannot do without, and 67 MB of zeroed padding: 5,980 GB/s); combine of 4096 tokens, K = 6,
+// width 2048 20.9 us (5,640).
 #include "mok_internal.cuh"
 #include "mok_ptx.cuh"
 #include "mok_route.cuh"
