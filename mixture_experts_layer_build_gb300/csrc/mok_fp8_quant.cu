@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kQThreads) fp8_dispatch_kernel(const uint16_t*
   for (int64_t item = warp; item < T * chunks; item += nwarps) {
     const int64_t t = item / chunks;
     const int c0 = static_cast<int>(item - t * chunks) * 1024 + lane * 16;
+    int row = lane < K ? __ldg(inv + t * K + lane) : -1;  // of the first 32 slots, beside the loads of x
     uint4 v[2][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kQThreads) fp8_dispatch_kernel(const uint16_t*
       }
     }
     for (int k0 = 0; k0 < K; k0 += 32) {
-      const int row = k0 + lane < K ? __ldg(inv + t * K + k0 + lane) : -1;
+      if (k0) row = k0 + lane < K ? __ldg(inv + t * K + k0 + lane) : -1;
       for (unsigned live = __ballot_sync(0xffffffffu, row >= 0); live; live &= live - 1) {
         const int64_t r = __shfl_sync(0xffffffffu, row, __ffs(live) - 1);
 #pragma unroll

@@ -88,8 +88,9 @@ __device__ __forceinline__ bool fp8_tile(const Fp8Problem& g, int u, int bn, Til
     return true;
   }
   // one 128-row block of an expert's rows, against a tile of its weights
-  if (rest >= __ldg(g.meta + 2)) return false;
+  const int blocks = __ldg(g.meta + 2);  // (both loads at once: the table has an entry for every CTA of the grid)
   const int4 b = __ldg(reinterpret_cast<const int4*>(g.mblocks) + rest);  // {expert, first row, valid rows, tile}
+  if (rest >= blocks) return false;
   t.batch = b.x;
   t.i0 = pt * 128;
   t.p0 = b.x * g.p_rows + t.i0;
