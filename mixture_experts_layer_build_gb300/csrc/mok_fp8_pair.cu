@@ -1,6 +1,6 @@
 // mok_fp8_pair.cu -- 8-bit products with a scale per 128 values for many rows: persistent CTA pairs.
 //
-// A cluster of two CTAs computes 256 x BN tiles with tcgen05.mma.cta_group::2: each CTA loads its own 128 rows of P and half
+// A cluster of two CTAs computes 256 x BN tiles (BN 256 or 128, of row-scaled products 192 as well) with tcgen05.mma.cta_group::2: each CTA loads its own 128 rows of P and half
 // of Q's rows, 32 KB per K block of 128 of a 256 x 256 tile.  The scales belong to whole K blocks, so every block's
 // products go to a TMEM accumulator of their own, one of 512 / BN in turn; eight warps per CTA drain it, two per TMEM lane
 // quarter with half of the columns each, times the block's scales into fp32 registers (BN / 2 per thread), while the
@@ -60,10 +60,21 @@ __device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
+// The same for 32 columns.
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 template <int BN, bool COLVEC>
 struct Cfg {
-  static constexpr int kLow = BN == 256 ? 56 : 72, kHigh = BN == 256 ? 224 : 216;  // registers per thread
   static constexpr int HB = BN / 2;      // columns of a drain thread
+  static constexpr int kLow = BN == 256 ? 56 : 72, kHigh = BN == 256 ? 224 : 216;  // registers per thread
+  static_assert(COLVEC || HB == 64 || HB == 128, "a thread's columns are in one block of 128");
+  static constexpr int kBox = HB % 64 == 0 ? 64 : 32;  // columns of a box of bf16 output (128 or 64 bytes)
   static constexpr int kAccs = 512 / BN; // accumulators in TMEM
   static constexpr uint32_t kQBytes = HB * 128, kStage = 16384 + kQBytes, kTx = 2 * kStage;
   static constexpr uint32_t kStaging = 4096;     // per drain warp: a box of 32 rows x 128 bytes
@@ -347,46 +358,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty(b), 0));
         };
-        // chunks of 32 registers, the next one on its way while this one is added
-        uint32_t v[2][32];
+        // chunks, the next one on its way while this one is added
         if constexpr (COLVEC) {
           // a thread holds 4 rows x HB / 4 columns, so that it needs few of the column scales (all of them, for a row per
           // thread, are 1024 cycles of shared memory per block: 8192 x 8192 x 8192 588 us)
+          constexpr int kW = HB % 64 == 0 ? 64 : 32, kChunks = 2 * HB / kW;  // 16 lanes x kW columns, lanes first
+          uint32_t v[2][kW / 2];
           const float* cs = sc + 128 + h * HB + (lane & 3) * 2;
           float rs[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) rs[i] = sc[q * 32 + (lane >> 2) + 8 * i];
-          constexpr int kChunks = HB / 32;  // 16 lanes x 64 columns, lanes first
-          auto load = [&](int i, uint32_t(&x)[32]) {
-            tmem_ld_16x256b_x8(lanes + (static_cast<uint32_t>(i & 1) * 16u << 16) + b * BN + (i >> 1) * 64, x);
+          auto load = [&](int i, uint32_t(&x)[kW / 2]) {
+            const uint32_t at = lanes + (static_cast<uint32_t>(i & 1) * 16u << 16) + b * BN + (i >> 1) * kW;
+            if constexpr (kW == 64) tmem_ld_16x256b_x8(at, x);
+            else tmem_ld_16x256b_x4(at, x);
           };
           load(0, v[0]);
-          float2 y[8];
+          float2 y[kW / 8];
 #pragma unroll
           for (int i = 0; i < kChunks; ++i) {
             if (!(i & 1)) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = *reinterpret_cast<const float2*>(cs + (i >> 1) * 64 + k * 8);
+              for (int k = 0; k < kW / 8; ++k) y[k] = *reinterpret_cast<const float2*>(cs + (i >> 1) * kW + k * 8);
             }
-            uint32_t(&x)[32] = v[i & 1];
+            uint32_t(&x)[kW / 2] = v[i & 1];
             tmem_ld_wait_for(x);
             if (i + 1 < kChunks) load(i + 1, v[(i + 1) & 1]);
             else release();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < kW / 8; ++k)
 #pragma unroll
               for (int o = 0; o < 2; ++o) {
                 float f0, f1;
                 const float s = rs[(i & 1) * 2 + o];
                 mul_f32x2(f0, f1, s, s, y[k].x, y[k].y);
-                float(&to)[HB] = acc;
-                const int at = i * 32 + k * 4 + o * 2;
-                fma_f32x2(to[at], to[at + 1], __uint_as_float(x[k * 4 + o * 2]), __uint_as_float(x[k * 4 + o * 2 + 1]), f0, f1,
-                          to[at], to[at + 1]);
+                const int at = i * (kW / 2) + k * 4 + o * 2;
+                fma_f32x2(acc[at], acc[at + 1], __uint_as_float(x[k * 4 + o * 2]), __uint_as_float(x[k * 4 + o * 2 + 1]), f0, f1,
+                          acc[at], acc[at + 1]);
               }
           }
         } else {
           const float s = sc[q * 32 + lane] * __shfl_sync(0xffffffffu, q_now, kb % 32);
+          uint32_t v[2][32];
           tmem_ld_32x32b_x32(lanes + b * BN, v[0]);
 #pragma unroll
           for (int c = 0; c < HB; c += 32) {
@@ -403,10 +416,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // The tile's 32 rows of this warp.  Where all of them are there: through shared memory, a box of 32 rows x 128 bytes
-      // at a time (in the 128-byte TMA swizzle: 16-byte chunk k of row r at k ^ (r & 7)); else straight from the registers.
+      // at a time (in the 128-byte TMA swizzle: 16-byte chunk k of row r at k ^ (r & 7); bf16 boxes of 32 columns in the 64-byte
+      // one, k ^ (r >> 1 & 3)); else straight from the registers.
       const int row0 = w.row0 + rank * 128 + q * 32;
       if (row0 >= w.row_end) continue;
       const bool boxes = row0 + 32 <= w.row_end;
+      auto bf16_at = [&](int r, int k) {  // chunk k of row r
+        return static_cast<uint32_t>(C::kBox == 64 ? r * 128 + ((k ^ (r & 7)) << 4) : r * 64 + ((k ^ (r >> 1 & 3)) << 4));
+      };
       auto begin = [&] {
         if (lane == 0) bulk_wait_read<0>();  // what was stored from here before has been read
         __syncwarp();
@@ -421,77 +438,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       if constexpr (COLVEC) {
         const int fr = lane >> 2, fc = lane & 3;  // row of the thread's first; its pair of columns in 8
-        if (boxes) {
-          constexpr int kPairs = 8;  // groups of 8 columns in 64
+        constexpr int kW = HB % 64 == 0 ? 64 : 32;
+        auto value = [&](int c, int o) {  // the thread's pair of columns in the 8 from c on, row fr + 8 o
+          return &acc[(c / kW * 2 + (o >> 1)) * (kW / 2) + c % kW / 8 * 4 + (o & 1) * 2];
+        };
+        if (boxes && !g.out_f32) {
 #pragma unroll
-          for (int i = 0; i < HB; i += 64) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {  // fp32: two boxes of 32 columns
-              if (half && !g.out_f32) continue;
-              const int c0 = j0 + i + half * 32;
-              if (c0 >= g.q_rows) continue;
-              begin();
-#pragma unroll
-              for (int o = 0; o < 4; ++o) {  // rows fr + 8 o
-                const int r = fr + 8 * o;
-                const uint32_t at = stage + static_cast<uint32_t>(r) * 128u;
-#pragma unroll
-                for (int k = 0; k < kPairs; ++k) {
-                  const float* x = &acc[(i / 32 + (o >> 1)) * 32 + k * 4 + (o & 1) * 2];
-                  if (!g.out_f32) {
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + static_cast<uint32_t>((k ^ (r & 7)) * 16 + fc * 4)),
-                                 "r"(pack_bf16x2(x[0], x[1]))
-                                 : "memory");
-                  } else if ((k >= 4) == (half == 1)) {
-                    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(
-                                     at + static_cast<uint32_t>((((k & 3) * 2 + (fc >> 1)) ^ (r & 7)) * 16 + (fc & 1) * 8)),
-                                 "f"(x[0]), "f"(x[1])
-                                 : "memory");
-                  }
-                }
-              }
-              send(c0);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < HB; i += 64)
+          for (int i = 0; i < HB; i += C::kBox) {
+            if (j0 + i >= g.q_rows) continue;
+            begin();
 #pragma unroll
             for (int o = 0; o < 4; ++o)
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int row = row0 + fr + 8 * o, col = j0 + i + k * 8 + fc * 2;
-                if (row >= w.row_end || col >= g.q_rows) continue;
-                const float* x = &acc[(i / 32 + (o >> 1)) * 32 + k * 4 + (o & 1) * 2];
-                const int64_t at = static_cast<int64_t>(row) * g.ldo + col;
-                if (g.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(g.out) + at) = make_float2(x[0], x[1]);
-                else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(g.out) + at) = pack_bf16x2(x[0], x[1]);
+              for (int k = 0; k < C::kBox / 8; ++k) {
+                const float* x = value(i + k * 8, o);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage + bf16_at(fr + 8 * o, k) + fc * 4),
+                             "r"(pack_bf16x2(x[0], x[1]))
+                             : "memory");
               }
+            send(j0 + i);
+          }
+        } else if (boxes) {
+#pragma unroll
+          for (int i = 0; i < HB; i += 32) {
+            if (j0 + i >= g.q_rows) continue;
+            begin();
+#pragma unroll
+            for (int o = 0; o < 4; ++o)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float* x = value(i + k * 8, o);
+                const int r = fr + 8 * o;
+                asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(
+                                 stage + static_cast<uint32_t>(r * 128 + ((k * 2 + (fc >> 1)) ^ (r & 7)) * 16 + (fc & 1) * 8)),
+                             "f"(x[0]), "f"(x[1])
+                             : "memory");
+              }
+            send(j0 + i);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < HB; i += 8)
+#pragma unroll
+            for (int o = 0; o < 4; ++o) {
+              const int row = row0 + fr + 8 * o, col = j0 + i + fc * 2;
+              if (row >= w.row_end || col >= g.q_rows) continue;
+              const float* x = value(i, o);
+              const int64_t at = static_cast<int64_t>(row) * g.ldo + col;
+              if (g.out_f32) *reinterpret_cast<float2*>(static_cast<float*>(g.out) + at) = make_float2(x[0], x[1]);
+              else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(g.out) + at) = pack_bf16x2(x[0], x[1]);
+            }
         }
       } else if (boxes) {
-        const uint32_t at = stage + static_cast<uint32_t>(lane) * 128u;
-        auto box = [&](const uint32_t(&x)[32], int c0) {
-          if (c0 >= g.q_rows) return;
-          begin();
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            st_shared_v4(at + (static_cast<uint32_t>(k ^ (lane & 7)) << 4), make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]));
-          send(c0);
-        };
-        uint32_t x[32];
         if (!g.out_f32) {
 #pragma unroll
-          for (int c = 0; c < HB; c += 64) {
+          for (int c = 0; c < HB; c += C::kBox) {
+            if (j0 + c >= g.q_rows) continue;
+            begin();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = pack_bf16x2(acc[c + 2 * k], acc[c + 2 * k + 1]);
-            box(x, j0 + c);
+            for (int k = 0; k < C::kBox / 8; ++k) {
+              const float* x = &acc[c + 8 * k];
+              st_shared_v4(stage + bf16_at(lane, k), make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                                pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])));
+            }
+            send(j0 + c);
           }
         } else {
 #pragma unroll
           for (int c = 0; c < HB; c += 32) {
+            if (j0 + c >= g.q_rows) continue;
+            begin();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(acc[c + k]);
-            box(x, j0 + c);
+            for (int k = 0; k < 8; ++k) {
+              const float* x = &acc[c + 4 * k];
+              st_shared_v4(stage + static_cast<uint32_t>(lane * 128 + ((k ^ (lane & 7)) << 4)),
+                           make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])));
+            }
+            send(j0 + c);
           }
         }
       } else if (row0 + lane < w.row_end) {
@@ -569,9 +592,14 @@ int pair_width(const Fp8Operand& p, const Fp8Operand& q, PairArgs a, int64_t out
       make_tmap_fp8(&m.p, p.q, static_cast<uint64_t>(p.cols), static_cast<uint64_t>(p.rows), static_cast<uint64_t>(p.ld), 128) &&
       make_tmap_fp8(&m.q, q.q, static_cast<uint64_t>(q.cols), static_cast<uint64_t>(q.rows) * q.batch,
                     static_cast<uint64_t>(q.ld), BN / 2) &&
-      (g.out_f32 ? make_tmap_f32(&m.out, g.out, N, R, 32, 32) : make_tmap_bf16(&m.out, g.out, N, R, 64, 32));
+      (g.out_f32      ? make_tmap_f32(&m.out, g.out, N, R, 32, 32)
+       : BN / 2 % 64 ? make_tmap_bf16_sw64(&m.out, g.out, N, R, 32, 32)
+                     : make_tmap_bf16(&m.out, g.out, N, R, 64, 32));
   if (!good) return static_cast<int>(cudaErrorInvalidValue);
-  return q.row_scales ? launch_pair<BN, true>(m, a, kind, stream) : launch_pair<BN, false>(m, a, kind, stream);
+  if constexpr (BN != 192) {
+    if (!q.row_scales) return launch_pair<BN, false>(m, a, kind, stream);
+  }
+  return launch_pair<BN, true>(m, a, kind, stream);
 }
 
 }  // namespace
@@ -592,14 +620,18 @@ int launch_fp8_pair(const Fp8Operand& p, const Fp8Operand& q, Fp8Problem g, int6
   a.pairs = pairs;
   const int64_t mats = g.mode == FP8_WGRAD ? g.experts : 1;
   const int64_t out_rows = p.rows * mats;
-  // The tile width of fewer rounds of tiles, a round as long as its K blocks (440 ns of 256 columns, 310 of 128) and 1 us
-  // besides.  A schedule's rows count as spread evenly, a weight gradient's K likewise.
+  // The tile width of fewest rounds of tiles, a round as long as its K blocks and 1 us besides.  (192 columns in row-scaled
+  // products only: with a scale per 128 x 128 values a block takes 420 ns of 192, hardly less than of 256.  1536 x 4096 over
+  // 8192: 82.8 us in tiles of 256, 69.5 of 192, 81.9 of 128.)  A schedule's rows count as spread evenly, a weight gradient's
+  // K likewise.
   const int64_t k = g.mode == FP8_WGRAD ? (g.k_blocks + g.experts - 1) / g.experts : g.k_blocks;
   auto cost = [&](int bn, int64_t ns) {
     const int64_t tiles = static_cast<int64_t>(g.p_tiles) * ((q.rows + bn - 1) / bn) * mats;
     return (tiles + pairs - 1) / pairs * (k * ns + 1000);
   };
-  if (cost(256, 440) <= cost(128, 310)) return pair_width<256>(p, q, a, out_rows, kind, stream);
+  const int64_t wide = cost(256, q.row_scales ? 615 : 450), narrow = cost(128, q.row_scales ? 400 : 310);
+  if (q.row_scales && cost(192, 490) < (wide < narrow ? wide : narrow)) return pair_width<192>(p, q, a, out_rows, kind, stream);
+  if (wide <= narrow) return pair_width<256>(p, q, a, out_rows, kind, stream);
   return pair_width<128>(p, q, a, out_rows, kind, stream);
 }
 
