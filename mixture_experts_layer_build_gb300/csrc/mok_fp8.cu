@@ -18,6 +18,13 @@ bool matrix_ok(const mok_fp8_matrix* m, int32_t batch) {
   return m->rows == 0 || m->cols == 0 || (ok16(m->q) && ok16(m->s));
 }
 
+// Whether an output of n bytes overlaps neither codes nor scales of a matrix.
+bool apart_from(const mok_fp8_matrix& m, const void* out, int64_t n) {
+  const int64_t scales = m.scaling == MOK_FP8_ROWS ? fp8_blocks(m.cols) * fp8_pitch(m.rows)
+                                                   : fp8_blocks(m.cols) * fp8_blocks(m.rows) * m.batch;
+  return apart(m.q, m.rows * m.ld * m.batch, out, n) && apart(m.s, scales * 4, out, n);
+}
+
 Fp8Operand operand(const mok_fp8_matrix& m) {
   return {m.q, m.s, m.rows, m.cols, m.ld, m.batch, m.scaling == MOK_FP8_ROWS};
 }
@@ -54,11 +61,11 @@ mok_status mok_fp8_matmul(const mok_fp8_matrix* a, const mok_fp8_matrix* b, void
   if (!matrix_ok(a, 1) || !matrix_ok(b, 1) || a->scaling != MOK_FP8_ROWS || a->cols != b->cols) return MOK_ERR_INVALID_ARG;
   if (b->rows < 8 || b->rows % 8 != 0 || (out_type != MOK_DT_BF16 && out_type != MOK_DT_FP32)) return MOK_ERR_INVALID_ARG;
   if (a->rows == 0) return MOK_OK;
-  if (!ok16(out)) return MOK_ERR_INVALID_ARG;
+  const int64_t bytes = a->rows * b->rows * (out_type == MOK_DT_FP32 ? 4 : 2);
+  if (!ok16(out) || !apart_from(*a, out, bytes) || !apart_from(*b, out, bytes)) return MOK_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->cols == 0)
-    return from_cuda(static_cast<int>(cudaMemsetAsync(
-        out, 0, static_cast<size_t>(a->rows) * b->rows * (out_type == MOK_DT_FP32 ? 4 : 2), s)));
+    return from_cuda(static_cast<int>(cudaMemsetAsync(out, 0, static_cast<size_t>(bytes), s)));
   return product(*a, nullptr, *b, out, out_type, false, status, s);
 }
 
@@ -74,7 +81,8 @@ mok_status mok_fp8_linear(const void* x, int64_t M, const mok_fp8_matrix* w, voi
   if (M < 0 || M > kMax || !matrix_ok(w, 1) || w->scaling != MOK_FP8_BLOCKS) return MOK_ERR_INVALID_ARG;
   if (w->rows < 8 || w->rows % 8 != 0 || w->cols < 8 || w->cols % 8 != 0) return MOK_ERR_INVALID_ARG;
   if (M == 0) return MOK_OK;
-  if (!ok16(x) || !ok16(out)) return MOK_ERR_INVALID_ARG;
+  const int64_t bytes = M * w->rows * 2;
+  if (!ok16(x) || !ok16(out) || !apart(x, M * w->cols * 2, out, bytes) || !apart_from(*w, out, bytes)) return MOK_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   mok_fp8_matrix a{};
   a.rows = M;
@@ -106,7 +114,8 @@ mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matri
   if (a->rows != z.rpad_max || a->cols != w->cols || w->cols < 8 || w->rows < 8 || w->rows % 8 != 0)
     return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return MOK_OK;
-  if (!ok16(out)) return MOK_ERR_INVALID_ARG;
+  const int64_t bytes = a->rows * w->rows * 2;
+  if (!ok16(out) || !apart_from(*a, out, bytes) || !apart_from(*w, out, bytes)) return MOK_ERR_INVALID_ARG;
   Fp8Problem g{};
   g.mode = FP8_GROUPED;
   g.k_blocks = static_cast<int32_t>(fp8_blocks(a->cols));
@@ -141,9 +150,9 @@ mok_status mok_fp8_grouped_wgrad(const mok_schedule* sched, const mok_fp8_matrix
   if ((dw_type != MOK_DT_BF16 && dw_type != MOK_DT_FP32) || !ok16(dw)) return MOK_ERR_INVALID_ARG;
   if (a->rows * z.E > kMax) return MOK_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (z.T == 0)
-    return from_cuda(static_cast<int>(cudaMemsetAsync(
-        dw, 0, static_cast<size_t>(z.E) * a->rows * b->rows * (dw_type == MOK_DT_FP32 ? 4 : 2), s)));
+  const int64_t bytes = static_cast<int64_t>(z.E) * a->rows * b->rows * (dw_type == MOK_DT_FP32 ? 4 : 2);
+  if (!apart_from(*a, dw, bytes) || !apart_from(*b, dw, bytes)) return MOK_ERR_INVALID_ARG;
+  if (z.T == 0) return from_cuda(static_cast<int>(cudaMemsetAsync(dw, 0, static_cast<size_t>(bytes), s)));
   Fp8Problem g{};
   g.mode = FP8_WGRAD;
   g.k_blocks = static_cast<int32_t>(fp8_blocks(z.rpad_max));

@@ -329,6 +329,10 @@ mok_status outputs_ok(const void* q, const void* s, const void* qt, const void* 
   if ((q && (!ok16(q) || !ok16(s))) || (qt && (!ok16(qt) || !ok16(st)))) return MOK_ERR_INVALID_ARG;
   return MOK_OK;
 }
+// Whether the codes of `rows` x `cols` values (of each of `batch`) spare x's n bytes.
+bool spare(const void* x, int64_t n, int64_t batch, int64_t rows, int64_t cols, const void* q, const void* qt) {
+  return apart(x, n, q, batch * rows * fp8_ld(cols)) && apart(x, n, qt, batch * cols * fp8_ld(rows));
+}
 }  // namespace
 
 extern "C" {
@@ -341,6 +345,7 @@ mok_status mok_fp8_quantize(const void* x, int64_t rows, int32_t cols, uint8_t* 
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
   const mok_status rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
+  if (!spare(x, rows * cols * 2, 1, rows, cols, q, qt)) return MOK_ERR_INVALID_ARG;
   const Fp8Source src{static_cast<const uint16_t*>(x), nullptr, nullptr, nullptr, rows, 1, 0};
   return launch_fp8_quantize(src, rows, cols, q, s, qt, st, K_FP8_QUANTIZE, static_cast<cudaStream_t>(stream)) ? MOK_ERR_CUDA
                                                                                                              : MOK_OK;
@@ -357,6 +362,7 @@ mok_status mok_fp8_quantize_routed(const mok_schedule* sched, int32_t gather, co
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
   rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
+  if (!spare(x, (gather ? z.T : z.rpad_max) * cols * 2, 1, z.rpad_max, cols, q, qt)) return MOK_ERR_INVALID_ARG;
   const Fp8Source src{static_cast<const uint16_t*>(x), sched->row_token, sched->meta, sched->inv, z.T, z.K, gather};
   return launch_fp8_quantize(src, z.rpad_max, cols, q, s, qt, st, gather ? K_FP8_DISPATCH : K_FP8_QUANTIZE,
                              static_cast<cudaStream_t>(stream))
@@ -372,6 +378,7 @@ mok_status mok_fp8_quantize_blocks(const void* x, int32_t batch, int64_t rows, i
   if ((!q && !qt) || (q != nullptr) != (s != nullptr) || (qt != nullptr) != (st != nullptr)) return MOK_ERR_INVALID_ARG;
   const mok_status rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
+  if (!spare(x, batch * rows * cols * 2, batch, rows, cols, q, qt)) return MOK_ERR_INVALID_ARG;
   QuantArgs p{};
   p.src.x = static_cast<const uint16_t*>(x);
   p.rows = rows;

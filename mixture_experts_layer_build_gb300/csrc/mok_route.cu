@@ -132,6 +132,9 @@ namespace {
 bool ok16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 mok_status from_cuda(int rc) { return rc == 0 ? MOK_OK : MOK_ERR_CUDA; }
 constexpr int32_t kMaxWidth = kMaxVecs * kRouteThreads * 8;  // 16384
+// Bytes of a bf16 tensor of tokens, and of routed rows.
+int64_t token_bytes(const Sizes& z, int32_t w) { return z.T * w * 2; }
+int64_t row_bytes(const Sizes& z, int32_t w) { return z.rpad_max * w * 2; }
 bool width_ok(int32_t w) { return w >= 8 && w % 8 == 0 && w <= kMaxWidth; }
 }  // namespace
 }  // namespace mok
@@ -146,7 +149,7 @@ mok_status mok_dispatch(const mok_schedule* sched, const void* x, int32_t width,
   if (rc != MOK_OK) return rc;
   if (!width_ok(width)) return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return MOK_OK;
-  if (!ok16(x) || !ok16(rows)) return MOK_ERR_INVALID_ARG;
+  if (!ok16(x) || !ok16(rows) || !apart(x, token_bytes(z, width), rows, row_bytes(z, width))) return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_gather_rows(plain_rows(x), sched->inv, sched->row_token, sched->meta, z.T, z.K, z.rpad_max, width,
                                       static_cast<uint16_t*>(rows), K_DISPATCH, static_cast<cudaStream_t>(stream)));
 }
@@ -157,7 +160,7 @@ mok_status mok_dispatch_backward(const mok_schedule* sched, const void* drows, i
   if (rc != MOK_OK) return rc;
   if (!width_ok(width)) return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return MOK_OK;
-  if (!ok16(drows) || !ok16(dx)) return MOK_ERR_INVALID_ARG;
+  if (!ok16(drows) || !ok16(dx) || !apart(dx, token_bytes(z, width), drows, row_bytes(z, width))) return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_combine(static_cast<const uint16_t*>(drows), sched->inv, nullptr, z.T, z.K, width,
                                   static_cast<uint16_t*>(dx), K_DISPATCH_BWD, static_cast<cudaStream_t>(stream)));
 }
@@ -169,6 +172,7 @@ mok_status mok_combine(const mok_schedule* sched, const void* rows, int32_t widt
   if (!width_ok(width)) return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return MOK_OK;
   if (!ok16(rows) || !ok16(out) || !sched->topk_weights) return MOK_ERR_INVALID_ARG;
+  if (!apart(out, token_bytes(z, width), rows, row_bytes(z, width))) return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_combine(static_cast<const uint16_t*>(rows), sched->inv, sched->topk_weights, z.T, z.K, width,
                                   static_cast<uint16_t*>(out), K_ROUTE_COMBINE, static_cast<cudaStream_t>(stream)));
 }
@@ -181,6 +185,11 @@ mok_status mok_combine_backward(const mok_schedule* sched, const void* rows, con
   if (!width_ok(width)) return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return MOK_OK;
   if (!ok16(rows) || !ok16(dout) || !ok16(drows) || !d_topk_weights || !sched->topk_weights) return MOK_ERR_INVALID_ARG;
+  const int64_t nr = row_bytes(z, width), nt = token_bytes(z, width), nw = z.R * 4;
+  if ((drows != rows && !apart(drows, nr, rows, nr)) || !apart(drows, nr, dout, nt) || !apart(d_topk_weights, nw, rows, nr) ||
+      !apart(d_topk_weights, nw, dout, nt) || !apart(d_topk_weights, nw, drows, nr) ||
+      !apart(d_topk_weights, nw, sched->topk_weights, nw))
+    return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_combine_backward(z, *sched, rows, dout, width, drows, d_topk_weights,
                                            static_cast<cudaStream_t>(stream)));
 }

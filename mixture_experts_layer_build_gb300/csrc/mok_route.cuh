@@ -7,4 +7,10 @@ namespace mok {
 // The sizes of a schedule with or without the layer's staging; MOK_OK when its tables are there.
 mok_status routed_sizes(const mok_schedule* s, Sizes* z);
 
+// Whether two ranges of device memory have no byte in common (null: nothing there).
+inline bool apart(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return !a || !b || na <= 0 || nb <= 0 || x + static_cast<uintptr_t>(na) <= y || y + static_cast<uintptr_t>(nb) <= x;
+}
+
 }  // namespace mok

@@ -49,6 +49,9 @@ def test_products(mok):
     assert f(good, good, dt=2) == BAD and f(good, good, out=None) == BAD and f(good, good, out=264) == BAD
     assert mok._lib.mok_fp8_matmul(None, ctypes.byref(good), 256, 0, None, None) == BAD
     assert f(m(rows=0), good) == OK  # nothing to do
+    b = m(q=1 << 20, s=2 << 20)
+    for out in (256, 256 + 32 * 64 - 16, (1 << 20) + 16, (2 << 20) - 16):  # over a's codes, their end, b's codes, b's scales
+        assert f(m(q=256, s=4096), b, out=out, dt=1) == BAD
 
 
 def test_linear(mok):
@@ -60,7 +63,8 @@ def test_linear(mok):
     assert f(256, 100, matrix(mok, cols=60, block=True), 256, 256, 1 << 20) == BAD
     assert f(None, 100, w, 256, 256, 1 << 20) == BAD and f(256, 100, w, 264, 256, 1 << 20) == BAD
     assert f(256, 100, w, 256, None, 1 << 20) == BAD and f(256, 100, w, 256, 272, 1 << 20) == BAD
-    assert f(256, 100, w, 256, 256, size(100, 64) - 1) == SMALL
+    assert f(256, 100, matrix(mok, block=True, q=1 << 22, s=1 << 23), 1 << 24, 256, size(100, 64) - 1) == SMALL
+    assert f(256, 4, w, 256, 256, 1 << 20) == BAD and f(256, 4, w, 256 + 4 * 128 - 16, 256, 1 << 20) == BAD  # out over x
     assert f(256, -1, w, 256, 256, 1 << 20) == BAD and f(None, 0, w, None, None, 0) == OK
 
 
@@ -73,6 +77,7 @@ def test_quantisation(mok):
     assert q(256, 4, 64, 256, 260, None, None, None) == BAD
     assert q(256, 65535 * 128 + 1, 64, 256, 256, None, None, None) == UNSUPPORTED
     assert q(None, 0, 64, None, None, None, None, None) == OK
+    assert q(256, 4, 64, 512, 8192, None, None, None) == BAD and q(256, 4, 64, None, None, 256 + 496, 8192, None) == BAD  # over x
     b = mok._lib.mok_fp8_quantize_blocks
     for batch, rows, cols in ((0, 64, 64), (1, 60, 64), (1, 64, 4), (1, 0, 64)):
         assert b(256, batch, rows, cols, 256, 256, None, None, None) == BAD
@@ -88,6 +93,13 @@ def test_routed_rows(mok):
             assert f(p, 256, width, 256, None) == BAD
         assert f(p, None, 64, 256, None) == BAD and f(p, 256, 64, 264, None) == BAD and f(None, 256, 64, 256, None) == BAD
     assert L.mok_combine_backward(p, 256, 256, 64, 256, None, None) == BAD
+    big = 1 << 24  # outputs over inputs: dispatch's rows and x, combine's rows and out, drows and rows but for the same buffer
+    n = s.rpad_max * 128
+    assert L.mok_dispatch(p, big + n - 16, 64, big, None) == BAD and L.mok_dispatch_backward(p, big, 64, big + 16, None) == BAD
+    assert L.mok_combine(p, big, 64, big + n - 16, None) == BAD
+    f = L.mok_combine_backward
+    assert f(p, big, 2 * big, 64, big + 16, 3 * big, None) == BAD and f(p, big, 2 * big, 64, 2 * big, 3 * big, None) == BAD
+    assert f(p, big, 2 * big, 64, 4 * big, big + 16, None) == BAD and f(p, big, 2 * big, 64, 4 * big, 256, None) == BAD
     assert L.mok_fp8_quantize_routed(p, 2, 256, 64, 256, 256, None, None, None) == BAD
     rows = s.rpad_max
     a, w = matrix(mok, rows=rows), matrix(mok, rows=16, batch=4, block=True)
