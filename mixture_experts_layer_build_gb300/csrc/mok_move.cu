@@ -556,7 +556,10 @@ int launch_gather_rows(const RowSrc& src, const int32_t* inv, const int32_t* row
                        cudaStream_t stream) {
   if (rpad_max <= 0) return 0;
   const int64_t vecs = H / 8;
-  const int grid = grid_for(T * ((vecs + 127) / 128) + rpad_max / 32, kMoveThreads / 32);
+  // with few tokens the padding rows are what there is to write: a warp each, up to 2048 (16 tokens, K = 8, E = 128, 4096
+  // wide 24.2 us with a warp for 32 rows of rpad_max, 15.2)
+  const int64_t R = T * K, experts = (rpad_max - R) / (kRowTile - 1), pads = (experts < R ? experts : R) * (kRowTile - 1);
+  const int grid = grid_for(T * ((vecs + 127) / 128) + (pads < 2048 ? pads : 2048), kMoveThreads / 32);
   trace_begin(stream, kind);
   uint4* d = reinterpret_cast<uint4*>(dst);
   if (vecs >= 32 * 4)

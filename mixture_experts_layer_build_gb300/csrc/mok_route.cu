@@ -21,24 +21,27 @@ constexpr int kRouteThreads = 256;
 // and for each of the token's slots read the expert's row, write the gradient's, and add up the dot product -- each
 // thread its own columns in ascending order, then a tree over the CTA: one fixed order.  Padding rows are dealt out
 // over all CTAs and zeroed, as in the layer's gather.  With drows in rows' own buffer a thread has read a vector
-// before it writes that vector.
+// before it writes that vector.  `parts` CTAs share a token's slots: with few tokens one by one they are a chain of
+// latencies (16 tokens, K = 8, E = 128, width 4096 31.8 us with one part).
 template <int VECS>
 __global__ void __launch_bounds__(kRouteThreads) combine_backward_kernel(
     const uint4* rows, const uint4* __restrict__ dout, const int32_t* __restrict__ inv, const float* __restrict__ s,
-    const int32_t* __restrict__ row_token, const int32_t* __restrict__ meta, int64_t T, int K, int vecs, uint4* drows,
-    float* __restrict__ ds) {
+    const int32_t* __restrict__ row_token, const int32_t* __restrict__ meta, int64_t T, int K, int parts, int vecs,
+    uint4* drows, float* __restrict__ ds) {
   pdl_wait();
-  __shared__ float part[2][kRouteThreads / 32];
+  __shared__ float warp_dot[2][kRouteThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int buf = 0;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+  for (int64_t i = blockIdx.x; i < T * parts; i += gridDim.x) {
+    const int64_t t = i / parts;
+    const int part = static_cast<int>(i - t * parts), k_end = K * (part + 1) / parts;
     uint4 d[VECS];
 #pragma unroll
     for (int u = 0; u < VECS; ++u) {
       const int c = threadIdx.x + u * kRouteThreads;
       d[u] = c < vecs ? __ldcs(dout + t * vecs + c) : make_uint4(0, 0, 0, 0);
     }
-    for (int k = 0; k < K; ++k) {
+    for (int k = K * part / parts; k < k_end; ++k) {
       const int64_t j = t * K + k;
       const int row = __ldg(inv + j);
       const float w = __ldg(s + j);
@@ -69,12 +72,12 @@ __global__ void __launch_bounds__(kRouteThreads) combine_backward_kernel(
       }
 #pragma unroll
       for (int x = 16; x >= 1; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
-      if (lane == 0) part[buf][warp] = dot;
+      if (lane == 0) warp_dot[buf][warp] = dot;
       __syncthreads();  // (two buffers: a warp that is a slot ahead writes the other one)
       if (threadIdx.x == 0) {
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kRouteThreads / 32; ++i) sum += part[buf][i];
+        for (int w8 = 0; w8 < kRouteThreads / 32; ++w8) sum += warp_dot[buf][w8];
         ds[j] = sum;
       }
       buf ^= 1;
@@ -99,7 +102,11 @@ int launch_combine_backward(const Sizes& z, const mok_schedule& s, const void* r
   const int vecs = width / 8, per = (vecs + kRouteThreads - 1) / kRouteThreads;
   const int sms = sm_count();
   if (sms <= 0) return static_cast<int>(cudaErrorInvalidDevice);
-  const int64_t want = z.T > (z.rpad_max + 255) / 256 ? z.T : (z.rpad_max + 255) / 256;
+  // parts of a token: as many as it takes to have four CTAs per SM, and as it has slots
+  const int64_t parts64 = z.T > 0 ? (4 * static_cast<int64_t>(sms) + z.T - 1) / z.T : 1;
+  const int parts = static_cast<int>(parts64 < z.K ? (parts64 > 0 ? parts64 : 1) : z.K);
+  const int64_t items = z.T * parts, pads = ((z.E < z.R ? z.E : z.R) * 127 + 7) / 8, zero = pads < 4 * sms ? pads : 4 * sms,
+                want = items > zero ? items : zero;  // CTAs: a padding row per warp, up to four of them per SM
   const int grid = static_cast<int>(want < 8 * sms ? want : 8 * sms);
   if (grid <= 0) return 0;
   trace_begin(stream, K_COMBINE_BWD);
@@ -107,7 +114,7 @@ int launch_combine_backward(const Sizes& z, const mok_schedule& s, const void* r
   auto run = [&](auto kernel) {
     e = launch_pdl(kernel, dim3(grid), dim3(kRouteThreads), 0, stream, static_cast<const uint4*>(rows),
                    static_cast<const uint4*>(dout), static_cast<const int32_t*>(s.inv), s.topk_weights,
-                   static_cast<const int32_t*>(s.row_token), static_cast<const int32_t*>(s.meta), z.T, z.K, vecs,
+                   static_cast<const int32_t*>(s.row_token), static_cast<const int32_t*>(s.meta), z.T, z.K, parts, vecs,
                    static_cast<uint4*>(drows), ds);
   };
   if (per <= 1) run(combine_backward_kernel<1>);
