@@ -32,8 +32,9 @@ namespace mok {
 namespace {
 
 // Warpgroup 0: warp 0 loads, warp 1 issues MMAs; warpgroups 1 and 2 drain.  A drain thread of a 256-column tile needs more
-// registers than a third of the SM's: the first group gives up of its own.  128 x 56 + 256 x 224 (and 128 x 72 + 256 x
-// 216) are the 384 x 168 that a launch has.
+// registers than a third of the SM's (168 of 384 threads): the first group gives up of its own.  What the groups have is at
+// most what the launch had: 128 x 72 + 256 x 216 = 384 x 168.  208 for the 256-column tiles: 8192 x 8192 x 8192 409 us, 414 with
+// 224, 453 with 200.
 constexpr int kThreads = 384;
 constexpr int kDrain = 4;  // the first drain warp
 constexpr int kMaxExperts = 1024;
@@ -72,7 +73,7 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
 template <int BN, bool COLVEC>
 struct Cfg {
   static constexpr int HB = BN / 2;      // columns of a drain thread
-  static constexpr int kLow = BN == 256 ? 56 : 72, kHigh = BN == 256 ? 224 : 216;  // registers per thread
+  static constexpr int kLow = 72, kHigh = BN == 256 ? 208 : 216;  // registers per thread
   static_assert(COLVEC || HB == 64 || HB == 128, "a thread's columns are in one block of 128");
   static constexpr int kBox = HB % 64 == 0 ? 64 : 32;  // columns of a box of bf16 output (128 or 64 bytes)
   static constexpr int kAccs = 512 / BN; // accumulators in TMEM
