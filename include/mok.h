@@ -583,8 +583,8 @@ MOK_API mok_status mok_combine_backward(const mok_schedule* sched, const void* r
  *                   first (a tile's rows are read together); the value of (r, c) is q[r][c] s[c/128][r];
  *   MOK_FP8_BLOCKS  a scale per 128 x 128 values, row-major: s [ceil(rows/128)][ceil(cols/128)].
  * Codes are row-major, K (the summed index) along the row, `ld` bytes between rows: a multiple of 16, >= cols.
- * Codes and scales start on a 16-byte boundary; no output may overlap an input (refused).  batch matrices of one shape follow one another: codes batch * rows * ld
- * bytes, scales likewise; every matrix has its own blocks.
+ * Codes and scales start on a 16-byte boundary; no output or workspace may overlap an input (refused).  batch matrices of
+ * one shape follow one another: codes batch * rows * ld bytes, scales likewise; every matrix has its own blocks.
  * Quantisation: t = max(amax of the block, 2^-50); scale = t / 448; code = E4M3(v * (448 / t)), round to nearest
  * even; both divisions and the product are rounded to fp32.  A block that holds a NaN or an infinity gets a NaN scale
  * and codes 0x7F (NaN).

@@ -94,6 +94,8 @@ mok_status mok_fp8_linear(const void* x, int64_t M, const mok_fp8_matrix* w, voi
   if (M <= kFp8XqRows) return product(a, x, *w, out, MOK_DT_BF16, false, status, st);
   if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MOK_ERR_INVALID_ARG;
   if (ws_bytes < mok_fp8_linear_workspace_bytes(M, w->cols)) return MOK_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t used = static_cast<int64_t>(mok_fp8_linear_workspace_bytes(M, w->cols));
+  if (!apart(ws, used, out, bytes) || !apart_from(*w, ws, used)) return MOK_ERR_INVALID_ARG;
   uint8_t* q = static_cast<uint8_t*>(ws);
   float* s = reinterpret_cast<float*>(q + (M * fp8_ld(w->cols) + 255) / 256 * 256);
   const mok_status rc = mok_fp8_quantize(x, M, static_cast<int32_t>(w->cols), q, s, nullptr, nullptr, stream);

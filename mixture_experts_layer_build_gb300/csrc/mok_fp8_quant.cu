@@ -329,9 +329,15 @@ mok_status outputs_ok(const void* q, const void* s, const void* qt, const void* 
   if ((q && (!ok16(q) || !ok16(s))) || (qt && (!ok16(qt) || !ok16(st)))) return MOK_ERR_INVALID_ARG;
   return MOK_OK;
 }
-// Whether the codes of `rows` x `cols` values (of each of `batch`) spare x's n bytes.
-bool spare(const void* x, int64_t n, int64_t batch, int64_t rows, int64_t cols, const void* q, const void* qt) {
-  return apart(x, n, q, batch * rows * fp8_ld(cols)) && apart(x, n, qt, batch * cols * fp8_ld(rows));
+// Whether codes and scales (of nscale and nscale_t floats) of `rows` x `cols` values (of each of `batch`) spare x's n bytes.
+bool spare(const void* x, int64_t n, int64_t batch, int64_t rows, int64_t cols, const void* q, const void* s, int64_t nscale,
+           const void* qt, const void* st, int64_t nscale_t) {
+  return apart(x, n, q, batch * rows * fp8_ld(cols)) && apart(x, n, s, nscale * 4) && apart(x, n, qt, batch * cols * fp8_ld(rows)) &&
+         apart(x, n, st, nscale_t * 4);
+}
+// The same with a scale per row and 128 columns.
+bool spare_rows(const void* x, int64_t n, int64_t rows, int64_t cols, const void* q, const void* s, const void* qt, const void* st) {
+  return spare(x, n, 1, rows, cols, q, s, fp8_blocks(cols) * fp8_pitch(rows), qt, st, fp8_blocks(rows) * fp8_pitch(cols));
 }
 }  // namespace
 
@@ -345,7 +351,7 @@ mok_status mok_fp8_quantize(const void* x, int64_t rows, int32_t cols, uint8_t* 
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
   const mok_status rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
-  if (!spare(x, rows * cols * 2, 1, rows, cols, q, qt)) return MOK_ERR_INVALID_ARG;
+  if (!spare_rows(x, rows * cols * 2, rows, cols, q, s, qt, st)) return MOK_ERR_INVALID_ARG;
   const Fp8Source src{static_cast<const uint16_t*>(x), nullptr, nullptr, nullptr, rows, 1, 0};
   return launch_fp8_quantize(src, rows, cols, q, s, qt, st, K_FP8_QUANTIZE, static_cast<cudaStream_t>(stream)) ? MOK_ERR_CUDA
                                                                                                              : MOK_OK;
@@ -362,7 +368,7 @@ mok_status mok_fp8_quantize_routed(const mok_schedule* sched, int32_t gather, co
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
   rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
-  if (!spare(x, (gather ? z.T : z.rpad_max) * cols * 2, 1, z.rpad_max, cols, q, qt)) return MOK_ERR_INVALID_ARG;
+  if (!spare_rows(x, (gather ? z.T : z.rpad_max) * cols * 2, z.rpad_max, cols, q, s, qt, st)) return MOK_ERR_INVALID_ARG;
   const Fp8Source src{static_cast<const uint16_t*>(x), sched->row_token, sched->meta, sched->inv, z.T, z.K, gather};
   return launch_fp8_quantize(src, z.rpad_max, cols, q, s, qt, st, gather ? K_FP8_DISPATCH : K_FP8_QUANTIZE,
                              static_cast<cudaStream_t>(stream))
@@ -375,10 +381,10 @@ mok_status mok_fp8_quantize_blocks(const void* x, int32_t batch, int64_t rows, i
   if (batch < 1 || rows < 8 || rows % 8 != 0 || cols < 8 || cols % 8 != 0) return MOK_ERR_INVALID_ARG;
   if (rows > kMaxRows || batch > 65535) return MOK_ERR_UNSUPPORTED;
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
-  if ((!q && !qt) || (q != nullptr) != (s != nullptr) || (qt != nullptr) != (st != nullptr)) return MOK_ERR_INVALID_ARG;
   const mok_status rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
-  if (!spare(x, batch * rows * cols * 2, batch, rows, cols, q, qt)) return MOK_ERR_INVALID_ARG;
+  const int64_t scales = batch * fp8_blocks(rows) * fp8_blocks(cols);
+  if (!spare(x, batch * rows * cols * 2, batch, rows, cols, q, s, scales, qt, st, scales)) return MOK_ERR_INVALID_ARG;
   QuantArgs p{};
   p.src.x = static_cast<const uint16_t*>(x);
   p.rows = rows;

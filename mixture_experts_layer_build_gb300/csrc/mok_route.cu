@@ -179,7 +179,9 @@ mok_status mok_combine(const mok_schedule* sched, const void* rows, int32_t widt
   if (!width_ok(width)) return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return MOK_OK;
   if (!ok16(rows) || !ok16(out) || !sched->topk_weights) return MOK_ERR_INVALID_ARG;
-  if (!apart(out, token_bytes(z, width), rows, row_bytes(z, width))) return MOK_ERR_INVALID_ARG;
+  if (!apart(out, token_bytes(z, width), rows, row_bytes(z, width)) ||
+      !apart(out, token_bytes(z, width), sched->topk_weights, z.R * 4))
+    return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_combine(static_cast<const uint16_t*>(rows), sched->inv, sched->topk_weights, z.T, z.K, width,
                                   static_cast<uint16_t*>(out), K_ROUTE_COMBINE, static_cast<cudaStream_t>(stream)));
 }
@@ -195,7 +197,7 @@ mok_status mok_combine_backward(const mok_schedule* sched, const void* rows, con
   const int64_t nr = row_bytes(z, width), nt = token_bytes(z, width), nw = z.R * 4;
   if ((drows != rows && !apart(drows, nr, rows, nr)) || !apart(drows, nr, dout, nt) || !apart(d_topk_weights, nw, rows, nr) ||
       !apart(d_topk_weights, nw, dout, nt) || !apart(d_topk_weights, nw, drows, nr) ||
-      !apart(d_topk_weights, nw, sched->topk_weights, nw))
+      !apart(d_topk_weights, nw, sched->topk_weights, nw) || !apart(drows, nr, sched->topk_weights, nw))
     return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_combine_backward(z, *sched, rows, dout, width, drows, d_topk_weights,
                                            static_cast<cudaStream_t>(stream)));

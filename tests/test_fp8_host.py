@@ -136,6 +136,25 @@ def test_routes_workspace(mok):
     assert f(None, n) == BAD and f(264, n) == BAD and f(256, n, None) == BAD and f(256, n - 1) == SMALL
 
 
+def test_scales_weights_and_workspaces_over_inputs(mok):
+    L, big = mok._lib, 1 << 24
+    q = L.mok_fp8_quantize
+    assert q(big, 4, 64, 2 * big, big + 496, None, None, None) == BAD  # scales over x
+    assert q(big, 4, 64, None, None, 2 * big, big - 240, None) == BAD
+    s = schedule(mok)
+    p, n = ctypes.byref(s), s.rpad_max * 128
+    assert L.mok_fp8_quantize_routed(p, 0, big, 64, 2 * big, big + n - 16, None, None, None) == BAD
+    assert L.mok_fp8_quantize_blocks(big, 2, 64, 64, 2 * big, big + 16, None, None, None) == BAD
+    assert L.mok_fp8_quantize_blocks(big, 2, 64, 64, None, None, 2 * big, big + 2 * 8192 - 16, None) == BAD
+    s.topk_weights = big  # of combine: its output, and its gradient's
+    assert L.mok_combine(p, 2 * big, 64, big, None) == BAD
+    assert L.mok_combine_backward(p, 2 * big, 3 * big, 64, big, 4 * big, None) == BAD
+    w = matrix(mok, block=True, q=1 << 22, s=1 << 23)
+    f = lambda x, out, ws: L.mok_fp8_linear(x, 100, ctypes.byref(w), out, ws, 1 << 20, None, None)  # noqa: E731
+    assert f(big, 2 * big, 2 * big) == BAD and f(big, 2 * big, 1 << 22) == BAD  # the workspace over out and w
+    assert f(big, 2 * big, big) == BAD and f(big, 2 * big, (1 << 23) - 256) == BAD  # over x; over w's scales
+
+
 # ---- the binding ----
 def placed(mok, device="cuda:0", T=4, E=2, K=1):
     ws = _tensors(device, ws=(64, U8))["ws"]
