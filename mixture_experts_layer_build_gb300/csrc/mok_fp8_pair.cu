@@ -1,14 +1,11 @@
 // mok_fp8_pair.cu -- 8-bit products with a scale per 128 values for many rows: persistent CTA pairs.
 //
-// A cluster of two CTAs computes 256 x BN tiles (BN 256 or 128, of row-scaled products 192 as well) with tcgen05.mma.cta_group::2: each CTA loads its own 128 rows of P and half
-// of Q's rows, 32 KB per K block of 128 of a 256 x 256 tile.  The scales belong to whole K blocks, so every block's
-// products go to a TMEM accumulator of their own, one of 512 / BN in turn; eight warps per CTA drain it, two per TMEM lane
-// quarter with half of the columns each, times the block's scales into fp32 registers (BN / 2 per thread), while the
-// MMAs fill the next one.  A tile's output goes through shared memory and leaves by TMA while the next tile's blocks are in
-// the tensor cores.
-//
-// (Measured and not taken: 256-column tiles on four accumulators of 128 columns, two MMA groups per K block, 8192 x 8192 x
-// 8192 504 us against 400: A is read from shared memory twice.)
+// A cluster of two CTAs computes 256 x BN tiles (BN 256 or 128, of row-scaled products 192 as well) with
+// tcgen05.mma.cta_group::2: each CTA loads its own 128 rows of P and half of Q's rows, 32 KB per K block of 128 of a 256 x 256
+// tile.  The scales belong to whole K blocks, so every block's products go to a TMEM accumulator of their own, one of
+// 512 / BN in turn; eight warps per CTA drain it, two per TMEM lane quarter with half of the columns each, times the
+// block's scales into fp32 registers (BN / 2 per thread), while the MMAs fill the next one.  A tile's output goes through
+// shared memory and leaves by TMA while the next tile's blocks are in the tensor cores.
 //
 // Modes: dense rows; a schedule's rows against one matrix per expert (the units of 256 rows are counted from the
 // expert counts on the device, by every CTA for itself); weight gradients, whose K blocks are the 128-row blocks
@@ -16,9 +13,9 @@
 //
 // What bounds it: an accumulator is free for new MMAs once all of its columns have been read, and there are two of 256
 // columns, so a K block takes half of MMAs + commit + drain + release: 0.43 us (0.30 where nothing is drained: the loads
-// from L2), of which the reads of TMEM are 0.04 and the multiply-adds 0.05.  Measured: 4096 x 7168 x 2048 56 us (2,150
-// TFLOP/s; a library product with one scale for all 43), 8192 x 8192 x 8192 416 us (2,640; 282), both operands row-scaled
-// 71 and 550: twice the multiply-adds, and column scales from shared memory.  Per tile 1.2 us more for its output.
+// from L2), of which the reads of TMEM are 0.04 and the multiply-adds 0.05.  Measured: 4096 x 7168 x 2048 55 us (2,170
+// TFLOP/s; a library product with one scale for all 43), 8192 x 8192 x 8192 409 us (2,690; 282), both operands row-scaled
+// 71 and 547: twice the multiply-adds, and column scales from shared memory.  Per tile 1.2 us more for its output.
 // Measured and not kept: a release at cluster scope per K block (a memory barrier: 110 us for 56); four accumulators of 128
 // columns, two MMA groups per block (504 us for 8192 cubed: A is read from shared memory twice); scales fetched by the
 // drain warps (a column-scaled block waits 0.15 us more); column scales broadcast to a thread per row (588 us for 550); four
