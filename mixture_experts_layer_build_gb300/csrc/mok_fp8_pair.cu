@@ -67,27 +67,34 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
       : "r"(taddr));
 }
 
-template <int BN, bool COLVEC>
+// ALT: the two drain warpgroups take tiles of 128 columns in turn, each with accumulators and scale slots of its own, so that
+// one's output leaves while the other drains: for row-scaled products with few K blocks, such as experts' weight gradients
+// (64 experts with 384 rows each, 1024 x 2048: 139 us in tiles of 256, 112 to 116 so; without any output 91, without
+// multiply-adds either 71; with one staging box per warp 121, stores straight from registers 140).
+template <int BN, bool COLVEC, bool ALT>
 struct Cfg {
-  static constexpr int HB = BN / 2;      // columns of a drain thread
-  static constexpr int kLow = 72, kHigh = BN == 256 ? 208 : 216;  // registers per thread
+  static_assert(!ALT || BN == 128, "a thread of an alternating group holds all of a tile's columns");
+  static constexpr int kGroups = ALT ? 2 : 1;
+  static constexpr int HB = ALT ? BN : BN / 2;  // columns of a drain thread
+  static constexpr int kLow = 72, kHigh = HB == 128 ? 208 : 216;  // registers per thread
   static_assert(COLVEC || HB == 64 || HB == 128, "a thread's columns are in one block of 128");
   static constexpr int kBox = HB % 64 == 0 ? 64 : 32;  // columns of a box of bf16 output (128 or 64 bytes)
-  static constexpr int kAccs = 512 / BN; // accumulators in TMEM
-  static constexpr uint32_t kQBytes = HB * 128, kStage = 16384 + kQBytes, kTx = 2 * kStage;
-  static constexpr uint32_t kStaging = 4096;     // per drain warp: a box of 32 rows x 128 bytes
-  // scales of a K block: the CTA's 128 rows', and (COLVEC) the tile's columns'.  A slot is filled again once the MMAs of
-  // kStages blocks before have ended, that is once the blocks two accumulators further back have been drained.
-  static constexpr int kSlots = BN == 256 ? 8 : 12;
+  static constexpr int kAccs = 512 / BN / kGroups;     // accumulators in TMEM, of a group
+  static constexpr uint32_t kQBytes = BN / 2 * 128, kStage = 16384 + kQBytes, kTx = 2 * kStage;
+  static constexpr int kBoxes = ALT ? 2 : 1;     // boxes of 32 rows x 128 bytes that a drain warp stages output in
+  static constexpr uint32_t kStaging = kBoxes * 4096;
+  // scales of a K block: the CTA's 128 rows', and (COLVEC) the tile's columns'.  A group's slot is filled again once the MMAs of
+  // kStages blocks before have ended, and so the group's blocks kAccs further back have been drained.
+  static constexpr int kSlots = ALT ? 8 : BN == 256 ? 8 : 12;
   static constexpr uint32_t kScales = 512 + (COLVEC ? BN * 4 : 0);
   static constexpr uint32_t kMost = 227328;      // 5 KB of 227 are static
-  static constexpr uint32_t kFixed = 1024 + 8 * kStaging + kSlots * kScales + 512;
+  static constexpr uint32_t kFixed = 1024 + 8 * kStaging + kGroups * kSlots * kScales + 512;
   static constexpr int kStages = (kMost - kFixed) / kStage < 8 ? (kMost - kFixed) / kStage : 8;
   static constexpr uint32_t kStagingOff = kStages * kStage;
   static constexpr uint32_t kScaleOff = kStagingOff + 8 * kStaging;
-  static constexpr uint32_t kBarOff = kScaleOff + kSlots * kScales;
+  static constexpr uint32_t kBarOff = kScaleOff + kGroups * kSlots * kScales;
   static constexpr uint32_t kSmem = 1024 + kBarOff + 512;
-  static_assert(2 * kStages + 2 * kAccs + 1 + kSlots <= 48, "barriers fit");
+  static_assert(2 * kStages + kGroups * (2 * kAccs + kSlots) + 1 <= 48, "barriers fit");
   static_assert(kSlots > kStages + kAccs, "scales stay until they are used");
 };
 
@@ -171,11 +178,11 @@ __device__ __forceinline__ int count_units(const Fp8Problem& g, int* prefix, int
   return total;
 }
 
-template <int BN, bool COLVEC>
+template <int BN, bool COLVEC, bool ALT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ PairMaps t, const PairArgs a) {
-  using C = Cfg<BN, COLVEC>;
-  constexpr int S = C::kStages, HB = C::HB, kAccs = C::kAccs;
+  using C = Cfg<BN, COLVEC, ALT>;
+  constexpr int S = C::kStages, HB = C::HB, kAccs = C::kAccs, kAll = C::kGroups * kAccs;
   extern __shared__ uint8_t smem_raw[];
   __shared__ int prefix[kMaxExperts];
   __shared__ int wsum[kThreads / 32];
@@ -192,8 +199,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (S + s); };
   auto tfull = [&](int b) { return bar0 + 8u * (2 * S + b); };
-  auto tempty = [&](int b) { return bar0 + 8u * (2 * S + kAccs + b); };
-  const uint32_t drain = bar0 + 8u * (2 * S + 2 * kAccs);
+  auto tempty = [&](int b) { return bar0 + 8u * (2 * S + kAll + b); };
+  const uint32_t drain = bar0 + 8u * (2 * S + 2 * kAll);
   auto sfull = [&](int i) { return drain + 8u * (1 + i); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
@@ -203,12 +210,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int b = 0; b < kAccs; ++b) {
+    for (int b = 0; b < kAll; ++b) {
       mbar_init(tfull(b), 1);
-      mbar_init(tempty(b), 16);  // eight warps of each CTA
+      mbar_init(tempty(b), 16 / C::kGroups);  // the warps that drain it, of both CTAs
     }
     mbar_init(drain, 1);
-    for (int i = 0; i < C::kSlots; ++i) mbar_init(sfull(i), 1);
+    for (int i = 0; i < C::kGroups * C::kSlots; ++i) mbar_init(sfull(i), 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&t.p);
@@ -232,7 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     int ahead = 0;
     auto load_q = [&](const Unit& w, int kb, int st) {
-      tma_load_2d_pair(base + st * C::kStage + 16384, &t.q, mapa_shared(full(st), 0), (w.kb0 + kb) * 128, w.q0 + rank * HB);
+      tma_load_2d_pair(base + st * C::kStage + 16384, &t.q, mapa_shared(full(st), 0), (w.kb0 + kb) * 128, w.q0 + rank * (BN / 2));
     };
     if (g.early_q && pair < units) {  // weights: nothing that still runs writes them
       Unit w;
@@ -245,7 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     }
     pdl_wait();
-    int st = 0, issued = 0, slot = 0;
+    int st = 0, issued = 0, slot = 0, slot2 = C::kSlots;  // (the other group's next one)
     uint32_t ph = 0;
     bool ok = true;
     for (int u = pair; u < units && ok; u += a.pairs) {
@@ -274,11 +281,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (qb) bulk_load(to + 512, g.sq + k * g.q_pitch + w.j0, qb, sfull(slot));
         }
         ++issued;
-        if (++slot == C::kSlots) slot = 0;
+        if (!ALT) slot = slot + 1 == C::kSlots ? 0 : slot + 1;
+        else slot = slot + 1 == C::kSlots ? 0 : slot + 1 == 2 * C::kSlots ? C::kSlots : slot + 1;
         if (++st == S) {
           st = 0;
           ph ^= 1u;
         }
+      }
+      if (ALT) {
+        const int x = slot;
+        slot = slot2;
+        slot2 = x;
       }
     }
     if (!ok && rank == 0 && lane == 0)  // let the copies in flight land: the last one of each stage
@@ -287,14 +300,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (rank == 0) {
       pdl_wait();  // the kernel in front may take its time: no bounded wait starts before its end
-      int st = 0, n = 0;
+      int st = 0, n = 0, n2 = 0, first = 0;  // the group's blocks, and the other's; the group's first accumulator
       uint32_t ph = 0;
       bool ok = true;
       for (int u = pair; u < units && ok; u += a.pairs) {
         Unit w;
         pair_unit(g, prefix, u, BN, w);
         for (int kb = 0; kb < w.count; ++kb, ++n) {
-          const int b = n % kAccs;
+          const int b = first + n % kAccs;
           const uint32_t read = static_cast<uint32_t>(n / kAccs - 1) & 1u;  // parity of that accumulator's last drain
           ok = (n < kAccs || warp_wait(tempty(b), read, abort_flag, g.status)) && warp_wait(full(st), ph, abort_flag, g.status);
           if (!ok) break;
@@ -313,6 +326,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             ph ^= 1u;
           }
         }
+        if (ALT) {
+          const int x = n;
+          n = n2;
+          n2 = x;
+          first ^= kAccs;
+        }
       }
       if (elect_one()) umma_commit_pair(drain);  // every MMA issued has ended before TMEM is freed, in both CTAs
     }
@@ -322,13 +341,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kHigh));
-    const int q = warp & 3, dw = warp - kDrain, h = dw >> 2;
+    const int q = warp & 3, dw = warp - kDrain, h = ALT ? 0 : dw >> 2, group = ALT ? dw >> 2 : 0;
     pdl_wait();
     const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * HB;
-    const uint32_t stage = base + C::kStagingOff + static_cast<uint32_t>(dw) * C::kStaging;
+    const uint32_t stage0 = base + C::kStagingOff + static_cast<uint32_t>(dw) * C::kStaging;
+    uint32_t stage = stage0;
     int n = 0;
     bool ok = true;
-    for (int u = pair; u < units; u += a.pairs) {
+    for (int u = pair + group * a.pairs; u < units; u += C::kGroups * a.pairs) {
       Unit w;
       pair_unit(g, prefix, u, BN, w);
       const int j0 = w.j0 + h * HB;
@@ -343,11 +363,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           q_now = q_next;
           if (kb + 32 + lane < w.count) q_next = __ldg(qs + kb + 32 + lane);
         }
-        const int slot = n % C::kSlots;
+        const int slot = group * C::kSlots + n % C::kSlots;
         ok = warp_wait(sfull(slot), static_cast<uint32_t>(n / C::kSlots) & 1u, abort_flag, g.status);
         if (!ok) break;
         const float* sc = reinterpret_cast<const float*>(smem + C::kScaleOff + slot * C::kScales);
-        const int b = n % kAccs;
+        const int b = group * kAccs + n % kAccs;
         ok = warp_wait(tfull(b), static_cast<uint32_t>(n / kAccs) & 1u, abort_flag, g.status);
         if (!ok) break;
         tc_fence_after();
@@ -423,7 +443,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         return static_cast<uint32_t>(C::kBox == 64 ? r * 128 + ((k ^ (r & 7)) << 4) : r * 64 + ((k ^ (r >> 1 & 3)) << 4));
       };
       auto begin = [&] {
-        if (lane == 0) bulk_wait_read<0>();  // what was stored from here before has been read
+        if (lane == 0) bulk_wait_read<C::kBoxes - 1>();  // what was stored from here before has been read
         __syncwarp();
       };
       auto send = [&](int c0) {
@@ -433,6 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_store_2d(&t.out, stage, c0, row0);
           bulk_commit();
         }
+        if (C::kBoxes == 2) stage = 2 * stage0 + 4096 - stage;
       };
       if constexpr (COLVEC) {
         const int fr = lane >> 2, fc = lane & 3;  // row of the thread's first; its pair of columns in 8
@@ -551,31 +572,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BN, bool COLVEC>
+template <int BN, bool COLVEC, bool ALT>
 int launch_pair(const PairMaps& maps, const PairArgs& a, int kind, cudaStream_t stream) {
-  using C = Cfg<BN, COLVEC>;
+  using C = Cfg<BN, COLVEC, ALT>;
   static DeviceOnce once;
   const int se = once.run([](int* d) { return static_cast<int>(cudaGetDevice(d)); },
                           [] {
                             // what setmaxnreg hands round must be what the launch has: a wait for more would not end
                             cudaFuncAttributes f;
-                            const cudaError_t e = cudaFuncGetAttributes(&f, fp8_pair_kernel<BN, COLVEC>);
+                            const cudaError_t e = cudaFuncGetAttributes(&f, fp8_pair_kernel<BN, COLVEC, ALT>);
                             if (e != cudaSuccess) return static_cast<int>(e);
                             if (f.numRegs * kThreads < 128 * C::kLow + 256 * C::kHigh)
                               return static_cast<int>(cudaErrorInvalidConfiguration);
-                            return static_cast<int>(cudaFuncSetAttribute(fp8_pair_kernel<BN, COLVEC>,
+                            return static_cast<int>(cudaFuncSetAttribute(fp8_pair_kernel<BN, COLVEC, ALT>,
                                                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                                          static_cast<int>(C::kSmem)));
                           },
                           static_cast<int>(cudaErrorInvalidDevice));
   if (se) return se;
   trace_begin(stream, kind);
-  const cudaError_t e = launch_pdl(fp8_pair_kernel<BN, COLVEC>, dim3(2 * a.pairs), dim3(kThreads), C::kSmem, stream, maps, a);
+  const cudaError_t e = launch_pdl(fp8_pair_kernel<BN, COLVEC, ALT>, dim3(2 * a.pairs), dim3(kThreads), C::kSmem, stream, maps, a);
   trace_end(stream);
   return static_cast<int>(e);
 }
 
-template <int BN>
+template <int BN, bool ALT = false>
 int pair_width(const Fp8Operand& p, const Fp8Operand& q, PairArgs a, int64_t out_rows, int kind, cudaStream_t stream) {
   Fp8Problem& g = a.g;
   g.q_tiles = static_cast<int32_t>((q.rows + BN - 1) / BN);
@@ -594,10 +615,10 @@ int pair_width(const Fp8Operand& p, const Fp8Operand& q, PairArgs a, int64_t out
        : BN / 2 % 64 ? make_tmap_bf16_sw64(&m.out, g.out, N, R, 32, 32)
                      : make_tmap_bf16(&m.out, g.out, N, R, 64, 32));
   if (!good) return static_cast<int>(cudaErrorInvalidValue);
-  if constexpr (BN != 192) {
-    if (!q.row_scales) return launch_pair<BN, false>(m, a, kind, stream);
+  if constexpr (BN != 192 && !ALT) {
+    if (!q.row_scales) return launch_pair<BN, false, false>(m, a, kind, stream);
   }
-  return launch_pair<BN, true>(m, a, kind, stream);
+  return launch_pair<BN, true, ALT>(m, a, kind, stream);
 }
 
 }  // namespace
@@ -618,18 +639,41 @@ int launch_fp8_pair(const Fp8Operand& p, const Fp8Operand& q, Fp8Problem g, int6
   a.pairs = pairs;
   const int64_t mats = g.mode == FP8_WGRAD ? g.experts : 1;
   const int64_t out_rows = p.rows * mats;
-  // The tile width of fewest rounds of tiles, a round as long as its K blocks and 1 us besides.  (192 columns in row-scaled
-  // products only: with a scale per 128 x 128 values a block takes 420 ns of 192, hardly less than of 256.  1536 x 4096 over
-  // 8192: 82.8 us in tiles of 256, 69.5 of 192, 81.9 of 128.)  A schedule's rows count as spread evenly, a weight gradient's
-  // K likewise.
-  const int64_t k = g.mode == FP8_WGRAD ? (g.k_blocks + g.experts - 1) / g.experts : g.k_blocks;
-  auto cost = [&](int bn, int64_t ns) {
-    const int64_t tiles = static_cast<int64_t>(g.p_tiles) * ((q.rows + bn - 1) / bn) * mats;
-    return (tiles + pairs - 1) / pairs * (k * ns + 1000);
+  // The tile width whose rounds of tiles take least.  A round takes its K blocks and what its output adds; with outputs beyond L2
+  // at least its bytes at the rate at which they were seen to leave.  (192 columns in row-scaled products only: with a scale per
+  // 128 x 128 values a block takes 420 ns of 192, hardly less than of 256.)  A schedule's rows count as spread evenly, a
+  // weight gradient's K likewise.
+  auto rounds = [&](int bn) {
+    return (static_cast<int64_t>(g.p_tiles) * ((q.rows + bn - 1) / bn) * mats + pairs - 1) / pairs;
   };
-  const int64_t wide = cost(256, q.row_scales ? 615 : 450), narrow = cost(128, q.row_scales ? 400 : 310);
-  if (q.row_scales && cost(192, 490) < (wide < narrow ? wide : narrow)) return pair_width<192>(p, q, a, out_rows, kind, stream);
-  if (wide <= narrow) return pair_width<256>(p, q, a, out_rows, kind, stream);
+  if (!q.row_scales) {
+    if (rounds(256) * (g.k_blocks * int64_t{450} + 1000) <= rounds(128) * (g.k_blocks * int64_t{310} + 1000))
+      return pair_width<256>(p, q, a, out_rows, kind, stream);
+    return pair_width<128>(p, q, a, out_rows, kind, stream);
+  }
+  // Row-scaled, us of 256, 192 and 128 columns, and of 128 in turn (ALT), fp32 output (bf16 output); the weight gradients are 64
+  // experts' of 1024 x 2048, their rows per expert:
+  //   1536 x 4096 over 8192         84.3        70.3        82.9       105
+  //   4096 x 4096 over 512          24.0 (19.0) 24.1 (20.1) 22.4 (19.4) 19.4 (17.7)
+  //   4096 x 4096 over 2048         52.3 (47.0) 52.9 (49.2) 56.4 (52.4) 62.7 (61.4)
+  //   1000 x 2056 over 1003         11.2        9.8         8.4        9.5
+  //   weight gradient, 96 rows      102 (53)    105 (66)    98 (69)    106 (53)
+  //   weight gradient, 384 rows     139 (106)   154 (123)   139 (121)  112 (96)
+  //   weight gradient, 768 rows     184 (151)   209 (176)   222 (186)  184 (180)
+  const int64_t esize = g.out_f32 ? 4 : 2;
+  const bool beyond_l2 = out_rows * q.rows * esize > (int64_t{1} << 27);
+  auto cost = [&](int bn, int64_t ns, int64_t out_ns, int64_t gbs) {
+    const int64_t blocks = g.mode == FP8_WGRAD ? ns * g.k_blocks / g.experts - ns / 2 : ns * g.k_blocks;
+    const int64_t least = beyond_l2 ? 256 * bn * esize * pairs / gbs : 0;
+    return rounds(bn) * (blocks + out_ns > least ? blocks + out_ns : least);
+  };
+  const bool f32 = g.out_f32;
+  const int64_t c256 = cost(256, 615, f32 ? 2800 : 1600, 5200), c192 = cost(192, 505, f32 ? 2300 : 1300, 5200),
+                c128 = cost(128, 400, f32 ? 1400 : 800, 5200), alt = cost(128, 520, f32 ? 300 : 0, 4800) + 1500;
+  const int64_t others = c256 < c192 ? (c256 < c128 ? c256 : c128) : (c192 < c128 ? c192 : c128);
+  if (alt < others) return pair_width<128, true>(p, q, a, out_rows, kind, stream);
+  if (c256 == others) return pair_width<256>(p, q, a, out_rows, kind, stream);
+  if (c192 == others) return pair_width<192>(p, q, a, out_rows, kind, stream);
   return pair_width<128>(p, q, a, out_rows, kind, stream);
 }
 
