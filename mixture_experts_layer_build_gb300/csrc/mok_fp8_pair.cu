@@ -13,13 +13,13 @@
 //
 // What bounds it: an accumulator is free for new MMAs once all of its columns have been read, and there are two of 256
 // columns, so a K block takes half of MMAs + commit + drain + release: 0.43 us (0.30 where nothing is drained: the loads
-// from L2), of which the reads of TMEM are 0.04 and the multiply-adds 0.05.  Measured: 4096 x 7168 x 2048 55 us (2,170
-// TFLOP/s; a library product with one scale for all 43), 8192 x 8192 x 8192 409 us (2,690; 282), both operands row-scaled
-// 71 and 547: twice the multiply-adds, and column scales from shared memory.  Per tile 1.2 us more for its output.
+// from L2), of which the reads of TMEM are 0.04 and the multiply-adds 0.05.  Measured: 4096 x 7168 x 2048 54 us (2,210
+// TFLOP/s; a library product with one scale for all 43), 8192 x 8192 x 8192 395 to 404 us (2,750; 282), both operands row-scaled
+// 71 and 542: twice the multiply-adds, and column scales from shared memory.  Per tile 1.2 us more for its output.
 // Measured and not kept: a release at cluster scope per K block (a memory barrier: 110 us for 56); four accumulators of 128
 // columns, two MMA groups per block (504 us for 8192 cubed: A is read from shared memory twice); scales fetched by the
 // drain warps (a column-scaled block waits 0.15 us more); column scales broadcast to a thread per row (588 us for 550); four
-// or six stages for five, two staging boxes per warp, the schedule's tables in shared memory (no change); the next
+// or six stages for five, the schedule's tables in shared memory, or read a tile ahead (no change); the next
 // kernel let start early (its waiting CTAs: a training step of 64 experts 490 us for 459).
 #include "mok_ffn.cuh"  // warp_wait, wait_landed, elect_one, ordered_tile
 #include "mok_fp8_gemm.cuh"
@@ -30,8 +30,8 @@ namespace {
 
 // Warpgroup 0: warp 0 loads, warp 1 issues MMAs; warpgroups 1 and 2 drain.  A drain thread of a 256-column tile needs more
 // registers than a third of the SM's (168 of 384 threads): the first group gives up of its own.  What the groups have is at
-// most what the launch had: 128 x 72 + 256 x 216 = 384 x 168.  208 for the 256-column tiles: 8192 x 8192 x 8192 409 us, 414 with
-// 224, 453 with 200.
+// most what the launch had: 128 x 72 + 256 x 216 = 384 x 168.  208 for threads of 128 columns: 8192 x 8192 x 8192 409 us, 414 with
+// 224, 453 with 200 (with one staging box).
 constexpr int kThreads = 384;
 constexpr int kDrain = 4;  // the first drain warp
 constexpr int kMaxExperts = 1024;
@@ -81,7 +81,10 @@ struct Cfg {
   static constexpr int kBox = HB % 64 == 0 ? 64 : 32;  // columns of a box of bf16 output (128 or 64 bytes)
   static constexpr int kAccs = 512 / BN / kGroups;     // accumulators in TMEM, of a group
   static constexpr uint32_t kQBytes = BN / 2 * 128, kStage = 16384 + kQBytes, kTx = 2 * kStage;
-  static constexpr int kBoxes = ALT ? 2 : 1;     // boxes of 32 rows x 128 bytes that a drain warp stages output in
+  // boxes of 32 rows x 128 bytes that a drain warp stages output in: with two, a box is written while the other one is read, for a
+  // stage of loads less (8192 x 8192 x 8192 407 us with one, 395 with two; tiles of 192 columns, 1536 x 4096 over 8192, 70.6 and
+  // 71.8; 128 columns alike)
+  static constexpr int kBoxes = ALT || BN == 256 ? 2 : 1;
   static constexpr uint32_t kStaging = kBoxes * 4096;
   // scales of a K block: the CTA's 128 rows', and (COLVEC) the tile's columns'.  A group's slot is filled again once the MMAs of
   // kStages blocks before have ended, and so the group's blocks kAccs further back have been drained.

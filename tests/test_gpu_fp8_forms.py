@@ -33,6 +33,33 @@ def test_widths_rounds_and_long_sums(mok, M, N, K, block):
         assert torch.equal(got, mok.fp8_matmul(a, b, out_dtype=dt))
 
 
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("N,H", [(1000, 1032), (264, 2056), (1024, 512)])
+def test_weight_gradients_of_uneven_experts(mok, N, H, dt):
+    """Many tiles of a K block or two beside one expert's of sixteen, and of experts without rows: tiles that are taken in turn
+    end out of step."""
+    T, E, K = 2500, 24, 2
+    _, n = gen(N)
+    ids = torch.stack([torch.where(torch.arange(T) < 2000, 0, 1 + torch.arange(T) % 9), 10 + torch.arange(T) * 7 % 11], 1)
+    ids = ids.to(device="cuda", dtype=torch.int32)
+    sched = mok.Routes(T, E, K).build(ids, torch.ones((T, K), device="cuda"))
+    _, segments, _ = ref.layout(ids, E)
+    assert segments[0][1] == 2000 and segments[-1][1] == 0
+    _, at = mok.dispatch_fp8(sched, n(T, H).to(BF), transposed=True, rows=False)
+    _, dt_ = mok.fp8_quantize(n(sched.c.rpad_max, N).to(BF), transposed=True, rows=False, sched=sched)
+    R = sched.c.rpad_max
+    dw = mok.fp8_grouped_wgrad(sched, dt_, at, out_dtype=dt)
+    av, xv = (ref.values(ref.decode(m.q)[:, :R], m.s[:, :m.rows].T, (1, 128)) for m in (dt_, at))
+    for e, (r0, rn) in enumerate(segments):
+        if rn:
+            near(dw[e], *both(av[:, r0:r0 + rn], xv[:, r0:r0 + rn]), -(-rn // 128), ("dw", e))
+        else:
+            assert (dw[e] == 0).all()
+    for _ in range(3):
+        assert torch.equal(dw, mok.fp8_grouped_wgrad(sched, dt_, at, out_dtype=dt))
+    assert mok.mok_read_device_status(sched) == 0
+
+
 @pytest.mark.parametrize("M", range(1, 18))
 def test_few_rows(mok, M):
     """Around the numbers of rows at which a linear takes another way."""
