@@ -33,15 +33,21 @@ __global__ void __launch_bounds__(kRouteThreads) combine_backward_kernel(
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int buf = 0;
   for (int64_t i = blockIdx.x; i < T * parts; i += gridDim.x) {
-    const int64_t t = i / parts;
-    const int part = static_cast<int>(i - t * parts), k_end = K * (part + 1) / parts;
+    int64_t t = i;
+    int k = 0, k_end = K;
+    if (parts > 1) {  // (divisions that a token of its own need not wait for)
+      t = i / parts;
+      const int part = static_cast<int>(i - t * parts);
+      k = K * part / parts;
+      k_end = K * (part + 1) / parts;
+    }
     uint4 d[VECS];
 #pragma unroll
     for (int u = 0; u < VECS; ++u) {
       const int c = threadIdx.x + u * kRouteThreads;
       d[u] = c < vecs ? __ldcs(dout + t * vecs + c) : make_uint4(0, 0, 0, 0);
     }
-    for (int k = K * part / parts; k < k_end; ++k) {
+    for (; k < k_end; ++k) {
       const int64_t j = t * K + k;
       const int row = __ldg(inv + j);
       const float w = __ldg(s + j);
