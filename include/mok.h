@@ -554,7 +554,8 @@ MOK_API mok_status mok_ffn_backward(const mok_ffn_shape* shape, const void* x, c
 
 /* A schedule without the layer's staging buffers: the tables of mok_build_schedule for the same arguments (they
  * do not depend on H, I or the precision), in a workspace of mok_routes_workspace_bytes bytes, 256-byte aligned.
- * out->ws is NULL: mok_forward, mok_backward and mok_ep_* refuse it. */
+ * out->ws is NULL: mok_forward, mok_backward and mok_ep_* refuse it.  mok_router_backward takes it, with the tokens' width
+ * from its shape: H has to be theirs there. */
 MOK_API size_t mok_routes_workspace_bytes(const mok_config* cfg, const mok_shape* shape);
 MOK_API mok_status mok_build_routes(const mok_config* cfg, const mok_shape* shape, const int32_t* topk_ids,
                                     const float* topk_weights, void* ws, size_t ws_bytes, mok_schedule* out,

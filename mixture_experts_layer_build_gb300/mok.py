@@ -518,6 +518,11 @@ def mok_router_backward(sched: Schedule, x: torch.Tensor, w_router: torch.Tensor
                         topk_weights: torch.Tensor, d_topk_weights: torch.Tensor, dw_router: torch.Tensor,
                         d_bias: torch.Tensor | None, dx: torch.Tensor, accumulate_dx: bool, ws: torch.Tensor,
                         stream=None):
+    s = sched.c.shape
+    for t, rows, cols, name in ((x, s.T, s.H, "x"), (w_router, s.H, s.E, "w_router"), (dw_router, s.H, s.E, "dw_router"),
+                                (dx, s.T, s.H, "dx")):
+        if t is not None and t.numel() != rows * cols:
+            raise ValueError(f"{name} must have the schedule's {rows} x {cols} values, got shape {tuple(t.shape)}")
     _check(_lib.mok_router_backward(ctypes.byref(sched.c), _ptr(x, torch.bfloat16, "x"),
                                     _ptr(w_router, torch.bfloat16, "w_router"), _ptr(topk_ids, torch.int32, "ids"),
                                     _ptr(topk_weights, torch.float32, "topk_weights"),
@@ -546,7 +551,7 @@ def router_backward(sched: Schedule, x: torch.Tensor, w_router: torch.Tensor, to
                     topk_weights: torch.Tensor, d_topk_weights: torch.Tensor, with_bias: bool = False,
                     dx: torch.Tensor | None = None, stream=None):
     """Allocating form: returns (dw_router [H,E] fp32, d_bias [E] fp32 or None, dx [T,H] bf16).  A
-    given dx receives the router's share added in place."""
+    given dx receives the router's share added in place.  T, H and E are the schedule's (a Routes is given its H)."""
     if stream is not None:
         with _on_stream(stream):
             return router_backward(sched, x, w_router, topk_ids, topk_weights, d_topk_weights, with_bias, dx)
@@ -917,10 +922,11 @@ def mok_build_routes(cfg: mok_config, shape: mok_shape, topk_ids: torch.Tensor, 
 class Routes:
     """Owner of the workspace of a schedule of T tokens, K of E experts each, for the calls on routed rows (dispatch,
     combine, the grouped products): the layer's own schedule serves them as well.  `rows`: rows of a buffer of routed
-    rows.  A schedule is valid until the next build on the same Routes."""
+    rows.  A schedule is valid until the next build on the same Routes.  H: the tokens' width, a multiple of 128, which
+    router_backward takes from the schedule (the calls on routed rows take any)."""
 
-    def __init__(self, T: int, E: int, K: int, cfg: mok_config | None = None, device="cuda"):
-        self.cfg, self.shape = cfg or make_config(0, 0), make_shape(T, 128, 128, E, K)
+    def __init__(self, T: int, E: int, K: int, cfg: mok_config | None = None, device="cuda", H: int = 128):
+        self.cfg, self.shape = cfg or make_config(0, 0), make_shape(T, H, 128, E, K)
         self.ws = torch.empty(mok_routes_workspace_bytes(self.cfg, self.shape), dtype=torch.uint8, device=device)
         self.rows = T * K + E * 127
 
