@@ -632,11 +632,11 @@ MOK_API mok_status mok_fp8_matmul(const mok_fp8_matrix* a, const mok_fp8_matrix*
                                   uint32_t* status, void* stream);
 
 /* Bytes of device workspace (256-byte aligned) of mok_fp8_linear: x's codes and scales; 256 where it needs none (few rows: ws
- * may then be NULL).  0 for an unsupported shape. */
+ * may then be NULL).  0 for an unsupported shape: K as below, 0 <= M <= 8,388,480. */
 MOK_API size_t mok_fp8_linear_workspace_bytes(int64_t M, int64_t K);
 
 /* out [M, N] bf16 = x w^T for x [M, K] bf16, quantised on the way as by mok_fp8_quantize; w [N, K] MOK_FP8_BLOCKS, batch 1.
- * K a positive multiple of 8. */
+ * K a positive multiple of 8; M as mok_fp8_quantize's rows. */
 MOK_API mok_status mok_fp8_linear(const void* x, int64_t M, const mok_fp8_matrix* w, void* out, void* ws, size_t ws_bytes,
                                   uint32_t* status, void* stream);
 

@@ -497,7 +497,8 @@ PyObject* fp8_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
         !all_on(x->device(), {wq, given, status}))
       Py_RETURN_NONE;
     const size_t bytes = mok_fp8_linear_workspace_bytes(M, w.cols);
-    if (!bytes) return PyLong_FromLong(MOK_ERR_INVALID_ARG);
+    if (!bytes)  // rows or columns that the call refuses: it says how
+      return PyLong_FromLong(mok_fp8_linear(x->data_ptr(), M, &w, nullptr, nullptr, 0, nullptr, nullptr));
     Tensor out[1];
     const int rc = on_device(*x, [&] {
       out[0] = given ? *given : make({M, w.rows}, *x, at::kBFloat16);

@@ -70,7 +70,7 @@ mok_status mok_fp8_matmul(const mok_fp8_matrix* a, const mok_fp8_matrix* b, void
 }
 
 size_t mok_fp8_linear_workspace_bytes(int64_t M, int64_t K) {
-  if (M < 0 || M > kMax || K < 8 || K % 8 != 0 || K > kMax) return 0;
+  if (M < 0 || M > kFp8MaxRows || K < 8 || K % 8 != 0 || K > kMax) return 0;
   if (M <= kFp8XqRows) return 256;  // none is used
   const int64_t codes = (M * fp8_ld(K) + 255) / 256 * 256, scales = fp8_blocks(K) * fp8_pitch(M) * 4;
   return static_cast<size_t>((codes + scales + 255) / 256 * 256 + 256);
@@ -78,8 +78,9 @@ size_t mok_fp8_linear_workspace_bytes(int64_t M, int64_t K) {
 
 mok_status mok_fp8_linear(const void* x, int64_t M, const mok_fp8_matrix* w, void* out, void* ws, size_t ws_bytes,
                           uint32_t* status, void* stream) {
-  if (M < 0 || M > kMax || !matrix_ok(w, 1) || w->scaling != MOK_FP8_BLOCKS) return MOK_ERR_INVALID_ARG;
+  if (M < 0 || !matrix_ok(w, 1) || w->scaling != MOK_FP8_BLOCKS) return MOK_ERR_INVALID_ARG;
   if (w->rows < 8 || w->rows % 8 != 0 || w->cols < 8 || w->cols % 8 != 0) return MOK_ERR_INVALID_ARG;
+  if (M > kFp8MaxRows) return MOK_ERR_UNSUPPORTED;
   if (M == 0) return MOK_OK;
   const int64_t bytes = M * w->rows * 2;
   if (!ok16(x) || !ok16(out) || !apart(x, M * w->cols * 2, out, bytes) || !apart_from(*w, out, bytes)) return MOK_ERR_INVALID_ARG;

@@ -18,6 +18,7 @@ namespace mok {
 constexpr int kFp8Block = 128;        // values per scale: a K block of the products
 constexpr float kFp8Max = 448.0f;
 constexpr float kFp8Least = 0x1p-50f;  // of a block's largest magnitude
+constexpr int64_t kFp8MaxRows = int64_t{65535} * kFp8Block;  // that a quantisation takes: row tiles in a grid's y
 
 inline int64_t fp8_ld(int64_t cols) { return (cols + 15) / 16 * 16; }       // bytes between rows of codes
 inline int64_t fp8_pitch(int64_t rows) { return (rows + 3) / 4 * 4; }       // floats between K blocks of row scales

@@ -322,8 +322,6 @@ int launch_fp8_quantize(const Fp8Source& src, int64_t rows, int32_t cols, uint8_
 using namespace mok;
 
 namespace {
-constexpr int64_t kMaxRows = int64_t{65535} * 128;  // row tiles in a grid's y
-
 mok_status outputs_ok(const void* q, const void* s, const void* qt, const void* st) {
   if ((!q && !qt) || (q != nullptr) != (s != nullptr) || (qt != nullptr) != (st != nullptr)) return MOK_ERR_INVALID_ARG;
   if ((q && (!ok16(q) || !ok16(s))) || (qt && (!ok16(qt) || !ok16(st)))) return MOK_ERR_INVALID_ARG;
@@ -346,7 +344,7 @@ extern "C" {
 mok_status mok_fp8_quantize(const void* x, int64_t rows, int32_t cols, uint8_t* q, float* s, uint8_t* qt, float* st,
                             void* stream) {
   if (rows < 0 || cols < 8 || cols % 8 != 0) return MOK_ERR_INVALID_ARG;
-  if (rows > kMaxRows) return MOK_ERR_UNSUPPORTED;
+  if (rows > kFp8MaxRows) return MOK_ERR_UNSUPPORTED;
   if (rows == 0) return MOK_OK;
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
   const mok_status rc = outputs_ok(q, s, qt, st);
@@ -363,7 +361,7 @@ mok_status mok_fp8_quantize_routed(const mok_schedule* sched, int32_t gather, co
   mok_status rc = routed_sizes(sched, &z);
   if (rc != MOK_OK) return rc;
   if (cols < 8 || cols % 8 != 0 || (gather != 0 && gather != 1)) return MOK_ERR_INVALID_ARG;
-  if (z.rpad_max > kMaxRows) return MOK_ERR_UNSUPPORTED;
+  if (z.rpad_max > kFp8MaxRows) return MOK_ERR_UNSUPPORTED;
   if (z.T == 0) return MOK_OK;
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
   rc = outputs_ok(q, s, qt, st);
@@ -379,7 +377,7 @@ mok_status mok_fp8_quantize_routed(const mok_schedule* sched, int32_t gather, co
 mok_status mok_fp8_quantize_blocks(const void* x, int32_t batch, int64_t rows, int32_t cols, uint8_t* q, float* s,
                                    uint8_t* qt, float* st, void* stream) {
   if (batch < 1 || rows < 8 || rows % 8 != 0 || cols < 8 || cols % 8 != 0) return MOK_ERR_INVALID_ARG;
-  if (rows > kMaxRows || batch > 65535) return MOK_ERR_UNSUPPORTED;
+  if (rows > kFp8MaxRows || batch > 65535) return MOK_ERR_UNSUPPORTED;
   if (!ok16(x)) return MOK_ERR_INVALID_ARG;
   const mok_status rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
