@@ -548,7 +548,7 @@ MOK_API mok_status mok_ffn_backward(const mok_ffn_shape* shape, const void* x, c
  * each expert's segment is padded to a multiple of 128 rows, the layout ends at row Rpad = meta[0], and
  * rows from there on are neither read nor written.  Widths are multiples of 8 values up to 16384, of the caller's choice
  * (not the shape's H); tensors start on a 16-byte boundary; an output that overlaps an
- * input is refused but where a call says so.  Slots whose id is invalid have no row: they
+ * input, or a table of the schedule, is refused but where a call says so.  Slots whose id is invalid have no row: they
  * contribute nothing and their gradients are 0.
  * ------------------------------------------------------------------------------------------- */
 
@@ -584,7 +584,7 @@ MOK_API mok_status mok_combine_backward(const mok_schedule* sched, const void* r
  *                   first (a tile's rows are read together); the value of (r, c) is q[r][c] s[c/128][r];
  *   MOK_FP8_BLOCKS  a scale per 128 x 128 values, row-major: s [ceil(rows/128)][ceil(cols/128)].
  * Codes are row-major, K (the summed index) along the row, `ld` bytes between rows: a multiple of 16, >= cols.
- * Codes and scales start on a 16-byte boundary; no output or workspace may overlap an input (refused).  batch matrices of
+ * Codes and scales start on a 16-byte boundary; no output or workspace may overlap an input or a table of the schedule (refused).  batch matrices of
  * one shape follow one another: codes batch * rows * ld bytes, scales likewise; every matrix has its own blocks.
  * Quantisation: t = max(amax of the block, 2^-50); scale = t / 448; code = E4M3(v * (448 / t)), round to nearest
  * even; both divisions and the product are rounded to fp32.  A block that holds a NaN or an infinity gets a NaN scale

@@ -118,7 +118,8 @@ mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matri
     return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return MOK_OK;
   const int64_t bytes = a->rows * w->rows * 2;
-  if (!ok16(out) || !apart_from(*a, out, bytes) || !apart_from(*w, out, bytes)) return MOK_ERR_INVALID_ARG;
+  if (!ok16(out) || !apart_from(*a, out, bytes) || !apart_from(*w, out, bytes) || !apart_from_tables(*sched, z, out, bytes))
+    return MOK_ERR_INVALID_ARG;
   Fp8Problem g{};
   g.mode = FP8_GROUPED;
   g.k_blocks = static_cast<int32_t>(fp8_blocks(a->cols));
@@ -154,7 +155,8 @@ mok_status mok_fp8_grouped_wgrad(const mok_schedule* sched, const mok_fp8_matrix
   if (a->rows * z.E > kMax) return MOK_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t bytes = static_cast<int64_t>(z.E) * a->rows * b->rows * (dw_type == MOK_DT_FP32 ? 4 : 2);
-  if (!apart_from(*a, dw, bytes) || !apart_from(*b, dw, bytes)) return MOK_ERR_INVALID_ARG;
+  if (!apart_from(*a, dw, bytes) || !apart_from(*b, dw, bytes) || !apart_from_tables(*sched, z, dw, bytes))
+    return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return from_cuda(static_cast<int>(cudaMemsetAsync(dw, 0, static_cast<size_t>(bytes), s)));
   Fp8Problem g{};
   g.mode = FP8_WGRAD;

@@ -367,6 +367,10 @@ mok_status mok_fp8_quantize_routed(const mok_schedule* sched, int32_t gather, co
   rc = outputs_ok(q, s, qt, st);
   if (rc != MOK_OK) return rc;
   if (!spare_rows(x, (gather ? z.T : z.rpad_max) * cols * 2, z.rpad_max, cols, q, s, qt, st)) return MOK_ERR_INVALID_ARG;
+  if (!apart_from_tables(*sched, z, q, z.rpad_max * fp8_ld(cols)) || !apart_from_tables(*sched, z, qt, cols * fp8_ld(z.rpad_max)) ||
+      !apart_from_tables(*sched, z, s, 4 * fp8_blocks(cols) * fp8_pitch(z.rpad_max)) ||
+      !apart_from_tables(*sched, z, st, 4 * fp8_blocks(z.rpad_max) * fp8_pitch(cols)))
+    return MOK_ERR_INVALID_ARG;
   const Fp8Source src{static_cast<const uint16_t*>(x), sched->row_token, sched->meta, sched->inv, z.T, z.K, gather};
   return launch_fp8_quantize(src, z.rpad_max, cols, q, s, qt, st, gather ? K_FP8_DISPATCH : K_FP8_QUANTIZE,
                              static_cast<cudaStream_t>(stream))

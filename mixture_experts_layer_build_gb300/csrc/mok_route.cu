@@ -141,6 +141,12 @@ mok_status routed_sizes(const mok_schedule* s, Sizes* z) {
   return MOK_OK;
 }
 
+bool apart_from_tables(const mok_schedule& s, const Sizes& z, const void* out, int64_t n) {
+  return apart(out, n, s.counts, 4 * static_cast<int64_t>(z.E)) && apart(out, n, s.poff, 4 * (static_cast<int64_t>(z.E) + 1)) &&
+         apart(out, n, s.inv, 4 * z.R) && apart(out, n, s.mblocks, 16 * z.mblocks_max) && apart(out, n, s.meta, 4 * 16) &&
+         apart(out, n, s.row_token, 4 * z.rpad_max);
+}
+
 namespace {
 bool ok16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 mok_status from_cuda(int rc) { return rc == 0 ? MOK_OK : MOK_ERR_CUDA; }
@@ -162,7 +168,9 @@ mok_status mok_dispatch(const mok_schedule* sched, const void* x, int32_t width,
   if (rc != MOK_OK) return rc;
   if (!width_ok(width)) return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return MOK_OK;
-  if (!ok16(x) || !ok16(rows) || !apart(x, token_bytes(z, width), rows, row_bytes(z, width))) return MOK_ERR_INVALID_ARG;
+  if (!ok16(x) || !ok16(rows) || !apart(x, token_bytes(z, width), rows, row_bytes(z, width)) ||
+      !apart_from_tables(*sched, z, rows, row_bytes(z, width)))
+    return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_gather_rows(plain_rows(x), sched->inv, sched->row_token, sched->meta, z.T, z.K, z.rpad_max, width,
                                       static_cast<uint16_t*>(rows), K_DISPATCH, static_cast<cudaStream_t>(stream)));
 }
@@ -173,7 +181,9 @@ mok_status mok_dispatch_backward(const mok_schedule* sched, const void* drows, i
   if (rc != MOK_OK) return rc;
   if (!width_ok(width)) return MOK_ERR_INVALID_ARG;
   if (z.T == 0) return MOK_OK;
-  if (!ok16(drows) || !ok16(dx) || !apart(dx, token_bytes(z, width), drows, row_bytes(z, width))) return MOK_ERR_INVALID_ARG;
+  if (!ok16(drows) || !ok16(dx) || !apart(dx, token_bytes(z, width), drows, row_bytes(z, width)) ||
+      !apart_from_tables(*sched, z, dx, token_bytes(z, width)))
+    return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_combine(static_cast<const uint16_t*>(drows), sched->inv, nullptr, z.T, z.K, width,
                                   static_cast<uint16_t*>(dx), K_DISPATCH_BWD, static_cast<cudaStream_t>(stream)));
 }
@@ -186,7 +196,8 @@ mok_status mok_combine(const mok_schedule* sched, const void* rows, int32_t widt
   if (z.T == 0) return MOK_OK;
   if (!ok16(rows) || !ok16(out) || !sched->topk_weights) return MOK_ERR_INVALID_ARG;
   if (!apart(out, token_bytes(z, width), rows, row_bytes(z, width)) ||
-      !apart(out, token_bytes(z, width), sched->topk_weights, z.R * 4))
+      !apart(out, token_bytes(z, width), sched->topk_weights, z.R * 4) ||
+      !apart_from_tables(*sched, z, out, token_bytes(z, width)))
     return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_combine(static_cast<const uint16_t*>(rows), sched->inv, sched->topk_weights, z.T, z.K, width,
                                   static_cast<uint16_t*>(out), K_ROUTE_COMBINE, static_cast<cudaStream_t>(stream)));
@@ -203,7 +214,8 @@ mok_status mok_combine_backward(const mok_schedule* sched, const void* rows, con
   const int64_t nr = row_bytes(z, width), nt = token_bytes(z, width), nw = z.R * 4;
   if ((drows != rows && !apart(drows, nr, rows, nr)) || !apart(drows, nr, dout, nt) || !apart(d_topk_weights, nw, rows, nr) ||
       !apart(d_topk_weights, nw, dout, nt) || !apart(d_topk_weights, nw, drows, nr) ||
-      !apart(d_topk_weights, nw, sched->topk_weights, nw) || !apart(drows, nr, sched->topk_weights, nw))
+      !apart(d_topk_weights, nw, sched->topk_weights, nw) || !apart(drows, nr, sched->topk_weights, nw) ||
+      !apart_from_tables(*sched, z, drows, nr) || !apart_from_tables(*sched, z, d_topk_weights, nw))
     return MOK_ERR_INVALID_ARG;
   return from_cuda(launch_combine_backward(z, *sched, rows, dout, width, drows, d_topk_weights,
                                            static_cast<cudaStream_t>(stream)));

@@ -13,4 +13,7 @@ inline bool apart(const void* a, int64_t na, const void* b, int64_t nb) {
   return !a || !b || na <= 0 || nb <= 0 || x + static_cast<uintptr_t>(na) <= y || y + static_cast<uintptr_t>(nb) <= x;
 }
 
+// Whether n bytes at `out` spare every table of a schedule that a call on routed rows reads.
+bool apart_from_tables(const mok_schedule& s, const Sizes& z, const void* out, int64_t n);
+
 }  // namespace mok
