@@ -621,12 +621,12 @@ MOK_API mok_status mok_fp8_quantize_routed(const mok_schedule* sched, int32_t ga
 /* Scales per 128 x 128 values (MOK_FP8_BLOCKS) of `batch` matrices x [batch, rows, cols] bf16, and the same codes
  * transposed: q [batch][rows][cols rounded up to 16], s [batch][ceil(rows/128)][ceil(cols/128)]; qt [batch][cols][rows
  * rounded up to 16], st [batch][ceil(cols/128)][ceil(rows/128)].  q and s, or qt and st, may be NULL.  rows and cols
- * positive multiples of 8. */
+ * positive multiples of 8, rows up to 8,388,480, batch up to 65,535. */
 MOK_API mok_status mok_fp8_quantize_blocks(const void* x, int32_t batch, int64_t rows, int32_t cols, uint8_t* q, float* s,
                                            uint8_t* qt, float* st, void* stream);
 
 /* out [M, N] = a b^T; a [M, K] MOK_FP8_ROWS, b [N, K] of either scaling, batch 1.  out of out_type (mok_dtype), rounded
- * once.  M, K >= 0 (K = 0 gives zeros), N a positive multiple of 8; each below 2^31 - 1024.  status: device word (bit
+ * once.  M, K >= 0 (K = 0 gives zeros), N a positive multiple of 8; each up to 2^31 - 1024.  status: device word (bit
  * (1 << mok_status code) per problem seen, never cleared here) or NULL. */
 MOK_API mok_status mok_fp8_matmul(const mok_fp8_matrix* a, const mok_fp8_matrix* b, void* out, int32_t out_type,
                                   uint32_t* status, void* stream);
@@ -641,13 +641,14 @@ MOK_API mok_status mok_fp8_linear(const void* x, int64_t M, const mok_fp8_matrix
                                   uint32_t* status, void* stream);
 
 /* out[r] = a[r] w[expert of r]^T for every routed row: a [rpad_max, K] MOK_FP8_ROWS, w [E][N, K] MOK_FP8_BLOCKS (batch =
- * E), out [rpad_max, N] bf16.  Padding rows of out are not written (nor what lies behind Rpad).  N a positive multiple of 8. */
+ * E), out [rpad_max, N] bf16.  Padding rows of out are not written (nor what lies behind Rpad).  N a positive multiple of 8, K
+ * at least 8, E N up to 2^31 - 1024. */
 MOK_API mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matrix* a, const mok_fp8_matrix* w,
                                           void* out, void* stream);
 
 /* dw[e] = sum over expert e's rows of a[:, r] b[:, r]^T: a [N, rpad_max], b [K, rpad_max] MOK_FP8_ROWS, transposed routed
  * rows as mok_fp8_quantize_routed writes them; dw [E, N, K] of dw_type (an expert without rows gets zeros).  K = b's rows: a
- * positive multiple of 8. */
+ * positive multiple of 8; N at least 8, E N up to 2^31 - 1024 (MOK_ERR_UNSUPPORTED beyond). */
 MOK_API mok_status mok_fp8_grouped_wgrad(const mok_schedule* sched, const mok_fp8_matrix* a, const mok_fp8_matrix* b,
                                          void* dw, int32_t dw_type, void* stream);
 

@@ -44,6 +44,8 @@ mok_status product(const mok_fp8_matrix& a, const void* x, const mok_fp8_matrix&
   // Pairs from about a quarter of the SMs' worth of 128 x 128 tiles on, or where K is short; below, tiles, which can split K.
   // Measured, tiles and pairs: 129 x 2048 x 7168 12.3 and 20.2 us, 512 x 1536 x 4096 13.0 and 13.4, 1003 x 1000 x 2056 10.2 and 9.7,
   // 256 x 1024 x 1024 7.0 and 6.6, 1024 x 2048 x 2048 13.7 and 9.5; both row-scaled 512 x 512 x 2048 7.8 and 10.6.
+  // The rule does not look at how long K is beyond that: over 7168, 300 x 2048 17.8 and 21.2, 512 x 1280 17.4 and 21.1 run on pairs
+  // all the same (160 x 2432 21.9 and 21.1, 256 x 2432 22.6 and 21.2; 600 x 4096 over 4096 37.8 and 19.2).
   if (a.rows > 128 && (4 * fp8_blocks(a.rows) * fp8_blocks(b.rows) >= sm_count() || g.k_blocks <= 8))
     return from_cuda(launch_fp8_pair(operand(a), operand(b), g, 0, K_FP8_PAIR, stream));
   return from_cuda(launch_fp8_tile(operand(a), x, operand(b), g, a.rows, 0, K_FP8_TILE, stream));
@@ -134,7 +136,9 @@ mok_status mok_fp8_grouped_matmul(const mok_schedule* sched, const mok_fp8_matri
   // an expert with rows has one block that is not full at most
   const int64_t blocks = (z.R < z.E ? z.R : z.E) + z.R / 128;
   // Pairs from about 48 rows per expert on.  Measured, tiles and pairs: 128 experts, K = 4096, N = 1536, 32 rows each 187 and 190
-  // us, 64 rows 243 and 192; 64 experts, K = 2048, N = 1024, 24 rows 35.2 and 45.1, 48 rows 45.3 and 45.1.
+  // us, 64 rows 243 and 192; 64 experts, K = 2048, N = 1024, 24 rows 35.2 and 45.1, 48 rows 45.3 and 45.1; 8 experts, K = 4096, N =
+  // 1536, 128 rows 21.5 and 20.6.  The rule does not look at how many units there are: 4 experts, K = 7168, N = 1024, 48 rows 18.2 and
+  // 22.1, 192 rows 18.9 and 22.2.
   if (z.R >= 48 * static_cast<int64_t>(z.E))
     return from_cuda(launch_fp8_pair(operand(*a), operand(*w), g, (z.R < z.E ? z.R : z.E) + z.R / 256, K_FP8_GROUPED_PAIR,
                                      static_cast<cudaStream_t>(stream)));

@@ -3,8 +3,9 @@
 //   t = max(amax, 2^-50), scale = t / 448, code = E4M3(v * (448 / t))
 //   C[m, n] = sum over K blocks b, ascending, of sa[b][m] sb[b][n] * (sum over k in b of a[m, k] b[n, k])
 //
-// The inner sums are exact in the tensor cores' fp32 accumulator to its last bits (K = 128: 32 products of two 4-bit
-// significands at a time); the outer one is fp32 fused multiply-adds.
+// The product of two codes is exact; a block's 128 of them are added in the tensor core's fp32 accumulator, which cannot hold
+// every such sum (they span 2^-18 to 2^25): the tests allow 127 additions of 2^-24 of the magnitudes.  The outer sum is fp32
+// fused multiply-adds.
 #pragma once
 #include <cuda.h>
 

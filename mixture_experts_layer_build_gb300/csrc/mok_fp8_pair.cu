@@ -19,7 +19,7 @@
 // Measured and not kept: a release at cluster scope per K block (a memory barrier: 110 us for 56); four accumulators of 128
 // columns, two MMA groups per block (504 us for 8192 cubed: A is read from shared memory twice); scales fetched by the
 // drain warps (a column-scaled block waits 0.15 us more); column scales broadcast to a thread per row (588 us for 550); four
-// or six stages for five, the schedule's tables in shared memory, or read a tile ahead (no change); the next
+// or six stages for five (with one staging box per warp; with two there is room for four), the schedule's tables in shared memory, or read a tile ahead (no change); the next
 // kernel let start early (its waiting CTAs: a training step of 64 experts 490 us for 459).
 #include "mok_ffn.cuh"  // warp_wait, wait_landed, elect_one, ordered_tile
 #include "mok_fp8_gemm.cuh"
