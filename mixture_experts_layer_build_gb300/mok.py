@@ -5,8 +5,8 @@ dtypes / devices / contiguity, passes ``data_ptr()``s and the current CUDA strea
 status codes into exceptions.  PyTorch provides device memory and streams.
 
 Importing this module loads the library and raises ``ImportError`` when it is missing; the norm,
-dropout and feed-forward calls go through a compiled module beside it and raise ``ImportError``
-without it.  There is no fallback path.
+dropout, feed-forward, routed-row and 8-bit calls go through a compiled module beside it and raise
+``ImportError`` without it.  There is no fallback path.
 """
 from __future__ import annotations
 
@@ -27,8 +27,8 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 
 class _MissingBinding:
-    """In place of the compiled binding of the norm, dropout and feed-forward calls where it cannot be loaded: the routed
-    layer does without it, those calls raise."""
+    """In place of the compiled binding of the norm, dropout, feed-forward, routed-row and 8-bit calls where it cannot be
+    loaded: the routed layer does without it, those calls raise."""
 
     def __init__(self, why: Exception):
         self._why = why
